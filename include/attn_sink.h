@@ -48,7 +48,7 @@
  *    are caught on the device: the offending load is skipped and a sticky
  *    device status is set, which attn_sink_device_status() reports.
  *  - One call takes at most 65535 requests (batch) in the forward, paged
- *    forward, decode and append entry points, and at most 65535 * 128 query
+ *    forward, decode, append, tree, compaction and eviction entry points, and at most 65535 * 128 query
  *    rows per request in the forward ones (each is one grid dimension of the
  *    launch); larger calls return ATTN_SINK_ERR_UNSUPPORTED.
  */
@@ -76,8 +76,11 @@ enum {
     ATTN_SINK_DEV_PAGE_OOB = 1,      /* a page-table entry was outside [0, num_pages)       */
     ATTN_SINK_DEV_SEQLEN_OOB = 2,    /* a sequence length exceeded max_pages * page_size    */
     ATTN_SINK_DEV_TIMEOUT = 4,       /* a pipeline wait ran out of time; the kernel gave up */
-    ATTN_SINK_DEV_LAYOUT = 8         /* the dynamic shared-memory base was not 1024-byte
+    ATTN_SINK_DEV_LAYOUT = 8,        /* the dynamic shared-memory base was not 1024-byte
                                         aligned; the forward kernel did nothing            */
+    ATTN_SINK_DEV_ORDER = 16,        /* attn_sink_kv_compact: a source token that is not after
+                                        the one before it, or lies before its destination  */
+    ATTN_SINK_DEV_TREE = 32          /* attn_sink_tree_paged: a parent outside [-1, own index) */
 };
 
 /*
@@ -338,6 +341,162 @@ int attn_sink_bwd_strided(const attn_bf16* q, const attn_bf16* k, const attn_bf1
                           attn_bf16* dq, attn_bf16* dk, attn_bf16* dv,
                           long long dq_row_stride, long long dk_row_stride, long long dv_row_stride,
                           float* dsink, void* stream);
+
+/*
+ * Rotary positions.  Pair i of a head's first rotary_dim dimensions -- elements
+ * i and i + rotary_dim/2, or 2i and 2i + 1 when interleaved != 0 -- becomes
+ *     (x cos a - y sin a, y cos a + x sin a) * attn_scale,
+ *     a = positions[row] * inv_freq[i]   (-a when inverse != 0),
+ * and dimensions rotary_dim .. head_dim - 1 are copied bit for bit.  The gradient
+ * of the rotation is the same call with inverse = 1.  Angles are reduced to
+ * 2^-32 of a turn for every int32 position (negative ones included).
+ *
+ *   q, q_out     (rows, hq, head_dim) bf16; q_out may be q
+ *   k, k_out     (rows, hkv, head_dim) bf16, or both NULL (then hkv is ignored);
+ *                k_out may be k
+ *   *_row_stride distances in elements between consecutive rows (0: contiguous);
+ *                0 or >= heads * head_dim, multiples of 8
+ *   positions    (rows,) int32 device
+ *   inv_freq     (rotary_dim / 2,) fp64 device, radians per position
+ * An output may be its own input (same pointer and stride); any other overlap
+ * of outputs with inputs or each other gives undefined values.
+ * Supported: head_dim 64 or 128; rotary_dim even, 2 .. head_dim; at most 16384
+ * heads (hq + hkv).
+ */
+int attn_sink_rope(const attn_bf16* q, attn_bf16* q_out, const attn_bf16* k, attn_bf16* k_out,
+                   long long q_row_stride, long long q_out_row_stride, long long k_row_stride,
+                   long long k_out_row_stride, const int32_t* positions, const double* inv_freq, int rows,
+                   int hq, int hkv, int head_dim, int rotary_dim, int interleaved, int inverse,
+                   float attn_scale, void* stream);
+
+/*
+ * attn_sink_rope on new tokens' queries and keys, with the rotated keys and the
+ * values written into a paged cache in the same launch (attn_sink_kv_append's
+ * slots, checks and status bits).
+ *
+ *   q, q_out        (total_new, hq, head_dim) bf16; q_out may be q
+ *   k_new, v_new    (total_new, hkv, head_dim) bf16
+ *   cu_new          (batch+1,) int32 device, or NULL: request b's one new row is row b
+ *   positions       (total_new,) int32 device, or NULL: the row's logical token.
+ *                   (Drafted trees pass prefix + depth.)
+ *   total_new       host row count of q, k_new and v_new; cu_new[batch] must not
+ *                   exceed it (rows past it are left alone, ATTN_SINK_DEV_SEQLEN_OOB)
+ * Rows of q_out behind the last request's are left as they were.  Everything
+ * else as in attn_sink_rope (forward rotation) and attn_sink_kv_append.
+ * Supported: head_dim 64 or 128; at most 16384 heads (hq + 2 hkv), 65535 requests.
+ */
+int attn_sink_rope_kv_append(const attn_bf16* q, attn_bf16* q_out, const attn_bf16* k_new,
+                             const attn_bf16* v_new, long long q_row_stride, long long q_out_row_stride,
+                             long long k_row_stride, long long v_row_stride, const int32_t* cu_new,
+                             const int32_t* positions, const double* inv_freq, const int32_t* seqlens,
+                             const int32_t* page_table, int max_pages, int batch, int total_new, int hq,
+                             int hkv, int head_dim, int rotary_dim, int page_size, int num_pages,
+                             int max_new, int interleaved, float attn_scale, attn_bf16* k_cache,
+                             attn_bf16* v_cache, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens over a paged cache (the check of a
+ * speculative draft).  Request b's rows [cu_seqlens_q[b], cu_seqlens_q[b+1]) are
+ * its n nodes, in the order of the last n of its seqlens_k[b] cached tokens
+ * (their K/V are in the cache already: attn_sink_kv_append or
+ * attn_sink_rope_kv_append).  Node i hangs on node parents[row i] of the same
+ * request, an earlier one, or on the prefix (the other P = seqlens_k[b] - n
+ * tokens) when that is -1.  Nodes on the prefix have depth 0, others one more
+ * than their parent; node i stands at position P + depth and sees the prefix,
+ * its ancestors and itself, each by the first/last-window rule on positions.
+ *
+ *   q            (total_q, hq, head_dim) bf16
+ *   parents      (total_q,) int32 device, each in [-1, own index in the request);
+ *                any other value is read as -1 and sets ATTN_SINK_DEV_TREE
+ *   max_seqlen_q host upper bound of n, at most 256.  Rows of a request past it
+ *                are left alone and set ATTN_SINK_DEV_SEQLEN_OOB.
+ *   max_seqlen_k host estimate of the largest seqlens_k: plans the split of the
+ *                keys over the GPU only (results do not depend on it but for rounding)
+ *   out          (total_q, hq, head_dim) bf16
+ *   lse          (hq, total_q) fp32, as in attn_sink_fwd; may be NULL
+ * A request with fewer cached tokens than nodes sees no key (out 0, lse the
+ * sink) and sets ATTN_SINK_DEV_SEQLEN_OOB.  Keys read through an out-of-range
+ * page id take no weight.  Rows of out and lse behind the last request's are
+ * left as they were.  Cache slots that a request does not own never reach its results.
+ * Supported: head_dim 64 or 128; hq % hkv == 0, hq / hkv <= 128; page_size a
+ * power of two >= 8.  No gradient.
+ */
+int attn_sink_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                         const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+                         const int32_t* seqlens_k, const int32_t* parents, int batch, int total_q, int hq,
+                         int hkv, int head_dim, int page_size, int num_pages, int max_seqlen_q,
+                         int max_seqlen_k, const float* sink, int win_first, int win_last, float scale,
+                         attn_bf16* out, float* lse, void* stream);
+
+/*
+ * Moves cached rows of each request down in its token order: for j < counts[b],
+ * token src[b][h][j] of request b becomes its token base[b] + j, in K and V, for
+ * KV head h (src_heads == hkv) or for all heads (src_heads == 1).  With base the
+ * prefix's length and src an accepted path's tokens, the drafted rows that were
+ * accepted follow the prefix.
+ *
+ *   src      (batch, src_heads, max_rows) int32 device: increasing tokens,
+ *            src[j] >= base + j; a row that breaks this sets ATTN_SINK_DEV_ORDER and
+ *            is skipped, and the rows after it of its list may hold either value
+ *   counts   (batch,) int32 device, at most max_rows
+ *   base     (batch,) int32 device, or NULL: 0
+ * In place and safe for any such src: a row is read before it is overwritten.
+ * Pages that two requests share must not be written by either.  k_cache and
+ * v_cache must be different tensors.  Supported: head_dim 64 or 128.
+ */
+int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,
+                         const int32_t* src, const int32_t* counts, const int32_t* base, int batch,
+                         int src_heads, int max_rows, int hkv, int head_dim, int page_size, int num_pages,
+                         void* stream);
+
+/*
+ * attn_sink_decode_paged that also accumulates the attention weight of every
+ * cached token:
+ *     weights[b][h][t] += sum_{g in h} exp(s_gt - LSE_g)
+ * over the query heads g of KV head h (weight_heads == hkv) or over all query
+ * heads (weight_heads == 1), for the visible tokens t of request b.  A token's
+ * weights of one call and query head sum to 1 less the sink's share.
+ *
+ *   weights  (batch, weight_heads, weight_cap) fp32 device, updated in place; the
+ *            caller sets new tokens' entries to 0 before their first call.  Tokens
+ *            t >= weight_cap are left out and set ATTN_SINK_DEV_SEQLEN_OOB.
+ * The sums have a fixed order (no atomics).  Scratch: 4 bytes per query head and
+ * token that the page table can hold (or the window can show), and request.
+ * Everything else as in attn_sink_decode_paged; hq at most 4096.
+ */
+int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                                   const int32_t* page_table, int max_pages, const int32_t* seqlens,
+                                   int batch, int hq, int hkv, int head_dim, int page_size, int num_pages,
+                                   const float* sink, int win_first, int win_last, float scale,
+                                   float* weights, int weight_heads, int weight_cap, attn_bf16* out,
+                                   float* lse, void* stream);
+
+/*
+ * Eviction by accumulated weight.  A request with more than `budget` cached
+ * tokens keeps its first keep_first, its last keep_last and, of the others, the
+ * budget - keep_first - keep_last of largest weight (equal weights, +0 and -0
+ * among them: the earlier token; NaN below every number); the kept tokens become
+ * its tokens 0 .. budget - 1, in their order.  Each KV head keeps tokens of its
+ * own (weight_heads == hkv) or all heads the same ones (weight_heads == 1).
+ * Requests of at most `budget` tokens keep everything.
+ *
+ *   k_cache, v_cache  moved in place (different tensors; a page that two requests
+ *                share must not be written by either)
+ *   weights      (batch, weight_heads, weight_cap) fp32; lengths past weight_cap are
+ *                cut there (ATTN_SINK_DEV_SEQLEN_OOB)
+ *   weights_out  the same shape, or weights itself: the kept tokens' weights,
+ *                then 0 up to weight_cap
+ *   kept         (batch, weight_heads, budget) int32: the kept tokens, increasing,
+ *                then -1
+ *   new_seqlens  (batch,) int32: min(length, budget); must not be seqlens
+ * Supported: head_dim 64 or 128; 1 <= budget, 0 <= keep_first, keep_last,
+ * keep_first + keep_last <= budget; at most 32767 weight heads, 65535 requests.
+ */
+int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,
+                          const int32_t* seqlens, const float* weights, int batch, int weight_heads,
+                          int weight_cap, int hkv, int head_dim, int page_size, int num_pages, int budget,
+                          int keep_first, int keep_last, float* weights_out, int32_t* kept,
+                          int32_t* new_seqlens, void* stream);
 
 /*
  * The visible token ranges of each decode request, as the decode kernels

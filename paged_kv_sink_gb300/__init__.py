@@ -13,13 +13,19 @@ from ._lib import (  # noqa: F401
     attn_sink_decode_paged,
     attn_sink_decode_paged_append,
     attn_sink_decode_paged_noalloc,
+    attn_sink_decode_paged_weights,
+    attn_sink_evict_paged,
     attn_sink_fwd,
     attn_sink_fwd_host,
     attn_sink_fwd_kvpacked,
     attn_sink_fwd_paged,
     attn_sink_fwd_qkvpacked,
     attn_sink_kv_append,
+    attn_sink_kv_compact,
+    attn_sink_rope,
+    attn_sink_rope_kv_append,
     attn_sink_selftest_wait,
+    attn_sink_tree_paged,
     attn_sink_visible_ranges,
     attn_sink_visible_slots,
     device_status,
@@ -29,7 +35,9 @@ from .autograd import (  # noqa: F401
     attn_sink_func,
     attn_sink_kvpacked_func,
     attn_sink_qkvpacked_func,
+    attn_sink_rope_func,
     attn_sink_varlen_func,
     attn_sink_varlen_kvpacked_func,
     attn_sink_varlen_qkvpacked_func,
 )
+from .rope import attn_sink_rope_freqs  # noqa: F401

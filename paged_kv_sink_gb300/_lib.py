@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_PKG, "libattn_sink.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4
 DEV_PAGE_OOB, DEV_SEQLEN_OOB, DEV_TIMEOUT, DEV_LAYOUT = 1, 2, 4, 8
+DEV_ORDER, DEV_TREE = 16, 32
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -42,6 +43,15 @@ _SIGS = {
                                       _P, _P, _P],
     "attn_sink_fwd_paged": [_P, _P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I,
                             _I, _I, _F, _P, _P, _P],
+    "attn_sink_rope": [_P, _P, _P, _P, _L, _L, _L, _L, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P],
+    "attn_sink_rope_kv_append": [_P, _P, _P, _P, _L, _L, _L, _L, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                 _I, _I, _I, _I, _F, _P, _P, _P],
+    "attn_sink_tree_paged": [_P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _I, _I, _F,
+                             _P, _P, _P],
+    "attn_sink_kv_compact": [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P],
+    "attn_sink_decode_paged_weights": [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _F, _P, _I, _I,
+                                       _P, _P, _P],
+    "attn_sink_evict_paged": [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P],
     "attn_sink_visible_ranges": [_P, _I, _I, _I, _P, _P],
     "attn_sink_visible_slots": [_P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P],
     "attn_sink_device_status": [_P],
@@ -401,6 +411,255 @@ def attn_sink_bwd(q, k, v, sink, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max
                              _ptr(dv), _ptr(dsink), _stream(stream))
     _check("attn_sink_bwd", rc)
     return dq, dk, dv, dsink
+
+
+# ---------------------------------------------------------------------------
+# Entry points around the cache: rotary positions, drafted trees, accumulated
+# weights and eviction.  Their tensors must share one CUDA device (the library
+# launches on it, whatever the current device is) and have the sizes that the
+# pointers' readers assume; both are checked here.
+
+
+def _expect(name, t, dtype, shape, device=None, contiguous=True):
+    """Type, device and shape of an argument; None in `shape` stands for any extent."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise TypeError(f"{name} is on {t.device}, the other tensors on {device}")
+    got = t.shape
+    if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
+        raise TypeError(f"{name} must have shape {shape}, got {tuple(got)}")
+    if contiguous and not t.is_contiguous():
+        raise TypeError(f"{name} must be contiguous")
+
+
+def _expect_rows(name, t, shape, device=None):
+    """A (rows, heads, d) bf16 tensor whose heads are contiguous within a row;
+    returns its row stride (0: contiguous)."""
+    _expect(name, t, torch.bfloat16, shape, device, contiguous=False)
+    if t.is_contiguous():
+        return 0
+    rows, heads, d = t.shape
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or t.stride(0) < heads * d:
+        raise TypeError(f"{name}: heads must be contiguous within a row and rows must not overlap")
+    return t.stride(0)
+
+
+def _run(name, device, stream, *args):
+    """Calls the entry point on `device` and `stream` (None: the device's current one)."""
+    raw = stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
+    if device.index == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            rc = getattr(lib(), name)(*args, raw)
+    if rc != OK:
+        _check(name, rc)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _expect_inv_freq(inv_freq, d, device):
+    _expect("inv_freq", inv_freq, torch.float64, (None,), device)
+    if not 1 <= inv_freq.shape[0] <= d // 2:
+        raise TypeError(f"inv_freq must hold 1 .. head_dim / 2 frequencies, got {inv_freq.shape[0]}")
+
+
+def _expect_cache(k_cache, v_cache, page_table, device, batch=None):
+    _expect("k_cache", k_cache, torch.bfloat16, (None, None, None, None), device)
+    _expect("v_cache", v_cache, torch.bfloat16, k_cache.shape, device)
+    _expect("page_table", page_table, torch.int32, (batch, None), device)
+
+
+def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0, inverse=False, q_out=None,
+                   k_out=None, stream=None):
+    """Rotary positions: rotates the first 2 * len(inv_freq) dimensions of every head
+    of q (T, Hq, d) and k (T, Hkv, d, or None) by positions (T,) int32 times inv_freq
+    (fp64, radians per position; see attn_sink_rope_freqs), by the negative angle
+    with `inverse` (the gradient).  Rows may be strided (column ranges of a packed
+    buffer); an output may be its own input.  Returns (q_out, k_out or None)."""
+    dev = q.device
+    q_rs = _expect_rows("q", q, (None, None, None))
+    T, hq, d = q.shape
+    _expect("positions", positions, torch.int32, (T,), dev)
+    _expect_inv_freq(inv_freq, d, dev)
+    if q_out is None:
+        q_out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
+    qo_rs = _expect_rows("q_out", q_out, q.shape, dev)
+    hkv = k_rs = ko_rs = 0
+    if k is not None:
+        k_rs = _expect_rows("k", k, (T, None, d), dev)
+        hkv = k.shape[1]
+        if k_out is None:
+            k_out = torch.empty((T, hkv, d), dtype=k.dtype, device=dev)
+        ko_rs = _expect_rows("k_out", k_out, k.shape, dev)
+    elif k_out is not None:
+        raise TypeError("k_out is given without k")
+    _run("attn_sink_rope", dev, stream, q.data_ptr(), q_out.data_ptr(), _addr(k), _addr(k_out), q_rs, qo_rs, k_rs,
+         ko_rs, positions.data_ptr(), inv_freq.data_ptr(), T, hq, hkv, d, 2 * inv_freq.shape[0],
+         1 if interleaved else 0, 1 if inverse else 0, float(attn_scale))
+    return q_out, k_out
+
+
+def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seqlens, inv_freq, cu_new=None,
+                             max_new=None, positions=None, interleaved=False, attn_scale=1.0, q_out=None,
+                             stream=None):
+    """Rotates the new tokens' q (T, Hq, d) into q_out, and k_new (T, Hkv, d) into the
+    paged caches together with v_new, in one launch (see attn_sink_kv_append for the
+    slots).  `positions` (T,) int32 defaults to each row's logical token.  Returns
+    q_out; a q_out that is allocated here holds zeros in rows behind the last
+    request's when cu_new is given."""
+    dev = q.device
+    q_rs = _expect_rows("q", q, (None, None, None))
+    T, hq, d = q.shape
+    k_rs = _expect_rows("k_new", k_new, (T, None, d), dev)
+    hkv = k_new.shape[1]
+    v_rs = _expect_rows("v_new", v_new, k_new.shape, dev)
+    _expect("seqlens", seqlens, torch.int32, (None,), dev)
+    B = seqlens.shape[0]
+    _expect_cache(k_cache, v_cache, page_table, dev, B)
+    npages, ps = k_cache.shape[:2]
+    if k_cache.shape[2] != hkv or k_cache.shape[3] != d:
+        raise TypeError(f"k_cache must have {hkv} heads of {d}, got {tuple(k_cache.shape)}")
+    _expect_inv_freq(inv_freq, d, dev)
+    if cu_new is None:
+        if T != B:
+            raise TypeError(f"without cu_new every request has one new row: got {T} rows, {B} requests")
+        max_new = 1 if max_new is None else max_new
+    else:
+        _expect("cu_new", cu_new, torch.int32, (B + 1,), dev)
+        if max_new is None:
+            max_new = int((cu_new[1:] - cu_new[:-1]).max()) if B else 0
+    if positions is not None:
+        _expect("positions", positions, torch.int32, (T,), dev)
+    if q_out is None:
+        q_out = (torch.empty if cu_new is None else torch.zeros)((T, hq, d), dtype=q.dtype, device=dev)
+    qo_rs = _expect_rows("q_out", q_out, q.shape, dev)
+    _run("attn_sink_rope_kv_append", dev, stream, q.data_ptr(), q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+         q_rs, qo_rs, k_rs, v_rs, _addr(cu_new), _addr(positions), inv_freq.data_ptr(), seqlens.data_ptr(),
+         page_table.data_ptr(), page_table.shape[1], B, T, hq, hkv, d, 2 * inv_freq.shape[0], ps, npages,
+         int(max_new), 1 if interleaved else 0, float(attn_scale), k_cache.data_ptr(), v_cache.data_ptr())
+    return q_out
+
+
+def attn_sink_tree_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_k, parents, max_seqlen_q,
+                         max_seqlen_k, sink=None, win_first=0, win_last=0, scale=0.0, out=None, lse=None,
+                         return_lse=True, stream=None):
+    """Attention of trees of drafted tokens (at most 256 a request) over a paged cache
+    that holds their K/V.  q (T, Hq, d); parents (T,) int32: the node's parent as an
+    index in its request, -1 on the prefix.  Returns (out, lse (Hq, T))."""
+    dev = q.device
+    _expect("q", q, torch.bfloat16, (None, None, None))
+    T, hq, d = q.shape
+    _expect("seqlens_k", seqlens_k, torch.int32, (None,), dev)
+    B = seqlens_k.shape[0]
+    _expect_cache(k_cache, v_cache, page_table, dev, B)
+    npages, ps, hkv, dc = k_cache.shape
+    if dc != d:
+        raise TypeError(f"k_cache must have heads of {d}, got {dc}")
+    _expect("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev)
+    _expect("parents", parents, torch.int32, (T,), dev)
+    if sink is not None:
+        _expect("sink", sink, torch.float32, (hq,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect("out", out, torch.bfloat16, q.shape, dev)
+    if lse is not None:
+        _expect("lse", lse, torch.float32, (hq, T), dev)
+    elif return_lse:
+        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
+    _run("attn_sink_tree_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         page_table.data_ptr(), page_table.shape[1], cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
+         parents.data_ptr(), B, T, hq, hkv, d, ps, npages, int(max_seqlen_q), int(max_seqlen_k), _addr(sink),
+         int(win_first), int(win_last), float(scale), out.data_ptr(), _addr(lse))
+    return out, lse
+
+
+def attn_sink_kv_compact(k_cache, v_cache, page_table, src, counts, base=None, stream=None):
+    """Moves cached rows in place: token src[b, (h,) j] of request b becomes its token
+    base[b] + j (base None: j) for j < counts[b].  src (B, m) or (B, Hkv, m) int32,
+    increasing, src[j] >= base + j.  Returns (k_cache, v_cache)."""
+    dev = k_cache.device
+    _expect_cache(k_cache, v_cache, page_table, dev)
+    npages, ps, hkv, d = k_cache.shape
+    B = page_table.shape[0]
+    _expect("src", src, torch.int32, (B, None) if src.dim() == 2 else (B, hkv, None), dev)
+    _expect("counts", counts, torch.int32, (B,), dev)
+    if base is not None:
+        _expect("base", base, torch.int32, (B,), dev)
+    _run("attn_sink_kv_compact", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+         page_table.shape[1], src.data_ptr(), counts.data_ptr(), _addr(base), B, 1 if src.dim() == 2 else hkv,
+         src.shape[-1], hkv, d, ps, npages)
+    return k_cache, v_cache
+
+
+def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, weights, sink=None, win_first=0,
+                                   win_last=0, scale=0.0, out=None, lse=None, return_lse=True, stream=None):
+    """attn_sink_decode_paged that also adds every visible token's attention weight to
+    weights (B, Hkv or 1, cap) fp32, summed over the query heads of the KV head (or
+    all).  Returns (out, lse)."""
+    dev = q.device
+    _expect("q", q, torch.bfloat16, (None, None, None))
+    B, hq, d = q.shape
+    _expect_cache(k_cache, v_cache, page_table, dev, B)
+    npages, ps, hkv, dc = k_cache.shape
+    if dc != d:
+        raise TypeError(f"k_cache must have heads of {d}, got {dc}")
+    _expect("seqlens", seqlens, torch.int32, (B,), dev)
+    _expect("weights", weights, torch.float32, (B, None, None), dev)
+    if sink is not None:
+        _expect("sink", sink, torch.float32, (hq,), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _expect("out", out, torch.bfloat16, q.shape, dev)
+    if lse is not None:
+        _expect("lse", lse, torch.float32, (B, hq), dev)
+    elif return_lse:
+        lse = torch.empty((B, hq), dtype=torch.float32, device=dev)
+    _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+         page_table.data_ptr(), page_table.shape[1], seqlens.data_ptr(), B, hq, hkv, d, ps, npages, _addr(sink),
+         int(win_first), int(win_last), float(scale), weights.data_ptr(), weights.shape[1], weights.shape[2],
+         out.data_ptr(), _addr(lse))
+    return out, lse
+
+
+def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget, keep_first=0, keep_last=0,
+                          weights_out=None, kept=None, new_seqlens=None, stream=None):
+    """Brings every request with more than `budget` cached tokens down to it: kept are
+    the first keep_first, the last keep_last and the others of largest weight
+    (ties: the earlier token), moved to the front in their order, in place; weights
+    (B, Hkv or 1, cap) fp32 follow them (into weights_out if given) and are 0 behind.
+    Returns (new_seqlens (B,), kept (B, Hkv or 1, budget), -1 padded)."""
+    dev = k_cache.device
+    _expect_cache(k_cache, v_cache, page_table, dev)
+    npages, ps, hkv, d = k_cache.shape
+    B = page_table.shape[0]
+    _expect("seqlens", seqlens, torch.int32, (B,), dev)
+    _expect("weights", weights, torch.float32, (B, None, None), dev)
+    heads, cap = weights.shape[1:]
+    budget = int(budget)
+    if weights_out is None:
+        weights_out = weights
+    else:
+        _expect("weights_out", weights_out, torch.float32, weights.shape, dev)
+    if kept is None:
+        kept = torch.empty((B, heads, max(budget, 0)), dtype=torch.int32, device=dev)
+    else:
+        _expect("kept", kept, torch.int32, (B, heads, budget), dev)
+    if new_seqlens is None:
+        new_seqlens = torch.empty_like(seqlens)
+    else:
+        _expect("new_seqlens", new_seqlens, torch.int32, (B,), dev)
+    _run("attn_sink_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
+         page_table.shape[1], seqlens.data_ptr(), weights.data_ptr(), B, heads, cap, hkv, d, ps, npages, budget,
+         int(keep_first), int(keep_last), weights_out.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr())
+    return new_seqlens, kept
 
 
 def attn_sink_visible_ranges(seqlens, win_first, win_last, stream=None):

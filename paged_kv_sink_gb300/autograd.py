@@ -87,6 +87,41 @@ class _AttnSinkVarlenKVPacked(torch.autograd.Function):
         return dq, dkv, dsink, None, None, None, None, None, None, None, None
 
 
+class _AttnSinkRope(torch.autograd.Function):
+    """Its backward is the same function by the negative angle, so gradients of
+    gradients work too."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, interleaved, attn_scale, inverse):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions, inv_freq)
+        ctx.args = (interleaved, attn_scale, inverse)
+        q_out, k_out = _lib.attn_sink_rope(q, k, positions, inv_freq, interleaved, attn_scale, inverse)
+        return q_out if k is None else (q_out, k_out)
+
+    @staticmethod
+    def backward(ctx, dq, dk=None):
+        positions, inv_freq = ctx.saved_tensors
+        interleaved, attn_scale, inverse = ctx.args
+        args = (positions, inv_freq, interleaved, attn_scale, not inverse)
+        dq, dk = (None if g is None or not need else g.contiguous()
+                  for g, need in zip((dq, dk), ctx.needs_input_grad))
+        if dq is not None and dk is not None:
+            dq, dk = _AttnSinkRope.apply(dq, dk, *args)
+        elif dq is not None:
+            dq = _AttnSinkRope.apply(dq, None, *args)
+        elif dk is not None:
+            dk = _AttnSinkRope.apply(dk, None, *args)
+        return dq, dk, None, None, None, None, None
+
+
+def attn_sink_rope_func(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0):
+    """Rotary positions (``attn_sink_rope``), differentiable in q (T, Hq, d) and k
+    (T, Hkv, d) or None; the gradient is the rotation by the negative angle.
+    Returns (q_out, k_out), or q_out alone without k."""
+    return _AttnSinkRope.apply(q, k, positions, inv_freq, bool(interleaved), float(attn_scale), False)
+
+
 def attn_sink_varlen_func(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
                           learnable_sink=None, causal=True, win_first=0, win_last=0, softmax_scale=None,
                           return_lse=False):

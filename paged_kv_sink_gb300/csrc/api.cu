@@ -12,10 +12,13 @@
 #include "bwd.h"
 #include "common.cuh"
 #include "decode.h"
+#include "evict.h"
 #include "host_io.h"
 #include "kv_append.h"
 #include "selftest.h"
 #include "prefill.h"
+#include "rope.h"
+#include "tree.h"
 
 namespace {
 
@@ -145,7 +148,7 @@ namespace {
 int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache, const int32_t* page_table,
                int max_pages, const int32_t* seqlens, int batch, int hq, int hkv, int head_dim, int page_size,
                int num_pages, const float* sink, int win_first, int win_last, float scale, attn_bf16* out,
-               float* lse, cudaStream_t s) {
+               float* lse, cudaStream_t s, attn::decode::Weights* w = nullptr) {
     attn::decode::Args a;
     a.q = q;
     a.k_cache = k_cache;
@@ -167,12 +170,20 @@ int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_
     a.group = hq / hkv;
     a.scale = attn::resolve_scale(scale, head_dim);
     attn::decode::Plan pl = attn::decode::make_plan(a);
+    // partials, then (accumulated weights only) statistics and scores
+    const size_t scores_at = (pl.part_o_bytes + pl.part_ml_bytes + (size_t)batch * hq * sizeof(float2) + 255) & ~size_t(255);
+    size_t bytes = pl.part_o_bytes + pl.part_ml_bytes;
+    if (w) bytes = scores_at + (size_t)batch * hkv * pl.hblocks * pl.nvis_max * 8 * pl.nt * sizeof(float);
     Scratch ws;
-    cudaError_t e = ws.alloc(pl.part_o_bytes + pl.part_ml_bytes, s);
+    cudaError_t e = ws.alloc(bytes, s);
     if (e != cudaSuccess) return cuda_fail(e, "decode: scratch allocation");
     float* part_o = static_cast<float*>(ws.ptr);
     float2* part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws.ptr) + pl.part_o_bytes);
-    e = attn::decode::launch(a, pl, part_o, part_ml, s);
+    if (w) {
+        w->stats = reinterpret_cast<float2*>(static_cast<char*>(ws.ptr) + pl.part_o_bytes + pl.part_ml_bytes);
+        w->scores = reinterpret_cast<float*>(static_cast<char*>(ws.ptr) + scores_at);
+    }
+    e = attn::decode::launch(a, pl, part_o, part_ml, s, w);
     if (e != cudaSuccess) return cuda_fail(e, "decode: launch");
     return ATTN_SINK_OK;
 }
@@ -574,6 +585,45 @@ int bwd_impl(const attn_bf16* q, const attn_bf16* k, const attn_bf16* v, const l
     return ATTN_SINK_OK;
 }
 
+// Checks shared by the rotary entry points.
+int check_rope(const char* who, int rows, int hq, int hkv, int min_hkv, long long heads, int head_dim, int rotary_dim,
+               float attn_scale) {
+    if (rows < 0 || hq <= 0 || hkv < min_hkv)
+        return fail(ATTN_SINK_ERR_INVALID, "%s: sizes must be non-negative (heads positive)", who);
+    if (head_dim != 64 && head_dim != 128)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64, 128)", who, head_dim);
+    if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2)
+        return fail(ATTN_SINK_ERR_INVALID, "%s: rotary_dim %d must be even, from 2 to head_dim", who, rotary_dim);
+    if (heads > 16384) return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: %lld heads above 16384", who, heads);
+    if (!isfinite(attn_scale)) return fail(ATTN_SINK_ERR_INVALID, "%s: attn_scale must be finite", who);
+    return ATTN_SINK_OK;
+}
+
+// Sizes of a paged cache.
+int check_cache(const char* who, int batch, int max_pages, int page_size, int num_pages) {
+    if (batch < 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0)
+        return fail(ATTN_SINK_ERR_INVALID, "%s: sizes must be positive (batch may be 0)", who);
+    if ((long long)num_pages * page_size >= (1LL << 31) || (long long)max_pages * page_size >= (1LL << 31))
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: cache slots must fit in int32", who);
+    return ATTN_SINK_OK;
+}
+
+// Heads of the entry points that move cache rows.
+int check_moves(const char* who, const char* name, int heads, int hkv, int head_dim) {
+    if (head_dim != 64 && head_dim != 128)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64, 128)", who, head_dim);
+    if (heads != 1 && heads != hkv) return fail(ATTN_SINK_ERR_INVALID, "%s: %s %d must be 1 or hkv", who, name, heads);
+    if (heads > kMaxGridDim / 2)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: %s %d above %d", who, name, heads, kMaxGridDim / 2);
+    if ((long long)hkv * head_dim * 2 >= (1LL << 31))
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: a token's row must be below 2 GiB", who);
+    return ATTN_SINK_OK;
+}
+
+const __nv_bfloat16* as_bf16(const attn_bf16* p) { return reinterpret_cast<const __nv_bfloat16*>(p); }
+__nv_bfloat16* as_bf16(attn_bf16* p) { return reinterpret_cast<__nv_bfloat16*>(p); }
+long long row_stride(long long rs, int heads, int head_dim) { return rs ? rs : (long long)heads * head_dim; }
+
 }  // namespace
 
 extern "C" {
@@ -611,6 +661,285 @@ int attn_sink_bwd_strided(const attn_bf16* q, const attn_bf16* k, const attn_bf1
                     dsink, stream);
 }
 
+int attn_sink_rope(const attn_bf16* q, attn_bf16* q_out, const attn_bf16* k, attn_bf16* k_out,
+                   long long q_row_stride, long long q_out_row_stride, long long k_row_stride,
+                   long long k_out_row_stride, const int32_t* positions, const double* inv_freq, int rows, int hq,
+                   int hkv, int head_dim, int rotary_dim, int interleaved, int inverse, float attn_scale,
+                   void* stream) {
+    t_last_error.clear();
+    if ((k == nullptr) != (k_out == nullptr))
+        return fail(ATTN_SINK_ERR_INVALID, "rope: k and k_out are given together or not at all");
+    if (!k) hkv = 0;
+    int rc = check_rope("rope", rows, hq, hkv, k ? 1 : 0, hq + (long long)hkv, head_dim, rotary_dim, attn_scale);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_stride("rope", "q", q_row_stride, hq, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope", "q_out", q_out_row_stride, hq, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope", "k", k_row_stride, hkv, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope", "k_out", k_out_row_stride, hkv, head_dim)) != ATTN_SINK_OK)
+        return rc;
+    if (rows == 0) return ATTN_SINK_OK;
+    if (!q || !q_out || !positions || !inv_freq) return fail(ATTN_SINK_ERR_INVALID, "rope: NULL tensor pointer");
+    if (!aligned16(q) || !aligned16(q_out) || (k && (!aligned16(k) || !aligned16(k_out))))
+        return fail(ATTN_SINK_ERR_INVALID, "rope: q, k and the outputs must be 16-byte aligned");
+    attn::rope::Args a = {};
+    a.q = as_bf16(q);
+    a.q_out = as_bf16(q_out);
+    a.k = as_bf16(k);
+    a.k_out = as_bf16(k_out);
+    a.q_rs = row_stride(q_row_stride, hq, head_dim);
+    a.q_out_rs = row_stride(q_out_row_stride, hq, head_dim);
+    a.k_rs = row_stride(k_row_stride, hkv, head_dim);
+    a.k_out_rs = row_stride(k_out_row_stride, hkv, head_dim);
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.rows = rows;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.inverse = inverse ? 1 : 0;
+    a.attn_scale = attn_scale;
+    cudaError_t e = attn::rope::launch(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_rope_kv_append(const attn_bf16* q, attn_bf16* q_out, const attn_bf16* k_new, const attn_bf16* v_new,
+                             long long q_row_stride, long long q_out_row_stride, long long k_row_stride,
+                             long long v_row_stride, const int32_t* cu_new, const int32_t* positions,
+                             const double* inv_freq, const int32_t* seqlens, const int32_t* page_table,
+                             int max_pages, int batch, int total_new, int hq, int hkv, int head_dim, int rotary_dim,
+                             int page_size, int num_pages, int max_new, int interleaved, float attn_scale,
+                             attn_bf16* k_cache, attn_bf16* v_cache, void* stream) {
+    t_last_error.clear();
+    int rc = check_rope("rope_kv_append", total_new, hq, hkv, 1, hq + 2LL * hkv, head_dim, rotary_dim, attn_scale);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_cache("rope_kv_append", batch, max_pages, page_size, num_pages)) != ATTN_SINK_OK) return rc;
+    if (max_new < 0) return fail(ATTN_SINK_ERR_INVALID, "rope_kv_append: max_new must be >= 0");
+    if ((rc = check_stride("rope_kv_append", "q", q_row_stride, hq, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope_kv_append", "q_out", q_out_row_stride, hq, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope_kv_append", "k_new", k_row_stride, hkv, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("rope_kv_append", "v_new", v_row_stride, hkv, head_dim)) != ATTN_SINK_OK)
+        return rc;
+    if (batch == 0 || max_new == 0 || total_new == 0) return ATTN_SINK_OK;
+    if (!q || !q_out || !k_new || !v_new || !inv_freq || !seqlens || !page_table || !k_cache || !v_cache)
+        return fail(ATTN_SINK_ERR_INVALID, "rope_kv_append: NULL tensor pointer");
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) ||
+        !aligned16(v_cache))
+        return fail(ATTN_SINK_ERR_INVALID, "rope_kv_append: tensors must be 16-byte aligned");
+    if (!cu_new && (max_new != 1 || total_new < batch))
+        return fail(ATTN_SINK_ERR_INVALID,
+                    "rope_kv_append: without cu_new every request appends one row (max_new 1, total_new = batch)");
+    if ((rc = check_grid("rope_kv_append", batch, 0)) != ATTN_SINK_OK) return rc;
+    attn::rope::Args a = {};
+    a.q = as_bf16(q);
+    a.q_out = as_bf16(q_out);
+    a.k = as_bf16(k_new);
+    a.v = as_bf16(v_new);
+    a.q_rs = row_stride(q_row_stride, hq, head_dim);
+    a.q_out_rs = row_stride(q_out_row_stride, hq, head_dim);
+    a.k_rs = row_stride(k_row_stride, hkv, head_dim);
+    a.v_rs = row_stride(v_row_stride, hkv, head_dim);
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.rows = total_new;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.head_dim = head_dim;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved ? 1 : 0;
+    a.attn_scale = attn_scale;
+    a.cu_new = cu_new;
+    a.seqlens = seqlens;
+    a.page_table = page_table;
+    a.k_cache = as_bf16(k_cache);
+    a.v_cache = as_bf16(v_cache);
+    a.max_pages = max_pages;
+    a.batch = batch;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.max_new = max_new;
+    cudaError_t e = attn::rope::launch(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "rope_kv_append: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                         const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+                         const int32_t* seqlens_k, const int32_t* parents, int batch, int total_q, int hq, int hkv,
+                         int head_dim, int page_size, int num_pages, int max_seqlen_q, int max_seqlen_k,
+                         const float* sink, int win_first, int win_last, float scale, attn_bf16* out, float* lse,
+                         void* stream) {
+    t_last_error.clear();
+    if (total_q < 0 || hq <= 0 || hkv <= 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || win_first < 0)
+        return fail(ATTN_SINK_ERR_INVALID, "tree_paged: sizes must be non-negative (heads positive)");
+    int rc = check_cache("tree_paged", batch, max_pages, page_size, num_pages);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (head_dim != 64 && head_dim != 128)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "tree_paged: head_dim %d not supported (64, 128)", head_dim);
+    if (hq % hkv || hq / hkv > 128)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "tree_paged: hq must be a multiple of hkv, at most 128 times it");
+    if (page_size < 8 || (page_size & (page_size - 1)))
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "tree_paged: page_size %d not supported (a power of two >= 8)",
+                    page_size);
+    if (max_seqlen_q > attn::tree::kMaxNodes)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "tree_paged: max_seqlen_q %d above %d nodes per request", max_seqlen_q,
+                    attn::tree::kMaxNodes);
+    if (batch == 0 || total_q == 0 || max_seqlen_q == 0) return ATTN_SINK_OK;
+    if (!q || !k_cache || !v_cache || !page_table || !cu_seqlens_q || !seqlens_k || !parents || !out)
+        return fail(ATTN_SINK_ERR_INVALID, "tree_paged: NULL tensor pointer");
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return fail(ATTN_SINK_ERR_INVALID, "tree_paged: tensors must be 16-byte aligned");
+    if ((rc = check_grid("tree_paged", batch, 0)) != ATTN_SINK_OK) return rc;
+    attn::tree::Args a = {};
+    a.q = q;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.page_table = page_table;
+    a.cu_q = cu_seqlens_q;
+    a.seqlens_k = seqlens_k;
+    a.parents = parents;
+    a.sink = sink;
+    a.out = out;
+    a.lse = lse;
+    a.max_pages = max_pages;
+    a.batch = batch;
+    a.total_q = total_q;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.head_dim = head_dim;
+    a.page_size = page_size;
+    a.num_pages = num_pages;
+    a.max_seqlen_q = max_seqlen_q;
+    a.max_seqlen_k = max_seqlen_k;
+    a.win_first = win_first;
+    a.win_last = win_last;
+    a.scale = attn::resolve_scale(scale, head_dim);
+    std::string err;
+    cudaError_t e = attn::tree::launch(a, static_cast<cudaStream_t>(stream), &err);
+    if (e != cudaSuccess)
+        return fail(ATTN_SINK_ERR_CUDA, "tree_paged: %s: %s", err.c_str(), cudaGetErrorString(e));
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,
+                         const int32_t* src, const int32_t* counts, const int32_t* base, int batch, int src_heads,
+                         int max_rows, int hkv, int head_dim, int page_size, int num_pages, void* stream) {
+    t_last_error.clear();
+    if (hkv <= 0 || max_rows < 0) return fail(ATTN_SINK_ERR_INVALID, "kv_compact: sizes must be non-negative (heads positive)");
+    int rc = check_cache("kv_compact", batch, max_pages, page_size, num_pages);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_moves("kv_compact", "src_heads", src_heads, hkv, head_dim)) != ATTN_SINK_OK) return rc;
+    if (batch == 0 || max_rows == 0) return ATTN_SINK_OK;
+    if (!k_cache || !v_cache || !page_table || !src || !counts)
+        return fail(ATTN_SINK_ERR_INVALID, "kv_compact: NULL tensor pointer");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(ATTN_SINK_ERR_INVALID, "kv_compact: caches must be 16-byte aligned");
+    if (k_cache == v_cache) return fail(ATTN_SINK_ERR_INVALID, "kv_compact: k_cache and v_cache must differ");
+    if ((rc = check_grid("kv_compact", batch, 0)) != ATTN_SINK_OK) return rc;
+    attn::evict::MoveArgs m = {};
+    m.k_cache = as_bf16(k_cache);
+    m.v_cache = as_bf16(v_cache);
+    m.page_table = page_table;
+    m.src = src;
+    m.counts = counts;
+    m.base = base;
+    m.max_pages = max_pages;
+    m.batch = batch;
+    m.heads = src_heads;
+    m.hkv = hkv;
+    m.head_dim = head_dim;
+    m.page_size = page_size;
+    m.num_pages = num_pages;
+    m.max_rows = max_rows;
+    cudaError_t e = attn::evict::launch_move(m, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_compact: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                                   const int32_t* page_table, int max_pages, const int32_t* seqlens, int batch,
+                                   int hq, int hkv, int head_dim, int page_size, int num_pages, const float* sink,
+                                   int win_first, int win_last, float scale, float* weights, int weight_heads,
+                                   int weight_cap, attn_bf16* out, float* lse, void* stream) {
+    t_last_error.clear();
+    int rc = attn::validate_decode("decode_weights", q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq,
+                                   hkv, head_dim, page_size, num_pages, win_first, out);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (weight_heads != 1 && weight_heads != hkv)
+        return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_heads %d must be 1 or hkv", weight_heads);
+    if (weight_cap < 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_cap must be >= 0");
+    if (hq > 4096) return fail(ATTN_SINK_ERR_UNSUPPORTED, "decode_weights: hq %d above 4096", hq);
+    if (batch == 0) return ATTN_SINK_OK;
+    if (!weights && weight_cap > 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: NULL weights");
+    attn::decode::Weights w = {};
+    w.weights = weights;
+    w.heads = weight_heads;
+    w.cap = weight_cap;
+    return run_decode(q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq, hkv, head_dim, page_size,
+                      num_pages, sink, win_first, win_last, scale, out, lse, static_cast<cudaStream_t>(stream), &w);
+}
+
+int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,
+                          const int32_t* seqlens, const float* weights, int batch, int weight_heads, int weight_cap,
+                          int hkv, int head_dim, int page_size, int num_pages, int budget, int keep_first,
+                          int keep_last, float* weights_out, int32_t* kept, int32_t* new_seqlens, void* stream) {
+    t_last_error.clear();
+    if (hkv <= 0 || weight_cap <= 0) return fail(ATTN_SINK_ERR_INVALID, "evict_paged: sizes must be positive");
+    int rc = check_cache("evict_paged", batch, max_pages, page_size, num_pages);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_moves("evict_paged", "weight_heads", weight_heads, hkv, head_dim)) != ATTN_SINK_OK) return rc;
+    if (budget < 1 || keep_first < 0 || keep_last < 0 || (long long)keep_first + keep_last > budget)
+        return fail(ATTN_SINK_ERR_INVALID,
+                    "evict_paged: budget must be positive and hold keep_first + keep_last (both >= 0)");
+    if (batch == 0) return ATTN_SINK_OK;
+    if (!k_cache || !v_cache || !page_table || !seqlens || !weights || !weights_out || !kept || !new_seqlens)
+        return fail(ATTN_SINK_ERR_INVALID, "evict_paged: NULL tensor pointer");
+    if (!aligned16(k_cache) || !aligned16(v_cache))
+        return fail(ATTN_SINK_ERR_INVALID, "evict_paged: caches must be 16-byte aligned");
+    if (k_cache == v_cache) return fail(ATTN_SINK_ERR_INVALID, "evict_paged: k_cache and v_cache must differ");
+    if (new_seqlens == seqlens)
+        return fail(ATTN_SINK_ERR_INVALID, "evict_paged: new_seqlens must not be seqlens (every head reads it)");
+    if ((rc = check_grid("evict_paged", batch, 0)) != ATTN_SINK_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch ws;
+    cudaError_t e = ws.alloc((size_t)batch * weight_heads * sizeof(int32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "evict_paged: scratch allocation");
+    attn::evict::SelectArgs a = {};
+    a.weights = weights;
+    a.weights_out = weights_out;
+    a.seqlens = seqlens;
+    a.new_seqlens = new_seqlens;
+    a.kept = kept;
+    a.first_moved = static_cast<int32_t*>(ws.ptr);
+    a.batch = batch;
+    a.heads = weight_heads;
+    a.cap = weight_cap;
+    a.budget = budget;
+    a.keep_first = keep_first;
+    a.keep_last = keep_last;
+    a.token_cap = (long long)max_pages * page_size;
+    if ((e = attn::evict::launch_select(a, s)) != cudaSuccess) return cuda_fail(e, "evict_paged: select launch");
+    attn::evict::MoveArgs m = {};
+    m.k_cache = as_bf16(k_cache);
+    m.v_cache = as_bf16(v_cache);
+    m.page_table = page_table;
+    m.src = kept;
+    m.counts = new_seqlens;
+    m.first_moved = a.first_moved;
+    m.max_pages = max_pages;
+    m.batch = batch;
+    m.heads = weight_heads;
+    m.hkv = hkv;
+    m.head_dim = head_dim;
+    m.page_size = page_size;
+    m.num_pages = num_pages;
+    m.max_rows = budget;
+    if ((e = attn::evict::launch_move(m, s)) != cudaSuccess) return cuda_fail(e, "evict_paged: move launch");
+    return ATTN_SINK_OK;
+}
+
 int attn_sink_device_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int bits = 0;
@@ -618,6 +947,9 @@ int attn_sink_device_status(void* stream) {
     if (!e) e = attn::prefill::status_exchange(s, &bits);
     if (!e) e = attn::bwd::status_exchange(s, &bits);
     if (!e) e = attn::kvappend::status_exchange(s, &bits);
+    if (!e) e = attn::rope::status_exchange(s, &bits);
+    if (!e) e = attn::tree::status_exchange(s, &bits);
+    if (!e) e = attn::evict::status_exchange(s, &bits);
     if (!e) e = attn::selftest::status_exchange(s, &bits);
     if (e) return cuda_fail(static_cast<cudaError_t>(e), "device_status");
     return bits;

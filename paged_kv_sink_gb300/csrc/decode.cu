@@ -29,6 +29,8 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace attn {
 namespace decode {
 
@@ -109,7 +111,8 @@ __device__ __forceinline__ Ranges request_ranges(const SplitParams& p, int b, bo
     return visible_ranges(L - 1, p.win_first, p.win_last);
 }
 
-template <int D, int NT, int NSTAGE>
+// kScores: also stores every score (log2 units) for decode_weights_kernel.
+template <int D, int NT, int NSTAGE, bool kScores>
 __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
     // Per staged token row: 1 if it holds a visible token read through a valid
@@ -257,6 +260,14 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParam
             const float x1 = ok0 ? sacc[nt][1] * p.scale_log2 : -INFINITY;
             const float x2 = ok1 ? sacc[nt][2] * p.scale_log2 : -INFINITY;
             const float x3 = ok1 ? sacc[nt][3] * p.scale_log2 : -INFINITY;
+            if constexpr (kScores) {
+                // four lanes fill the 32 bytes of a token's 8 heads
+                const long long v = v0 + c * kChunk + crow;
+                float* dst = p.scores + ((((long long)b * gridDim.y + blockIdx.y) * p.scores_cap + v) * NT + nt) * 8 +
+                             2 * (lane & 3);
+                if (v < v1) *reinterpret_cast<float2*>(dst) = make_float2(x0, x1);
+                if (v + 8 < v1) *reinterpret_cast<float2*>(dst + 8 * 8 * NT) = make_float2(x2, x3);
+            }
             const float mx0 = warp_max_g(fmaxf(x0, x2));
             const float mx1 = warp_max_g(fmaxf(x1, x3));
             const float mn0 = fmaxf(m_run[nt][0], mx0);
@@ -358,6 +369,7 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, 
     float M = sg;
     for (int s = 0; s < nsplit; ++s) M = fmaxf(M, p.part_ml[base + s].x);
     float o = 0.f, lse_v;
+    float2 st = make_float2(INFINITY, 0.f);  // 2^(x - st.x) * st.y is a token's weight: 0 here
     if (M == -INFINITY || M == INFINITY) {
         // nothing visible and no sink, or an infinite sink taking all the mass
         lse_v = M;
@@ -371,9 +383,61 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, 
         }
         o = acc / Z;
         lse_v = (M + log2f(Z)) * ATTN_LN2;
+        st = make_float2(M, 1.f / Z);
     }
+    if (p.stats && dd == 0) p.stats[(size_t)b * p.hq + h] = st;
     out[((size_t)b * p.hq + h) * D + dd] = __float2bfloat16_rn(o);
     if (lse && dd == 0) lse[(size_t)b * p.hq + h] = lse_v;
+}
+
+// Adds every visible token's attention weight to its accumulator:
+//     w[b][head][t] += sum_h exp(s_ht - LSE_h)
+// over the query heads h of KV head `head`, or over all query heads when the
+// weights have one head.  One thread per visible token reads the scores that the
+// split kernel stored (4 bytes per query head and token, against 4 d for the K
+// and V row of a KV head) in a fixed order, so the sums do not depend on
+// scheduling.  An accumulator past its capacity is left out.
+constexpr int kWeightThreads = 256;
+template <int NT>
+__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const SplitParams p, float* weights, int heads,
+                                                                        int cap) {
+    extern __shared__ float2 st[];  // one per query head (padded to 8 NT per head block)
+    const int head = blockIdx.y, b = blockIdx.z;
+    const int blocks = p.hq / p.group * p.hblocks / heads;  // head blocks that this accumulator sums
+    constexpr int H = 8 * NT;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the combine grid's statistics
+    for (int e = threadIdx.x; e < blocks * H; e += kWeightThreads) {
+        const int gb = head * blocks + e / H, j = e % H;  // head block, head in it
+        const int in_group = gb % p.hblocks * H + j;
+        st[e] = in_group < p.group ? p.stats[(size_t)b * p.hq + gb / p.hblocks * p.group + in_group]
+                                   : make_float2(INFINITY, 0.f);
+    }
+    __syncthreads();
+    const Ranges r = request_ranges(p, b, false);
+    const int nvis = visible_count(r);
+    for (long long v = (long long)blockIdx.x * kWeightThreads + threadIdx.x; v < nvis;
+         v += (long long)gridDim.x * kWeightThreads) {
+        const int t = visible_token(r, (int)v);
+        if (t >= cap) {
+            raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+            continue;
+        }
+        float sum = 0.f;
+        for (int i = 0; i < blocks; ++i) {
+            const long long hb = (long long)b * (p.hq / p.group) * p.hblocks + head * blocks + i;
+            const float4* x = reinterpret_cast<const float4*>(p.scores + (hb * p.scores_cap + v) * H);
+#pragma unroll
+            for (int q = 0; q < H / 4; ++q) {
+                const float4 y = x[q];
+                const float2* s4 = st + i * H + q * 4;
+                sum += fast_exp2(y.x - s4[0].x) * s4[0].y;
+                sum += fast_exp2(y.y - s4[1].x) * s4[1].y;
+                sum += fast_exp2(y.z - s4[2].x) * s4[2].y;
+                sum += fast_exp2(y.w - s4[3].x) * s4[3].y;
+            }
+        }
+        weights[((size_t)b * heads + head) * cap + t] += sum;
+    }
 }
 
 // Test hooks: the visible ranges and slots exactly as the split kernel derives them.
@@ -457,10 +521,10 @@ Plan make_plan(const Args& a) {
     return pl;
 }
 
-template <int D, int NT, int NSTAGE>
+template <int D, int NT, int NSTAGE, bool kScores>
 static cudaError_t launch_split(const SplitParams& sp, const Plan& pl, int batch, int hkv, cudaStream_t s) {
     const int smem = NSTAGE * 2 * kChunk * D * 2;
-    auto kern = decode_split_kernel<D, NT, NSTAGE>;
+    auto kern = decode_split_kernel<D, NT, NSTAGE, kScores>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     dim3 grid(pl.max_splits, hkv * pl.hblocks, batch);
@@ -468,7 +532,8 @@ static cudaError_t launch_split(const SplitParams& sp, const Plan& pl, int batch
     return cudaGetLastError();
 }
 
-cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s) {
+cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s,
+                   const Weights* w) {
     SplitParams sp;
     sp.q = reinterpret_cast<const __nv_bfloat16*>(a.q);
     sp.k_cache = reinterpret_cast<const __nv_bfloat16*>(a.k_cache);
@@ -489,17 +554,23 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     sp.hblocks = pl.hblocks;
     sp.group = a.group;
     sp.scale_log2 = a.scale * ATTN_LOG2E;
+    sp.scores = w ? w->scores : nullptr;
+    sp.stats = w ? w->stats : nullptr;
+    sp.scores_cap = pl.nvis_max;
     sp.page_shift = -1;
     for (int sh = 0; sh < 31; ++sh)
         if ((1 << sh) == a.page_size) sp.page_shift = sh;
     if (a.batch == 0) return cudaSuccess;
     cudaError_t e;
-    if (a.head_dim == 64)
-        e = pl.nt == 1 ? launch_split<64, 1, 3>(sp, pl, a.batch, a.hkv, s)
-                       : launch_split<64, 2, 3>(sp, pl, a.batch, a.hkv, s);
-    else
-        e = pl.nt == 1 ? launch_split<128, 1, 3>(sp, pl, a.batch, a.hkv, s)
-                       : launch_split<128, 2, 3>(sp, pl, a.batch, a.hkv, s);
+    auto split = [&](auto scores) {
+        constexpr bool kS = decltype(scores)::value;
+        if (a.head_dim == 64)
+            return pl.nt == 1 ? launch_split<64, 1, 3, kS>(sp, pl, a.batch, a.hkv, s)
+                              : launch_split<64, 2, 3, kS>(sp, pl, a.batch, a.hkv, s);
+        return pl.nt == 1 ? launch_split<128, 1, 3, kS>(sp, pl, a.batch, a.hkv, s)
+                          : launch_split<128, 2, 3, kS>(sp, pl, a.batch, a.hkv, s);
+    };
+    e = w ? split(std::true_type{}) : split(std::false_type{});
     if (e != cudaSuccess) return e;
     // The combine starts as a programmatic dependent of the split grid: its
     // launch and CTA set-up overlap the split kernel's last wave.
@@ -521,6 +592,17 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     else
         e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<128>, sp, sink, out, lse);
     if (e != cudaSuccess) return e;
+    if (w) {
+        const long long blocks = (pl.nvis_max + kWeightThreads - 1) / kWeightThreads;
+        cfg.gridDim = dim3((unsigned)blocks, w->heads, a.batch);
+        cfg.blockDim = dim3(kWeightThreads);
+        cfg.dynamicSmemBytes = (size_t)a.hkv / w->heads * pl.hblocks * 8 * pl.nt * sizeof(float2);
+        if (pl.nt == 1)
+            e = cudaLaunchKernelEx(&cfg, decode_weights_kernel<1>, sp, w->weights, w->heads, w->cap);
+        else
+            e = cudaLaunchKernelEx(&cfg, decode_weights_kernel<2>, sp, w->weights, w->heads, w->cap);
+        if (e != cudaSuccess) return e;
+    }
     return cudaGetLastError();
 }
 

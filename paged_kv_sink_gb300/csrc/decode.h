@@ -24,6 +24,10 @@ struct SplitParams {
     int split_tokens, max_splits, hblocks, group;
     int page_shift;    // log2(page_size) when it is a power of two, else -1
     float scale_log2;  // softmax scale * log2(e)
+    // Accumulated attention weights only (else NULL):
+    float* scores;         // (batch, hkv * hblocks, scores_cap, 8 nt) scores of the visible tokens, log2 units
+    float2* stats;         // (batch, hq): (reference, 1 / denominator) of each query head's softmax
+    long long scores_cap;  // visible tokens of the longest possible request
 };
 
 // Validated arguments of attn_sink_decode_paged.
@@ -50,8 +54,18 @@ struct Plan {
     size_t part_o_bytes, part_ml_bytes;
 };
 
+// Accumulators of attn_sink_decode_paged_weights and their scratch.
+struct Weights {
+    float* weights;  // (batch, heads, cap), heads 1 or hkv
+    int heads, cap;
+    float* scores;
+    float2* stats;
+};
+
 Plan make_plan(const Args& a);
-cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s);
+// w != NULL: also adds every visible token's attention weight to w->weights.
+cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s,
+                   const Weights* w = nullptr);
 cudaError_t launch_visible_ranges(const int32_t* seqlens, int batch, int win_first, int win_last,
                                   int32_t* ranges, cudaStream_t s);
 cudaError_t launch_visible_slots(const int32_t* seqlens, const int32_t* page_table, int max_pages,

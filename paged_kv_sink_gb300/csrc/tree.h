@@ -1,0 +1,36 @@
+// Host/device interface of the drafted-tree attention kernels (tree.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include <string>
+
+namespace attn {
+namespace tree {
+
+constexpr int kMaxNodes = 256;  // drafted tokens of one request
+
+struct Args {
+    const void* q;
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* page_table;
+    const int32_t* cu_q;
+    const int32_t* seqlens_k;
+    const int32_t* parents;
+    const float* sink;
+    void* out;
+    float* lse;
+    int max_pages, batch, total_q, hq, hkv, head_dim, page_size, num_pages, max_seqlen_q, max_seqlen_k;
+    int win_first, win_last;
+    float scale;
+};
+
+cudaError_t launch(const Args& a, cudaStream_t s, std::string* what);
+int status_exchange(cudaStream_t s, int* host_bits);
+
+}  // namespace tree
+}  // namespace attn

@@ -1,0 +1,235 @@
+"""Attention of drafted trees over a paged cache against the fp64 definition.
+
+Tolerances: the weights P are rounded to bf16 before P V (2^-8 of each) and the
+output once more (2^-8 of its value), so |O - O*| <= 2^-8 (sum P |v| + |O*|); the
+fp32 scores, exponentials and sums add less than 2^-13 of sum P |v|.  LSE is off by
+no more than the largest score: d + 8 fp32 roundings (2^-24) of sum |q k| scale
+(below 15 for these inputs), 1.3e-4, and the exponentials' 2^-21."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops_oracle as co
+from cache_ops import cu, paged, same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ext():
+    from paged_kv_sink_gb300 import build
+    build.build()
+    import paged_kv_sink_gb300 as ext
+    return ext
+
+
+def make(prefix, nodes, hq, hkv, d, page, seed=0, sink=True, kind="random"):
+    k_cache, v_cache, table, sl = paged([p + n for p, n in zip(prefix, nodes)], hkv, d, page, seed)
+    g = torch.Generator().manual_seed(seed + 1)
+    q = torch.randn(sum(nodes), hq, d, generator=g).bfloat16()
+    sk = torch.rand(hq, generator=g) * 6 - 2 if sink else None
+    parents = []
+    for n in nodes:
+        if kind == "chain":
+            parents += list(range(-1, n - 1))
+        elif kind == "roots":
+            parents += [-1] * n
+        else:
+            parents += [int(torch.randint(-1, i, (1,), generator=g)) if i else -1 for i in range(n)]
+    return dict(q=q, k=k_cache, v=v_cache, table=table, sl=sl, cu=cu(nodes), parents=torch.tensor(parents).int(),
+                sink=sk, prefix=prefix, nodes=nodes)
+
+
+def run(ext, x, first=0, last=0, scale=0.0, max_k=None, **kw):
+    dev = {n: None if x[n] is None else x[n].cuda() for n in ("q", "k", "v", "table", "sl", "cu", "parents", "sink")}
+    out, lse = ext.attn_sink_tree_paged(dev["q"], dev["k"], dev["v"], dev["table"], dev["cu"], dev["sl"],
+                                        dev["parents"], max(x["nodes"] + [0]), max_k or int(max(x["sl"])),
+                                        sink=dev["sink"], win_first=first, win_last=last, scale=scale, **kw)
+    torch.cuda.synchronize()
+    return out.cpu(), None if lse is None else lse.cpu()
+
+
+def check(x, out, lse, first=0, last=0, scale=0.0, requests=None):
+    row, d = 0, x["q"].shape[2]
+    for b, (p, n) in enumerate(zip(x["prefix"], x["nodes"])):
+        if n and (requests is None or b in requests):
+            seen = co.tree_seen(x["parents"][row:row + n].tolist(), p, first, last)
+            used = np.nonzero(seen.any(0))[0]
+            k, v = (co.tokens(x[c], x["table"][b], p + n)[used] for c in ("k", "v"))
+            O, L, _, A = co.attend(x["q"][row:row + n], k, v, seen[:, used],
+                                   None if x["sink"] is None else x["sink"].numpy(), scale or d ** -0.5)
+            err = np.abs(co.to_np(out[row:row + n]) - O)
+            bound = 2.0 ** -8 * (A + np.abs(O)) + 2.0 ** -13 * A
+            assert np.all(err <= bound), (b, float((err - bound).max()))
+            np.testing.assert_allclose(lse[:, row:row + n].numpy(), L, atol=1.5e-4)
+        row += n
+
+
+CASES = [
+    # prefix, nodes, hq, hkv, d, page, first, last, kind
+    ([40], [1], 8, 1, 64, 16, 0, 0, "random"),
+    ([0, 1, 127, 128, 129], [5, 1, 1, 2, 3], 8, 2, 64, 16, 0, 0, "random"),     # empty and tile-edge prefixes
+    ([500, 3, 1000], [17, 64, 33], 16, 2, 64, 8, 0, 0, "random"),
+    ([300, 0], [256, 200], 8, 2, 64, 128, 0, 0, "random"),                      # the largest trees
+    ([200], [130], 4, 4, 64, 32, 0, 0, "chain"),                                # group 1, nodes past one tile
+    ([90, 700], [16, 5], 12, 2, 128, 64, 0, 0, "roots"),                        # group 6
+    ([250], [40], 20, 1, 64, 16, 0, 0, "random"),                               # group 20
+    ([64, 300], [9, 30], 40, 1, 128, 16, 0, 0, "random"),                       # group 40
+    ([30], [7], 128, 1, 64, 16, 0, 0, "random"),                                # group 128: one node a tile
+    ([2000, 10], [24, 12], 16, 2, 64, 16, 100, 300, "random"),                  # windows with a gap
+    ([600, 129], [20, 40], 8, 2, 128, 64, 4, 9, "chain"),                       # ancestors leave the window
+    ([600], [20], 8, 2, 64, 16, 0, 1, "chain"),                                 # each sees itself alone
+    ([900], [6], 8, 2, 64, 256, 0, 128, "random"),                              # pages above a tile
+    ([9000], [12], 64, 8, 64, 16, 1024, 7168, "random"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"p{max(c[0])}n{max(c[1])}hq{c[2]}-{c[3]}d{c[4]}w{c[6]}-{c[7]}{c[8]}")
+def test_tree_matches_definition(ext, case):
+    prefix, nodes, hq, hkv, d, page, first, last, kind = case
+    x = make(prefix, nodes, hq, hkv, d, page, seed=len(nodes) + hq, kind=kind)
+    out, lse = run(ext, x, first, last)
+    assert ext.device_status() == 0
+    check(x, out, lse, first, last)
+
+
+def test_without_sink_with_scale_and_wrong_length_estimates(ext):
+    x = make([300, 2500, 77], [4, 19, 8], 8, 2, 64, 16, sink=False)
+    out, lse = run(ext, x, scale=0.3)
+    check(x, out, lse, scale=0.3)
+    for max_k in (1, 100000):  # plans the split only
+        out, lse = run(ext, x, scale=0.3, max_k=max_k)
+        check(x, out, lse, scale=0.3)
+    out, none = run(ext, x, scale=0.3, return_lse=False)
+    assert none is None
+
+
+def test_many_requests_and_no_nodes(ext):
+    g = torch.Generator().manual_seed(5)
+    prefix = torch.randint(0, 400, (40,), generator=g).tolist()
+    nodes = torch.randint(0, 12, (40,), generator=g).tolist()
+    x = make(prefix, nodes, 8, 2, 64, 16, seed=6)
+    out, lse = run(ext, x)
+    check(x, out, lse)
+    x = make([10], [0], 8, 2, 64, 16)
+    assert run(ext, x)[0].shape == (0, 8, 64)
+
+
+def test_a_chain_equals_the_paged_forward(ext):
+    x = make([700, 33], [60, 130], 16, 2, 64, 16, kind="chain")
+    for first, last in ((0, 0), (20, 100)):
+        out, lse = run(ext, x, first, last)
+        ref, ref_lse = ext.attn_sink_fwd_paged(x["q"].cuda(), x["k"].cuda(), x["v"].cuda(), x["table"].cuda(),
+                                               x["cu"].cuda(), x["sl"].cuda(), 130, int(max(x["sl"])),
+                                               sink=x["sink"].cuda(), win_first=first, win_last=last)
+        check(x, out, lse, first, last)
+        check(x, ref.cpu(), ref_lse.cpu(), first, last)
+
+
+@pytest.mark.parametrize("sink", [80.0, float("inf"), float("-inf"), -50.0])
+def test_sink_limits(ext, sink):
+    x = make([50, 400], [3, 9], 8, 2, 64, 16)
+    x["sink"] = torch.full((8,), sink)
+    out, lse = run(ext, x)
+    if sink == float("inf"):
+        assert torch.all(out == 0) and torch.all(torch.isposinf(lse))
+    else:
+        if sink == float("-inf"):
+            x["sink"] = None
+        check(x, out, lse)
+
+
+def test_large_scores(ext):
+    """Scores of a few hundred that grow along the keys: the running maximum moves often.
+    The fp32 score error grows with sum |q k| scale (60 times the usual): LSE 1e-2, and the
+    weights by the same factor e^(2 * 1e-2)."""
+    x = make([600], [10], 8, 2, 64, 16, seed=9)
+    rows = x["k"].view(-1, 2, 64)
+    for t in range(610):
+        rows[int(co.slot(x["table"][0].numpy(), 16, [t])[0])] *= 0.05 * (t % 300)
+    x["q"] *= 4
+    out, lse = run(ext, x)
+    seen = co.tree_seen(x["parents"].tolist(), 600)
+    k, v = (co.tokens(x[c], x["table"][0], 610) for c in ("k", "v"))
+    O, L, _, A = co.attend(x["q"], k, v, seen, x["sink"].numpy(), 0.125)
+    np.testing.assert_allclose(lse.numpy(), L, atol=1e-2)
+    assert np.all(np.abs(co.to_np(out) - O) <= 2.0 ** -8 * (A + np.abs(O)) + 2.1e-2 * A)
+
+
+def test_rows_of_other_requests_stay(ext):
+    """Rows of out and lse behind the last request's keep what they held."""
+    x = make([30], [5], 8, 2, 64, 16)
+    q = torch.cat([x["q"], torch.full((4, 8, 64), float("nan")).bfloat16()])
+    out, lse = torch.full((9, 8, 64), 3.0).bfloat16().cuda(), torch.full((8, 9), 3.0).cuda()
+    y = dict(x, q=q, parents=torch.cat([x["parents"], torch.full((4,), -7).int()]))
+    run(ext, y, out=out, lse=lse)
+    assert ext.device_status() == 0
+    check(x, out.cpu()[:5], lse.cpu()[:, :5])
+    assert torch.all(out[5:] == 3) and torch.all(lse[:, 5:] == 3)
+
+
+def test_bad_parents_pages_and_lengths_raise_status(ext):
+    x = make([60, 60, 60], [6, 6, 6], 8, 2, 64, 16)
+    ext.device_status()
+    y = dict(x, parents=x["parents"].clone())
+    y["parents"][6:9] = torch.tensor([0, 1, -9])   # request 1: its own index, itself, below -1
+    out, lse = run(ext, y)
+    assert ext.device_status() == ext._lib.DEV_TREE
+    y["parents"][6:9] = -1                         # is what they are read as
+    check(y, out, lse)
+    y = dict(x, table=x["table"].clone())
+    y["table"][1, 1] = 10 ** 6
+    out, lse = run(ext, y)
+    assert ext.device_status() == ext._lib.DEV_PAGE_OOB
+    check(x, out, lse, requests=(0, 2))
+    # request 1 without its tokens 16..31: a prefix of 44 tokens with page 1 left out
+    z = dict(x, table=x["table"].clone(), sl=x["sl"].clone(), prefix=[60, 44, 60])
+    z["table"][1, 1:4] = x["table"][1, 2:5]
+    z["sl"][1] = 50
+    check(z, out, lse, requests=(1,))
+    y = dict(x, sl=torch.tensor([66, 4, 10 ** 6]).int())
+    out, lse = run(ext, y, max_k=100)
+    assert ext.device_status() & ext._lib.DEV_SEQLEN_OOB
+    check(x, out, lse, requests=(0,))
+    assert torch.all(out[6:12] == 0) and torch.allclose(lse[:, 6:12], x["sink"][:, None])
+    out = torch.full((18, 8, 64), 3.0).bfloat16().cuda()
+    ext.device_status()
+    run(ext, dict(x, nodes=[2, 2, 2]), out=out)    # the grid may cover more rows than max_seqlen_q, or not
+    assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
+    assert torch.all(out[2:6] == 3)
+
+
+def test_two_graphs_and_two_streams(ext):
+    """Two captured calls replayed on two streams at once, and an eager one between, do
+    not share scratch."""
+    xs = [make([900, 50], [12, 3], 16, 2, 64, 16, seed=s) for s in (20, 21)]
+    names = ("q", "k", "v", "table", "sl", "cu", "parents", "sink")
+    devs = [{n: x[n].cuda() for n in names} for x in xs]
+
+    def call(d, out, lse):
+        ext.attn_sink_tree_paged(d["q"], d["k"], d["v"], d["table"], d["cu"], d["sl"], d["parents"], 12, 912,
+                                 sink=d["sink"], out=out, lse=lse)
+
+    outs = [(torch.empty_like(d["q"]), torch.empty(16, 15, device="cuda")) for d in devs]
+    graphs = []
+    for d, o in zip(devs, outs):
+        call(d, *o)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(d, *o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for o in outs:
+            o[0].zero_(), o[1].zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = (torch.empty_like(devs[0]["q"]), torch.empty(16, 15, device="cuda"))
+        call(devs[0], *eager)
+        torch.cuda.synchronize()
+        for x, o in zip(xs, outs):
+            check(x, o[0].cpu(), o[1].cpu())
+        assert same(eager[0], outs[0][0]) and same(eager[1], outs[0][1])
