@@ -29,7 +29,16 @@ struct Args {
     float scale;
 };
 
-cudaError_t launch(const Args& a, cudaStream_t s, std::string* what);
+// Row tiles, splits of the keys and scratch sizes.
+struct Plan {
+    int npt, mtiles;  // nodes per 128-row tile, row tiles of the largest request
+    int split_tiles;  // 128-key tiles per split
+    int splits;       // 1: no scratch, no combine
+    size_t part_o_bytes, part_ml_bytes;
+};
+
+Plan make_plan(const Args& a);
+cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s, std::string* what);
 int status_exchange(cudaStream_t s, int* host_bits);
 
 }  // namespace tree

@@ -168,6 +168,46 @@ def test_rows_of_other_requests_stay(ext):
     assert torch.all(out[5:] == 3) and torch.all(lse[:, 5:] == 3)
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 64)])
+def test_infinities_and_nans_reach_only_who_sees_them(ext, d, page):
+    """A drafted token whose K or V holds infinities or NaNs changes its descendants
+    alone; tokens in the window's gap change nobody."""
+    nodes = 40
+    x = make([300], [nodes], 8, 2, d, page, seed=13, sink=True)
+    first, last = 10, 120                       # the gap: tokens 10 .. 180
+    want, want_lse = run(ext, x, first, last)
+    seen = co.tree_seen(x["parents"].tolist(), 300, first, last)
+    for t in range(10, 180):
+        s = co.slot(x["table"][0].numpy(), page, t)
+        x["k"].view(-1, 2, d)[s] = float("nan")
+        x["v"].view(-1, 2, d)[s] = float("inf")
+    out, lse = run(ext, x, first, last)
+    assert same(out, want) and same(lse, want_lse)
+    v = x["v"].view(-1, 2, d)
+    at = [int(co.slot(x["table"][0].numpy(), page, 300 + i)) for i in range(nodes)]
+    v[at[5], 0, 3], v[at[7], 1, 60], v[at[9], 0, 3] = float("inf"), float("nan"), float("-inf")
+    out, lse = run(ext, x, first, last)
+    assert same(lse, want_lse)
+    for i in range(nodes):
+        for h in range(8):
+            row = want[i, h].clone()
+            if h < 4 and seen[i, 305]:
+                row[3] = float("inf")
+            if h < 4 and seen[i, 309]:
+                row[3] = float("nan") if seen[i, 305] else float("-inf")
+            if h >= 4 and seen[i, 307]:
+                row[60] = float("nan")
+            assert torch.equal(row.isnan(), out[i, h].isnan()), (i, h)
+            assert torch.equal(row.nan_to_num(7.0, 8.0, 9.0), out[i, h].nan_to_num(7.0, 8.0, 9.0)), (i, h)
+    x["k"].view(-1, 2, d)[at[11], 1] = float("nan")
+    out2, lse2 = run(ext, x, first, last)
+    for i in range(nodes):
+        keep = slice(0, 4) if seen[i, 311] else slice(0, 8)
+        assert same(lse2[keep, i], lse[keep, i])
+        if seen[i, 311]:
+            assert torch.all(lse2[4:, i].isnan())
+
+
 def test_bad_parents_pages_and_lengths_raise_status(ext):
     x = make([60, 60, 60], [6, 6, 6], 8, 2, 64, 16)
     ext.device_status()
