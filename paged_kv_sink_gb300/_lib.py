@@ -417,17 +417,35 @@ def attn_sink_bwd(q, k, v, sink, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max
 # Entry points around the cache: rotary positions, drafted trees, accumulated
 # weights and eviction.  Their tensors must share one CUDA device (the library
 # launches on it, whatever the current device is) and have the sizes that the
-# pointers' readers assume; both are checked here.
+# pointers' readers assume; both are checked here.  A small call costs more on
+# the host than on the GPU, so each function first tests its usual arguments in one
+# expression (_is) and only otherwise goes through _expect, which names the
+# argument that is wrong.
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
-def _expect(name, t, dtype, shape, device=None, contiguous=True):
+def _is(t, dtype, dev, shape):
+    """Whether t is a contiguous CUDA tensor of this type, device index and shape."""
+    return t.dtype is dtype and t.get_device() == dev and t.shape == shape and t.is_contiguous()
+
+
+def _device(name, t):
+    """Device index of the call's first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return dev
+
+
+def _expect(name, t, dtype, dev, shape, contiguous=True):
     """Type, device and shape of an argument; None in `shape` stands for any extent."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise TypeError(f"{name} is on {t.device}, the other tensors on {device}")
+    if t.get_device() != dev:
+        raise TypeError(f"{name} is on {t.device}, the call's first tensor on cuda:{dev}")
     got = t.shape
     if len(got) != len(shape) or any(w is not None and w != g for w, g in zip(shape, got)):
         raise TypeError(f"{name} must have shape {shape}, got {tuple(got)}")
@@ -435,44 +453,59 @@ def _expect(name, t, dtype, shape, device=None, contiguous=True):
         raise TypeError(f"{name} must be contiguous")
 
 
-def _expect_rows(name, t, shape, device=None):
+def _expect_rows(name, t, dev, shape):
     """A (rows, heads, d) bf16 tensor whose heads are contiguous within a row;
     returns its row stride (0: contiguous)."""
-    _expect(name, t, torch.bfloat16, shape, device, contiguous=False)
+    if t.dtype is not _BF16 or t.get_device() != dev or t.dim() != 3 or t.shape != shape:
+        _expect(name, t, _BF16, dev, shape, contiguous=False)
     if t.is_contiguous():
         return 0
-    rows, heads, d = t.shape
+    _, heads, d = t.shape
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d) or t.stride(0) < heads * d:
         raise TypeError(f"{name}: heads must be contiguous within a row and rows must not overlap")
     return t.stride(0)
 
 
-def _run(name, device, stream, *args):
-    """Calls the entry point on `device` and `stream` (None: the device's current one)."""
-    raw = stream.cuda_stream if stream is not None else torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = getattr(lib(), name)(*args, raw)
+def _expect_inv_freq(inv_freq, dev, d):
+    if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != dev or inv_freq.dim() != 1:
+        _expect("inv_freq", inv_freq, torch.float64, dev, (None,))
+    n = inv_freq.shape[0]
+    if not 1 <= n <= d // 2:
+        raise TypeError(f"inv_freq must hold 1 .. head_dim / 2 frequencies, got {n}")
+    if not inv_freq.is_contiguous():
+        raise TypeError("inv_freq must be contiguous")
+    return 2 * n
+
+
+def _expect_cache(k_cache, v_cache, page_table, dev, batch=None, d=None):
+    """Returns (num_pages, page_size, hkv, d, max_pages)."""
+    shape = k_cache.shape
+    if len(shape) != 4 or (d is not None and shape[3] != d) or not _is(k_cache, _BF16, dev, shape):
+        _expect("k_cache", k_cache, _BF16, dev, (None, None, None, d))
+    if not _is(v_cache, _BF16, dev, shape):
+        _expect("v_cache", v_cache, _BF16, dev, shape)
+    if page_table.dim() != 2 or not _is(page_table, _I32, dev, (page_table.shape[0] if batch is None else batch,
+                                                                page_table.shape[1])):
+        _expect("page_table", page_table, _I32, dev, (batch, None))
+    return (*shape, page_table.shape[1])
+
+
+_entry = {}
+
+
+def _run(name, dev, stream, *args):
+    """Calls the entry point on device `dev` and `stream` (None: the device's current one)."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
     else:
-        with torch.cuda.device(device):
-            rc = getattr(lib(), name)(*args, raw)
+        with torch.cuda.device(dev):
+            rc = fn(*args, raw)
     if rc != OK:
         _check(name, rc)
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _expect_inv_freq(inv_freq, d, device):
-    _expect("inv_freq", inv_freq, torch.float64, (None,), device)
-    if not 1 <= inv_freq.shape[0] <= d // 2:
-        raise TypeError(f"inv_freq must hold 1 .. head_dim / 2 frequencies, got {inv_freq.shape[0]}")
-
-
-def _expect_cache(k_cache, v_cache, page_table, device, batch=None):
-    _expect("k_cache", k_cache, torch.bfloat16, (None, None, None, None), device)
-    _expect("v_cache", v_cache, torch.bfloat16, k_cache.shape, device)
-    _expect("page_table", page_table, torch.int32, (batch, None), device)
 
 
 def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0, inverse=False, q_out=None,
@@ -482,26 +515,31 @@ def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0,
     (fp64, radians per position; see attn_sink_rope_freqs), by the negative angle
     with `inverse` (the gradient).  Rows may be strided (column ranges of a packed
     buffer); an output may be its own input.  Returns (q_out, k_out or None)."""
-    dev = q.device
-    q_rs = _expect_rows("q", q, (None, None, None))
+    dev = _device("q", q)
+    q_rs = _expect_rows("q", q, dev, (None, None, None) if q.dim() != 3 else q.shape)
     T, hq, d = q.shape
-    _expect("positions", positions, torch.int32, (T,), dev)
-    _expect_inv_freq(inv_freq, d, dev)
+    if not _is(positions, _I32, dev, (T,)):
+        _expect("positions", positions, _I32, dev, (T,))
+    r = _expect_inv_freq(inv_freq, dev, d)
     if q_out is None:
-        q_out = torch.empty((T, hq, d), dtype=q.dtype, device=dev)
-    qo_rs = _expect_rows("q_out", q_out, q.shape, dev)
+        q_out, qo_rs = torch.empty_like(q, memory_format=torch.contiguous_format), 0
+    else:
+        qo_rs = _expect_rows("q_out", q_out, dev, q.shape)
     hkv = k_rs = ko_rs = 0
+    kp = kop = None
     if k is not None:
-        k_rs = _expect_rows("k", k, (T, None, d), dev)
+        k_rs = _expect_rows("k", k, dev, (T, None if k.dim() != 3 else k.shape[1], d))
         hkv = k.shape[1]
         if k_out is None:
-            k_out = torch.empty((T, hkv, d), dtype=k.dtype, device=dev)
-        ko_rs = _expect_rows("k_out", k_out, k.shape, dev)
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        else:
+            ko_rs = _expect_rows("k_out", k_out, dev, k.shape)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise TypeError("k_out is given without k")
-    _run("attn_sink_rope", dev, stream, q.data_ptr(), q_out.data_ptr(), _addr(k), _addr(k_out), q_rs, qo_rs, k_rs,
-         ko_rs, positions.data_ptr(), inv_freq.data_ptr(), T, hq, hkv, d, 2 * inv_freq.shape[0],
-         1 if interleaved else 0, 1 if inverse else 0, float(attn_scale))
+    _run("attn_sink_rope", dev, stream, q.data_ptr(), q_out.data_ptr(), kp, kop, q_rs, qo_rs, k_rs, ko_rs,
+         positions.data_ptr(), inv_freq.data_ptr(), T, hq, hkv, d, r, 1 if interleaved else 0, 1 if inverse else 0,
+         attn_scale)
     return q_out, k_out
 
 
@@ -511,39 +549,61 @@ def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seql
     """Rotates the new tokens' q (T, Hq, d) into q_out, and k_new (T, Hkv, d) into the
     paged caches together with v_new, in one launch (see attn_sink_kv_append for the
     slots).  `positions` (T,) int32 defaults to each row's logical token.  Returns
-    q_out; a q_out that is allocated here holds zeros in rows behind the last
-    request's when cu_new is given."""
-    dev = q.device
-    q_rs = _expect_rows("q", q, (None, None, None))
+    q_out, whose rows behind the last request's are left as they were (unset in a
+    q_out that is allocated here)."""
+    dev = _device("q", q)
+    q_rs = _expect_rows("q", q, dev, (None, None, None) if q.dim() != 3 else q.shape)
     T, hq, d = q.shape
-    k_rs = _expect_rows("k_new", k_new, (T, None, d), dev)
-    hkv = k_new.shape[1]
-    v_rs = _expect_rows("v_new", v_new, k_new.shape, dev)
-    _expect("seqlens", seqlens, torch.int32, (None,), dev)
-    B = seqlens.shape[0]
-    _expect_cache(k_cache, v_cache, page_table, dev, B)
-    npages, ps = k_cache.shape[:2]
-    if k_cache.shape[2] != hkv or k_cache.shape[3] != d:
-        raise TypeError(f"k_cache must have {hkv} heads of {d}, got {tuple(k_cache.shape)}")
-    _expect_inv_freq(inv_freq, d, dev)
+    B = seqlens.shape[0] if seqlens.dim() == 1 else None
+    if B is None or not _is(seqlens, _I32, dev, (B,)):
+        _expect("seqlens", seqlens, _I32, dev, (None,))
+    npages, ps, hkv, _, max_pages = _expect_cache(k_cache, v_cache, page_table, dev, B, d)
+    k_rs = _expect_rows("k_new", k_new, dev, (T, hkv, d))
+    v_rs = _expect_rows("v_new", v_new, dev, (T, hkv, d))
+    r = _expect_inv_freq(inv_freq, dev, d)
+    cu = pos = None
     if cu_new is None:
         if T != B:
             raise TypeError(f"without cu_new every request has one new row: got {T} rows, {B} requests")
         max_new = 1 if max_new is None else max_new
     else:
-        _expect("cu_new", cu_new, torch.int32, (B + 1,), dev)
+        if not _is(cu_new, _I32, dev, (B + 1,)):
+            _expect("cu_new", cu_new, _I32, dev, (B + 1,))
+        cu = cu_new.data_ptr()
         if max_new is None:
             max_new = int((cu_new[1:] - cu_new[:-1]).max()) if B else 0
     if positions is not None:
-        _expect("positions", positions, torch.int32, (T,), dev)
+        if not _is(positions, _I32, dev, (T,)):
+            _expect("positions", positions, _I32, dev, (T,))
+        pos = positions.data_ptr()
     if q_out is None:
-        q_out = (torch.empty if cu_new is None else torch.zeros)((T, hq, d), dtype=q.dtype, device=dev)
-    qo_rs = _expect_rows("q_out", q_out, q.shape, dev)
+        q_out, qo_rs = torch.empty_like(q, memory_format=torch.contiguous_format), 0
+    else:
+        qo_rs = _expect_rows("q_out", q_out, dev, q.shape)
     _run("attn_sink_rope_kv_append", dev, stream, q.data_ptr(), q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
-         q_rs, qo_rs, k_rs, v_rs, _addr(cu_new), _addr(positions), inv_freq.data_ptr(), seqlens.data_ptr(),
-         page_table.data_ptr(), page_table.shape[1], B, T, hq, hkv, d, 2 * inv_freq.shape[0], ps, npages,
-         int(max_new), 1 if interleaved else 0, float(attn_scale), k_cache.data_ptr(), v_cache.data_ptr())
+         q_rs, qo_rs, k_rs, v_rs, cu, pos, inv_freq.data_ptr(), seqlens.data_ptr(), page_table.data_ptr(), max_pages, B,
+         T, hq, hkv, d, r, ps, npages, max_new, 1 if interleaved else 0, attn_scale, k_cache.data_ptr(),
+         v_cache.data_ptr())
     return q_out
+
+
+def _outputs(q, dev, lse_shape, sink, out, lse, return_lse):
+    """Checks or makes the outputs of an attention call; returns them and the pointers
+    of sink, out and lse."""
+    hq = q.shape[1]
+    if sink is not None and not _is(sink, _F32, dev, (hq,)):
+        _expect("sink", sink, _F32, dev, (hq,))
+    if out is None:
+        out = torch.empty_like(q)
+    elif not _is(out, _BF16, dev, q.shape):
+        _expect("out", out, _BF16, dev, q.shape)
+    if lse is not None:
+        if not _is(lse, _F32, dev, lse_shape):
+            _expect("lse", lse, _F32, dev, lse_shape)
+    elif return_lse:
+        lse = q.new_empty(lse_shape, dtype=_F32)
+    return (out, lse, None if sink is None else sink.data_ptr(), out.data_ptr(),
+            None if lse is None else lse.data_ptr())
 
 
 def attn_sink_tree_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_k, parents, max_seqlen_q,
@@ -552,31 +612,22 @@ def attn_sink_tree_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_
     """Attention of trees of drafted tokens (at most 256 a request) over a paged cache
     that holds their K/V.  q (T, Hq, d); parents (T,) int32: the node's parent as an
     index in its request, -1 on the prefix.  Returns (out, lse (Hq, T))."""
-    dev = q.device
-    _expect("q", q, torch.bfloat16, (None, None, None))
+    dev = _device("q", q)
+    if q.dim() != 3 or not _is(q, _BF16, dev, q.shape):
+        _expect("q", q, _BF16, dev, (None, None, None))
     T, hq, d = q.shape
-    _expect("seqlens_k", seqlens_k, torch.int32, (None,), dev)
-    B = seqlens_k.shape[0]
-    _expect_cache(k_cache, v_cache, page_table, dev, B)
-    npages, ps, hkv, dc = k_cache.shape
-    if dc != d:
-        raise TypeError(f"k_cache must have heads of {d}, got {dc}")
-    _expect("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev)
-    _expect("parents", parents, torch.int32, (T,), dev)
-    if sink is not None:
-        _expect("sink", sink, torch.float32, (hq,), dev)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _expect("out", out, torch.bfloat16, q.shape, dev)
-    if lse is not None:
-        _expect("lse", lse, torch.float32, (hq, T), dev)
-    elif return_lse:
-        lse = torch.empty((hq, T), dtype=torch.float32, device=dev)
+    B = seqlens_k.shape[0] if seqlens_k.dim() == 1 else None
+    if B is None or not _is(seqlens_k, _I32, dev, (B,)):
+        _expect("seqlens_k", seqlens_k, _I32, dev, (None,))
+    npages, ps, hkv, _, max_pages = _expect_cache(k_cache, v_cache, page_table, dev, B, d)
+    if not _is(cu_seqlens_q, _I32, dev, (B + 1,)):
+        _expect("cu_seqlens_q", cu_seqlens_q, _I32, dev, (B + 1,))
+    if not _is(parents, _I32, dev, (T,)):
+        _expect("parents", parents, _I32, dev, (T,))
+    out, lse, sp, op, lp = _outputs(q, dev, (hq, T), sink, out, lse, return_lse)
     _run("attn_sink_tree_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         page_table.data_ptr(), page_table.shape[1], cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(),
-         parents.data_ptr(), B, T, hq, hkv, d, ps, npages, int(max_seqlen_q), int(max_seqlen_k), _addr(sink),
-         int(win_first), int(win_last), float(scale), out.data_ptr(), _addr(lse))
+         page_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), parents.data_ptr(), B, T, hq,
+         hkv, d, ps, npages, max_seqlen_q, max_seqlen_k, sp, win_first, win_last, scale, op, lp)
     return out, lse
 
 
@@ -584,17 +635,21 @@ def attn_sink_kv_compact(k_cache, v_cache, page_table, src, counts, base=None, s
     """Moves cached rows in place: token src[b, (h,) j] of request b becomes its token
     base[b] + j (base None: j) for j < counts[b].  src (B, m) or (B, Hkv, m) int32,
     increasing, src[j] >= base + j.  Returns (k_cache, v_cache)."""
-    dev = k_cache.device
-    _expect_cache(k_cache, v_cache, page_table, dev)
-    npages, ps, hkv, d = k_cache.shape
-    B = page_table.shape[0]
-    _expect("src", src, torch.int32, (B, None) if src.dim() == 2 else (B, hkv, None), dev)
-    _expect("counts", counts, torch.int32, (B,), dev)
+    dev = _device("k_cache", k_cache)
+    npages, ps, hkv, d, max_pages = _expect_cache(k_cache, v_cache, page_table, dev)
+    B, heads = page_table.shape[0], 1 if src.dim() == 2 else hkv
+    want = (B, src.shape[-1] if src.dim() else None) if heads == 1 and src.dim() == 2 else (B, hkv, src.shape[-1] if src.dim() else None)
+    if not _is(src, _I32, dev, want):
+        _expect("src", src, _I32, dev, want)
+    if not _is(counts, _I32, dev, (B,)):
+        _expect("counts", counts, _I32, dev, (B,))
+    bp = None
     if base is not None:
-        _expect("base", base, torch.int32, (B,), dev)
-    _run("attn_sink_kv_compact", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-         page_table.shape[1], src.data_ptr(), counts.data_ptr(), _addr(base), B, 1 if src.dim() == 2 else hkv,
-         src.shape[-1], hkv, d, ps, npages)
+        if not _is(base, _I32, dev, (B,)):
+            _expect("base", base, _I32, dev, (B,))
+        bp = base.data_ptr()
+    _run("attn_sink_kv_compact", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_pages,
+         src.data_ptr(), counts.data_ptr(), bp, B, heads, want[-1], hkv, d, ps, npages)
     return k_cache, v_cache
 
 
@@ -603,29 +658,20 @@ def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, wei
     """attn_sink_decode_paged that also adds every visible token's attention weight to
     weights (B, Hkv or 1, cap) fp32, summed over the query heads of the KV head (or
     all).  Returns (out, lse)."""
-    dev = q.device
-    _expect("q", q, torch.bfloat16, (None, None, None))
+    dev = _device("q", q)
+    if q.dim() != 3 or not _is(q, _BF16, dev, q.shape):
+        _expect("q", q, _BF16, dev, (None, None, None))
     B, hq, d = q.shape
-    _expect_cache(k_cache, v_cache, page_table, dev, B)
-    npages, ps, hkv, dc = k_cache.shape
-    if dc != d:
-        raise TypeError(f"k_cache must have heads of {d}, got {dc}")
-    _expect("seqlens", seqlens, torch.int32, (B,), dev)
-    _expect("weights", weights, torch.float32, (B, None, None), dev)
-    if sink is not None:
-        _expect("sink", sink, torch.float32, (hq,), dev)
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _expect("out", out, torch.bfloat16, q.shape, dev)
-    if lse is not None:
-        _expect("lse", lse, torch.float32, (B, hq), dev)
-    elif return_lse:
-        lse = torch.empty((B, hq), dtype=torch.float32, device=dev)
+    npages, ps, hkv, _, max_pages = _expect_cache(k_cache, v_cache, page_table, dev, B, d)
+    if not _is(seqlens, _I32, dev, (B,)):
+        _expect("seqlens", seqlens, _I32, dev, (B,))
+    shape = weights.shape
+    if len(shape) != 3 or shape[0] != B or not _is(weights, _F32, dev, shape):
+        _expect("weights", weights, _F32, dev, (B, None, None))
+    out, lse, sp, op, lp = _outputs(q, dev, (B, hq), sink, out, lse, return_lse)
     _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         page_table.data_ptr(), page_table.shape[1], seqlens.data_ptr(), B, hq, hkv, d, ps, npages, _addr(sink),
-         int(win_first), int(win_last), float(scale), weights.data_ptr(), weights.shape[1], weights.shape[2],
-         out.data_ptr(), _addr(lse))
+         page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages, sp, win_first, win_last, scale,
+         weights.data_ptr(), shape[1], shape[2], op, lp)
     return out, lse
 
 
@@ -636,29 +682,31 @@ def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget
     (ties: the earlier token), moved to the front in their order, in place; weights
     (B, Hkv or 1, cap) fp32 follow them (into weights_out if given) and are 0 behind.
     Returns (new_seqlens (B,), kept (B, Hkv or 1, budget), -1 padded)."""
-    dev = k_cache.device
-    _expect_cache(k_cache, v_cache, page_table, dev)
-    npages, ps, hkv, d = k_cache.shape
+    dev = _device("k_cache", k_cache)
+    npages, ps, hkv, d, max_pages = _expect_cache(k_cache, v_cache, page_table, dev)
     B = page_table.shape[0]
-    _expect("seqlens", seqlens, torch.int32, (B,), dev)
-    _expect("weights", weights, torch.float32, (B, None, None), dev)
-    heads, cap = weights.shape[1:]
+    if not _is(seqlens, _I32, dev, (B,)):
+        _expect("seqlens", seqlens, _I32, dev, (B,))
+    shape = weights.shape
+    if len(shape) != 3 or shape[0] != B or not _is(weights, _F32, dev, shape):
+        _expect("weights", weights, _F32, dev, (B, None, None))
+    _, heads, cap = shape
     budget = int(budget)
     if weights_out is None:
         weights_out = weights
-    else:
-        _expect("weights_out", weights_out, torch.float32, weights.shape, dev)
+    elif not _is(weights_out, _F32, dev, shape):
+        _expect("weights_out", weights_out, _F32, dev, shape)
     if kept is None:
-        kept = torch.empty((B, heads, max(budget, 0)), dtype=torch.int32, device=dev)
-    else:
-        _expect("kept", kept, torch.int32, (B, heads, budget), dev)
+        kept = seqlens.new_empty((B, heads, max(budget, 0)))
+    elif not _is(kept, _I32, dev, (B, heads, budget)):
+        _expect("kept", kept, _I32, dev, (B, heads, budget))
     if new_seqlens is None:
         new_seqlens = torch.empty_like(seqlens)
-    else:
-        _expect("new_seqlens", new_seqlens, torch.int32, (B,), dev)
-    _run("attn_sink_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(),
-         page_table.shape[1], seqlens.data_ptr(), weights.data_ptr(), B, heads, cap, hkv, d, ps, npages, budget,
-         int(keep_first), int(keep_last), weights_out.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr())
+    elif not _is(new_seqlens, _I32, dev, (B,)):
+        _expect("new_seqlens", new_seqlens, _I32, dev, (B,))
+    _run("attn_sink_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_pages,
+         seqlens.data_ptr(), weights.data_ptr(), B, heads, cap, hkv, d, ps, npages, budget, keep_first, keep_last,
+         weights_out.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr())
     return new_seqlens, kept
 
 

@@ -104,14 +104,21 @@ class _AttnSinkRope(torch.autograd.Function):
         positions, inv_freq = ctx.saved_tensors
         interleaved, attn_scale, inverse = ctx.args
         args = (positions, inv_freq, interleaved, attn_scale, not inverse)
-        dq, dk = (None if g is None or not need else g.contiguous()
-                  for g, need in zip((dq, dk), ctx.needs_input_grad))
+        need_q, need_k = ctx.needs_input_grad[:2]
+        dq = dq.contiguous() if need_q and dq is not None else None
+        dk = dk.contiguous() if need_k and dk is not None else None
+        if torch.is_grad_enabled():  # create_graph
+            rotate = _AttnSinkRope.apply
+        else:
+            def rotate(*x):
+                a, b = _lib.attn_sink_rope(*x)
+                return a if b is None else (a, b)
         if dq is not None and dk is not None:
-            dq, dk = _AttnSinkRope.apply(dq, dk, *args)
+            dq, dk = rotate(dq, dk, *args)
         elif dq is not None:
-            dq = _AttnSinkRope.apply(dq, None, *args)
+            dq = rotate(dq, None, *args)
         elif dk is not None:
-            dk = _AttnSinkRope.apply(dk, None, *args)
+            dk = rotate(dk, None, *args)
         return dq, dk, None, None, None, None, None
 
 

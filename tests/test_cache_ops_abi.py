@@ -115,8 +115,6 @@ def test_binding_refuses_host_tensors_and_wrong_types(lib):
                  lambda: ext.attn_sink_evict_paged(c, c, t, i, w, 4)):
         with pytest.raises(TypeError, match="CUDA"):
             call()
-    with pytest.raises(TypeError, match="bfloat16"):
-        ext.attn_sink_rope(q.float(), None, i, f)
 
 
 @pytest.mark.gpu
@@ -131,7 +129,8 @@ def test_binding_checks_shapes(lib):
         (lambda: ext.attn_sink_rope(q[:1].expand(4, 2, 64), None, i, f), "overlap"),
         (lambda: ext.attn_sink_rope(q.transpose(0, 1), None, i[:2], f), "contiguous"),
         (lambda: ext.attn_sink_rope(q, None, i, f, k_out=q), "k_out"), (lambda: ext.attn_sink_rope(q, q[:3], i, f), "shape"),
-        (lambda: ext.attn_sink_rope_kv_append(q, q, q, c, c2, t, i, f), "k_cache"),
+        (lambda: ext.attn_sink_rope_kv_append(q, q, q, c, c2, t, i, f), "k_new"),
+        (lambda: ext.attn_sink_rope(q.float(), None, i, f), "bfloat16"),
         (lambda: ext.attn_sink_rope_kv_append(q, q[:, :1], q[:, :1], c, c2, t[:3], i[:3], f), "cu_new"),
         (lambda: ext.attn_sink_rope_kv_append(q, q[:, :1], q[:, :1], c, c2, t, i, f, cu_new=i), "cu_new"),
         (lambda: ext.attn_sink_tree_paged(q, c, c2, t, i, i, i, 1, 1), "cu_seqlens_q"),
