@@ -17,8 +17,10 @@
 //
 // It is bound by memory: every input element is read once and every output
 // element written once.  A block takes a few rows: it computes their r/2 sines
-// and cosines once into shared memory, for all heads, and then moves units of
-// 16 elements (8 pairs) with 16-byte loads and stores.
+// and cosines once into shared memory, for all heads, and moves units of 16
+// elements (8 pairs) with 16-byte loads and stores, kBatch units a thread in
+// flight.  The first batch is loaded before the angles are computed, so that one
+// latency hides the other.
 #include "common.cuh"
 #include "rope.h"
 
@@ -27,6 +29,17 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 8;  // rows per block
+constexpr int kBatch = 4;    // units in flight per thread
+
+// How a head is cut into units, each moved by one thread.
+//   kHalfVec (half layout, h = r/2 a multiple of 8): 16 elements, the pairs 8u ..
+//     8u + 7 (elements 8u and 8u + h, 8 each) or 16 copied elements at 16u.
+//   kInterleaved: 16 elements at 16u.
+//   kHalfAny (half layout, any h): 8 elements at 8u.  Their partners lie at any
+//     alignment in another thread's unit, so a warp, which holds whole heads, passes
+//     its units through shared memory.  Pair by pair loads and stores of 2 bytes
+//     took 325 us on 16384 rows of 72 heads of 64 (r = 50), this takes 99 us.
+enum Layout { kHalfVec, kInterleaved, kHalfAny };
 
 struct Unit {
     uint32_t a[4], b[4];
@@ -40,31 +53,17 @@ __device__ __forceinline__ void st16(__nv_bfloat16* p, const uint32_t (&r)[4]) {
     *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// How a unit's 16 elements lie in its head.
-enum Layout { kHalfVec, kInterleaved, kHalfScalar };
+// Place of pair p's (cosine, sine) in a row's table: the pairs that the threads of
+// a warp read together (the same p % 8) are neighbours.
+template <int D>
+__device__ __forceinline__ int cs_at(int p) {
+    return (p & 7) * (D / 16) + (p >> 3);
+}
 
-// Unit u of a head holds pair slots 8u .. 8u + 7.  Slots below h = r/2 are the
-// rotated pairs; slot p >= h stands for the two copied elements 2p and 2p + 1.
-//   kHalfVec (h a multiple of 8): the unit is elements 8u and 8u + h, 8 each, or
-//     16 copied elements at 16u.
-//   kInterleaved: the unit is elements 16u .. 16u + 15.
-//   kHalfScalar (any h): pair by pair.
 template <Layout kL>
 __device__ __forceinline__ void load_unit(Unit& x, const __nv_bfloat16* head, int u, int h) {
-    if constexpr (kL == kHalfScalar) {
-        const uint16_t* e = reinterpret_cast<const uint16_t*>(head);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int p = 8 * u + j;
-            const uint32_t lo = p < h ? e[p] : e[2 * p], hi = p < h ? e[p + h] : e[2 * p + 1];
-            if (j & 1) {
-                x.a[j >> 1] |= lo << 16;
-                x.b[j >> 1] |= hi << 16;
-            } else {
-                x.a[j >> 1] = lo;
-                x.b[j >> 1] = hi;
-            }
-        }
+    if constexpr (kL == kHalfAny) {
+        ld16(x.a, head + 8 * u);
     } else {
         const bool split = kL == kHalfVec && 8 * u < h;
         const int o = split ? 8 * u : 16 * u;
@@ -75,15 +74,8 @@ __device__ __forceinline__ void load_unit(Unit& x, const __nv_bfloat16* head, in
 
 template <Layout kL>
 __device__ __forceinline__ void store_unit(const Unit& x, __nv_bfloat16* head, int u, int h) {
-    if constexpr (kL == kHalfScalar) {
-        uint16_t* e = reinterpret_cast<uint16_t*>(head);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int p = 8 * u + j;
-            const int sh = (j & 1) * 16;
-            e[p < h ? p : 2 * p] = (uint16_t)(x.a[j >> 1] >> sh);
-            e[p < h ? p + h : 2 * p + 1] = (uint16_t)(x.b[j >> 1] >> sh);
-        }
+    if constexpr (kL == kHalfAny) {
+        st16(head + 8 * u, x.a);
     } else {
         const bool split = kL == kHalfVec && 8 * u < h;
         const int o = split ? 8 * u : 16 * u;
@@ -92,34 +84,45 @@ __device__ __forceinline__ void store_unit(const Unit& x, __nv_bfloat16* head, i
     }
 }
 
-// Rotates the unit's slots below h; the others keep their bits (a copied
-// element may be an infinity or a NaN).
-template <Layout kL>
-__device__ __forceinline__ void rotate_unit(Unit& x, const float2* cs, int u, int h) {
+// Rotates the unit's elements of the first 2h dimensions; the others keep their
+// bits (a copied element may be an infinity or a NaN).  `head` is the head's copy in
+// shared memory (kHalfAny only).
+template <int D, Layout kL>
+__device__ __forceinline__ void rotate_unit(Unit& x, const float2* cs, const uint16_t* head, int u, int h) {
     if constexpr (kL == kInterleaved) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int p = 8 * u + j;
-            if (p < h) {
+            if (8 * u + j < h) {
                 uint32_t& w = j < 4 ? x.a[j] : x.b[j - 4];
-                const float2 c = cs[p];
+                const float2 c = cs[j * (D / 16) + u];
                 const float e = bf16_lo(w), o = bf16_hi(w);
                 w = pack_bf16x2(e * c.x - o * c.y, o * c.x + e * c.y);
             }
         }
-    } else {
+    } else if constexpr (kL == kHalfVec) {
+        if (8 * u < h) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int p = 8 * u + 2 * j;
-            if (p < h) {
-                const float2 c0 = cs[p], c1 = cs[p + 1 < h ? p + 1 : p];
+            for (int j = 0; j < 4; ++j) {
+                const float2 c0 = cs[(2 * j) * (D / 16) + u], c1 = cs[(2 * j + 1) * (D / 16) + u];
                 const float e0 = bf16_lo(x.a[j]), e1 = bf16_hi(x.a[j]);
                 const float o0 = bf16_lo(x.b[j]), o1 = bf16_hi(x.b[j]);
-                const uint32_t a = pack_bf16x2(e0 * c0.x - o0 * c0.y, e1 * c1.x - o1 * c1.y);
-                const uint32_t b = pack_bf16x2(o0 * c0.x + e0 * c0.y, o1 * c1.x + e1 * c1.y);
-                const uint32_t keep = p + 1 < h ? 0u : 0xffff0000u;  // an odd h: slot h is copied
-                x.a[j] = (x.a[j] & keep) | (a & ~keep);
-                x.b[j] = (x.b[j] & keep) | (b & ~keep);
+                x.a[j] = pack_bf16x2(e0 * c0.x - o0 * c0.y, e1 * c1.x - o1 * c1.y);
+                x.b[j] = pack_bf16x2(o0 * c0.x + e0 * c0.y, o1 * c1.x + e1 * c1.y);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int e = 8 * u + j;
+            if (e < 2 * h) {
+                const bool first = e < h;
+                const float2 c = cs[cs_at<D>(first ? e : e - h)];
+                const float other = __uint_as_float((uint32_t)head[first ? e + h : e - h] << 16);
+                uint32_t& w = x.a[j >> 1];
+                const float own = (j & 1) ? bf16_hi(w) : bf16_lo(w);
+                const float y = first ? own * c.x - other * c.y : own * c.x + other * c.y;
+                const uint32_t bits = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                w = (j & 1) ? (w & 0xffffu) | bits << 16 : (w & 0xffff0000u) | bits;
             }
         }
     }
@@ -130,10 +133,13 @@ __device__ __forceinline__ void rotate_unit(Unit& x, const float2* cs, int u, in
 // the division of a unit's index by the number of heads into a multiplication.
 template <int D, Layout kL, bool kAppend>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const Args p, int tile, uint32_t heads_mul) {
-    extern __shared__ float2 cs[];  // (tile, h)
+    extern __shared__ float2 cs[];  // (tile, D / 2)
+    __shared__ uint4 stage[kL == kHalfAny ? kBatch * kThreads : 1];
     __shared__ long long slot[kMaxRows];
-    constexpr int U = D / 16;
-    constexpr int kLogU = U == 4 ? 2 : 3;
+    __shared__ unsigned long long turn[D / 2];
+    constexpr int U = kL == kHalfAny ? D / 8 : D / 16;
+    constexpr int kLogU = U == 4 ? 2 : U == 8 ? 3 : 4;
+    constexpr int kWarpUnits = kBatch * 32;
     const int h = p.rotary_dim / 2;
     const int b = blockIdx.y;
     int n0 = 0, n = p.rows;
@@ -152,12 +158,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args p, int tile, 
     const int m = min(tile, n - r0);
     if (m <= 0) return;
 
-    int L = 0;
+    int t0 = 0;  // logical token of the request's first new row
     if constexpr (kAppend) {
-        L = p.seqlens[b];
-        const int n_all = p.cu_new ? p.cu_new[b + 1] - n0 : 1;
+        t0 = p.seqlens[b] - (p.cu_new ? p.cu_new[b + 1] - n0 : 1);
         if (threadIdx.x < m) {
-            const int t = L - n_all + r0 + (int)threadIdx.x;
+            const int t = t0 + r0 + (int)threadIdx.x;
             long long sl = -1;
             if (t < 0 || t / p.page_size >= p.max_pages) {
                 raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
@@ -170,53 +175,84 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args p, int tile, 
             }
             slot[threadIdx.x] = sl;
         }
-        L -= n_all;
     }
-    for (int e = threadIdx.x; e < m * h; e += kThreads) {
-        const int r = e / h, i = e - r * h;
-        const int pos = p.positions ? p.positions[n0 + r0 + r] : L + r0 + r;
-        const double f = p.inv_freq[i] * 0.15915494309189535;  // turns per position
-        const unsigned long long turn = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
-        const int a = (int)(uint32_t)((turn * (unsigned long long)(long long)pos) >> 32);
-        float sn, cn;
-        sincospif((float)a * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: half turns
-        if (p.inverse) sn = -sn;
-        cs[e] = make_float2(cn * p.attn_scale, sn * p.attn_scale);
+    if (threadIdx.x < h) {
+        const double f = p.inv_freq[threadIdx.x] * 0.15915494309189535;  // turns per position
+        turn[threadIdx.x] = __double2ull_rz((f - floor(f)) * 18446744073709551616.0);
     }
-    __syncthreads();
 
     const int heads = p.hq + (p.k ? p.hkv : 0) + (kAppend ? p.hkv : 0);
     const int total = (m * heads) << kLogU;
-    for (int idx = threadIdx.x; idx < total; idx += kThreads) {
-        const int u = idx & (U - 1), rh = idx >> kLogU;
-        const int r = heads_mul ? (int)__umulhi((uint32_t)rh, heads_mul) : rh, hd = rh - r * heads;
+    // Row, head and unit of an index; the source row of that head.
+    auto place = [&](int idx, int& r, int& hd) {
+        const int rh = idx >> kLogU;
+        r = heads_mul ? (int)__umulhi((uint32_t)rh, heads_mul) : rh;
+        hd = rh - r * heads;
+    };
+    auto source = [&](int r, int hd) -> const __nv_bfloat16* {
         const long long row = n0 + r0 + r;
-        const __nv_bfloat16* src;
-        __nv_bfloat16* dst;
-        bool turn = true;
-        if (hd < p.hq) {
-            src = p.q + row * p.q_rs + hd * D;
-            dst = p.q_out + row * p.q_out_rs + hd * D;
-        } else if (hd < p.hq + p.hkv) {
-            const int kh = hd - p.hq;
-            src = p.k + row * p.k_rs + kh * D;
-            if constexpr (kAppend) {
-                if (slot[r] < 0) continue;
-                dst = p.k_cache + ((size_t)slot[r] * p.hkv + kh) * D;
-            } else {
-                dst = p.k_out + row * p.k_out_rs + kh * D;
+        if (hd < p.hq) return p.q + row * p.q_rs + hd * D;
+        hd -= p.hq;
+        if (hd < p.hkv) return p.k + row * p.k_rs + hd * D;
+        return p.v + row * p.v_rs + (hd - p.hkv) * D;
+    };
+    for (int base = threadIdx.x; base - (int)threadIdx.x < total; base += kBatch * kThreads) {
+        Unit x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int idx = base + i * kThreads;
+            if (idx < total) {
+                int r, hd;
+                place(idx, r, hd);
+                load_unit<kL>(x[i], source(r, hd), idx & (U - 1), h);
             }
-        } else {
-            const int vh = hd - p.hq - p.hkv;
-            if (slot[r] < 0) continue;
-            src = p.v + row * p.v_rs + vh * D;
-            dst = p.v_cache + ((size_t)slot[r] * p.hkv + vh) * D;
-            turn = false;
         }
-        Unit x;
-        load_unit<kL>(x, src, u, h);
-        if (turn) rotate_unit<kL>(x, cs + r * h, u, h);
-        store_unit<kL>(x, dst, u, h);
+        if (base == (int)threadIdx.x) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < m * h; e += kThreads) {
+                const int r = e / h, i = e - r * h;
+                const int pos = p.positions ? p.positions[n0 + r0 + r] : t0 + r0 + r;
+                const int a = (int)(uint32_t)((turn[i] * (unsigned long long)(long long)pos) >> 32);
+                float sn, cn;
+                sincospif((float)a * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: half turns
+                if (p.inverse) sn = -sn;
+                cs[r * (D / 2) + cs_at<D>(i)] = make_float2(cn * p.attn_scale, sn * p.attn_scale);
+            }
+            __syncthreads();
+        }
+        uint4* const mine = stage + (threadIdx.x >> 5) * kWarpUnits;  // this warp's units
+        if constexpr (kL == kHalfAny) {
+            __syncwarp();  // the previous batch has been read
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                mine[i * 32 + (threadIdx.x & 31)] = make_uint4(x[i].a[0], x[i].a[1], x[i].a[2], x[i].a[3]);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int idx = base + i * kThreads;
+            if (idx >= total) continue;
+            int r, hd;
+            place(idx, r, hd);
+            const int u = idx & (U - 1);
+            const long long row = n0 + r0 + r;
+            __nv_bfloat16* dst;
+            if (hd < p.hq) {
+                dst = p.q_out + row * p.q_out_rs + hd * D;
+            } else if (!kAppend) {
+                dst = p.k_out + row * p.k_out_rs + (hd - p.hq) * D;
+            } else {
+                if (slot[r] < 0) continue;
+                const int c = hd - p.hq;
+                dst = c < p.hkv ? p.k_cache + ((size_t)slot[r] * p.hkv + c) * D
+                                : p.v_cache + ((size_t)slot[r] * p.hkv + c - p.hkv) * D;
+            }
+            const uint16_t* head = nullptr;
+            if constexpr (kL == kHalfAny)
+                head = reinterpret_cast<const uint16_t*>(mine + i * 32 + ((threadIdx.x & 31) & ~(U - 1)));
+            if (!kAppend || hd < p.hq + p.hkv) rotate_unit<D, kL>(x[i], cs + r * (D / 2), head, u, h);
+            store_unit<kL>(x[i], dst, u, h);
+        }
     }
 }
 
@@ -229,7 +265,7 @@ static cudaError_t launch_d(const Args& a, cudaStream_t s) {
     int tile = a.rows / (152 * 8);
     tile = tile < 1 ? 1 : tile > kMaxRows ? kMaxRows : tile;
     const dim3 grid((unsigned)((longest + tile - 1) / tile), append ? a.batch : 1);
-    const size_t smem = (size_t)tile * (a.rotary_dim / 2) * sizeof(float2);
+    const size_t smem = (size_t)tile * (D / 2) * sizeof(float2);
     const uint32_t mul = heads == 1 ? 0u : (uint32_t)(((1ull << 32) + heads - 1) / heads);
     if (append)
         rope_kernel<D, kL, true><<<grid, kThreads, smem, s>>>(a, tile, mul);
@@ -239,14 +275,14 @@ static cudaError_t launch_d(const Args& a, cudaStream_t s) {
 }
 
 cudaError_t launch(const Args& a, cudaStream_t s) {
-    const Layout l = a.interleaved ? kInterleaved : a.rotary_dim % 16 == 0 ? kHalfVec : kHalfScalar;
+    const Layout l = a.interleaved ? kInterleaved : a.rotary_dim % 16 == 0 ? kHalfVec : kHalfAny;
     if (a.head_dim == 64)
         return l == kInterleaved ? launch_d<64, kInterleaved>(a, s)
                : l == kHalfVec   ? launch_d<64, kHalfVec>(a, s)
-                                 : launch_d<64, kHalfScalar>(a, s);
+                                 : launch_d<64, kHalfAny>(a, s);
     return l == kInterleaved ? launch_d<128, kInterleaved>(a, s)
            : l == kHalfVec   ? launch_d<128, kHalfVec>(a, s)
-                             : launch_d<128, kHalfScalar>(a, s);
+                             : launch_d<128, kHalfAny>(a, s);
 }
 
 ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
