@@ -490,7 +490,7 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
  *                then -1
  *   new_seqlens  (batch,) int32: min(length, budget); must not be seqlens
  * Supported: head_dim 64 or 128; 1 <= budget, 0 <= keep_first, keep_last,
- * keep_first + keep_last <= budget; at most 32767 weight heads, 65535 requests.
+ * keep_first + keep_last <= budget; at most 21845 weight heads, 65535 requests.
  */
 int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,
                           const int32_t* seqlens, const float* weights, int batch, int weight_heads,

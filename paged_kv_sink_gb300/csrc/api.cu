@@ -613,8 +613,8 @@ int check_moves(const char* who, const char* name, int heads, int hkv, int head_
     if (head_dim != 64 && head_dim != 128)
         return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64, 128)", who, head_dim);
     if (heads != 1 && heads != hkv) return fail(ATTN_SINK_ERR_INVALID, "%s: %s %d must be 1 or hkv", who, name, heads);
-    if (heads > kMaxGridDim / 2)
-        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: %s %d above %d", who, name, heads, kMaxGridDim / 2);
+    if (heads > kMaxGridDim / 3)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: %s %d above %d", who, name, heads, kMaxGridDim / 3);
     if ((long long)hkv * head_dim * 2 >= (1LL << 31))
         return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: a token's row must be below 2 GiB", who);
     return ATTN_SINK_OK;
@@ -915,7 +915,6 @@ int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t*
     if (e != cudaSuccess) return cuda_fail(e, "evict_paged: scratch allocation");
     attn::evict::SelectArgs a = {};
     a.weights = weights;
-    a.weights_out = weights_out;
     a.seqlens = seqlens;
     a.new_seqlens = new_seqlens;
     a.kept = kept;
@@ -943,6 +942,9 @@ int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t*
     m.page_size = page_size;
     m.num_pages = num_pages;
     m.max_rows = budget;
+    m.weights = weights;
+    m.weights_out = weights_out;
+    m.cap = weight_cap;
     if ((e = attn::evict::launch_move(m, s)) != cudaSuccess) return cuda_fail(e, "evict_paged: move launch");
     return ATTN_SINK_OK;
 }
