@@ -170,8 +170,8 @@ int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_
     a.group = hq / hkv;
     a.scale = attn::resolve_scale(scale, head_dim);
     attn::decode::Plan pl = attn::decode::make_plan(a);
-    // partials, then (accumulated weights only) statistics and scores
-    const size_t scores_at = (pl.part_o_bytes + pl.part_ml_bytes + (size_t)batch * hq * sizeof(float2) + 255) & ~size_t(255);
+    // partials, then (accumulated weights only) scores
+    const size_t scores_at = (pl.part_o_bytes + pl.part_ml_bytes + 255) & ~size_t(255);
     size_t bytes = pl.part_o_bytes + pl.part_ml_bytes;
     if (w) bytes = scores_at + (size_t)batch * hkv * pl.hblocks * pl.nvis_max * 8 * pl.nt * sizeof(float);
     Scratch ws;
@@ -179,10 +179,7 @@ int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_
     if (e != cudaSuccess) return cuda_fail(e, "decode: scratch allocation");
     float* part_o = static_cast<float*>(ws.ptr);
     float2* part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws.ptr) + pl.part_o_bytes);
-    if (w) {
-        w->stats = reinterpret_cast<float2*>(static_cast<char*>(ws.ptr) + pl.part_o_bytes + pl.part_ml_bytes);
-        w->scores = reinterpret_cast<float*>(static_cast<char*>(ws.ptr) + scores_at);
-    }
+    if (w) w->scores = reinterpret_cast<float*>(static_cast<char*>(ws.ptr) + scores_at);
     e = attn::decode::launch(a, pl, part_o, part_ml, s, w);
     if (e != cudaSuccess) return cuda_fail(e, "decode: launch");
     return ATTN_SINK_OK;

@@ -111,7 +111,7 @@ __device__ __forceinline__ Ranges request_ranges(const SplitParams& p, int b, bo
     return visible_ranges(L - 1, p.win_first, p.win_last);
 }
 
-// kScores: also stores every score (log2 units) for decode_weights_kernel.
+// kScores: also stores every score (log2 units) for decode_finish_kernel.
 template <int D, int NT, int NSTAGE, bool kScores>
 __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
@@ -353,23 +353,15 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParam
     }
 }
 
+// Merges the `nsplit` partials of (request b, query head h), dimension dd.
 template <int D>
-__global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, const float* __restrict__ sink,
-                                                          __nv_bfloat16* __restrict__ out,
-                                                          float* __restrict__ lse) {
-    const int h = blockIdx.x, b = blockIdx.y, dd = threadIdx.x;
-    const Ranges r = request_ranges(p, b, false);
-    const int nvis = visible_count(r);
-    const int nsplit = (int)(((long long)nvis + p.split_tokens - 1) / p.split_tokens);
+__device__ __forceinline__ void merge_splits(const SplitParams& p, int b, int h, int dd, int nsplit,
+                                             const float* sink, __nv_bfloat16* out, float* lse) {
     const size_t base = ((size_t)b * p.hq + h) * p.max_splits;
     const float sg = sink ? sink[h] * ATTN_LOG2E : -INFINITY;
-    // the split grid (this launch's programmatic predecessor) has completed and
-    // its partials are visible past this point
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     float M = sg;
     for (int s = 0; s < nsplit; ++s) M = fmaxf(M, p.part_ml[base + s].x);
     float o = 0.f, lse_v;
-    float2 st = make_float2(INFINITY, 0.f);  // 2^(x - st.x) * st.y is a token's weight: 0 here
     if (M == -INFINITY || M == INFINITY) {
         // nothing visible and no sink, or an infinite sink taking all the mass
         lse_v = M;
@@ -383,60 +375,147 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, 
         }
         o = acc / Z;
         lse_v = (M + log2f(Z)) * ATTN_LN2;
-        st = make_float2(M, 1.f / Z);
     }
-    if (p.stats && dd == 0) p.stats[(size_t)b * p.hq + h] = st;
     out[((size_t)b * p.hq + h) * D + dd] = __float2bfloat16_rn(o);
     if (lse && dd == 0) lse[(size_t)b * p.hq + h] = lse_v;
 }
 
-// Adds every visible token's attention weight to its accumulator:
-//     w[b][head][t] += sum_h exp(s_ht - LSE_h)
-// over the query heads h of KV head `head`, or over all query heads when the
-// weights have one head.  One thread per visible token reads the scores that the
-// split kernel stored (4 bytes per query head and token, against 4 d for the K
-// and V row of a KV head) in a fixed order, so the sums do not depend on
-// scheduling.  An accumulator past its capacity is left out.
-constexpr int kWeightThreads = 256;
-template <int NT>
-__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const SplitParams p, float* weights, int heads,
-                                                                        int cap) {
-    extern __shared__ float2 st[];  // one per query head (padded to 8 NT per head block)
-    const int head = blockIdx.y, b = blockIdx.z;
-    const int blocks = p.hq / p.group * p.hblocks / heads;  // head blocks that this accumulator sums
-    constexpr int H = 8 * NT;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the combine grid's statistics
-    for (int e = threadIdx.x; e < blocks * H; e += kWeightThreads) {
-        const int gb = head * blocks + e / H, j = e % H;  // head block, head in it
-        const int in_group = gb % p.hblocks * H + j;
-        st[e] = in_group < p.group ? p.stats[(size_t)b * p.hq + gb / p.hblocks * p.group + in_group]
-                                   : make_float2(INFINITY, 0.f);
-    }
-    __syncthreads();
+template <int D>
+__global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, const float* __restrict__ sink,
+                                                          __nv_bfloat16* __restrict__ out,
+                                                          float* __restrict__ lse) {
+    const int h = blockIdx.x, b = blockIdx.y, dd = threadIdx.x;
     const Ranges r = request_ranges(p, b, false);
     const int nvis = visible_count(r);
-    for (long long v = (long long)blockIdx.x * kWeightThreads + threadIdx.x; v < nvis;
-         v += (long long)gridDim.x * kWeightThreads) {
-        const int t = visible_token(r, (int)v);
-        if (t >= cap) {
-            raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-            continue;
-        }
-        float sum = 0.f;
-        for (int i = 0; i < blocks; ++i) {
-            const long long hb = (long long)b * (p.hq / p.group) * p.hblocks + head * blocks + i;
-            const float4* x = reinterpret_cast<const float4*>(p.scores + (hb * p.scores_cap + v) * H);
+    const int nsplit = (int)(((long long)nvis + p.split_tokens - 1) / p.split_tokens);
+    // the split grid (this launch's programmatic predecessor) has completed and
+    // its partials are visible past this point
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    merge_splits<D>(p, b, h, dd, nsplit, sink, out, lse);
+}
+
+// What follows the split grid when attention weights are accumulated, in one launch:
+// the first `wblocks` blocks in x add every visible token's weight to its
+// accumulator,
+//     w[b][head][t] += sum_h exp(s_ht - LSE_h)
+// over the query heads h of KV head `head`, or over all query heads when the
+// weights have one head; the others merge the splits' outputs as
+// decode_combine_kernel does.
+// A weights block takes the statistics of its heads from the partials itself, so
+// nothing waits for the merge.  The scores that the split kernel stored (4 bytes per
+// query head and token, against 4 d for a KV head's K and V row) are read once, 8
+// tokens a thread in flight; the sums have a fixed order.  Requests are taken last
+// first: the scores written last may still be in L2.
+constexpr int kWeightThreads = 256;
+template <int NT>
+constexpr int kWeightTokens = NT == 1 ? 8 : 4;  // tokens per thread
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const SplitParams p, const float* sink,
+                                                                       __nv_bfloat16* out, float* lse, float* weights,
+                                                                       int heads, int cap, int wblocks, int tokens) {
+    constexpr int H = 8 * NT;
+    const int b = (int)(gridDim.z - 1 - blockIdx.z), tid = threadIdx.x;
+    const Ranges r = request_ranges(p, b, false);
+    const int nvis = visible_count(r);
+    const int nsplit = (int)(((long long)nvis + p.split_tokens - 1) / p.split_tokens);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials and scores are complete
+
+    if ((int)blockIdx.x >= wblocks) {
+        const int m = ((int)blockIdx.x - wblocks) * heads + blockIdx.y;
+        const int h = m * (kWeightThreads / D) + tid / D, dd = tid % D;
+        if (h < p.hq) merge_splits<D>(p, b, h, dd, nsplit, sink, out, lse);
+        return;
+    }
+    if ((long long)blockIdx.x * tokens >= nvis) return;
+    extern __shared__ float2 st[];  // (reference, 1 / denominator) of each query head, padded to H per head block
+    const int head = blockIdx.y, hkv = p.hq / p.group;
+    const int blocks = hkv * p.hblocks / heads;  // head blocks that this accumulator sums
+    // The first head block's scores and the accumulators are requested before the
+    // statistics, which take two more loads in a row.
+    constexpr int kT = kWeightTokens<NT>;
+    const float* xs = p.scores + ((long long)b * hkv * p.hblocks + head * blocks) * p.scores_cap * H;
+    float* w = weights + ((size_t)b * heads + head) * cap;
+    int v = 0, v1 = 0;  // this thread's first token, the chunk's end
+    float4 y[kT][H / 4];
+    float sum[kT];
+    auto load = [&](int i) {
 #pragma unroll
-            for (int q = 0; q < H / 4; ++q) {
-                const float4 y = x[q];
-                const float2* s4 = st + i * H + q * 4;
-                sum += fast_exp2(y.x - s4[0].x) * s4[0].y;
-                sum += fast_exp2(y.y - s4[1].x) * s4[1].y;
-                sum += fast_exp2(y.z - s4[2].x) * s4[2].y;
-                sum += fast_exp2(y.w - s4[3].x) * s4[3].y;
+        for (int k = 0; k < kT; ++k)
+            if (v + k * kWeightThreads < v1) {
+                const float4* x = reinterpret_cast<const float4*>(xs + (i * p.scores_cap + v + k * kWeightThreads) * H);
+#pragma unroll
+                for (int q = 0; q < H / 4; ++q) y[k][q] = __ldcs(x + q);
+            }
+    };
+    auto start = [&](long long v0) {
+        v = (int)v0 + tid;
+        v1 = (int)min((long long)nvis, v0 + tokens);
+        load(0);
+#pragma unroll
+        for (int k = 0; k < kT; ++k) {
+            sum[k] = 0.f;
+            if (v + k * kWeightThreads < v1) {
+                const int t = visible_token(r, v + k * kWeightThreads);
+                if (t < cap)
+                    sum[k] = w[t];
+                else
+                    raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
             }
         }
-        weights[((size_t)b * heads + head) * cap + t] += sum;
+    };
+    start((long long)blockIdx.x * tokens);
+    // Eight lanes per query head.
+    for (int e = tid >> 3; e < (blocks * H + 31) / 32 * 32; e += kWeightThreads / 8) {
+        const int gb = head * blocks + e / H, j = gb % p.hblocks * H + e % H;  // head block; head in its group
+        const bool in = e < blocks * H && j < p.group;
+        const int h = in ? gb / p.hblocks * p.group + j : 0;
+        const float2* ml = p.part_ml + ((size_t)b * p.hq + h) * p.max_splits;
+        const float sg = sink ? sink[h] * ATTN_LOG2E : -INFINITY;
+        float M = sg;
+        for (int s = tid & 7; s < nsplit; s += 8) M = fmaxf(M, ml[s].x);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float Z = 0.f;
+        for (int s = tid & 7; s < nsplit; s += 8) Z += ml[s].y * fast_exp2(ml[s].x - ref);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) Z += __shfl_xor_sync(0xffffffffu, Z, o);
+        Z += fast_exp2(sg - ref);
+        // 2^(x - st.x) * st.y is a token's weight: 0 where nothing is visible, under an
+        // infinite sink and for heads that do not exist
+        const bool some = in && M != -INFINITY && M != INFINITY;
+        if ((tid & 7) == 0 && e < blocks * H) st[e] = some ? make_float2(M, 1.f / Z) : make_float2(INFINITY, 0.f);
+    }
+    __syncthreads();
+    for (long long v0 = (long long)blockIdx.x * tokens;;) {
+        for (int i = 0; i < blocks; ++i) {
+            float add[kT];
+#pragma unroll
+            for (int k = 0; k < kT; ++k) {
+                add[k] = 0.f;
+#pragma unroll
+                for (int q = 0; q < H / 4; ++q) {
+                    const float2* s4 = st + i * H + q * 4;
+                    add[k] += fast_exp2(y[k][q].x - s4[0].x) * s4[0].y;
+                    add[k] += fast_exp2(y[k][q].y - s4[1].x) * s4[1].y;
+                    add[k] += fast_exp2(y[k][q].z - s4[2].x) * s4[2].y;
+                    add[k] += fast_exp2(y[k][q].w - s4[3].x) * s4[3].y;
+                }
+            }
+            if (i + 1 < blocks) load(i + 1);
+#pragma unroll
+            for (int k = 0; k < kT; ++k) sum[k] += add[k];
+        }
+#pragma unroll
+        for (int k = 0; k < kT; ++k)
+            if (v + k * kWeightThreads < v1) {
+                const int t = visible_token(r, v + k * kWeightThreads);
+                if (t < cap) w[t] = sum[k];
+            }
+        v0 += (long long)wblocks * tokens;
+        if (v0 >= nvis) break;
+        start(v0);
     }
 }
 
@@ -555,7 +634,6 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     sp.group = a.group;
     sp.scale_log2 = a.scale * ATTN_LOG2E;
     sp.scores = w ? w->scores : nullptr;
-    sp.stats = w ? w->stats : nullptr;
     sp.scores_cap = pl.nvis_max;
     sp.page_shift = -1;
     for (int sh = 0; sh < 31; ++sh)
@@ -587,22 +665,29 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     cfg.numAttrs = 1;
     const float* sink = a.sink;
     float* lse = a.lse;
-    if (a.head_dim == 64)
-        e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<64>, sp, sink, out, lse);
-    else
-        e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<128>, sp, sink, out, lse);
-    if (e != cudaSuccess) return e;
     if (w) {
-        const long long blocks = (pl.nvis_max + kWeightThreads - 1) / kWeightThreads;
-        cfg.gridDim = dim3((unsigned)blocks, w->heads, a.batch);
+        // Tokens per step of a weights block: all that its threads hold once that gives
+        // every SM several blocks, else 512.  With many blocks each takes two steps of
+        // the longest request: blocks of shorter requests that find nothing to do cost a
+        // microsecond each (two fit an SM).
+        const long long units = (long long)a.batch * w->heads;
+        const int most = kWeightThreads * (pl.nt == 1 ? kWeightTokens<1> : kWeightTokens<2>);
+        const int tokens = (pl.nvis_max + most - 1) / most * units >= 4 * 152 ? most : 512;
+        int wblocks = (int)((pl.nvis_max + tokens - 1) / tokens);
+        if (wblocks * units >= 16 * 152) wblocks = (wblocks + 1) / 2;
+        const int per_block = kWeightThreads / a.head_dim, merges = (a.hq + per_block - 1) / per_block;
+        cfg.gridDim = dim3((unsigned)(wblocks + (merges + w->heads - 1) / w->heads), w->heads, a.batch);
         cfg.blockDim = dim3(kWeightThreads);
         cfg.dynamicSmemBytes = (size_t)a.hkv / w->heads * pl.hblocks * 8 * pl.nt * sizeof(float2);
-        if (pl.nt == 1)
-            e = cudaLaunchKernelEx(&cfg, decode_weights_kernel<1>, sp, w->weights, w->heads, w->cap);
-        else
-            e = cudaLaunchKernelEx(&cfg, decode_weights_kernel<2>, sp, w->weights, w->heads, w->cap);
-        if (e != cudaSuccess) return e;
+        auto finish = a.head_dim == 64 ? (pl.nt == 1 ? decode_finish_kernel<64, 1> : decode_finish_kernel<64, 2>)
+                                       : (pl.nt == 1 ? decode_finish_kernel<128, 1> : decode_finish_kernel<128, 2>);
+        e = cudaLaunchKernelEx(&cfg, finish, sp, sink, out, lse, w->weights, w->heads, w->cap, wblocks, tokens);
+    } else if (a.head_dim == 64) {
+        e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<64>, sp, sink, out, lse);
+    } else {
+        e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<128>, sp, sink, out, lse);
     }
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 

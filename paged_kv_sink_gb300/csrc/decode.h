@@ -26,7 +26,6 @@ struct SplitParams {
     float scale_log2;  // softmax scale * log2(e)
     // Accumulated attention weights only (else NULL):
     float* scores;         // (batch, hkv * hblocks, scores_cap, 8 nt) scores of the visible tokens, log2 units
-    float2* stats;         // (batch, hq): (reference, 1 / denominator) of each query head's softmax
     long long scores_cap;  // visible tokens of the longest possible request
 };
 
@@ -59,7 +58,6 @@ struct Weights {
     float* weights;  // (batch, heads, cap), heads 1 or hkv
     int heads, cap;
     float* scores;
-    float2* stats;
 };
 
 Plan make_plan(const Args& a);
