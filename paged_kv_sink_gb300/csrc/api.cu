@@ -816,12 +816,10 @@ int attn_sink_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const att
     const attn::tree::Plan pl = attn::tree::make_plan(a);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Scratch ws;
-    cudaError_t e = ws.alloc(pl.part_o_bytes + pl.part_ml_bytes, s);
+    cudaError_t e = ws.alloc(pl.part_o_bytes + pl.part_ml_bytes + pl.first_bytes, s);
     if (e != cudaSuccess) return cuda_fail(e, "tree_paged: scratch allocation");
-    float* part_o = static_cast<float*>(ws.ptr);
-    float2* part_ml = reinterpret_cast<float2*>(static_cast<char*>(ws.ptr) + pl.part_o_bytes);
     std::string err;
-    e = attn::tree::launch(a, pl, part_o, part_ml, s, &err);
+    e = attn::tree::launch(a, pl, ws.ptr, s, &err);
     if (e != cudaSuccess)
         return fail(ATTN_SINK_ERR_CUDA, "tree_paged: %s: %s", err.c_str(), cudaGetErrorString(e));
     return ATTN_SINK_OK;

@@ -15,18 +15,31 @@
 // K / V are read once for all of it; a tile per query head, as in the paged
 // forward, would leave 7/8 of its rows empty and read K / V eight times.
 //
-// The keys of a (request, KV head, row tile) are cut into splits of whole
-// 128-key tiles, one CTA each:
-//   warp 0      TMA producer: Q once, then the K tiles, page segment by segment
-//   warp 1      TMEM allocator, issues S = Q K^T (128 x 128, operands in shared memory)
+// The unit of work is a step: one 128-key tile of one (request, row tile), for one KV
+// head.  The grid is one wave of persistent CTAs (two per SM at d 64, one at d 128) in
+// gangs of one CTA per KV head.  The gangs share all steps of the batch out evenly,
+// each a run of consecutive steps: requests of any lengths balance, and only the first
+// and the last row tile of a run can be incomplete.  (A gang reads whole token rows:
+// CTAs that were each at another place of the cache read 128 bytes of 1 KB rows at a
+// time, 4.1 TB/s against 5.8.)  A run is cut into segments (the steps of one row
+// tile); the pipeline goes on across them.  In a CTA
+//   warp 0      TMA producer of the K tiles, page segment by page segment
+//   warp 1      TMEM allocator, loads Q once per segment and issues S = Q K^T (128 x
+//               128, operands in shared memory)
 //   warp 2      TMA producer of the V tiles
 //   warp 3      issues O += P V (P read from TMEM)
 //   warps 4..7  softmax, one row per thread, in the manner of the paged forward:
 //               against a running reference that starts at the sink and moves only
 //               when a value exceeds it by 2^64.  The sink itself is added once, at
 //               the end.
-// With more than one split, un-normalised fp32 partials go through scratch to
-// tree_combine_kernel; with one, the CTA writes the output itself.
+// A segment that has all key tiles of its row tile writes the output; the others leave
+// un-normalised fp32 partials (two places per run and KV head), which
+// tree_combine_kernel merges.
+//
+// Row tiles of one request read the same keys, but far apart in time when each gang
+// has one run: L2 must hold all K / V for them to be read once.  Where it does not, the
+// steps are handed out in rounds: run i goes to gang i mod gangs, runs are shorter, and
+// the gangs work on 64 MB of K / V at a time.
 //
 // Masks: prefix tiles that every row sees whole are not masked at all.  In the
 // others each thread builds the 128-bit visibility of its row: ranges for the
@@ -47,6 +60,11 @@ using namespace sm103;
 
 constexpr int BM = 128, BN = 128;
 constexpr int kStages = 3;  // K and V rings
+constexpr int kBadRing = 4;  // segments that the V producer may be ahead, + 1
+constexpr int kMinSteps = 2;   // of a run
+constexpr int kRoundSteps = 8;  // of a run where a gang has several
+constexpr int kMaxRounds = 8;
+constexpr long long kRoundBytes = 64ll << 20;
 constexpr int kThreads = 256;
 // 128 registers per thread at launch, moved from the control warps to the softmax
 // warps: 128 * 40 + 128 * 216 = 256 * 128.
@@ -66,24 +84,6 @@ struct Cfg {
     static constexpr bool kTwoPerSm = D == 64;
 };
 
-template <int D>
-struct __align__(1024) Smem {
-    uint8_t q[Cfg<D>::kTile];
-    uint8_t k[kStages][Cfg<D>::kTile];
-    uint8_t v[kStages][Cfg<D>::kTile];
-    uint64_t q_full;
-    uint64_t k_full[kStages], k_empty[kStages];
-    uint64_t v_full[kStages], v_empty[kStages];
-    uint64_t s_full, s_free, p_full, o_done;  // one phase per key tile
-    uint64_t final_bar, final_pv;
-    uint64_t v_fix;    // V tiles that need their rows looked at land here first
-    uint64_t v_fixed;  // all of them have been
-    uint32_t tmem_base;
-    int abort;
-    uint32_t v_bad[kMaxNodes / 32];  // nodes whose V row holds an infinity or a NaN
-    uint8_t parent[kMaxNodes];       // parent + 1
-};
-
 struct Params {
     const float* sink;
     const int32_t* cu_q;
@@ -93,22 +93,23 @@ struct Params {
     const __nv_bfloat16* v_cache;
     __nv_bfloat16* out;
     float* lse;
-    float* part_o;    // (batch, units, splits, 128, D) fp32, un-normalised
-    float2* part_ml;  // (batch, units, splits, 128): (reference in log2 units, sum)
-    int max_pages, page_shift, seg_shift, num_pages;
+    float* part_o;       // (runs, hkv, 2, 128, D) fp32, un-normalised
+    float2* part_ml;     // (runs, hkv, 2, 128): (reference in log2 units, sum)
+    long long* first;    // (batch + 1): steps before each request; then the steps per run
+    int max_rounds;      // runs per gang that the scratch has room for
+    int batch, max_pages, page_shift, seg_shift, num_pages;
     int hq, hkv, group, total_q, max_q;
-    int npt, mtiles;   // nodes per row tile, row tiles of the largest request
-    int split_tiles, splits;
+    int npt;  // nodes per row tile
     int win_first, win_last;
     float scale_log2;
 };
 
-// What a CTA (or a combine warp) derives of its request.
+// What the kernels derive of a request.
 struct Request {
     int q_start, n, L, P;  // first row, nodes, cached tokens, prefix
-    int rows;              // nodes that get results
+    int rows, mtiles;      // nodes that get results, row tiles of them
     int ta, tb, ntiles;    // key tiles [0, ta) and [tb, ...), ntiles in all
-    int per_split, nsplit;
+    __device__ __forceinline__ int tile(int it) const { return it < ta ? it : tb + (it - ta); }
 };
 
 __device__ __forceinline__ Request request(const Params& p, int b, bool report) {
@@ -123,6 +124,7 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
         if (r.L > cap) r.L = (int)cap;
     }
     r.rows = r.q_start < 0 ? 0 : max(0, min(min(r.n, p.max_q), p.total_q - r.q_start));
+    r.mtiles = (r.rows + p.npt - 1) / p.npt;
     if (r.L < r.n) r.L = 0;  // the nodes are not in the cache: nothing is seen
     r.P = max(0, r.L - r.n);
     const int t_end = (r.L + BN - 1) / BN;
@@ -133,16 +135,119 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
         r.tb = min(max(r.ta, lo / BN), t_end);
     }
     r.ntiles = r.ta + (t_end - r.tb);
-    r.per_split = max(p.split_tiles, (r.ntiles + p.splits - 1) / p.splits);
-    r.nsplit = (r.ntiles + r.per_split - 1) / r.per_split;
     return r;
 }
+
+__device__ __forceinline__ long long steps_of(const Request& r) { return (long long)r.mtiles * r.ntiles; }
+
+// The runs of steps of a gang: their first requests and steps in those.
+struct Runs {
+    long long per_run, total;
+    int gang, gangs;
+    int start_b[kMaxRounds], start_step[kMaxRounds];
+};
+
+// A CTA's run of steps, segment by segment.  Each control warp and the softmax
+// warpgroup walk a cursor of their own, kept in shared memory: it is read a few times
+// per tile, and the control warps have 40 registers.
+struct Cursor {
+    Request rq;
+    int b, mt, it0, ntiles;  // request, row tile, first key tile and key tiles of the segment
+    int round, in_run;       // run of this gang; segments of the run before this one
+    int left;                // steps of the run from this segment on
+
+    __device__ __forceinline__ void start(const Params& p, const Runs& runs) {
+        round = 0;
+        start_run(p, runs);
+    }
+    __device__ __forceinline__ void start_run(const Params& p, const Runs& runs) {
+        const long long first = ((long long)round * runs.gangs + runs.gang) * runs.per_run;
+        left = (int)max(0ll, min(runs.per_run, runs.total - first));
+        in_run = 0;
+        if (left == 0) return;
+        b = runs.start_b[round];
+        rq = request(p, b, false);
+        mt = runs.start_step[round] / rq.ntiles;
+        it0 = runs.start_step[round] - mt * rq.ntiles;
+        ntiles = min(rq.ntiles - it0, left);
+    }
+    // To the next segment; false at the end of the last run.  All threads of the warp call it, or
+    // (kGroup) all 128 of the softmax warpgroup.
+    template <bool kGroup>
+    __device__ __forceinline__ bool next(const Params& p, const Runs& runs) {
+        sync<kGroup>();
+        if (threadIdx.x % (kGroup ? 128 : 32) == 0) {
+            left -= ntiles;
+            if (left > 0) {
+                it0 = 0;
+                ++in_run;
+                if (++mt == rq.mtiles) {
+                    mt = 0;
+                    do rq = request(p, ++b, false);
+                    while (steps_of(rq) == 0);
+                }
+                ntiles = min(rq.ntiles, left);
+            } else if (++round < kMaxRounds) {
+                start_run(p, runs);  // left = 0 behind the last step of all
+            }
+        }
+        sync<kGroup>();
+        return left > 0;
+    }
+    template <bool kGroup>
+    static __device__ __forceinline__ void sync() {
+        if constexpr (kGroup)
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        else
+            __syncwarp();
+    }
+    __device__ __forceinline__ int tile(int it) const { return rq.tile(it0 + it); }
+    __device__ __forceinline__ bool whole() const { return it0 == 0 && ntiles == rq.ntiles; }
+    // the segment reaches drafted tokens
+    __device__ __forceinline__ bool drafts() const { return (tile(ntiles - 1) + 1) * BN > rq.P; }
+};
+
+template <int D>
+struct __align__(1024) Smem {
+    uint8_t q[Cfg<D>::kTile];
+    uint8_t k[kStages][Cfg<D>::kTile];
+    uint8_t v[kStages][Cfg<D>::kTile];
+    uint64_t q_full, q_empty;  // one phase per segment
+    uint64_t k_full[kStages], k_empty[kStages];
+    uint64_t v_full[kStages], v_empty[kStages];
+    uint64_t s_full, s_free, p_full, o_done;  // one phase per key tile
+    uint64_t final_bar, final_pv;
+    uint64_t v_fix;  // V tiles that need their rows looked at land here first
+    uint32_t tmem_base;
+    int abort;
+    Runs runs;
+    Cursor cursor[5];  // warps 0 .. 3, softmax
+    uint32_t v_bad[kBadRing][kMaxNodes / 32];  // per segment: nodes whose V row holds an infinity or a NaN
+    union {
+        uint8_t parent[kMaxNodes];      // parent + 1
+        long long sums[2][kThreads / 32];  // while the runs are looked for
+    };
+};
 
 // Waits that ignore the abort flag (they drain work in flight before shared
 // memory and TMEM are released); still bounded in time.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     int dummy = 0;
     mbar_wait(bar, parity, &dummy);
+}
+
+// Whether x holds in all 128 threads of the softmax warpgroup (also a barrier of theirs).
+__device__ __forceinline__ bool group_all(bool x) {
+    uint32_t y;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(y)
+        : "r"((uint32_t)x)
+        : "memory");
+    return y != 0;
 }
 
 __device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
@@ -177,27 +282,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Row tiles of one (KV head, split) are neighbours in the grid (they share its
-    // K / V in L2), then the KV heads (which share the cache's token rows).
-    const int mt = blockIdx.x % p.mtiles;
-    const int kvh = blockIdx.x / p.mtiles % p.hkv;
-    const int split = blockIdx.x / p.mtiles / p.hkv;
-    const int b = blockIdx.y;
-
-    const Request rq = request(p, b, threadIdx.x == 0 && blockIdx.x == 0);
-    const int node0 = mt * p.npt;
-    if (node0 >= rq.rows) return;
-    const bool direct = p.splits == 1;
-    const int it0 = split * rq.per_split;
-    const int ntiles = min(rq.per_split, rq.ntiles - it0);  // of this CTA
-    if (ntiles <= 0 && !(direct && split == 0)) return;
-    const int L = rq.L, P = rq.P;
-    // Tile `it` of this CTA's list.
-    auto tile_of = [&](int it) { return it0 + it < rq.ta ? it0 + it : rq.tb + (it0 + it - rq.ta); };
-    const bool drafts = ntiles > 0 && (tile_of(ntiles - 1) + 1) * BN > P;  // the list reaches drafted tokens
-
+    const int kvh = blockIdx.x % p.hkv, gang = blockIdx.x / p.hkv, gangs = gridDim.x / p.hkv;
     if (threadIdx.x == 0) {
         mbar_init(&S.q_full, 1);
+        mbar_init(&S.q_empty, 1);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&S.k_full[s], 1);
             mbar_init(&S.k_empty[s], 1);
@@ -211,19 +299,83 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init(&S.final_bar, 1);
         mbar_init(&S.final_pv, 1);
         mbar_init(&S.v_fix, 1);
-        mbar_init(&S.v_fixed, 1);
         S.abort = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x < kMaxNodes / 32) S.v_bad[threadIdx.x] = 0;
-    for (int i = threadIdx.x; i < min(rq.rows, node0 + p.npt); i += kThreads) {
-        int pr = p.parents[rq.q_start + i];
-        if (pr < -1 || pr >= i) {
-            raise_status(ATTN_SINK_DEV_TREE);
-            pr = -1;
+    if (threadIdx.x < kBadRing * kMaxNodes / 32) S.v_bad[0][threadIdx.x] = 0;
+    // This gang's runs: the batch's steps are counted, then the requests that hold the
+    // runs' first steps are looked for, 256 requests at a time.
+    const int tid = threadIdx.x;
+    // Sums over the CTA of 256 requests' steps (prefix sums) and key tiles.
+    long long steps = 0, inc = 0, sum_steps = 0, sum_keys = 0;
+    auto scan = [&](int i0, bool report) {
+        steps = 0;
+        long long k = 0;
+        if (i0 + tid < p.batch) {
+            const Request rq = request(p, i0 + tid, report);
+            steps = steps_of(rq);
+            if (rq.mtiles > 0) k = rq.ntiles;
         }
-        S.parent[i] = (uint8_t)(pr + 1);
+        inc = steps;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+            k += __shfl_xor_sync(0xffffffffu, k, o);
+        }
+        __syncthreads();  // the previous sums have been read
+        if (lane == 31) {
+            S.sums[0][warp] = inc;
+            S.sums[1][warp] = k;
+        }
+        __syncthreads();
+        sum_steps = sum_keys = 0;
+#pragma unroll
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) inc += S.sums[0][w];
+            sum_steps += S.sums[0][w];
+            sum_keys += S.sums[1][w];
+        }
+    };
+    long long total = 0, keys = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
+        scan(i0, blockIdx.x == 0);
+        total += sum_steps;
+        keys += sum_keys;
     }
+    // Rounds: K / V bytes over kRoundBytes if row tiles share them and runs stay long.
+    int rounds = 1;
+    if (total > keys + keys / 8) {
+        const long long by_bytes = (keys * p.hkv * (2 * BN * D * 2) + kRoundBytes - 1) / kRoundBytes;
+        rounds = (int)max(1ll, min(min((long long)p.max_rounds, by_bytes), total / (kRoundSteps * (long long)gangs)));
+    }
+    const long long runs = (long long)gangs * rounds;
+    const long long per_run = max((long long)kMinSteps, (total + runs - 1) / runs);
+    if (blockIdx.x != 0 && gang * per_run >= total) return;
+    long long before = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
+        if (p.batch > kThreads) scan(i0, false);
+        const long long at = before + inc - steps;
+        for (int k = 0; k < rounds; ++k) {
+            const long long w = ((long long)k * gangs + gang) * per_run;
+            if (steps > 0 && at <= w && w < at + steps) {
+                S.runs.start_b[k] = i0 + tid;
+                S.runs.start_step[k] = (int)(w - at);
+            }
+        }
+        if (blockIdx.x == 0 && i0 + tid < p.batch) p.first[i0 + tid] = at;
+        before += sum_steps;
+    }
+    if (tid == 0) {
+        S.runs.per_run = per_run;
+        S.runs.total = total;
+        S.runs.gang = gang;
+        S.runs.gangs = gangs;
+        if (blockIdx.x == 0) p.first[p.batch] = per_run;
+    }
+    if (total == 0) return;
+    __syncthreads();  // the runs' starts are known to all, and S.sums has been read
+    if (tid < 5) S.cursor[tid].start(p, S.runs);
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -233,10 +385,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int* abort = &S.abort;
+    Cursor& c = S.cursor[warp < 4 ? warp : 4];
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
-        if ((warp == 0 || warp == 2) && ntiles > 0) {
+        if (warp == 0 || warp == 2) {
             // -------------------------------------------------------- producers
             // Converged warps: lane i resolves the physical slot of the tile's i-th
             // page segment and issues its copies.
@@ -246,84 +399,93 @@ __global__ void __launch_bounds__(kThreads, 2)
             uint8_t* dst0 = is_k ? S.k[0] : S.v[0];
             const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
             const int nseg = BN >> p.seg_shift;
-            if (lane == 0) {
-                prefetch_tmap(tm);
-                if (is_k) {
-                    mbar_expect_tx(&S.q_full, (uint32_t)(p.npt * p.group) * (D * 2));
-#pragma unroll
-                    for (int a = 0; a < C::kAtoms; ++a)
-                        tma_load_3d(S.q + a * kAtom, &tm_q, &S.q_full, 64 * a, kvh * p.group, rq.q_start + node0);
-                }
-            }
+            if (lane == 0) prefetch_tmap(tm);
             // Rows of a V tile that no row of the request may see enter P V as
             // zeros, whatever the memory holds (a weight of 0 times a NaN would not
             // vanish): rows past the last token, in the window's gap, or read through
             // a bad page id.  A drafted token's infinities and NaNs are zeroed too,
             // and added by the rows that see that token at the end.  Such tiles land on
             // v_fix and are released to the tensor core once they are clean.
-            const int gap0 = p.win_last > 0 ? p.win_first : 0;
-            const int gap1 = p.win_last > 0 ? min(P, P + 1 - p.win_last) : 0;
-            int fixes = 0;
-            int it = 0;
-            for (; it < ntiles; ++it) {
-                const int st = it % kStages;
-                if (it >= kStages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], ((it / kStages) - 1) & 1, abort)))
-                    break;
-                const int j0 = tile_of(it) * BN;
-                int slot = 0;
-                bool bad = false;
-                const int j = j0 + (lane << p.seg_shift);
-                if (lane < nseg && j < L) {
-                    const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + (j >> p.page_shift));
-                    bad = (unsigned)pg >= (unsigned)p.num_pages;
-                    if (!bad) slot = (pg << p.page_shift) | (j & ((1 << p.page_shift) - 1));
+            int fixes = 0, segs = 0;
+            int n = 0;  // tiles so far
+            bool ok = true;
+            do {
+                const int L = c.rq.L, P = c.rq.P;
+                const int gap0 = p.win_last > 0 ? p.win_first : 0;
+                const int gap1 = p.win_last > 0 ? P + 1 - p.win_last : 0;
+                // this lane's page id of a tile (0 for none), requested a tile ahead
+                auto segment_page = [&](int j0) -> int {
+                    const int j = j0 + (lane << p.seg_shift);
+                    return lane < nseg && j < L ? __ldg(p.page_table + (size_t)c.b * p.max_pages + (j >> p.page_shift))
+                                                : 0;
+                };
+                int next = segment_page(c.tile(0) * BN);
+                for (int it = 0; it < c.ntiles; ++it, ++n) {
+                    const int st = n % kStages;
+                    const int pg = next;
+                    if (it + 1 < c.ntiles) next = segment_page(c.tile(it + 1) * BN);
+                    if (n >= kStages && !__all_sync(0xffffffffu, mbar_wait(&empty[st], ((n / kStages) - 1) & 1, abort))) {
+                        ok = false;
+                        break;
+                    }
+                    const int j0 = c.tile(it) * BN;
+                    const int j = j0 + (lane << p.seg_shift);
+                    const bool bad = (unsigned)pg >= (unsigned)p.num_pages;
                     if (bad && is_k) raise_status(ATTN_SINK_DEV_PAGE_OOB);
-                }
-                const uint32_t bad_segs = __ballot_sync(0xffffffffu, bad);
-                const bool fix = !is_k && (j0 + BN > P || bad_segs || (j0 < gap1 && j0 + BN > gap0));
-                uint64_t* bar = fix ? &S.v_fix : &full[st];
-                if (lane == 0) mbar_expect_tx(bar, kTile);
-                __syncwarp();
-                if (lane < nseg) {
-                    uint8_t* dst = dst0 + st * kTile + ((uint32_t)lane << p.seg_shift) * 128u;
+                    // segments past the last token and bad ones read slot 0
+                    const int slot = bad || j >= L ? 0 : (pg << p.page_shift) | (j & ((1 << p.page_shift) - 1));
+                    const uint32_t bad_segs = __ballot_sync(0xffffffffu, bad);
+                    const bool fix = !is_k && (j0 + BN > P || bad_segs || (j0 < gap1 && j0 + BN > gap0));
+                    uint64_t* bar = fix ? &S.v_fix : &full[st];
+                    if (lane == 0) mbar_expect_tx(bar, kTile);
+                    __syncwarp();
+                    if (lane < nseg) {
+                        uint8_t* dst = dst0 + st * kTile + ((uint32_t)lane << p.seg_shift) * 128u;
 #pragma unroll
-                    for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(dst + a * kAtom, tm, bar, 64 * a, kvh, slot);
-                }
-                if (fix) {
-                    const uint32_t parity = fixes++ & 1;
-                    if (!__all_sync(0xffffffffu, mbar_wait(&S.v_fix, parity, abort))) break;
-                    // Key row r of an atom is the 128 bytes at r * 128 (the swizzle
-                    // permutes 16-byte chunks within a row).
-                    for (int e = lane; e < (int)(kTile / 16); e += 32) {
-                        const int r = (e >> 3) & (BN - 1), t = j0 + r;
-                        uint4* cell = reinterpret_cast<uint4*>(dst0 + st * kTile) + e;
-                        if (t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u)) {
-                            *cell = make_uint4(0u, 0u, 0u, 0u);
-                        } else if (t >= P) {
-                            const uint4 x = *cell;
-                            if (nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) || nonfinite_pair(x.w)) {
-                                *cell = make_uint4(finite_pair(x.x), finite_pair(x.y), finite_pair(x.z), finite_pair(x.w));
-                                if (t - P < kMaxNodes) atomicOr(&S.v_bad[(t - P) >> 5], 1u << ((t - P) & 31));
+                        for (int a = 0; a < C::kAtoms; ++a) tma_load_3d(dst + a * kAtom, tm, bar, 64 * a, kvh, slot);
+                    }
+                    if (fix) {
+                        const uint32_t parity = fixes++ & 1;
+                        if (!__all_sync(0xffffffffu, mbar_wait(&S.v_fix, parity, abort))) {
+                            ok = false;
+                            break;
+                        }
+                        // Key row r of an atom is the 128 bytes at r * 128 (the swizzle
+                        // permutes 16-byte chunks within a row).
+                        for (int e = lane; e < (int)(kTile / 16); e += 32) {
+                            const int r = (e >> 3) & (BN - 1), t = j0 + r;
+                            uint4* cell = reinterpret_cast<uint4*>(dst0 + st * kTile) + e;
+                            if (t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u)) {
+                                *cell = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (t >= P) {
+                                const uint4 x = *cell;
+                                if (nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) ||
+                                    nonfinite_pair(x.w)) {
+                                    *cell = make_uint4(finite_pair(x.x), finite_pair(x.y), finite_pair(x.z),
+                                                       finite_pair(x.w));
+                                    if (t - P < kMaxNodes)
+                                        atomicOr(&S.v_bad[segs % kBadRing][(t - P) >> 5], 1u << ((t - P) & 31));
+                                }
                             }
                         }
+                        __threadfence_block();
+                        fence_proxy_async_smem();  // the tensor core reads through the async proxy
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&full[st]);
                     }
-                    fence_proxy_async_smem();  // the tensor core reads through the async proxy
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&full[st]);
                 }
-            }
+                ++segs;
+            } while (ok && c.next<false>(p, S.runs));
+            // Drain: every copy issued must have landed before the CTA exits.
             if (lane == 0) {
-                if (!is_k) mbar_arrive(&S.v_fixed);
-                // Drain: every copy issued must have landed before the CTA exits.
-                if (is_k) drain_wait(&S.q_full, 0);
                 if (fixes > 0) drain_wait(&S.v_fix, (fixes - 1) & 1);
                 for (int st = 0; st < kStages; ++st) {
-                    const int n = it > st ? (it - st + kStages - 1) / kStages : 0;
-                    if (n > 0) drain_wait(&full[st], (n - 1) & 1);
+                    const int m = n > st ? (n - st + kStages - 1) / kStages : 0;
+                    if (m > 0) drain_wait(&full[st], (m - 1) & 1);
                 }
             }
             __syncwarp();
-        } else if ((warp == 1 || warp == 3) && ntiles > 0) {
+        } else {
             // -------------------------------------------------------- MMA issuers
             constexpr uint32_t idS = idesc_bf16_f32(BM, BN, false, false);
             constexpr uint32_t idO = idesc_bf16_f32(BM, D, false, true);
@@ -334,35 +496,57 @@ __global__ void __launch_bounds__(kThreads, 2)
                 return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
             };
             bool ok = true;
+            int n = 0, segs = 0;  // tiles, segments so far
             if (warp == 1) {
-                ok = wait_all(&S.q_full, 0);
-                for (int it = 0; ok && it < ntiles; ++it) {
-                    if (!(ok = wait_all(&S.k_full[it % kStages], (it / kStages) & 1))) break;
-                    if (it > 0 && !(ok = wait_all(&S.s_free, (it - 1) & 1))) break;
-                    tc_fence_after();
-                    const uint64_t dk = dk0 + (it % kStages) * (kTile >> 4);
+                // Q is loaded by this warp, as soon as the previous segment's last S has
+                // read its predecessor: K is on its way by then.
+                if (lane == 0) prefetch_tmap(&tm_q);
+                do {
+                    if (segs > 0 && !(ok = wait_all(&S.q_empty, (segs - 1) & 1))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(&S.q_full, (uint32_t)(p.npt * p.group) * (D * 2));
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t o = (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2;
-                        umma_ss_e(tmem + cS, dq + o, dk + o, idS, kk > 0);
+                        for (int a = 0; a < C::kAtoms; ++a)
+                            tma_load_3d(S.q + a * kAtom, &tm_q, &S.q_full, 64 * a, kvh * p.group,
+                                        c.rq.q_start + c.mt * p.npt);
                     }
-                    umma_commit_e(&S.s_full);
-                    umma_commit_e(&S.k_empty[it % kStages]);
-                }
+                    __syncwarp();
+                    if (!(ok = wait_all(&S.q_full, segs & 1))) {
+                        if (lane == 0) drain_wait(&S.q_full, segs & 1);  // the copy lands before the CTA exits
+                        break;
+                    }
+                    for (int it = 0; it < c.ntiles; ++it, ++n) {
+                        if (!(ok = wait_all(&S.k_full[n % kStages], (n / kStages) & 1))) break;
+                        if (n > 0 && !(ok = wait_all(&S.s_free, (n - 1) & 1))) break;
+                        tc_fence_after();
+                        const uint64_t dk = dk0 + (n % kStages) * (kTile >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t o = (kk >> 2) * (kAtom >> 4) + (kk & 3) * 2;
+                            umma_ss_e(tmem + cS, dq + o, dk + o, idS, kk > 0);
+                        }
+                        umma_commit_e(&S.s_full);
+                        umma_commit_e(&S.k_empty[n % kStages]);
+                    }
+                    if (ok) umma_commit_e(&S.q_empty);
+                    ++segs;
+                } while (ok && c.next<false>(p, S.runs));
                 umma_commit_e(&S.final_bar);
                 drain_wait(&S.final_bar, 0);
             } else {
-                for (int it = 0; ok && it < ntiles; ++it) {
-                    if (!(ok = wait_all(&S.v_full[it % kStages], (it / kStages) & 1))) break;
-                    if (!(ok = wait_all(&S.p_full, it & 1))) break;
-                    tc_fence_after();
-                    const uint64_t dv = dv0 + (it % kStages) * (kTile >> 4);
+                do {
+                    for (int it = 0; it < c.ntiles; ++it, ++n) {
+                        if (!(ok = wait_all(&S.v_full[n % kStages], (n / kStages) & 1))) break;
+                        if (!(ok = wait_all(&S.p_full, n & 1))) break;
+                        tc_fence_after();
+                        const uint64_t dv = dv0 + (n % kStages) * (kTile >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < BN / 16; ++kk)
-                        umma_ts_e(tmem + cO, tmem + cP + kk * 8, dv + 128 * kk, idO, (it > 0 || kk > 0) ? 1u : 0u);
-                    umma_commit_e(&S.o_done);
-                    umma_commit_e(&S.v_empty[it % kStages]);
-                }
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            umma_ts_e(tmem + cO, tmem + cP + kk * 8, dv + 128 * kk, idO, (it > 0 || kk > 0) ? 1u : 0u);
+                        umma_commit_e(&S.o_done);
+                        umma_commit_e(&S.v_empty[n % kStages]);
+                    }
+                } while (ok && c.next<false>(p, S.runs));
                 umma_commit_e(&S.final_pv);
                 drain_wait(&S.final_pv, 0);
             }
@@ -376,33 +560,50 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t tS = tmem + lane_base + cS;
         const uint32_t tO = tmem + lane_base + cO;
         const uint32_t tP = tmem + lane_base + cP;
-        const int node = node0 + r / p.group, g = r % p.group;
-        const bool valid = r < p.npt * p.group && node < rq.rows;
+        const int row_node = r / p.group, g = r % p.group;
+        const float sl2 = p.scale_log2;
+        const int nseg = BN >> p.seg_shift;
+        // Page id of this lane's segment of a tile (0 for none), requested a tile ahead:
+        // keys that are read through a bad one are masked.
+        auto segment_page = [&](int j0) -> int {
+            const int j = j0 + (lane << p.seg_shift);
+            return lane < nseg && j < c.rq.L ? __ldg(p.page_table + (size_t)c.b * p.max_pages + (j >> p.page_shift)) : 0;
+        };
+        bool ok = true;
+        int n = 0, segs = 0;  // tiles, segments so far
+        do {
+        const int P = c.rq.P, ntiles = c.ntiles;
+        const int node = c.mt * p.npt + row_node;
+        const bool valid = r < p.npt * p.group && node < c.rq.rows;
         const bool work = __any_sync(0xffffffffu, valid);  // else only the barriers' arrivals
         const int h = kvh * p.group + g;
+        const bool drafts = c.drafts();
+        int page = segment_page(c.tile(0) * BN);
+        if (drafts || p.win_last > 0) {
+            // the parents that this row tile's walks can meet
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the previous segment's have been read
+            for (int i = r; i < min(c.rq.rows, (c.mt + 1) * p.npt); i += 128) {
+                int pr = p.parents[c.rq.q_start + i];
+                if (pr < -1 || pr >= i) {
+                    raise_status(ATTN_SINK_DEV_TREE);
+                    pr = -1;
+                }
+                S.parent[i] = (uint8_t)(pr + 1);
+            }
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
         const float sg = p.sink && valid ? p.sink[h] * ATTN_LOG2E : -INFINITY;
-        const float sl2 = p.scale_log2;
         float m_ref = sg == INFINITY ? -INFINITY : sg;
         float l = 0.f;
         int pos = P;  // this row's position
         if (p.win_last > 0 && valid)
             for (int a = S.parent[node]; a > 0; a = S.parent[a - 1]) ++pos;
-        const int pos_max = P + max(rq.n, 1) - 1;  // of any node
-        const int nseg = BN >> p.seg_shift;
-        // Whether this lane's page segment of a tile is read through a bad page id.
-        auto segment_bad = [&](int j0) -> bool {
-            const int j = j0 + (lane << p.seg_shift);
-            if (lane >= nseg || j >= L) return false;
-            const int pg = __ldg(p.page_table + (size_t)b * p.max_pages + (j >> p.page_shift));
-            return (unsigned)pg >= (unsigned)p.num_pages;
-        };
-        bool next_bad = ntiles > 0 && segment_bad(tile_of(0) * BN);
-        bool ok = true;
-        for (int it = 0; it < ntiles; ++it) {
-            const int j0 = tile_of(it) * BN;
-            const uint32_t bad_segs = __ballot_sync(0xffffffffu, next_bad);
-            if (it + 1 < ntiles) next_bad = segment_bad(tile_of(it + 1) * BN);
-            ok = mbar_wait(&S.s_full, it & 1, abort);
+        const int pos_max = P + max(c.rq.n, 1) - 1;  // of any node
+        for (int it = 0; it < ntiles; ++it, ++n) {
+            const int j0 = c.tile(it) * BN;
+            const uint32_t bad_segs = __ballot_sync(0xffffffffu, (unsigned)page >= (unsigned)p.num_pages);
+            if (it + 1 < ntiles) page = segment_page(c.tile(it + 1) * BN);
+            ok = mbar_wait(&S.s_full, n & 1, abort);
             if (!__all_sync(0xffffffffu, ok)) {
                 ok = false;
                 break;
@@ -411,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // The previous P V must be complete before P is overwritten or O rescaled.
             auto wait_prev_pv = [&]() -> bool {
                 if (it == 0) return true;
-                const bool done = __all_sync(0xffffffffu, mbar_wait(&S.o_done, (it - 1) & 1, abort));
+                const bool done = __all_sync(0xffffffffu, mbar_wait(&S.o_done, (n - 1) & 1, abort));
                 if (done) tc_fence_after();
                 return done;
             };
@@ -585,12 +786,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 
         // -------------------------------------------------------------- epilogue
-        if (ok && ntiles > 0) ok = mbar_wait(&S.o_done, (ntiles - 1) & 1, abort);
-        if (ok && drafts) ok = mbar_wait(&S.v_fixed, 0, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        const bool have = ok && ntiles > 0;
-        if (have) tc_fence_after();
-        const bool store = valid && ok;
+        // The four warps go on or give up together (a warp that gave up alone would
+        // leave the others waiting at the next group barrier).
+        if (ok) ok = mbar_wait(&S.o_done, (n - 1) & 1, abort);
+        ok = group_all(ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool direct = c.whole();
         // Direct output: the sink joins the sum, and the row is normalised.
         float f = 1.f, lse_v = 0.f;
         if (direct) {
@@ -606,32 +808,29 @@ __global__ void __launch_bounds__(kThreads, 2)
                 lse_v = (M + log2f(Z)) * ATTN_LN2;
             }
         }
-        const int row = rq.q_start + node;
-        const size_t unit = ((size_t)b * p.hkv + kvh) * p.mtiles + mt;
-        const size_t part = (unit * p.splits + split) * BM + r;
+        const int row = c.rq.q_start + node;
+        // a run's first segment has the first place, any other the second
+        const size_t part = ((((size_t)c.round * gangs + gang) * p.hkv + kvh) * 2 + (c.in_run > 0)) * BM + r;
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)row * p.hq + h) * D);
         float4* pdst = reinterpret_cast<float4*>(p.part_o + part * D);
+        uint32_t* const v_bad = S.v_bad[segs % kBadRing];
+        const bool any_bad = drafts && __any_sync(0xffffffffu, lane < kMaxNodes / 32 && v_bad[lane] != 0);
 #pragma unroll 1
         for (int ch = 0; ch < D / 32; ++ch) {
             float u[32];
-            if (have) {  // warp-uniform: every lane takes part in the collective load
-                uint32_t raw[32];
-                tmem_ld32(tO + ch * 32, raw);
-                tmem_ld_wait();
+            uint32_t raw[32];
+            tmem_ld32(tO + ch * 32, raw);
+            tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = l != 0.f ? __uint_as_float(raw[i]) : 0.f;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = 0.f;
-            }
-            if (store && drafts) {
+            for (int i = 0; i < 32; ++i) u[i] = l != 0.f ? __uint_as_float(raw[i]) : 0.f;
+            if (valid && any_bad) {
                 // Infinities and NaNs of drafted tokens' V that this row sees.
                 int at = pos;
                 for (int a = node + 1; a > 0; a = S.parent[a - 1], --at) {
                     const int t = P + a - 1;
-                    if (!(S.v_bad[(a - 1) >> 5] >> ((a - 1) & 31) & 1u)) continue;
+                    if (!(v_bad[(a - 1) >> 5] >> ((a - 1) & 31) & 1u)) continue;
                     if (p.win_last > 0 && at >= p.win_first && at <= pos - p.win_last) continue;
-                    const int pg = p.page_table[(size_t)b * p.max_pages + (t >> p.page_shift)];
+                    const int pg = p.page_table[(size_t)c.b * p.max_pages + (t >> p.page_shift)];
                     const size_t sl = ((size_t)pg << p.page_shift) | (t & ((1 << p.page_shift) - 1));
                     const __nv_bfloat16* v = p.v_cache + (sl * p.hkv + kvh) * D + ch * 32;
 #pragma unroll
@@ -641,24 +840,31 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
             }
-            if (store && direct) {
+            if (valid && direct) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int q = 0; q < 4; ++q) {
                     uint4 wv;
-                    wv.x = pack_bf16x2(u[8 * c + 0] * f, u[8 * c + 1] * f);
-                    wv.y = pack_bf16x2(u[8 * c + 2] * f, u[8 * c + 3] * f);
-                    wv.z = pack_bf16x2(u[8 * c + 4] * f, u[8 * c + 5] * f);
-                    wv.w = pack_bf16x2(u[8 * c + 6] * f, u[8 * c + 7] * f);
-                    dst[ch * 4 + c] = wv;
+                    wv.x = pack_bf16x2(u[8 * q + 0] * f, u[8 * q + 1] * f);
+                    wv.y = pack_bf16x2(u[8 * q + 2] * f, u[8 * q + 3] * f);
+                    wv.z = pack_bf16x2(u[8 * q + 4] * f, u[8 * q + 5] * f);
+                    wv.w = pack_bf16x2(u[8 * q + 6] * f, u[8 * q + 7] * f);
+                    dst[ch * 4 + q] = wv;
                 }
-            } else if (store) {
+            } else if (valid) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c)
-                    pdst[ch * 8 + c] = make_float4(u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+                for (int q = 0; q < 8; ++q)
+                    pdst[ch * 8 + q] = make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
             }
         }
-        if (store && direct && p.lse) p.lse[(size_t)h * p.total_q + row] = lse_v;
-        if (store && !direct) p.part_ml[part] = make_float2(l != 0.f ? m_ref : -INFINITY, l);
+        if (valid && direct && p.lse) p.lse[(size_t)h * p.total_q + row] = lse_v;
+        if (valid && !direct) p.part_ml[part] = make_float2(l != 0.f ? m_ref : -INFINITY, l);
+        if (any_bad) {  // the place is free for a later segment
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (r < kMaxNodes / 32) v_bad[r] = 0;
+        }
+        tc_fence_before();  // O has been read: the next segment's P V may overwrite it
+        ++segs;
+        } while (c.next<true>(p, S.runs));
     }
 
     tc_fence_before();
@@ -669,47 +875,70 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 }
 
-// Merges the splits of a row in log-sum-exp form and adds the sink once.  One warp
-// per (node, query head); lane = D / 32 dimensions.
+// Merges the segments of a row in log-sum-exp form and adds the sink once.  One warp
+// per node and 8 query heads of a KV head, whose partial rows are neighbours; lane = D
+// / 32 dimensions.
 constexpr int kCombineWarps = 8;
+constexpr int kCombineRows = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const Params p) {
     constexpr int V = D / 32;
+    using Vec = typename std::conditional<V == 2, float2, float4>::type;
     const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int idx = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);  // (node, query head)
-    const int node = idx / p.hq, h = idx - node * p.hq;
+    const int blocks = (p.group + kCombineRows - 1) / kCombineRows;  // of a KV head's query heads
+    const int idx = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+    const int node = idx / (p.hkv * blocks), kvh = idx / blocks % p.hkv, g0 = idx % blocks * kCombineRows;
     const Request rq = request(p, b, false);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
     if (node >= rq.rows) return;
-    const int kvh = h / p.group, mt = node / p.npt;
-    const int r = (node - mt * p.npt) * p.group + (h - kvh * p.group);
-    const size_t unit = ((size_t)b * p.hkv + kvh) * p.mtiles + mt;
-    const float sg = p.sink ? p.sink[h] * ATTN_LOG2E : -INFINITY;
-    const float2* ml = p.part_ml + unit * p.splits * BM + r;
-    const float* po = p.part_o + (unit * p.splits * BM + r) * D + lane * V;
+    const int heads = min(kCombineRows, p.group - g0), h0 = kvh * p.group + g0;
+    const int mt = node / p.npt, r0 = (node - mt * p.npt) * p.group + g0;
+    // The row tile's steps [u0, u1) lie in the runs c0 .. c1.
+    const long long per_run = p.first[p.batch];
+    const long long u0 = p.first[b] + (long long)mt * rq.ntiles, u1 = u0 + rq.ntiles;
+    const int c0 = (int)(u0 / per_run), c1 = rq.ntiles > 0 ? (int)((u1 - 1) / per_run) : c0 - 1;
+    if (c0 == c1) return;  // one run had all of it and wrote the output
+    // A run's first segment has the first place, any other the second.
+    auto place = [&](int c) { return (((size_t)c * p.hkv + kvh) * 2 + (c == c0 && u0 > c * per_run)) * BM + r0; };
+    // Lane k of the first 8 keeps the statistics of row k.
+    const bool has = lane < heads;
+    const float sg = has && p.sink ? p.sink[h0 + lane] * ATTN_LOG2E : -INFINITY;
     float M = sg;
-    for (int s = 0; s < rq.nsplit; ++s) M = fmaxf(M, ml[(size_t)s * BM].x);
-    float o[V] = {}, lse_v = M;
-    if (M != INFINITY && M != -INFINITY) {
-        float Z = fast_exp2(sg - M);
-#pragma unroll 4
-        for (int s = 0; s < rq.nsplit; ++s) {
-            const float2 x = ml[(size_t)s * BM];
-            if (x.y == 0.f) continue;  // nothing seen in this split
-            const float f = fast_exp2(x.x - M);
-            Z += x.y * f;
+    for (int c = c0; c <= c1; ++c)
+        if (has) M = fmaxf(M, p.part_ml[place(c) + lane].x);
+    const bool some = M != INFINITY && M != -INFINITY;
+    float Z = some ? fast_exp2(sg - M) : 1.f;
+    float o[kCombineRows][V] = {};
+    for (int c = c0; c <= c1; ++c) {
+        const size_t at = place(c);
+        const float2 x = has ? p.part_ml[at + lane] : make_float2(0.f, 0.f);
+        const float w = some && x.y != 0.f ? fast_exp2(x.x - M) : 0.f;  // 0: nothing seen in this segment
+        if (w != 0.f) Z += x.y * w;
+        Vec u[kCombineRows];
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += po[(size_t)s * BM * D + v] * f;
+        for (int k = 0; k < kCombineRows; ++k)
+            if (k < heads) u[k] = reinterpret_cast<const Vec*>(p.part_o + (at + k) * D)[lane];
+#pragma unroll
+        for (int k = 0; k < kCombineRows; ++k) {
+            const float f = __shfl_sync(0xffffffffu, w, k);
+            if (k >= heads || f == 0.f) continue;
+            const float* v = reinterpret_cast<const float*>(&u[k]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[k][i] += v[i] * f;
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] /= Z;
-        lse_v = (M + log2f(Z)) * ATTN_LN2;
     }
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)(rq.q_start + node) * p.hq + h) * D + lane * V);
+    const float inv = some ? 1.f / Z : 0.f;
+    const size_t row = (size_t)rq.q_start + node;
 #pragma unroll
-    for (int v = 0; v < V; v += 2) dst[v / 2] = pack_bf16x2(o[v], o[v + 1]);
-    if (p.lse && lane == 0) p.lse[(size_t)h * p.total_q + rq.q_start + node] = lse_v;
+    for (int k = 0; k < kCombineRows; ++k) {
+        const float f = __shfl_sync(0xffffffffu, inv, k);
+        if (k >= heads) continue;
+        uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.hq + h0 + k) * D + lane * V);
+#pragma unroll
+        for (int i = 0; i < V; i += 2) dst[i / 2] = f == 0.f ? 0u : pack_bf16x2(o[k][i] * f, o[k][i + 1] * f);
+    }
+    if (has && p.lse) p.lse[(size_t)(h0 + lane) * p.total_q + row] = some ? (M + log2f(Z)) * ATTN_LN2 : M;
 }
 
 // ---------------------------------------------------------------------------
@@ -753,32 +982,22 @@ static cudaError_t make_map(CUtensorMap* m, const void* base, int D, int heads, 
 
 Plan make_plan(const Args& a) {
     Plan pl;
-    const int group = a.hq / a.hkv;
-    pl.npt = BM / group;
-    pl.mtiles = (a.max_seqlen_q + pl.npt - 1) / pl.npt;
-    // Splits: key tiles per CTA so that one wave covers the work if that is at most
-    // 8 tiles each, and otherwise about six waves of at least 8 tiles, so that
-    // requests of unequal lengths even out.
-    const long long slots = 152LL * (a.head_dim == 64 ? 2 : 1);
-    const long long units = (long long)a.batch * a.hkv * pl.mtiles;
-    long long keys = a.max_seqlen_k > 0 ? a.max_seqlen_k : 1;
-    if (a.win_last > 0 && keys > (long long)a.win_first + a.win_last + a.max_seqlen_q)
-        keys = (long long)a.win_first + a.win_last + a.max_seqlen_q;
-    const long long tiles = (keys + BN - 1) / BN;
-    const long long one_wave = (tiles * units + slots - 1) / slots;
-    const long long six_waves = (tiles * units + 6 * slots - 1) / (6 * slots);
-    long long per = one_wave <= 8 ? one_wave : six_waves < 8 ? 8 : six_waves;
-    if (per > tiles) per = tiles;
-    pl.split_tiles = (int)per;
-    pl.splits = (int)((tiles + per - 1) / per);
-    pl.part_o_bytes = pl.splits > 1 ? (size_t)units * pl.splits * BM * a.head_dim * sizeof(float) : 0;
-    pl.part_ml_bytes = pl.splits > 1 ? (size_t)units * pl.splits * BM * sizeof(float2) : 0;
+    const int slots = 152 * (a.head_dim == 64 ? 2 : 1);
+    pl.ctas = slots >= a.hkv ? slots / a.hkv * a.hkv : a.hkv;
+    // The kernel knows the true lengths; here they bound the scratch.
+    const int npt = BM / (a.hq / a.hkv);
+    const double bytes = (double)a.batch * a.hkv * a.max_seqlen_k * a.head_dim * 4;
+    const double rounds = a.max_seqlen_q <= npt ? 1. : bytes / (double)kRoundBytes + 1.;
+    pl.rounds = rounds < kMaxRounds ? (int)rounds : kMaxRounds;
+    const size_t runs = (size_t)pl.ctas * pl.rounds;
+    pl.part_o_bytes = runs * 2 * BM * a.head_dim * sizeof(float);
+    pl.part_ml_bytes = runs * 2 * BM * sizeof(float2);
+    pl.first_bytes = ((size_t)a.batch + 1) * sizeof(long long);
     return pl;
 }
 
 template <int D>
-static cudaError_t launch_d(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s,
-                            std::string* what) {
+static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaStream_t s, std::string* what) {
     static_assert(sizeof(Smem<64>) <= 113 * 1024, "two CTAs per SM at head dim 64");
     static_assert(sizeof(Smem<128>) + 1024 <= 227 * 1024, "shared memory at head dim 128");
     Params p;
@@ -790,8 +1009,11 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, float* part_o, float2
     p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
     p.out = static_cast<__nv_bfloat16*>(a.out);
     p.lse = a.lse;
-    p.part_o = part_o;
-    p.part_ml = part_ml;
+    p.part_o = static_cast<float*>(scratch);
+    p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + pl.part_o_bytes);
+    p.first = reinterpret_cast<long long*>(static_cast<char*>(scratch) + pl.part_o_bytes + pl.part_ml_bytes);
+    p.max_rounds = pl.rounds;
+    p.batch = a.batch;
     p.max_pages = a.max_pages;
     p.page_shift = 0;
     while ((1 << p.page_shift) < a.page_size) ++p.page_shift;
@@ -802,17 +1024,14 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, float* part_o, float2
     p.group = a.hq / a.hkv;
     p.total_q = a.total_q;
     p.max_q = a.max_seqlen_q;
-    p.npt = pl.npt;
-    p.mtiles = pl.mtiles;
-    p.split_tiles = pl.split_tiles;
-    p.splits = pl.splits;
+    p.npt = BM / p.group;
     p.win_first = a.win_first;
     p.win_last = a.win_last;
     p.scale_log2 = a.scale * ATTN_LOG2E;
     CUtensorMap tq, tk, tv;
     cudaError_t e;
     const long long slots = (long long)a.num_pages * a.page_size;
-    if ((e = make_map(&tq, a.q, D, a.hq, a.total_q, p.group, pl.npt, what)) != cudaSuccess) return e;
+    if ((e = make_map(&tq, a.q, D, a.hq, a.total_q, p.group, p.npt, what)) != cudaSuccess) return e;
     if ((e = make_map(&tk, a.k_cache, D, a.hkv, slots, 1, 1 << p.seg_shift, what)) != cudaSuccess) return e;
     if ((e = make_map(&tv, a.v_cache, D, a.hkv, slots, 1, 1 << p.seg_shift, what)) != cudaSuccess) return e;
     const size_t smem = sizeof(Smem<D>) + (Cfg<D>::kTwoPerSm ? 0 : 1024);
@@ -821,15 +1040,14 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, float* part_o, float2
         *what = "smem attribute";
         return e;
     }
-    const dim3 grid((unsigned)((long long)pl.splits * a.hkv * pl.mtiles), a.batch);
-    tree_kernel<D><<<grid, kThreads, smem, s>>>(tq, tk, tv, p);
+    tree_kernel<D><<<pl.ctas, kThreads, smem, s>>>(tq, tk, tv, p);
     if ((e = cudaGetLastError()) != cudaSuccess) {
         *what = "launch";
         return e;
     }
-    if (pl.splits == 1) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)a.max_seqlen_q * a.hq + kCombineWarps - 1) / kCombineWarps), a.batch);
+    const long long warps = (long long)a.max_seqlen_q * a.hkv * ((p.group + kCombineRows - 1) / kCombineRows);
+    cfg.gridDim = dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps), a.batch);
     cfg.blockDim = dim3(kCombineWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -842,9 +1060,8 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, float* part_o, float2
     return e;
 }
 
-cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s, std::string* what) {
-    return a.head_dim == 64 ? launch_d<64>(a, pl, part_o, part_ml, s, what)
-                            : launch_d<128>(a, pl, part_o, part_ml, s, what);
+cudaError_t launch(const Args& a, const Plan& pl, void* scratch, cudaStream_t s, std::string* what) {
+    return a.head_dim == 64 ? launch_d<64>(a, pl, scratch, s, what) : launch_d<128>(a, pl, scratch, s, what);
 }
 
 ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)

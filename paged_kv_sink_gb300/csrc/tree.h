@@ -29,16 +29,15 @@ struct Args {
     float scale;
 };
 
-// Row tiles, splits of the keys and scratch sizes.
+// Grid and scratch sizes.
 struct Plan {
-    int npt, mtiles;  // nodes per 128-row tile, row tiles of the largest request
-    int split_tiles;  // 128-key tiles per split
-    int splits;       // 1: no scratch, no combine
-    size_t part_o_bytes, part_ml_bytes;
+    int ctas;    // persistent CTAs
+    int rounds;  // runs of steps per gang of hkv CTAs, at most
+    size_t part_o_bytes, part_ml_bytes, first_bytes;
 };
 
 Plan make_plan(const Args& a);
-cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml, cudaStream_t s, std::string* what);
+cudaError_t launch(const Args& a, const Plan& pl, void* scratch, cudaStream_t s, std::string* what);
 int status_exchange(cudaStream_t s, int* host_bits);
 
 }  // namespace tree
