@@ -36,15 +36,9 @@
 // un-normalised fp32 partials (two places per run and KV head), which
 // tree_combine_kernel merges.
 //
-// Row tiles of one request read the same keys, but far apart in time when each gang
-// has one run: L2 must hold all K / V for them to be read once.  Where it does not, the
-// steps are handed out in rounds: run i goes to gang i mod gangs, runs are shorter, and
-// the gangs work on 64 MB of K / V at a time.
-//
 // Masks: prefix tiles that every row sees whole are not masked at all.  In the
 // others each thread builds the 128-bit visibility of its row: ranges for the
-// prefix, and its ancestors' bits by walking up the parents (bytes in shared
-// memory), once per tile.
+// prefix, and its ancestors' bits by walking up the parents, once per tile.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -61,10 +55,9 @@ using namespace sm103;
 constexpr int BM = 128, BN = 128;
 constexpr int kStages = 3;  // K and V rings
 constexpr int kBadRing = 4;  // segments that the V producer may be ahead, + 1
-constexpr int kMinSteps = 2;   // of a run
-constexpr int kRoundSteps = 8;  // of a run where a gang has several
-constexpr int kMaxRounds = 8;
-constexpr long long kRoundBytes = 64ll << 20;
+constexpr int kSegRing = 6;  // segments that the K producer may be ahead of the softmax, + 1
+constexpr int kTileRing = 8;  // tiles that the K producer may be ahead of the softmax, + 1, and more
+constexpr int kMinSteps = 2;  // of a run
 constexpr int kThreads = 256;
 // 128 registers per thread at launch, moved from the control warps to the softmax
 // warps: 128 * 40 + 128 * 216 = 256 * 128.
@@ -96,7 +89,6 @@ struct Params {
     float* part_o;       // (runs, hkv, 2, 128, D) fp32, un-normalised
     float2* part_ml;     // (runs, hkv, 2, 128): (reference in log2 units, sum)
     long long* first;    // (batch + 1): steps before each request; then the steps per run
-    int max_rounds;      // runs per gang that the scratch has room for
     int batch, max_pages, page_shift, seg_shift, num_pages;
     int hq, hkv, group, total_q, max_q;
     int npt;  // nodes per row tile
@@ -140,71 +132,49 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
 
 __device__ __forceinline__ long long steps_of(const Request& r) { return (long long)r.mtiles * r.ntiles; }
 
-// The runs of steps of a gang: their first requests and steps in those.
-struct Runs {
-    long long per_run, total;
-    int gang, gangs;
-    int start_b[kMaxRounds], start_step[kMaxRounds];
+// The key tiles [it0, it0 + ntiles) of one row tile: what a CTA works on at a time.
+struct Segment {
+    Request rq;
+    int b, mt, it0, ntiles;  // request, row tile
+    __device__ __forceinline__ int tile(int it) const { return rq.tile(it0 + it); }
+    __device__ __forceinline__ bool whole() const { return it0 == 0 && ntiles == rq.ntiles; }
+    // it reaches drafted tokens
+    __device__ __forceinline__ bool drafts() const { return (tile(ntiles - 1) + 1) * BN > rq.P; }
 };
 
-// A CTA's run of steps, segment by segment.  Each control warp and the softmax
-// warpgroup walk a cursor of their own, kept in shared memory: it is read a few times
-// per tile, and the control warps have 40 registers.
-struct Cursor {
-    Request rq;
-    int b, mt, it0, ntiles;  // request, row tile, first key tile and key tiles of the segment
-    int round, in_run;       // run of this gang; segments of the run before this one
-    int left;                // steps of the run from this segment on
+// A gang's run of steps, segment by segment.  Warps 0 to 2 walk a cursor of their own,
+// kept in shared memory (it is read a few times per tile, and the warps have 40
+// registers); warp 0 hands its segments on to warp 3 and the softmax, which find them
+// there when its first tile arrives.
+struct Cursor : Segment {
+    int left;  // steps of the run from this segment on
 
-    __device__ __forceinline__ void start(const Params& p, const Runs& runs) {
-        round = 0;
-        start_run(p, runs);
-    }
-    __device__ __forceinline__ void start_run(const Params& p, const Runs& runs) {
-        const long long first = ((long long)round * runs.gangs + runs.gang) * runs.per_run;
-        left = (int)max(0ll, min(runs.per_run, runs.total - first));
-        in_run = 0;
-        if (left == 0) return;
-        b = runs.start_b[round];
+    __device__ __forceinline__ void start(const Params& p, int b0, int step, int steps) {
+        b = b0;
+        left = steps;
         rq = request(p, b, false);
-        mt = runs.start_step[round] / rq.ntiles;
-        it0 = runs.start_step[round] - mt * rq.ntiles;
+        mt = step / rq.ntiles;
+        it0 = step - mt * rq.ntiles;
         ntiles = min(rq.ntiles - it0, left);
     }
-    // To the next segment; false at the end of the last run.  All threads of the warp call it, or
-    // (kGroup) all 128 of the softmax warpgroup.
-    template <bool kGroup>
-    __device__ __forceinline__ bool next(const Params& p, const Runs& runs) {
-        sync<kGroup>();
-        if (threadIdx.x % (kGroup ? 128 : 32) == 0) {
+    // To the next segment; false at the run's end.  A converged warp calls it.
+    __device__ __forceinline__ bool next(const Params& p) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
             left -= ntiles;
             if (left > 0) {
                 it0 = 0;
-                ++in_run;
                 if (++mt == rq.mtiles) {
                     mt = 0;
                     do rq = request(p, ++b, false);
                     while (steps_of(rq) == 0);
                 }
                 ntiles = min(rq.ntiles, left);
-            } else if (++round < kMaxRounds) {
-                start_run(p, runs);  // left = 0 behind the last step of all
             }
         }
-        sync<kGroup>();
+        __syncwarp();
         return left > 0;
     }
-    template <bool kGroup>
-    static __device__ __forceinline__ void sync() {
-        if constexpr (kGroup)
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-        else
-            __syncwarp();
-    }
-    __device__ __forceinline__ int tile(int it) const { return rq.tile(it0 + it); }
-    __device__ __forceinline__ bool whole() const { return it0 == 0 && ntiles == rq.ntiles; }
-    // the segment reaches drafted tokens
-    __device__ __forceinline__ bool drafts() const { return (tile(ntiles - 1) + 1) * BN > rq.P; }
 };
 
 template <int D>
@@ -220,12 +190,13 @@ struct __align__(1024) Smem {
     uint64_t v_fix;  // V tiles that need their rows looked at land here first
     uint32_t tmem_base;
     int abort;
-    Runs runs;
-    Cursor cursor[5];  // warps 0 .. 3, softmax
+    int start_b, start_step, run;  // the run's first request, step in it, and length
+    Cursor cursor[3];              // warps 0 to 2
+    uint32_t bad_segs[kTileRing];              // per tile: page segments read through a bad page id
     uint32_t v_bad[kBadRing][kMaxNodes / 32];  // per segment: nodes whose V row holds an infinity or a NaN
     union {
-        uint8_t parent[kMaxNodes];      // parent + 1
-        long long sums[2][kThreads / 32];  // while the runs are looked for
+        Segment segment[kSegRing];
+        long long sums[kThreads / 32];  // while the run is looked for
     };
 };
 
@@ -303,79 +274,53 @@ __global__ void __launch_bounds__(kThreads, 2)
         fence_mbar_init();
     }
     if (threadIdx.x < kBadRing * kMaxNodes / 32) S.v_bad[0][threadIdx.x] = 0;
-    // This gang's runs: the batch's steps are counted, then the requests that hold the
-    // runs' first steps are looked for, 256 requests at a time.
+    // This gang's run: the batch's steps are counted, then the request that holds the
+    // run's first step is looked for, 256 requests at a time.
     const int tid = threadIdx.x;
-    // Sums over the CTA of 256 requests' steps (prefix sums) and key tiles.
-    long long steps = 0, inc = 0, sum_steps = 0, sum_keys = 0;
+    // Steps of 256 requests: this thread's, up to and including it, of all.
+    long long steps = 0, inc = 0, sum_steps = 0;
     auto scan = [&](int i0, bool report) {
-        steps = 0;
-        long long k = 0;
-        if (i0 + tid < p.batch) {
-            const Request rq = request(p, i0 + tid, report);
-            steps = steps_of(rq);
-            if (rq.mtiles > 0) k = rq.ntiles;
-        }
+        steps = i0 + tid < p.batch ? steps_of(request(p, i0 + tid, report)) : 0;
         inc = steps;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
-            k += __shfl_xor_sync(0xffffffffu, k, o);
         }
         __syncthreads();  // the previous sums have been read
-        if (lane == 31) {
-            S.sums[0][warp] = inc;
-            S.sums[1][warp] = k;
-        }
+        if (lane == 31) S.sums[warp] = inc;
         __syncthreads();
-        sum_steps = sum_keys = 0;
+        sum_steps = 0;
 #pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) inc += S.sums[0][w];
-            sum_steps += S.sums[0][w];
-            sum_keys += S.sums[1][w];
+            if (w < warp) inc += S.sums[w];
+            sum_steps += S.sums[w];
         }
     };
-    long long total = 0, keys = 0;
+    long long total = 0;
     for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
         scan(i0, blockIdx.x == 0);
         total += sum_steps;
-        keys += sum_keys;
     }
-    // Rounds: K / V bytes over kRoundBytes if row tiles share them and runs stay long.
-    int rounds = 1;
-    if (total > keys + keys / 8) {
-        const long long by_bytes = (keys * p.hkv * (2 * BN * D * 2) + kRoundBytes - 1) / kRoundBytes;
-        rounds = (int)max(1ll, min(min((long long)p.max_rounds, by_bytes), total / (kRoundSteps * (long long)gangs)));
-    }
-    const long long runs = (long long)gangs * rounds;
-    const long long per_run = max((long long)kMinSteps, (total + runs - 1) / runs);
-    if (blockIdx.x != 0 && gang * per_run >= total) return;
+    const long long per_run = max((long long)kMinSteps, (total + gangs - 1) / gangs);
+    const long long w0 = gang * per_run;
+    if (blockIdx.x != 0 && w0 >= total) return;
     long long before = 0;
     for (int i0 = 0; i0 < p.batch; i0 += kThreads) {
         if (p.batch > kThreads) scan(i0, false);
         const long long at = before + inc - steps;
-        for (int k = 0; k < rounds; ++k) {
-            const long long w = ((long long)k * gangs + gang) * per_run;
-            if (steps > 0 && at <= w && w < at + steps) {
-                S.runs.start_b[k] = i0 + tid;
-                S.runs.start_step[k] = (int)(w - at);
-            }
+        if (steps > 0 && at <= w0 && w0 < at + steps) {
+            S.start_b = i0 + tid;
+            S.start_step = (int)(w0 - at);
         }
         if (blockIdx.x == 0 && i0 + tid < p.batch) p.first[i0 + tid] = at;
         before += sum_steps;
     }
-    if (tid == 0) {
-        S.runs.per_run = per_run;
-        S.runs.total = total;
-        S.runs.gang = gang;
-        S.runs.gangs = gangs;
-        if (blockIdx.x == 0) p.first[p.batch] = per_run;
-    }
+    if (blockIdx.x == 0 && tid == 0) p.first[p.batch] = per_run;
     if (total == 0) return;
-    __syncthreads();  // the runs' starts are known to all, and S.sums has been read
-    if (tid < 5) S.cursor[tid].start(p, S.runs);
+    if (tid == 0) S.run = (int)min(per_run, total - w0);
+    __syncthreads();  // the run is known to all, and S.sums has been read
+    if (tid < 3) S.cursor[tid].start(p, S.start_b, S.start_step, S.run);
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -385,7 +330,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int* abort = &S.abort;
-    Cursor& c = S.cursor[warp < 4 ? warp : 4];
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsCtrl));
@@ -394,6 +338,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             // Converged warps: lane i resolves the physical slot of the tile's i-th
             // page segment and issues its copies.
             const bool is_k = warp == 0;
+            Cursor& c = S.cursor[warp];
             uint64_t* full = is_k ? S.k_full : S.v_full;
             uint64_t* empty = is_k ? S.k_empty : S.v_empty;
             uint8_t* dst0 = is_k ? S.k[0] : S.v[0];
@@ -428,6 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         ok = false;
                         break;
                     }
+                    if (is_k && it == 0 && lane == 0) S.segment[segs % kSegRing] = c;  // released with the tile
                     const int j0 = c.tile(it) * BN;
                     const int j = j0 + (lane << p.seg_shift);
                     const bool bad = (unsigned)pg >= (unsigned)p.num_pages;
@@ -437,7 +383,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const uint32_t bad_segs = __ballot_sync(0xffffffffu, bad);
                     const bool fix = !is_k && (j0 + BN > P || bad_segs || (j0 < gap1 && j0 + BN > gap0));
                     uint64_t* bar = fix ? &S.v_fix : &full[st];
-                    if (lane == 0) mbar_expect_tx(bar, kTile);
+                    if (lane == 0) {
+                        if (is_k) S.bad_segs[n % kTileRing] = bad_segs;
+                        mbar_expect_tx(bar, kTile);
+                    }
                     __syncwarp();
                     if (lane < nseg) {
                         uint8_t* dst = dst0 + st * kTile + ((uint32_t)lane << p.seg_shift) * 128u;
@@ -475,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 ++segs;
-            } while (ok && c.next<false>(p, S.runs));
+            } while (ok && c.next(p));
             // Drain: every copy issued must have landed before the CTA exits.
             if (lane == 0) {
                 if (fixes > 0) drain_wait(&S.v_fix, (fixes - 1) & 1);
@@ -498,6 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             bool ok = true;
             int n = 0, segs = 0;  // tiles, segments so far
             if (warp == 1) {
+                Cursor& c = S.cursor[1];
                 // Q is loaded by this warp, as soon as the previous segment's last S has
                 // read its predecessor: K is on its way by then.
                 if (lane == 0) prefetch_tmap(&tm_q);
@@ -530,23 +480,26 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     if (ok) umma_commit_e(&S.q_empty);
                     ++segs;
-                } while (ok && c.next<false>(p, S.runs));
+                } while (ok && c.next(p));
                 umma_commit_e(&S.final_bar);
                 drain_wait(&S.final_bar, 0);
             } else {
-                do {
-                    for (int it = 0; it < c.ntiles; ++it, ++n) {
-                        if (!(ok = wait_all(&S.v_full[n % kStages], (n / kStages) & 1))) break;
-                        if (!(ok = wait_all(&S.p_full, n & 1))) break;
-                        tc_fence_after();
-                        const uint64_t dv = dv0 + (n % kStages) * (kTile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            umma_ts_e(tmem + cO, tmem + cP + kk * 8, dv + 128 * kk, idO, (it > 0 || kk > 0) ? 1u : 0u);
-                        umma_commit_e(&S.o_done);
-                        umma_commit_e(&S.v_empty[n % kStages]);
+                for (int it = 0, ntiles = 0, left = S.run; left > 0; --left, ++n) {
+                    if (!(ok = wait_all(&S.v_full[n % kStages], (n / kStages) & 1))) break;
+                    if (!(ok = wait_all(&S.p_full, n & 1))) break;
+                    tc_fence_after();
+                    if (it == ntiles) {  // the first tile of a segment
+                        it = 0;
+                        ntiles = S.segment[segs++ % kSegRing].ntiles;
                     }
-                } while (ok && c.next<false>(p, S.runs));
+                    const uint64_t dv = dv0 + (n % kStages) * (kTile >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < BN / 16; ++kk)
+                        umma_ts_e(tmem + cO, tmem + cP + kk * 8, dv + 128 * kk, idO, (it > 0 || kk > 0) ? 1u : 0u);
+                    umma_commit_e(&S.o_done);
+                    umma_commit_e(&S.v_empty[n % kStages]);
+                    ++it;
+                }
                 umma_commit_e(&S.final_pv);
                 drain_wait(&S.final_pv, 0);
             }
@@ -560,55 +513,50 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t tS = tmem + lane_base + cS;
         const uint32_t tO = tmem + lane_base + cO;
         const uint32_t tP = tmem + lane_base + cP;
-        const int row_node = r / p.group, g = r % p.group;
+        const int row_node = r / p.group, h = kvh * p.group + r % p.group;
+        const float sink = p.sink ? p.sink[h] * ATTN_LOG2E : -INFINITY;
         const float sl2 = p.scale_log2;
         const int nseg = BN >> p.seg_shift;
-        // Page id of this lane's segment of a tile (0 for none), requested a tile ahead:
-        // keys that are read through a bad one are masked.
-        auto segment_page = [&](int j0) -> int {
-            const int j = j0 + (lane << p.seg_shift);
-            return lane < nseg && j < c.rq.L ? __ldg(p.page_table + (size_t)c.b * p.max_pages + (j >> p.page_shift)) : 0;
-        };
-        bool ok = true;
-        int n = 0, segs = 0;  // tiles, segments so far
-        do {
-        const int P = c.rq.P, ntiles = c.ntiles;
+        int left = S.run, n = 0, segs = 0;  // tiles to come; tiles and segments so far
+        while (left > 0) {
+        // The four warps go on or give up together (a warp that gave up alone would
+        // leave the others waiting at the next group barrier).
+        bool ok = mbar_wait(&S.s_full, n & 1, abort);
+        if (!group_all(ok)) break;
+        const Segment& c = S.segment[segs % kSegRing];  // arrived with its first tile
+        const int P = c.rq.P, q_start = c.rq.q_start, ntiles = c.ntiles;
+        const int32_t* const pages = p.page_table + (size_t)c.b * p.max_pages;
+        const int t_gap = c.rq.ta - c.it0, t0 = c.it0, t1 = c.rq.tb - c.rq.ta + c.it0;
+        auto tile_of = [&](int it) { return it < t_gap ? t0 + it : t1 + it; };
         const int node = c.mt * p.npt + row_node;
         const bool valid = r < p.npt * p.group && node < c.rq.rows;
         const bool work = __any_sync(0xffffffffu, valid);  // else only the barriers' arrivals
-        const int h = kvh * p.group + g;
         const bool drafts = c.drafts();
-        int page = segment_page(c.tile(0) * BN);
-        if (drafts || p.win_last > 0) {
-            // the parents that this row tile's walks can meet
-            asm volatile("bar.sync 1, 128;" ::: "memory");  // the previous segment's have been read
-            for (int i = r; i < min(c.rq.rows, (c.mt + 1) * p.npt); i += 128) {
-                int pr = p.parents[c.rq.q_start + i];
-                if (pr < -1 || pr >= i) {
-                    raise_status(ATTN_SINK_DEV_TREE);
-                    pr = -1;
-                }
-                S.parent[i] = (uint8_t)(pr + 1);
-            }
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-        }
-        const float sg = p.sink && valid ? p.sink[h] * ATTN_LOG2E : -INFINITY;
+        // parent + 1 of the node a - 1 (0: the prefix)
+        auto up = [&](int a) -> int {
+            const int pr = __ldg(p.parents + q_start + a - 1);
+            if (pr >= -1 && pr < a - 1) return pr + 1;
+            raise_status(ATTN_SINK_DEV_TREE);
+            return 0;
+        };
+        const float sg = valid ? sink : -INFINITY;
         float m_ref = sg == INFINITY ? -INFINITY : sg;
         float l = 0.f;
         int pos = P;  // this row's position
         if (p.win_last > 0 && valid)
-            for (int a = S.parent[node]; a > 0; a = S.parent[a - 1]) ++pos;
+            for (int a = up(node + 1); a > 0; a = up(a)) ++pos;
         const int pos_max = P + max(c.rq.n, 1) - 1;  // of any node
         for (int it = 0; it < ntiles; ++it, ++n) {
-            const int j0 = c.tile(it) * BN;
-            const uint32_t bad_segs = __ballot_sync(0xffffffffu, (unsigned)page >= (unsigned)p.num_pages);
-            if (it + 1 < ntiles) page = segment_page(c.tile(it + 1) * BN);
-            ok = mbar_wait(&S.s_full, n & 1, abort);
-            if (!__all_sync(0xffffffffu, ok)) {
-                ok = false;
-                break;
+            const int j0 = tile_of(it) * BN;
+            if (it > 0) {
+                ok = mbar_wait(&S.s_full, n & 1, abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
             }
             tc_fence_after();
+            const uint32_t bad_segs = S.bad_segs[n % kTileRing];
             // The previous P V must be complete before P is overwritten or O rescaled.
             auto wait_prev_pv = [&]() -> bool {
                 if (it == 0) return true;
@@ -655,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int w = 0; w < 4; ++w) vis[w] = below(c_hi, w) & (below(f_hi, w) | ~below(w_lo, w));
                 if (jmax >= P && valid) {
                     int at = pos;  // the walked token's position
-                    for (int a = node + 1; a > 0; a = S.parent[a - 1], --at) {
+                    for (int a = node + 1; a > 0; a = up(a), --at) {
                         const int c = P + a - 1 - j0;
                         const bool in = p.win_last <= 0 || at < p.win_first || at > pos - p.win_last;
                         const uint32_t bit = in && c >= 0 && c < BN ? 1u << (c & 31) : 0u;
@@ -786,11 +734,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 
         // -------------------------------------------------------------- epilogue
-        // The four warps go on or give up together (a warp that gave up alone would
-        // leave the others waiting at the next group barrier).
         if (ok) ok = mbar_wait(&S.o_done, (n - 1) & 1, abort);
-        ok = group_all(ok);
-        if (!ok) break;
+        if (!group_all(ok)) break;
         tc_fence_after();
         const bool direct = c.whole();
         // Direct output: the sink joins the sum, and the row is normalised.
@@ -808,9 +753,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 lse_v = (M + log2f(Z)) * ATTN_LN2;
             }
         }
-        const int row = c.rq.q_start + node;
+        const int row = q_start + node;
         // a run's first segment has the first place, any other the second
-        const size_t part = ((((size_t)c.round * gangs + gang) * p.hkv + kvh) * 2 + (c.in_run > 0)) * BM + r;
+        const size_t part = (((size_t)gang * p.hkv + kvh) * 2 + (segs > 0)) * BM + r;
         uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)row * p.hq + h) * D);
         float4* pdst = reinterpret_cast<float4*>(p.part_o + part * D);
         uint32_t* const v_bad = S.v_bad[segs % kBadRing];
@@ -826,11 +771,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (valid && any_bad) {
                 // Infinities and NaNs of drafted tokens' V that this row sees.
                 int at = pos;
-                for (int a = node + 1; a > 0; a = S.parent[a - 1], --at) {
+                for (int a = node + 1; a > 0; a = up(a), --at) {
                     const int t = P + a - 1;
                     if (!(v_bad[(a - 1) >> 5] >> ((a - 1) & 31) & 1u)) continue;
                     if (p.win_last > 0 && at >= p.win_first && at <= pos - p.win_last) continue;
-                    const int pg = p.page_table[(size_t)c.b * p.max_pages + (t >> p.page_shift)];
+                    const int pg = pages[t >> p.page_shift];
                     const size_t sl = ((size_t)pg << p.page_shift) | (t & ((1 << p.page_shift) - 1));
                     const __nv_bfloat16* v = p.v_cache + (sl * p.hkv + kvh) * D + ch * 32;
 #pragma unroll
@@ -864,7 +809,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         tc_fence_before();  // O has been read: the next segment's P V may overwrite it
         ++segs;
-        } while (c.next<true>(p, S.runs));
+        left -= ntiles;
+        }
     }
 
     tc_fence_before();
@@ -876,23 +822,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Merges the segments of a row in log-sum-exp form and adds the sink once.  One warp
-// per node and 8 query heads of a KV head, whose partial rows are neighbours; lane = D
-// / 32 dimensions.
+// per node and kRows query heads of a KV head, whose partial rows are neighbours; lane
+// = D / 32 dimensions.  Eight rows a warp keep as many loads in flight; with few rows
+// (a wave of warps holds them) a warp has one, and its segments' loads overlap.
 constexpr int kCombineWarps = 8;
-constexpr int kCombineRows = 8;
 
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const Params p) {
     constexpr int V = D / 32;
     using Vec = typename std::conditional<V == 2, float2, float4>::type;
     const int lane = threadIdx.x & 31, b = blockIdx.y;
-    const int blocks = (p.group + kCombineRows - 1) / kCombineRows;  // of a KV head's query heads
+    const int blocks = (p.group + kRows - 1) / kRows;  // of a KV head's query heads
     const int idx = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-    const int node = idx / (p.hkv * blocks), kvh = idx / blocks % p.hkv, g0 = idx % blocks * kCombineRows;
+    const int node = idx / (p.hkv * blocks), kvh = idx / blocks % p.hkv, g0 = idx % blocks * kRows;
     const Request rq = request(p, b, false);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
     if (node >= rq.rows) return;
-    const int heads = min(kCombineRows, p.group - g0), h0 = kvh * p.group + g0;
+    const int heads = min(kRows, p.group - g0), h0 = kvh * p.group + g0;
     const int mt = node / p.npt, r0 = (node - mt * p.npt) * p.group + g0;
     // The row tile's steps [u0, u1) lie in the runs c0 .. c1.
     const long long per_run = p.first[p.batch];
@@ -905,22 +851,24 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const bool has = lane < heads;
     const float sg = has && p.sink ? p.sink[h0 + lane] * ATTN_LOG2E : -INFINITY;
     float M = sg;
+#pragma unroll 8
     for (int c = c0; c <= c1; ++c)
         if (has) M = fmaxf(M, p.part_ml[place(c) + lane].x);
     const bool some = M != INFINITY && M != -INFINITY;
     float Z = some ? fast_exp2(sg - M) : 1.f;
-    float o[kCombineRows][V] = {};
+    float o[kRows][V] = {};
+#pragma unroll(kRows == 1 ? 8 : 1)
     for (int c = c0; c <= c1; ++c) {
         const size_t at = place(c);
         const float2 x = has ? p.part_ml[at + lane] : make_float2(0.f, 0.f);
         const float w = some && x.y != 0.f ? fast_exp2(x.x - M) : 0.f;  // 0: nothing seen in this segment
         if (w != 0.f) Z += x.y * w;
-        Vec u[kCombineRows];
+        Vec u[kRows];
 #pragma unroll
-        for (int k = 0; k < kCombineRows; ++k)
+        for (int k = 0; k < kRows; ++k)
             if (k < heads) u[k] = reinterpret_cast<const Vec*>(p.part_o + (at + k) * D)[lane];
 #pragma unroll
-        for (int k = 0; k < kCombineRows; ++k) {
+        for (int k = 0; k < kRows; ++k) {
             const float f = __shfl_sync(0xffffffffu, w, k);
             if (k >= heads || f == 0.f) continue;
             const float* v = reinterpret_cast<const float*>(&u[k]);
@@ -931,7 +879,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const float inv = some ? 1.f / Z : 0.f;
     const size_t row = (size_t)rq.q_start + node;
 #pragma unroll
-    for (int k = 0; k < kCombineRows; ++k) {
+    for (int k = 0; k < kRows; ++k) {
         const float f = __shfl_sync(0xffffffffu, inv, k);
         if (k >= heads) continue;
         uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (row * p.hq + h0 + k) * D + lane * V);
@@ -984,14 +932,8 @@ Plan make_plan(const Args& a) {
     Plan pl;
     const int slots = 152 * (a.head_dim == 64 ? 2 : 1);
     pl.ctas = slots >= a.hkv ? slots / a.hkv * a.hkv : a.hkv;
-    // The kernel knows the true lengths; here they bound the scratch.
-    const int npt = BM / (a.hq / a.hkv);
-    const double bytes = (double)a.batch * a.hkv * a.max_seqlen_k * a.head_dim * 4;
-    const double rounds = a.max_seqlen_q <= npt ? 1. : bytes / (double)kRoundBytes + 1.;
-    pl.rounds = rounds < kMaxRounds ? (int)rounds : kMaxRounds;
-    const size_t runs = (size_t)pl.ctas * pl.rounds;
-    pl.part_o_bytes = runs * 2 * BM * a.head_dim * sizeof(float);
-    pl.part_ml_bytes = runs * 2 * BM * sizeof(float2);
+    pl.part_o_bytes = (size_t)pl.ctas * 2 * BM * a.head_dim * sizeof(float);
+    pl.part_ml_bytes = (size_t)pl.ctas * 2 * BM * sizeof(float2);
     pl.first_bytes = ((size_t)a.batch + 1) * sizeof(long long);
     return pl;
 }
@@ -1012,7 +954,6 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
     p.part_o = static_cast<float*>(scratch);
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + pl.part_o_bytes);
     p.first = reinterpret_cast<long long*>(static_cast<char*>(scratch) + pl.part_o_bytes + pl.part_ml_bytes);
-    p.max_rounds = pl.rounds;
     p.batch = a.batch;
     p.max_pages = a.max_pages;
     p.page_shift = 0;
@@ -1046,7 +987,8 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
         return e;
     }
     cudaLaunchConfig_t cfg = {};
-    const long long warps = (long long)a.max_seqlen_q * a.hkv * ((p.group + kCombineRows - 1) / kCombineRows);
+    const int rows = (long long)a.batch * a.max_seqlen_q * a.hq <= 152 * 32 ? 1 : 8;
+    const long long warps = (long long)a.max_seqlen_q * a.hkv * ((p.group + rows - 1) / rows);
     cfg.gridDim = dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps), a.batch);
     cfg.blockDim = dim3(kCombineWarps * 32);
     cfg.stream = s;
@@ -1055,7 +997,8 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p);
+    e = rows == 1 ? cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, 1>, p)
+                  : cudaLaunchKernelEx(&cfg, tree_combine_kernel<D, 8>, p);
     if (e != cudaSuccess) *what = "combine launch";
     return e;
 }

@@ -31,8 +31,7 @@ struct Args {
 
 // Grid and scratch sizes.
 struct Plan {
-    int ctas;    // persistent CTAs
-    int rounds;  // runs of steps per gang of hkv CTAs, at most
+    int ctas;  // persistent CTAs, in gangs of hkv
     size_t part_o_bytes, part_ml_bytes, first_bytes;
 };
 
