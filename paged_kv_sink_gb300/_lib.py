@@ -601,7 +601,7 @@ def _outputs(q, dev, lse_shape, sink, out, lse, return_lse):
         if not _is(lse, _F32, dev, lse_shape):
             _expect("lse", lse, _F32, dev, lse_shape)
     elif return_lse:
-        lse = q.new_empty(lse_shape, dtype=_F32)
+        lse = torch.empty(lse_shape, dtype=_F32, device=q.device)
     return (out, lse, None if sink is None else sink.data_ptr(), out.data_ptr(),
             None if lse is None else lse.data_ptr())
 
@@ -697,7 +697,7 @@ def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget
     elif not _is(weights_out, _F32, dev, shape):
         _expect("weights_out", weights_out, _F32, dev, shape)
     if kept is None:
-        kept = seqlens.new_empty((B, heads, max(budget, 0)))
+        kept = torch.empty((B, heads, max(budget, 0)), dtype=_I32, device=seqlens.device)
     elif not _is(kept, _I32, dev, (B, heads, budget)):
         _expect("kept", kept, _I32, dev, (B, heads, budget))
     if new_seqlens is None:
