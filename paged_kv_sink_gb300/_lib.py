@@ -539,7 +539,7 @@ def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0,
         raise TypeError("k_out is given without k")
     _run("attn_sink_rope", dev, stream, q.data_ptr(), q_out.data_ptr(), kp, kop, q_rs, qo_rs, k_rs, ko_rs,
          positions.data_ptr(), inv_freq.data_ptr(), T, hq, hkv, d, r, 1 if interleaved else 0, 1 if inverse else 0,
-         attn_scale)
+         float(attn_scale))
     return q_out, k_out
 
 
@@ -582,7 +582,7 @@ def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seql
         qo_rs = _expect_rows("q_out", q_out, dev, q.shape)
     _run("attn_sink_rope_kv_append", dev, stream, q.data_ptr(), q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
          q_rs, qo_rs, k_rs, v_rs, cu, pos, inv_freq.data_ptr(), seqlens.data_ptr(), page_table.data_ptr(), max_pages, B,
-         T, hq, hkv, d, r, ps, npages, max_new, 1 if interleaved else 0, attn_scale, k_cache.data_ptr(),
+         T, hq, hkv, d, r, ps, npages, int(max_new), 1 if interleaved else 0, float(attn_scale), k_cache.data_ptr(),
          v_cache.data_ptr())
     return q_out
 
@@ -627,7 +627,8 @@ def attn_sink_tree_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_
     out, lse, sp, op, lp = _outputs(q, dev, (hq, T), sink, out, lse, return_lse)
     _run("attn_sink_tree_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          page_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), parents.data_ptr(), B, T, hq,
-         hkv, d, ps, npages, max_seqlen_q, max_seqlen_k, sp, win_first, win_last, scale, op, lp)
+         hkv, d, ps, npages, int(max_seqlen_q), int(max_seqlen_k), sp, int(win_first), int(win_last), float(scale), op,
+         lp)
     return out, lse
 
 
@@ -637,8 +638,9 @@ def attn_sink_kv_compact(k_cache, v_cache, page_table, src, counts, base=None, s
     increasing, src[j] >= base + j.  Returns (k_cache, v_cache)."""
     dev = _device("k_cache", k_cache)
     npages, ps, hkv, d, max_pages = _expect_cache(k_cache, v_cache, page_table, dev)
-    B, heads = page_table.shape[0], 1 if src.dim() == 2 else hkv
-    want = (B, src.shape[-1] if src.dim() else None) if heads == 1 and src.dim() == 2 else (B, hkv, src.shape[-1] if src.dim() else None)
+    B, shared = page_table.shape[0], src.dim() == 2
+    most = src.shape[-1] if src.dim() else None
+    want = (B, most) if shared else (B, hkv, most)
     if not _is(src, _I32, dev, want):
         _expect("src", src, _I32, dev, want)
     if not _is(counts, _I32, dev, (B,)):
@@ -649,7 +651,7 @@ def attn_sink_kv_compact(k_cache, v_cache, page_table, src, counts, base=None, s
             _expect("base", base, _I32, dev, (B,))
         bp = base.data_ptr()
     _run("attn_sink_kv_compact", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_pages,
-         src.data_ptr(), counts.data_ptr(), bp, B, heads, want[-1], hkv, d, ps, npages)
+         src.data_ptr(), counts.data_ptr(), bp, B, 1 if shared else hkv, most, hkv, d, ps, npages)
     return k_cache, v_cache
 
 
@@ -670,8 +672,8 @@ def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, wei
         _expect("weights", weights, _F32, dev, (B, None, None))
     out, lse, sp, op, lp = _outputs(q, dev, (B, hq), sink, out, lse, return_lse)
     _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages, sp, win_first, win_last, scale,
-         weights.data_ptr(), shape[1], shape[2], op, lp)
+         page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages, sp, int(win_first),
+         int(win_last), float(scale), weights.data_ptr(), shape[1], shape[2], op, lp)
     return out, lse
 
 
@@ -705,8 +707,8 @@ def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget
     elif not _is(new_seqlens, _I32, dev, (B,)):
         _expect("new_seqlens", new_seqlens, _I32, dev, (B,))
     _run("attn_sink_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_pages,
-         seqlens.data_ptr(), weights.data_ptr(), B, heads, cap, hkv, d, ps, npages, budget, keep_first, keep_last,
-         weights_out.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr())
+         seqlens.data_ptr(), weights.data_ptr(), B, heads, cap, hkv, d, ps, npages, budget,
+         int(keep_first), int(keep_last), weights_out.data_ptr(), kept.data_ptr(), new_seqlens.data_ptr())
     return new_seqlens, kept
 
 

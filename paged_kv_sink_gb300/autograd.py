@@ -125,7 +125,9 @@ class _AttnSinkRope(torch.autograd.Function):
 def attn_sink_rope_func(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0):
     """Rotary positions (``attn_sink_rope``), differentiable in q (T, Hq, d) and k
     (T, Hkv, d) or None; the gradient is the rotation by the negative angle.
-    Returns (q_out, k_out), or q_out alone without k."""
+    Returns (q_out, k_out), or q_out alone without k.  Forward and backward can be
+    captured in a CUDA graph; as with any autograd function, no eager graph of the
+    same leaves may be alive then (torch would join its stream to the capture)."""
     return _AttnSinkRope.apply(q, k, positions, inv_freq, bool(interleaved), float(attn_scale), False)
 
 

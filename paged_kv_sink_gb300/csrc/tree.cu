@@ -132,14 +132,21 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
 
 __device__ __forceinline__ long long steps_of(const Request& r) { return (long long)r.mtiles * r.ntiles; }
 
+// Prefix tokens [first, end) that nodes on the prefix see as part of the last window
+// and the deepest possible node does not (at most kMaxNodes - 1 of them).
+__device__ __forceinline__ int some_first(const Params& p, const Request& r) {
+    return p.win_last > 0 ? max(max(0, p.win_first), r.P + 1 - p.win_last) : 0;
+}
+__device__ __forceinline__ int some_end(const Params& p, const Request& r) {
+    return p.win_last > 0 ? max(0, min(r.P, r.P + min(r.n, kMaxNodes) - p.win_last)) : 0;
+}
+
 // The key tiles [it0, it0 + ntiles) of one row tile: what a CTA works on at a time.
 struct Segment {
     Request rq;
     int b, mt, it0, ntiles;  // request, row tile
     __device__ __forceinline__ int tile(int it) const { return rq.tile(it0 + it); }
     __device__ __forceinline__ bool whole() const { return it0 == 0 && ntiles == rq.ntiles; }
-    // it reaches drafted tokens
-    __device__ __forceinline__ bool drafts() const { return (tile(ntiles - 1) + 1) * BN > rq.P; }
 };
 
 // A gang's run of steps, segment by segment.  Warps 0 to 2 walk a cursor of their own,
@@ -193,7 +200,9 @@ struct __align__(1024) Smem {
     int start_b, start_step, run;  // the run's first request, step in it, and length
     Cursor cursor[3];              // warps 0 to 2
     uint32_t bad_segs[kTileRing];              // per tile: page segments read through a bad page id
-    uint32_t v_bad[kBadRing][kMaxNodes / 32];  // per segment: nodes whose V row holds an infinity or a NaN
+    // Per segment: tokens that some rows see and others do not whose V row holds an
+    // infinity or a NaN; nodes, then prefix tokens at the window's start.
+    uint32_t v_bad[kBadRing][2 * kMaxNodes / 32];
     union {
         Segment segment[kSegRing];
         long long sums[kThreads / 32];  // while the run is looked for
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         S.abort = 0;
         fence_mbar_init();
     }
-    if (threadIdx.x < kBadRing * kMaxNodes / 32) S.v_bad[0][threadIdx.x] = 0;
+    if (threadIdx.x < kBadRing * 2 * kMaxNodes / 32) S.v_bad[0][threadIdx.x] = 0;
     // This gang's run: the batch's steps are counted, then the request that holds the
     // run's first step is looked for, 256 requests at a time.
     const int tid = threadIdx.x;
@@ -348,9 +357,11 @@ __global__ void __launch_bounds__(kThreads, 2)
             // Rows of a V tile that no row of the request may see enter P V as
             // zeros, whatever the memory holds (a weight of 0 times a NaN would not
             // vanish): rows past the last token, in the window's gap, or read through
-            // a bad page id.  A drafted token's infinities and NaNs are zeroed too,
-            // and added by the rows that see that token at the end.  Such tiles land on
-            // v_fix and are released to the tensor core once they are clean.
+            // a bad page id.  Of tokens that only some rows see (drafted ones, and the
+            // first ones of the last window, which deeper nodes have left behind)
+            // infinities and NaNs are zeroed too, and added at the end by the rows that
+            // see them.  Such tiles land on v_fix and are released to the tensor core
+            // once they are clean.
             int fixes = 0, segs = 0;
             int n = 0;  // tiles so far
             bool ok = true;
@@ -358,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int L = c.rq.L, P = c.rq.P;
                 const int gap0 = p.win_last > 0 ? p.win_first : 0;
                 const int gap1 = p.win_last > 0 ? P + 1 - p.win_last : 0;
+                const int some0 = some_first(p, c.rq), some1 = some_end(p, c.rq);
                 // this lane's page id of a tile (0 for none), requested a tile ahead
                 auto segment_page = [&](int j0) -> int {
                     const int j = j0 + (lane << p.seg_shift);
@@ -381,7 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // segments past the last token and bad ones read slot 0
                     const int slot = bad || j >= L ? 0 : (pg << p.page_shift) | (j & ((1 << p.page_shift) - 1));
                     const uint32_t bad_segs = __ballot_sync(0xffffffffu, bad);
-                    const bool fix = !is_k && (j0 + BN > P || bad_segs || (j0 < gap1 && j0 + BN > gap0));
+                    const bool fix = !is_k && (j0 + BN > P || bad_segs != 0 || (j0 < gap1 && j0 + BN > gap0) ||
+                                               (j0 < some1 && j0 + BN > some0));
                     uint64_t* bar = fix ? &S.v_fix : &full[st];
                     if (lane == 0) {
                         if (is_k) S.bad_segs[n % kTileRing] = bad_segs;
@@ -406,14 +419,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                             uint4* cell = reinterpret_cast<uint4*>(dst0 + st * kTile) + e;
                             if (t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u)) {
                                 *cell = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (t >= P) {
+                            } else if (t >= P || (t >= some0 && t < some1)) {
                                 const uint4 x = *cell;
                                 if (nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) ||
                                     nonfinite_pair(x.w)) {
                                     *cell = make_uint4(finite_pair(x.x), finite_pair(x.y), finite_pair(x.z),
                                                        finite_pair(x.w));
-                                    if (t - P < kMaxNodes)
-                                        atomicOr(&S.v_bad[segs % kBadRing][(t - P) >> 5], 1u << ((t - P) & 31));
+                                    const int i = t >= P ? t - P : kMaxNodes + t - some0;
+                                    if (t < P || i < kMaxNodes)
+                                        atomicOr(&S.v_bad[segs % kBadRing][i >> 5], 1u << (i & 31));
                                 }
                             }
                         }
@@ -519,297 +533,300 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int nseg = BN >> p.seg_shift;
         int left = S.run, n = 0, segs = 0;  // tiles to come; tiles and segments so far
         while (left > 0) {
-        // The four warps go on or give up together (a warp that gave up alone would
-        // leave the others waiting at the next group barrier).
-        bool ok = mbar_wait(&S.s_full, n & 1, abort);
-        if (!group_all(ok)) break;
-        const Segment& c = S.segment[segs % kSegRing];  // arrived with its first tile
-        const int P = c.rq.P, q_start = c.rq.q_start, ntiles = c.ntiles;
-        const int32_t* const pages = p.page_table + (size_t)c.b * p.max_pages;
-        const int t_gap = c.rq.ta - c.it0, t0 = c.it0, t1 = c.rq.tb - c.rq.ta + c.it0;
-        auto tile_of = [&](int it) { return it < t_gap ? t0 + it : t1 + it; };
-        const int node = c.mt * p.npt + row_node;
-        const bool valid = r < p.npt * p.group && node < c.rq.rows;
-        const bool work = __any_sync(0xffffffffu, valid);  // else only the barriers' arrivals
-        const bool drafts = c.drafts();
-        // parent + 1 of the node a - 1 (0: the prefix)
-        auto up = [&](int a) -> int {
-            const int pr = __ldg(p.parents + q_start + a - 1);
-            if (pr >= -1 && pr < a - 1) return pr + 1;
-            raise_status(ATTN_SINK_DEV_TREE);
-            return 0;
-        };
-        const float sg = valid ? sink : -INFINITY;
-        float m_ref = sg == INFINITY ? -INFINITY : sg;
-        float l = 0.f;
-        int pos = P;  // this row's position
-        if (p.win_last > 0 && valid)
-            for (int a = up(node + 1); a > 0; a = up(a)) ++pos;
-        const int pos_max = P + max(c.rq.n, 1) - 1;  // of any node
-        for (int it = 0; it < ntiles; ++it, ++n) {
-            const int j0 = tile_of(it) * BN;
-            if (it > 0) {
-                ok = mbar_wait(&S.s_full, n & 1, abort);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-            }
-            tc_fence_after();
-            const uint32_t bad_segs = S.bad_segs[n % kTileRing];
-            // The previous P V must be complete before P is overwritten or O rescaled.
-            auto wait_prev_pv = [&]() -> bool {
-                if (it == 0) return true;
-                const bool done = __all_sync(0xffffffffu, mbar_wait(&S.o_done, (n - 1) & 1, abort));
-                if (done) tc_fence_after();
-                return done;
+            // The four warps go on or give up together (a warp that gave up alone would
+            // leave the others waiting at the next group barrier).
+            bool ok = mbar_wait(&S.s_full, n & 1, abort);
+            if (!group_all(ok)) break;
+            const Segment& c = S.segment[segs % kSegRing];  // arrived with its first tile
+            const int P = c.rq.P, q_start = c.rq.q_start, ntiles = c.ntiles;
+            const int32_t* const pages = p.page_table + (size_t)c.b * p.max_pages;
+            const int t_gap = c.rq.ta - c.it0, t0 = c.it0, t1 = c.rq.tb - c.rq.ta + c.it0;
+            auto tile_of = [&](int it) { return it < t_gap ? t0 + it : t1 + it; };
+            const int node = c.mt * p.npt + row_node;
+            const bool valid = r < p.npt * p.group && node < c.rq.rows;
+            const bool work = __any_sync(0xffffffffu, valid);  // else only the barriers' arrivals
+            // parent + 1 of the node a - 1 (0: the prefix)
+            auto up = [&](int a) -> int {
+                const int pr = __ldg(p.parents + q_start + a - 1);
+                if (pr >= -1 && pr < a - 1) return pr + 1;
+                raise_status(ATTN_SINK_DEV_TREE);
+                return 0;
             };
-            if (!work) {
-                tc_fence_before();
-                mbar_arrive(&S.s_free);
-                if (!(ok = wait_prev_pv())) break;
-                mbar_arrive(&S.p_full);
-                continue;
-            }
-            uint32_t s[4][32];
-            tmem_ld32(tS, s[0]);
-            tmem_ld32(tS + 32, s[1]);
-            tmem_ld_wait();
-            tmem_ld32(tS + 64, s[2]);
-            tmem_ld32(tS + 96, s[3]);
-            bool s_in = false;
-            auto finish_s_load = [&]() {
-                if (s_in) return;
-                s_in = true;
-                tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(&S.s_free);
-            };
-
-            const int jmax = j0 + BN - 1;
-            const bool full = jmax < P && !bad_segs &&
-                              (p.win_last <= 0 || jmax < p.win_first || j0 > pos_max - p.win_last);
-            uint32_t vis[4] = {0u, 0u, 0u, 0u};
-            if (!full) {
-                // Prefix columns [0, c_hi), less the window's gap [f_hi, w_lo).
-                const int c_hi = min(max(P - j0, 0), BN);
-                const int f_hi = p.win_last > 0 ? p.win_first - j0 : BN;
-                const int w_lo = p.win_last > 0 ? pos + 1 - p.win_last - j0 : 0;
-                auto below = [](int c, int w) -> uint32_t {  // bits of word w for columns < c
-                    const int k = c - 32 * w;
-                    return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
-                };
-#pragma unroll
-                for (int w = 0; w < 4; ++w) vis[w] = below(c_hi, w) & (below(f_hi, w) | ~below(w_lo, w));
-                if (jmax >= P && valid) {
-                    int at = pos;  // the walked token's position
-                    for (int a = node + 1; a > 0; a = up(a), --at) {
-                        const int c = P + a - 1 - j0;
-                        const bool in = p.win_last <= 0 || at < p.win_first || at > pos - p.win_last;
-                        const uint32_t bit = in && c >= 0 && c < BN ? 1u << (c & 31) : 0u;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            if ((c >> 5) == w) vis[w] |= bit;
+            const float sg = valid ? sink : -INFINITY;
+            float m_ref = sg == INFINITY ? -INFINITY : sg;
+            float l = 0.f;
+            int pos = P;  // this row's position
+            if (p.win_last > 0 && valid)
+                for (int a = up(node + 1); a > 0; a = up(a)) ++pos;
+            const int pos_max = P + max(c.rq.n, 1) - 1;  // of any node
+            for (int it = 0; it < ntiles; ++it, ++n) {
+                const int j0 = tile_of(it) * BN;
+                if (it > 0) {
+                    ok = mbar_wait(&S.s_full, n & 1, abort);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
                     }
                 }
-                if (bad_segs) {
-                    const uint32_t seg = (p.seg_shift >= 5 ? 0xffffffffu : (1u << (1 << p.seg_shift)) - 1u);
-                    for (int i = 0; i < nseg; ++i)
-                        if (bad_segs >> i & 1u) {
-                            const int c = i << p.seg_shift, len = 1 << p.seg_shift;
+                tc_fence_after();
+                const uint32_t bad_segs = S.bad_segs[n % kTileRing];
+                // The previous P V must be complete before P is overwritten or O rescaled.
+                auto wait_prev_pv = [&]() -> bool {
+                    if (it == 0) return true;
+                    const bool done = __all_sync(0xffffffffu, mbar_wait(&S.o_done, (n - 1) & 1, abort));
+                    if (done) tc_fence_after();
+                    return done;
+                };
+                if (!work) {
+                    tc_fence_before();
+                    mbar_arrive(&S.s_free);
+                    if (!(ok = wait_prev_pv())) break;
+                    mbar_arrive(&S.p_full);
+                    continue;
+                }
+                uint32_t s[4][32];
+                tmem_ld32(tS, s[0]);
+                tmem_ld32(tS + 32, s[1]);
+                tmem_ld_wait();
+                tmem_ld32(tS + 64, s[2]);
+                tmem_ld32(tS + 96, s[3]);
+                bool s_in = false;
+                auto finish_s_load = [&]() {
+                    if (s_in) return;
+                    s_in = true;
+                    tmem_ld_wait();
+                    tc_fence_before();
+                    mbar_arrive(&S.s_free);
+                };
+
+                const int jmax = j0 + BN - 1;
+                const bool full = jmax < P && !bad_segs &&
+                                  (p.win_last <= 0 || jmax < p.win_first || j0 > pos_max - p.win_last);
+                uint32_t vis[4] = {0u, 0u, 0u, 0u};
+                if (!full) {
+                    // Prefix columns [0, c_hi), less the window's gap [f_hi, w_lo).
+                    const int c_hi = min(max(P - j0, 0), BN);
+                    const int f_hi = p.win_last > 0 ? p.win_first - j0 : BN;
+                    const int w_lo = p.win_last > 0 ? pos + 1 - p.win_last - j0 : 0;
+                    auto below = [](int c, int w) -> uint32_t {  // bits of word w for columns < c
+                        const int k = c - 32 * w;
+                        return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u;
+                    };
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) vis[w] = below(c_hi, w) & (below(f_hi, w) | ~below(w_lo, w));
+                    if (jmax >= P && valid) {
+                        int at = pos;  // the walked token's position
+                        for (int a = node + 1; a > 0; a = up(a), --at) {
+                            const int c = P + a - 1 - j0;
+                            const bool in = p.win_last <= 0 || at < p.win_first || at > pos - p.win_last;
+                            const uint32_t bit = in && c >= 0 && c < BN ? 1u << (c & 31) : 0u;
 #pragma unroll
                             for (int w = 0; w < 4; ++w)
-                                if ((c >> 5) <= w && (c + len - 1) >> 5 >= w) vis[w] &= ~(seg << (c & 31));
+                                if ((c >> 5) == w) vis[w] |= bit;
                         }
-                }
-            }
-            auto mask_half = [&](auto hfc) {
-                constexpr int hf = decltype(hfc)::value;
+                    }
+                    if (bad_segs) {
+                        const uint32_t seg = (p.seg_shift >= 5 ? 0xffffffffu : (1u << (1 << p.seg_shift)) - 1u);
+                        for (int i = 0; i < nseg; ++i)
+                            if (bad_segs >> i & 1u) {
+                                const int c = i << p.seg_shift, len = 1 << p.seg_shift;
 #pragma unroll
-                for (int c = 2 * hf; c < 2 * hf + 2; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(vis[c] >> i & 1u)) s[c][i] = __float_as_uint(-INFINITY);
-            };
-            uint32_t w[64];
-            auto exps_half = [&](auto hfc, float m_use) -> float {
-                constexpr int hf = decltype(hfc)::value;
-                const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
-                uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int e = 32 * hf; e < 32 * hf + 32; ++e) {
-                    const int i0 = 2 * e;
-                    const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[i0 >> 5][i0 & 31]),
-                                                      __uint_as_float(s[(i0 + 1) >> 5][(i0 + 1) & 31])),
-                                              sc2, nm2);
-                    float y0, y1;
-                    f2_unpack(y, y0, y1);
-                    const float x0 = fast_exp2(y0), x1 = fast_exp2(y1);
-                    acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
-                    w[e] = pack_bf16x2(x0, x1);
+                                for (int w = 0; w < 4; ++w)
+                                    if ((c >> 5) <= w && (c + len - 1) >> 5 >= w) vis[w] &= ~(seg << (c & 31));
+                            }
+                    }
                 }
-                float sum = 0.f;
+                auto mask_half = [&](auto hfc) {
+                    constexpr int hf = decltype(hfc)::value;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float lo, hi;
-                    f2_unpack(acc2[e], lo, hi);
-                    sum += lo + hi;
-                }
-                return sum;
-            };
-            using H0 = std::integral_constant<int, 0>;
-            using H1 = std::integral_constant<int, 1>;
-            // Fast path: against the current reference, without the row maximum; every
-            // value is <= 2^64 unless a half's sum says otherwise.  Rows without a
-            // node have no say.
-            bool slow = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
-            bool stored0 = false;
-            float rs = 0.f;
-            if (!slow) {
-                if (!full) mask_half(H0{});
-                const float rs0 = exps_half(H0{}, m_ref);
-                finish_s_load();
-                const bool ok0 = !__any_sync(0xffffffffu, valid && !(rs0 <= kFastSumLimit));
-                if (!(ok = wait_prev_pv())) break;
-                if (ok0) {
-                    tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
-                    stored0 = true;
-                }
-                if (!full) mask_half(H1{});
-                const float rs1 = exps_half(H1{}, m_ref);
-                const bool ok1 = !__any_sync(0xffffffffu, valid && !(rs1 <= kFastSumLimit));
-                if (ok0 && ok1) {
-                    rs = rs0 + rs1;
-                    tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+                    for (int c = 2 * hf; c < 2 * hf + 2; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(vis[c] >> i & 1u)) s[c][i] = __float_as_uint(-INFINITY);
+                };
+                uint32_t w[64];
+                auto exps_half = [&](auto hfc, float m_use) -> float {
+                    constexpr int hf = decltype(hfc)::value;
+                    const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
+                    uint64_t acc2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+                    for (int e = 32 * hf; e < 32 * hf + 32; ++e) {
+                        const int i0 = 2 * e;
+                        const uint64_t y = f2_fma(f2_pack(__uint_as_float(s[i0 >> 5][i0 & 31]),
+                                                          __uint_as_float(s[(i0 + 1) >> 5][(i0 + 1) & 31])),
+                                                  sc2, nm2);
+                        float y0, y1;
+                        f2_unpack(y, y0, y1);
+                        const float x0 = fast_exp2(y0), x1 = fast_exp2(y1);
+                        acc2[e & 3] = f2_add(acc2[e & 3], f2_pack(x0, x1));
+                        w[e] = pack_bf16x2(x0, x1);
+                    }
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo, hi;
+                        f2_unpack(acc2[e], lo, hi);
+                        sum += lo + hi;
+                    }
+                    return sum;
+                };
+                using H0 = std::integral_constant<int, 0>;
+                using H1 = std::integral_constant<int, 1>;
+                // Fast path: against the current reference, without the row maximum; every
+                // value is <= 2^64 unless a half's sum says otherwise.  Rows without a
+                // node have no say.
+                bool slow = __any_sync(0xffffffffu, valid && m_ref == -INFINITY);
+                bool stored0 = false;
+                float rs = 0.f;
+                if (!slow) {
+                    if (!full) mask_half(H0{});
+                    const float rs0 = exps_half(H0{}, m_ref);
+                    finish_s_load();
+                    const bool ok0 = !__any_sync(0xffffffffu, valid && !(rs0 <= kFastSumLimit));
+                    if (!(ok = wait_prev_pv())) break;
+                    if (ok0) {
+                        tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
+                        stored0 = true;
+                    }
+                    if (!full) mask_half(H1{});
+                    const float rs1 = exps_half(H1{}, m_ref);
+                    const bool ok1 = !__any_sync(0xffffffffu, valid && !(rs1 <= kFastSumLimit));
+                    if (ok0 && ok1) {
+                        rs = rs0 + rs1;
+                        tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+                    } else {
+                        slow = true;
+                    }
                 } else {
-                    slow = true;
-                }
-            } else {
-                finish_s_load();
-                if (!full) {
-                    mask_half(H0{});
-                    mask_half(H1{});
-                }
-                if (!(ok = wait_prev_pv())) break;
-            }
-            if (slow) {
-                float mc[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const uint32_t* x = &s[k >> 1][(k & 1) * 16];
-                    float m = max3f(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
-#pragma unroll
-                    for (int i = 3; i < 15; i += 2) m = max3f(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-                    mc[k] = fmaxf(m, __uint_as_float(x[15]));
-                }
-                const float mx = max3f(max3f(mc[0], mc[1], mc[2]), max3f(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
-                const float m_new = fmaxf(m_ref, mx * sl2);
-                const bool resc = m_new > m_ref + kRescaleThreshold;
-                const float alpha = resc ? fast_exp2(m_ref - m_new) : 1.f;
-                if (resc) {
-                    l *= alpha;
-                    m_ref = m_new;
-                }
-                const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                rs = exps_half(H0{}, m_use) + exps_half(H1{}, m_use);
-                if (it > 0 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-                    for (int ch = 0; ch < D / 32; ++ch) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + ch * 32, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + ch * 32, o);
+                    finish_s_load();
+                    if (!full) {
+                        mask_half(H0{});
+                        mask_half(H1{});
                     }
+                    if (!(ok = wait_prev_pv())) break;
                 }
-                if (stored0) tmem_st_wait();  // the first half's earlier store lands before its rewrite
-                tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
-                tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+                if (slow) {
+                    float mc[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint32_t* x = &s[k >> 1][(k & 1) * 16];
+                        float m = max3f(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+#pragma unroll
+                        for (int i = 3; i < 15; i += 2) m = max3f(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                        mc[k] = fmaxf(m, __uint_as_float(x[15]));
+                    }
+                    const float mx = max3f(max3f(mc[0], mc[1], mc[2]), max3f(mc[3], mc[4], mc[5]), fmaxf(mc[6], mc[7]));
+                    const float m_new = fmaxf(m_ref, mx * sl2);
+                    const bool resc = m_new > m_ref + kRescaleThreshold;
+                    const float alpha = resc ? fast_exp2(m_ref - m_new) : 1.f;
+                    if (resc) {
+                        l *= alpha;
+                        m_ref = m_new;
+                    }
+                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                    rs = exps_half(H0{}, m_use) + exps_half(H1{}, m_use);
+                    if (it > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + ch * 32, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                            tmem_st32(tO + ch * 32, o);
+                        }
+                    }
+                    if (stored0) tmem_st_wait();  // the first half's earlier store lands before its rewrite
+                    tmem_st32(tP, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
+                    tmem_st32(tP + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
+                }
+                l += rs;
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(&S.p_full);
             }
-            l += rs;
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&S.p_full);
-        }
 
-        // -------------------------------------------------------------- epilogue
-        if (ok) ok = mbar_wait(&S.o_done, (n - 1) & 1, abort);
-        if (!group_all(ok)) break;
-        tc_fence_after();
-        const bool direct = c.whole();
-        // Direct output: the sink joins the sum, and the row is normalised.
-        float f = 1.f, lse_v = 0.f;
-        if (direct) {
-            const float m = l != 0.f ? m_ref : -INFINITY;
-            const float M = fmaxf(m, sg);
-            if (M == INFINITY || M == -INFINITY) {
-                f = 0.f;
-                lse_v = M;
-            } else {
-                f = l != 0.f ? fast_exp2(m - M) : 0.f;
-                const float Z = l * f + fast_exp2(sg - M);
-                f = l != 0.f ? f / Z : 0.f;
-                lse_v = (M + log2f(Z)) * ATTN_LN2;
+            // -------------------------------------------------------------- epilogue
+            if (ok) ok = mbar_wait(&S.o_done, (n - 1) & 1, abort);
+            if (!group_all(ok)) break;
+            tc_fence_after();
+            const bool direct = c.whole();
+            // Direct output: the sink joins the sum, and the row is normalised.
+            float f = 1.f, lse_v = 0.f;
+            if (direct) {
+                const float m = l != 0.f ? m_ref : -INFINITY;
+                const float M = fmaxf(m, sg);
+                if (M == INFINITY || M == -INFINITY) {
+                    f = 0.f;
+                    lse_v = M;
+                } else {
+                    f = l != 0.f ? fast_exp2(m - M) : 0.f;
+                    const float Z = l * f + fast_exp2(sg - M);
+                    f = l != 0.f ? f / Z : 0.f;
+                    lse_v = (M + log2f(Z)) * ATTN_LN2;
+                }
             }
-        }
-        const int row = q_start + node;
-        // a run's first segment has the first place, any other the second
-        const size_t part = (((size_t)gang * p.hkv + kvh) * 2 + (segs > 0)) * BM + r;
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)row * p.hq + h) * D);
-        float4* pdst = reinterpret_cast<float4*>(p.part_o + part * D);
-        uint32_t* const v_bad = S.v_bad[segs % kBadRing];
-        const bool any_bad = drafts && __any_sync(0xffffffffu, lane < kMaxNodes / 32 && v_bad[lane] != 0);
+            const int row = q_start + node;
+            // a run's first segment has the first place, any other the second
+            const size_t part = (((size_t)gang * p.hkv + kvh) * 2 + (segs > 0)) * BM + r;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)row * p.hq + h) * D);
+            float4* pdst = reinterpret_cast<float4*>(p.part_o + part * D);
+            uint32_t* const v_bad = S.v_bad[segs % kBadRing];
+            const bool any_bad = __any_sync(0xffffffffu, lane < 2 * kMaxNodes / 32 && v_bad[lane] != 0);
 #pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-            float u[32];
-            uint32_t raw[32];
-            tmem_ld32(tO + ch * 32, raw);
-            tmem_ld_wait();
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float u[32];
+                uint32_t raw[32];
+                tmem_ld32(tO + ch * 32, raw);
+                tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = l != 0.f ? __uint_as_float(raw[i]) : 0.f;
-            if (valid && any_bad) {
-                // Infinities and NaNs of drafted tokens' V that this row sees.
-                int at = pos;
-                for (int a = node + 1; a > 0; a = up(a), --at) {
-                    const int t = P + a - 1;
-                    if (!(v_bad[(a - 1) >> 5] >> ((a - 1) & 31) & 1u)) continue;
-                    if (p.win_last > 0 && at >= p.win_first && at <= pos - p.win_last) continue;
-                    const int pg = pages[t >> p.page_shift];
-                    const size_t sl = ((size_t)pg << p.page_shift) | (t & ((1 << p.page_shift) - 1));
-                    const __nv_bfloat16* v = p.v_cache + (sl * p.hkv + kvh) * D + ch * 32;
+                for (int i = 0; i < 32; ++i) u[i] = l != 0.f ? __uint_as_float(raw[i]) : 0.f;
+                if (valid && any_bad) {
+                    // Infinities and NaNs in V of tokens that this row sees.
+                    auto add = [&](int t) {
+                        const int pg = pages[t >> p.page_shift];
+                        const size_t sl = ((size_t)pg << p.page_shift) | (t & ((1 << p.page_shift) - 1));
+                        const __nv_bfloat16* v = p.v_cache + (sl * p.hkv + kvh) * D + ch * 32;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float x = __bfloat162float(v[i]);
-                        if (!(fabsf(x) < INFINITY)) u[i] += x;
+                        for (int i = 0; i < 32; ++i) {
+                            const float x = __bfloat162float(v[i]);
+                            if (!(fabsf(x) < INFINITY)) u[i] += x;
+                        }
+                    };
+                    int at = pos;
+                    for (int a = node + 1; a > 0; a = up(a), --at)
+                        if ((v_bad[(a - 1) >> 5] >> ((a - 1) & 31) & 1u) &&
+                            (p.win_last <= 0 || at < p.win_first || at > pos - p.win_last))
+                            add(P + a - 1);
+                    const int some0 = some_first(p, c.rq);
+                    for (int i = max(0, pos + 1 - p.win_last - some0); p.win_last > 0 && i < kMaxNodes; ++i)
+                        if (v_bad[(kMaxNodes + i) >> 5] >> (i & 31) & 1u) add(some0 + i);
+                }
+                if (valid && direct) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint4 wv;
+                        wv.x = pack_bf16x2(u[8 * q + 0] * f, u[8 * q + 1] * f);
+                        wv.y = pack_bf16x2(u[8 * q + 2] * f, u[8 * q + 3] * f);
+                        wv.z = pack_bf16x2(u[8 * q + 4] * f, u[8 * q + 5] * f);
+                        wv.w = pack_bf16x2(u[8 * q + 6] * f, u[8 * q + 7] * f);
+                        dst[ch * 4 + q] = wv;
                     }
+                } else if (valid) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        pdst[ch * 8 + q] = make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
                 }
             }
-            if (valid && direct) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint4 wv;
-                    wv.x = pack_bf16x2(u[8 * q + 0] * f, u[8 * q + 1] * f);
-                    wv.y = pack_bf16x2(u[8 * q + 2] * f, u[8 * q + 3] * f);
-                    wv.z = pack_bf16x2(u[8 * q + 4] * f, u[8 * q + 5] * f);
-                    wv.w = pack_bf16x2(u[8 * q + 6] * f, u[8 * q + 7] * f);
-                    dst[ch * 4 + q] = wv;
-                }
-            } else if (valid) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    pdst[ch * 8 + q] = make_float4(u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+            if (valid && direct && p.lse) p.lse[(size_t)h * p.total_q + row] = lse_v;
+            if (valid && !direct) p.part_ml[part] = make_float2(l != 0.f ? m_ref : -INFINITY, l);
+            if (any_bad) {  // the place is free for a later segment
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (r < 2 * kMaxNodes / 32) v_bad[r] = 0;
             }
-        }
-        if (valid && direct && p.lse) p.lse[(size_t)h * p.total_q + row] = lse_v;
-        if (valid && !direct) p.part_ml[part] = make_float2(l != 0.f ? m_ref : -INFINITY, l);
-        if (any_bad) {  // the place is free for a later segment
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            if (r < kMaxNodes / 32) v_bad[r] = 0;
-        }
-        tc_fence_before();  // O has been read: the next segment's P V may overwrite it
-        ++segs;
-        left -= ntiles;
+            tc_fence_before();  // O has been read: the next segment's P V may overwrite it
+            ++segs;
+            left -= ntiles;
         }
     }
 

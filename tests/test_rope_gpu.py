@@ -45,7 +45,7 @@ def rows(T, hq, hkv, d, seed=0):
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("T,hq,hkv,d,r", [(1, 1, 1, 64, 64), (37, 8, 2, 64, 64), (5, 12, 12, 64, 18), (9, 3, 1, 64, 2),
                                           (300, 6, 2, 128, 128), (7, 5, 5, 128, 34), (2, 64, 8, 128, 114),
-                                          (33, 40, 2, 128, 64), (3000, 4, 1, 64, 48)])
+                                          (33, 40, 2, 128, 64), (3000, 4, 1, 64, 48), (9, 700, 301, 64, 64)])
 def test_rope_matches_definition(ext, T, hq, hkv, d, r, interleaved):
     q, k = rows(T, hq, hkv, d)
     g = torch.Generator().manual_seed(1)
@@ -208,6 +208,26 @@ def test_rope_append_skips_bad_rows(ext):
     assert status & ext._lib.DEV_SEQLEN_OOB
     kc, status = call(table, sl, [3, 3, 3], 3, total=7)  # cu_new says 9 rows, the tensors hold 7
     assert status == ext._lib.DEV_SEQLEN_OOB
+
+
+def test_rope_training_step_in_a_graph(ext):
+    """Forward and gradient captured together, replayed on new gradients."""
+    q, k = (x.cuda().requires_grad_() for x in rows(50, 4, 2, 64, seed=14))
+    dq, dk = (x.cuda() for x in rows(50, 4, 2, 64, seed=15))
+    pos, (f, m) = torch.arange(50).int().cuda(), ext.attn_sink_rope_freqs(64)
+    torch.autograd.grad(ext.attn_sink_rope_func(q, k, pos, f), (q, k), (dq, dk))  # no eager graph stays alive
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = ext.attn_sink_rope_func(q, k, pos, f)
+        got = torch.autograd.grad(y, (q, k), (dq, dk))
+    dq.mul_(2.0)
+    g.replay()
+    torch.cuda.synchronize()
+    want = ext.attn_sink_rope(dq, dk, pos, f, inverse=True)
+    assert same(got[0], want[0]) and same(got[1], want[1])
+    want = ext.attn_sink_rope(q.detach(), k.detach(), pos, f)
+    assert same(y[0].detach(), want[0]) and same(y[1].detach(), want[1])
 
 
 def test_rope_in_a_graph_and_on_another_stream(ext):

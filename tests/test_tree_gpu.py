@@ -115,6 +115,23 @@ def test_many_requests_and_no_nodes(ext):
     assert run(ext, x)[0].shape == (0, 8, 64)
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(160, 160, 128), (320, 320, 64), (301, 301, 64)])
+def test_more_kv_heads_than_resident_blocks(ext, hq, hkv, d):
+    x = make([140, 20], [3, 2], hq, hkv, d, 16, seed=17)
+    out, lse = run(ext, x)
+    check(x, out, lse)
+
+
+def test_more_requests_than_threads(ext):
+    """The shares of the batch are found 256 requests at a time."""
+    g = torch.Generator().manual_seed(6)
+    prefix = torch.randint(0, 200, (600,), generator=g).tolist()
+    nodes = [n if b % 7 else 0 for b, n in enumerate(torch.randint(0, 4, (600,), generator=g).tolist())]
+    x = make(prefix, nodes, 4, 1, 64, 16, seed=18)
+    out, lse = run(ext, x)
+    check(x, out, lse)
+
+
 def test_a_chain_equals_the_paged_forward(ext):
     x = make([700, 33], [60, 130], 16, 2, 64, 16, kind="chain")
     for first, last in ((0, 0), (20, 100)):
@@ -186,6 +203,9 @@ def test_infinities_and_nans_reach_only_who_sees_them(ext, d, page):
     v = x["v"].view(-1, 2, d)
     at = [int(co.slot(x["table"][0].numpy(), page, 300 + i)) for i in range(nodes)]
     v[at[5], 0, 3], v[at[7], 1, 60], v[at[9], 0, 3] = float("inf"), float("nan"), float("-inf")
+    # a prefix token that the window shows to nodes of depth 0 and 1 only
+    v[int(co.slot(x["table"][0].numpy(), page, 182)), 0, 40] = float("inf")
+    assert 0 < seen[:, 182].sum() < nodes
     out, lse = run(ext, x, first, last)
     assert same(lse, want_lse)
     for i in range(nodes):
@@ -195,6 +215,8 @@ def test_infinities_and_nans_reach_only_who_sees_them(ext, d, page):
                 row[3] = float("inf")
             if h < 4 and seen[i, 309]:
                 row[3] = float("nan") if seen[i, 305] else float("-inf")
+            if h < 4 and seen[i, 182]:
+                row[40] = float("inf")
             if h >= 4 and seen[i, 307]:
                 row[60] = float("nan")
             assert torch.equal(row.isnan(), out[i, h].isnan()), (i, h)
