@@ -543,6 +543,24 @@ def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0,
     return q_out, k_out
 
 
+def rope_checked(q, k, positions, inv_freq, interleaved, attn_scale, inverse):
+    """attn_sink_rope for contiguous q and k (or None) whose forward call has passed its
+    checks: the backward's call, which runs on autograd's thread, where the
+    interpreter's time counts most."""
+    T, hq, d = q.shape
+    q_out = torch.empty_like(q)
+    kp = kop = k_out = None
+    hkv = 0
+    if k is not None:
+        k_out = torch.empty_like(k)
+        hkv = k.shape[1]
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    _run("attn_sink_rope", q.get_device(), None, q.data_ptr(), q_out.data_ptr(), kp, kop, 0, 0, 0, 0,
+         positions.data_ptr(), inv_freq.data_ptr(), T, hq, hkv, d, 2 * inv_freq.shape[0], 1 if interleaved else 0,
+         1 if inverse else 0, attn_scale)
+    return q_out, k_out
+
+
 def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seqlens, inv_freq, cu_new=None,
                              max_new=None, positions=None, interleaved=False, attn_scale=1.0, q_out=None,
                              stream=None):

@@ -103,23 +103,20 @@ class _AttnSinkRope(torch.autograd.Function):
     def backward(ctx, dq, dk=None):
         positions, inv_freq = ctx.saved_tensors
         interleaved, attn_scale, inverse = ctx.args
-        args = (positions, inv_freq, interleaved, attn_scale, not inverse)
         need_q, need_k = ctx.needs_input_grad[:2]
         dq = dq.contiguous() if need_q and dq is not None else None
         dk = dk.contiguous() if need_k and dk is not None else None
+        if dq is None and dk is None:
+            return None, None, None, None, None, None, None
+        first, second = (dq, dk) if dq is not None else (dk, None)
         if torch.is_grad_enabled():  # create_graph
-            rotate = _AttnSinkRope.apply
+            got = _AttnSinkRope.apply(first, second, positions, inv_freq, interleaved, attn_scale, not inverse)
+            first, second = (got, None) if second is None else got
         else:
-            def rotate(*x):
-                a, b = _lib.attn_sink_rope(*x)
-                return a if b is None else (a, b)
-        if dq is not None and dk is not None:
-            dq, dk = rotate(dq, dk, *args)
-        elif dq is not None:
-            dq = rotate(dq, None, *args)
-        elif dk is not None:
-            dk = rotate(dk, None, *args)
-        return dq, dk, None, None, None, None, None
+            first, second = _lib.rope_checked(first, second, positions, inv_freq, interleaved, attn_scale, not inverse)
+        if dq is None:
+            first, second = None, first
+        return first, second, None, None, None, None, None
 
 
 def attn_sink_rope_func(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0):
