@@ -410,14 +410,15 @@ int attn_sink_rope_kv_append(const attn_bf16* q, attn_bf16* q_out, const attn_bf
  *                any other value is read as -1 and sets ATTN_SINK_DEV_TREE
  *   max_seqlen_q host upper bound of n, at most 256.  Rows of a request past it
  *                are left alone and set ATTN_SINK_DEV_SEQLEN_OOB.
- *   max_seqlen_k host estimate of the largest seqlens_k: plans the split of the
- *                keys over the GPU only (results do not depend on it but for rounding)
+ *   max_seqlen_k host bound of seqlens_k, as attn_sink_fwd_paged takes it; at present
+ *                only checked (>= 0): the keys are split by the lengths on the device
  *   out          (total_q, hq, head_dim) bf16
  *   lse          (hq, total_q) fp32, as in attn_sink_fwd; may be NULL
  * A request with fewer cached tokens than nodes sees no key (out 0, lse the
  * sink) and sets ATTN_SINK_DEV_SEQLEN_OOB.  Keys read through an out-of-range
  * page id take no weight.  Rows of out and lse behind the last request's are
- * left as they were.  Cache slots that a request does not own never reach its results.
+ * left as they were.  Cache slots that a request does not own never reach its results,
+ * and a cached token's infinities and NaNs only the nodes that see it.
  * Supported: head_dim 64 or 128; hq % hkv == 0, hq / hkv <= 128; page_size a
  * power of two >= 8.  No gradient.
  */
@@ -460,9 +461,11 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
  *   weights  (batch, weight_heads, weight_cap) fp32 device, updated in place; the
  *            caller sets new tokens' entries to 0 before their first call.  Tokens
  *            t >= weight_cap are left out and set ATTN_SINK_DEV_SEQLEN_OOB.
- * The sums have a fixed order (no atomics).  Scratch: 4 bytes per query head and
- * token that the page table can hold (or the window can show), and request.
- * Everything else as in attn_sink_decode_paged; hq at most 4096.
+ * The sums have a fixed order (no atomics).  Scratch: 4 bytes per query head (those
+ * of a KV head rounded up to 8, or to 16 above 8), request and token that the page
+ * table can hold (or the window can show).  Everything else as in
+ * attn_sink_decode_paged; hq at most 4096, and with weight_heads == 1 at most 6144
+ * query heads rounded up like that.
  */
 int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
                                    const int32_t* page_table, int max_pages, const int32_t* seqlens,

@@ -600,10 +600,15 @@ int check_rope(const char* who, int rows, int hq, int hkv, int min_hkv, long lon
 int check_cache(const char* who, int batch, int max_pages, int page_size, int num_pages) {
     if (batch < 0 || max_pages <= 0 || page_size <= 0 || num_pages <= 0)
         return fail(ATTN_SINK_ERR_INVALID, "%s: sizes must be positive (batch may be 0)", who);
-    if ((long long)num_pages * page_size >= (1LL << 31) || (long long)max_pages * page_size >= (1LL << 31))
-        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: cache slots must fit in int32", who);
+    // A request's tokens stay so far below 2^31 that the end of a tile or batch of them does not wrap.
+    if ((long long)num_pages * page_size >= (1LL << 31) || (long long)max_pages * page_size > (1LL << 31) - 65536)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: cache slots must fit in int32, a request's stay 65536 below", who);
     return ATTN_SINK_OK;
 }
+
+// Query heads (of every KV head rounded up to 8, or to 16 above 8) whose statistics a
+// block of the weights' accumulation keeps in 48 KB of shared memory.
+constexpr int kMaxWeightHeads = 6144;
 
 // Heads of the entry points that move cache rows.
 int check_moves(const char* who, const char* name, int heads, int hkv, int head_dim) {
@@ -809,7 +814,6 @@ int attn_sink_tree_paged(const attn_bf16* q, const attn_bf16* k_cache, const att
     a.page_size = page_size;
     a.num_pages = num_pages;
     a.max_seqlen_q = max_seqlen_q;
-    a.max_seqlen_k = max_seqlen_k;
     a.win_first = win_first;
     a.win_last = win_last;
     a.scale = attn::resolve_scale(scale, head_dim);
@@ -829,7 +833,8 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
                          const int32_t* src, const int32_t* counts, const int32_t* base, int batch, int src_heads,
                          int max_rows, int hkv, int head_dim, int page_size, int num_pages, void* stream) {
     t_last_error.clear();
-    if (hkv <= 0 || max_rows < 0) return fail(ATTN_SINK_ERR_INVALID, "kv_compact: sizes must be non-negative (heads positive)");
+    if (hkv <= 0 || max_rows < 0)
+        return fail(ATTN_SINK_ERR_INVALID, "kv_compact: sizes must be non-negative (heads positive)");
     int rc = check_cache("kv_compact", batch, max_pages, page_size, num_pages);
     if (rc != ATTN_SINK_OK) return rc;
     if ((rc = check_moves("kv_compact", "src_heads", src_heads, hkv, head_dim)) != ATTN_SINK_OK) return rc;
@@ -873,6 +878,10 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
         return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_heads %d must be 1 or hkv", weight_heads);
     if (weight_cap < 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_cap must be >= 0");
     if (hq > 4096) return fail(ATTN_SINK_ERR_UNSUPPORTED, "decode_weights: hq %d above 4096", hq);
+    const int group = hq / hkv, padded = group <= 8 ? 8 : (group + 15) / 16 * 16;
+    if ((long long)(hkv / weight_heads) * padded > kMaxWeightHeads)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "decode_weights: weight_heads 1 sums at most %d padded query heads",
+                    kMaxWeightHeads);
     if (batch == 0) return ATTN_SINK_OK;
     if (!weights && weight_cap > 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: NULL weights");
     attn::decode::Weights w = {};

@@ -106,7 +106,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs p,
     const int n = min(L, p.budget);
     if (tid == 0 && part == 0 && head == 0) p.new_seqlens[b] = n;
     if (L <= p.budget) {  // the same for the whole cluster
-        for (int t = part * kSelThreads + tid; t < p.budget; t += parts * kSelThreads) kept[t] = t < L ? t : -1;
+        for (uint32_t t = part * kSelThreads + tid; t < (uint32_t)p.budget; t += parts * kSelThreads)
+            kept[t] = t < (uint32_t)L ? (int)t : -1;
         if (tid == 0 && part == 0) p.first_moved[at] = n;
         return;
     }
@@ -123,7 +124,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs p,
         r0 = a0 + round * kRound;
         len = min(kRound, a1 - r0);
         for (int k = tid; k < len; k += kSelThreads)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(keys + k)), "l"(w + r0 + k) : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(keys + k)), "l"(w + r0 + k)
+                         : "memory");
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 4
         for (int k = tid; k < len; k += kSelThreads) {
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs p,
                         x[q] = q < parts ? *reinterpret_cast<const uint4*>(cl.map_shared_rank(h, q) + d0 - 3)
                                          : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int q = 0; q < kMaxCluster; ++q) c[0] += x[q].w, c[1] += x[q].z, c[2] += x[q].y, c[3] += x[q].x;
+                    for (int q = 0; q < kMaxCluster; ++q)
+                        c[0] += x[q].w, c[1] += x[q].z, c[2] += x[q].y, c[3] += x[q].x;
                 }
             }
             if (pass == 0 && tid == 0) c[0] = 0;
@@ -297,7 +300,7 @@ __device__ __forceinline__ void move_weights(const float* w, float* wo, const in
             if (j < n) wo[j] = x[i];
         }
     }
-    for (int t = n + (int)threadIdx.x; t < cap; t += kMoveThreads) wo[t] = 0.f;
+    for (uint32_t t = n + threadIdx.x; t < (uint32_t)cap; t += kMoveThreads) wo[t] = 0.f;
 }
 
 // It is bound by memory.  32 requests brought from 8k - 16k tokens to 4096 (8 KV heads
@@ -318,9 +321,10 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs p, in
     const int32_t* src = p.src + at * p.max_rows;
     int n = p.counts[b];
     const int base = p.base ? p.base[b] : 0;
-    if (n > p.max_rows || n < 0 || base < 0) {
+    const int tokens = p.max_pages * p.page_size;  // that the page table holds
+    if (n > p.max_rows || n < 0 || base < 0 || n > tokens - base) {
         if (tid == 0 && blockIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-        n = base < 0 ? 0 : max(0, min(n, p.max_rows));
+        n = base < 0 ? 0 : max(0, min(min(n, p.max_rows), tokens - base));
     }
     if (is_weights) {
         if (blockIdx.x == 0) move_weights(p.weights + at * p.cap, p.weights_out + at * p.cap, src, n, p.cap);
@@ -425,7 +429,8 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     // 8192 tokens do (2 us a digit).
     const long long cap = a.cap < a.token_cap ? a.cap : a.token_cap;
     int parts = 1;
-    while (parts < kMaxCluster && (long long)a.batch * a.heads * parts * 2 <= 152 && cap / (2 * parts) >= 8192) parts *= 2;
+    while (parts < kMaxCluster && (long long)a.batch * a.heads * parts * 2 <= 152 && cap / (2 * parts) >= 8192)
+        parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.heads * parts), a.batch);
     cfg.blockDim = dim3(kSelThreads);

@@ -24,7 +24,7 @@ struct Args {
     const float* sink;
     void* out;
     float* lse;
-    int max_pages, batch, total_q, hq, hkv, head_dim, page_size, num_pages, max_seqlen_q, max_seqlen_k;
+    int max_pages, batch, total_q, hq, hkv, head_dim, page_size, num_pages, max_seqlen_q;
     int win_first, win_last;
     float scale;
 };

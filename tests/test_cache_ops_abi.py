@@ -88,6 +88,18 @@ def test_weights_refusals(lib, kw, rc, text):
     assert weights(lib, **kw) == rc and text in lib.attn_sink_last_error()
 
 
+@pytest.mark.parametrize("kw,rc,text", [
+    (dict(hq=1024, hkv=1024, heads=1), -2, b"6144"), (dict(hq=4000, hkv=400, heads=1), -2, b"6144"),
+    (dict(hq=4096, hkv=512, heads=1, w=None), -1, b"NULL")])
+def test_weights_refuse_more_heads_than_one_accumulator_sums(lib, kw, rc, text):
+    assert weights(lib, **kw) == rc and text in lib.attn_sink_last_error()
+
+
+def test_requests_that_reach_the_end_of_int32_are_refused(lib):
+    for call in (append, tree, compact):
+        assert call(lib, mp=(1 << 27) - 1) == -2 and b"int32" in lib.attn_sink_last_error()
+
+
 def evict(lib, kc=P, vc=Q, sl=P, batch=2, heads=1, cap=64, hkv=2, d=64, budget=16, first=1, last=2, new=Q, kept=P):
     return lib.attn_sink_evict_paged(kc, vc, P, 4, sl, P, batch, heads, cap, hkv, d, 16, 8, budget, first, last, P, kept,
                                      new, None)

@@ -113,6 +113,20 @@ def test_weights_with_bad_pages_infinite_sinks_and_a_short_accumulator(ext):
     assert status == ext._lib.DEV_PAGE_OOB and torch.all(w == 0)
 
 
+@pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (24, 2)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_weights_of_infinite_keys(ext, hq, hkv, shared):
+    # token 5's scores are -inf for every head: its weight is 0, and the others sum to 1 per head
+    k, v, table, sl = paged([40], hkv, 64, 16, seed=8)
+    q = torch.rand(1, hq, 64, generator=torch.Generator().manual_seed(6)).bfloat16() + 0.5
+    k.view(-1, hkv, 64)[co.slot(table[0].numpy(), 16, np.array([5]))] = float("-inf")
+    w = torch.zeros(1, 1 if shared else hkv, 40, device="cuda")
+    ext.attn_sink_decode_paged_weights(q.cuda(), k.cuda(), v.cuda(), table.cuda(), sl.cuda(), w)
+    w = w.cpu()
+    assert ext.device_status() == 0 and torch.all(w[:, :, 5] == 0)
+    np.testing.assert_allclose(w.sum(-1).numpy(), hq / w.shape[1], rtol=3e-4)
+
+
 # ---------------------------------------------------------------------------
 # Eviction.
 
@@ -285,6 +299,18 @@ def test_compact_skips_rows_out_of_order(ext):
     kc, status = call([[5, 6, 9], [1, 2, 3]], [9, -1])          # more rows than the list, fewer than none
     assert status == ext._lib.DEV_SEQLEN_OOB
     assert same(kc.view(-1, 2, 64)[one], k.view(-1, 2, 64)[one])
+
+
+def test_compact_refuses_destinations_past_the_page_table(ext):
+    k, v, table, sl = paged([64], 2, 64, 16, seed=12)
+    tokens = table.shape[1] * 16
+    src = torch.tensor([[1, 2, 3, 4]]).int().cuda()
+    ext.device_status()
+    for base in (tokens, 2 ** 31 - 3, 2 ** 31 - 1, -1):
+        kc, vc = k.cuda(), v.cuda()
+        ext.attn_sink_kv_compact(kc, vc, table.cuda(), src, torch.tensor([4]).int().cuda(), torch.tensor([base]).int().cuda())
+        assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
+        assert same(kc.cpu(), k) and same(vc.cpu(), v)
 
 
 def test_evict_and_weights_in_a_graph(ext):
