@@ -87,6 +87,12 @@ class _AttnSinkVarlenKVPacked(torch.autograd.Function):
         return dq, dkv, dsink, None, None, None, None, None, None, None, None
 
 
+def _aligned_rows(t):
+    """t contiguous and 16-byte aligned (a gradient may be a piece of a flat buffer)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _AttnSinkRope(torch.autograd.Function):
     """Its backward is the same function by the negative angle, so gradients of
     gradients work too."""
@@ -104,8 +110,8 @@ class _AttnSinkRope(torch.autograd.Function):
         positions, inv_freq = ctx.saved_tensors
         interleaved, attn_scale, inverse = ctx.args
         need_q, need_k = ctx.needs_input_grad[:2]
-        dq = dq.contiguous() if need_q and dq is not None else None
-        dk = dk.contiguous() if need_k and dk is not None else None
+        dq = _aligned_rows(dq) if need_q and dq is not None else None
+        dk = _aligned_rows(dk) if need_k and dk is not None else None
         if dq is None and dk is None:
             return None, None, None, None, None, None, None
         first, second = (dq, dk) if dq is not None else (dk, None)

@@ -127,6 +127,21 @@ def test_rope_gradient(ext, interleaved):
     assert np.all(np.abs(co.to_np(g1) - want.sum(0, keepdims=True)) <= 2.0 ** -7 * np.abs(want).sum(0, keepdims=True))
 
 
+@pytest.mark.parametrize("ahead", [1, 8])
+def test_rope_gradient_from_a_flat_buffer(ext, ahead):
+    # the gradient is a piece of a flat buffer, aligned to 2 bytes or to 16
+    q, _ = rows(9, 3, 1, 64, seed=6)
+    dq, _ = rows(9, 3, 1, 64, seed=7)
+    pos = torch.arange(9).int()
+    f, _ = ext.attn_sink_rope_freqs(64)
+    ql = q.cuda().requires_grad_()
+    y = ext.attn_sink_rope_func(ql, None, pos.cuda(), f)
+    other = torch.zeros(ahead, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    flat = torch.cat([other, y.reshape(-1)])
+    flat.backward(torch.cat([torch.zeros(ahead).bfloat16(), dq.reshape(-1)]).cuda())
+    check(ql.grad, dq, pos, f, False, inverse=True)
+
+
 def test_rope_gradient_of_the_gradient(ext):
     q, k = rows(6, 2, 1, 64, seed=6)
     pos, (f, _) = torch.arange(6).int().cuda(), ext.attn_sink_rope_freqs(64)
