@@ -874,6 +874,7 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
     int rc = attn::validate_decode("decode_weights", q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq,
                                    hkv, head_dim, page_size, num_pages, win_first, out);
     if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_cache("decode_weights", batch, max_pages, page_size, num_pages)) != ATTN_SINK_OK) return rc;
     if (weight_heads != 1 && weight_heads != hkv)
         return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_heads %d must be 1 or hkv", weight_heads);
     if (weight_cap < 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_cap must be >= 0");

@@ -44,15 +44,19 @@
 //   * At d 128 (one row tile a request) the cache's reads.  32 requests of 8 to 32 nodes, 32
 //     heads over 8, 1024 + 7168 tokens visible: 190 - 197 us, 5.5 - 5.7 TB/s.  (One CTA per
 //     (request, row tile, KV head, range of keys), dispatched by the hardware: 222 us.)
-//   * At d 64 with full tiles the softmax: 128 x 128 exponentials a step, two CTAs an SM,
-//     1.175 us a step, 1086 TFLOP/s.  16 requests of 1k to 16k tokens and 16 to 64
-//     nodes, 64 heads over 8, take 139 - 143 us: of the tiles' rows 81 % hold a node; about
-//     12 us are the start, the last tile's latency and the merge; without the runs 163 us.
-//   * One request: latency.  7 nodes over 2000 tokens 14.3 us.
-// With plain fp32 arithmetic, a CTA per node and KV head, the first two took 19.7 and 21.8 ms.
+//   * At d 64 with several row tiles a request the slowest CTA.  16 requests of 1k to 16k
+//     tokens and 16 to 64 nodes, 64 heads over 8: 137 - 140 us for 87 steps a CTA.  The
+//     first S is ready after 7 us, a step takes 1.2 us (two CTAs an SM; 1.1 to 1.5, as an
+//     SM's two softmax phases fall together or apart; 1086 TFLOP/s at 1.175 us), the
+//     median CTA ends 10 us before the last, the merge takes 4.5 us.  Each row tile reads
+//     K and V for itself, 777 MB from HBM for 301 MB, and 81 % of the tiles' rows hold a node.
+//   * One request: latency.  7 nodes over 2000 tokens 13.7 us: first S after 3.7 us, two
+//     steps and the epilogue 4.5, the merge 3.
+// With plain fp32 arithmetic, a CTA per node and KV head, the first two took 19.7 and 21.8
+// ms; without the runs the second 163 us.
 // Measured and left out: runs cut into rounds of shorter ones (slower), two gangs in
-// lockstep on neighbouring row tiles (two row tiles a request at d 128 168 us against
-// 178, everything else 3 - 8 % slower).
+// lockstep on neighbouring row tiles (465 MB instead of 777 in the second case, but no
+// faster: the slowest CTA stays), tensor memory allocated before the runs are known.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
@@ -103,7 +107,7 @@ struct Params {
     float* part_o;       // (runs, hkv, 2, 128, D) fp32, un-normalised
     float2* part_ml;     // (runs, hkv, 2, 128): (reference in log2 units, sum)
     long long* first;    // (batch + 1): steps before each request; then the steps per run
-    int batch, max_pages, page_shift, seg_shift, num_pages;
+    int gangs, batch, max_pages, page_shift, seg_shift, num_pages;
     int hq, hkv, group, total_q, max_q;
     int npt;  // nodes per row tile
     int win_first, win_last;
@@ -145,6 +149,11 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
 }
 
 __device__ __forceinline__ long long steps_of(const Request& r) { return (long long)r.mtiles * r.ntiles; }
+
+// Steps of each gang's run.
+__device__ __forceinline__ long long run_steps(long long total, int gangs) {
+    return max((long long)kMinSteps, (total + gangs - 1) / gangs);
+}
 
 // Prefix tokens [first, end) that nodes on the prefix see as part of the last window
 // and the deepest possible node does not (at most kMaxNodes - 1 of them).
@@ -276,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = blockIdx.x % p.hkv, gang = blockIdx.x / p.hkv, gangs = gridDim.x / p.hkv;
+    const int kvh = blockIdx.x % p.hkv, gang = blockIdx.x / p.hkv;
     if (threadIdx.x == 0) {
         mbar_init(&S.q_full, 1);
         mbar_init(&S.q_empty, 1);
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         scan(i0, blockIdx.x == 0);
         total += sum_steps;
     }
-    const long long per_run = max((long long)kMinSteps, (total + gangs - 1) / gangs);
+    const long long per_run = run_steps(total, p.gangs);
     const long long w0 = gang * per_run;
     if (blockIdx.x != 0 && w0 >= total) return;
     long long before = 0;
@@ -857,58 +866,81 @@ __global__ void __launch_bounds__(kThreads, 2)
 // per node and kRows query heads of a KV head, whose partial rows are neighbours; lane
 // = D / 32 dimensions.  Eight rows a warp keep as many loads in flight; with few rows
 // (a wave of warps holds them) a warp has one, and its segments' loads overlap.
+// It is bound by latency: one pass loads statistics and partials together, and with few
+// rows the place of the partials is worked out while the tree kernel still runs (with
+// many, most blocks start when it has ended, and read it).  Two passes, with the place
+// read: 7 nodes over 2000 tokens 14.4 us instead of 13.6, 64 nodes over 8000 30.1
+// instead of 27.8, 16 requests of 16 nodes 67.9 instead of 65.0.
 constexpr int kCombineWarps = 8;
 
 template <int D, int kRows>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const Params p) {
     constexpr int V = D / 32;
     using Vec = typename std::conditional<V == 2, float2, float4>::type;
-    const int lane = threadIdx.x & 31, b = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, b = blockIdx.y;
     const int blocks = (p.group + kRows - 1) / kRows;  // of a KV head's query heads
-    const int idx = blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+    const int idx = blockIdx.x * kCombineWarps + (tid >> 5);
     const int node = idx / (p.hkv * blocks), kvh = idx / blocks % p.hkv, g0 = idx % blocks * kRows;
     const Request rq = request(p, b, false);
+    long long before = 0, per_run = 0;  // steps of the requests before this one; of a run
+    const bool early = kRows == 1 && p.batch <= kCombineWarps * 32;
+    if (early) {
+        __shared__ long long sums[kCombineWarps][2];
+        long long steps = tid < p.batch ? steps_of(request(p, tid, false)) : 0, earlier = tid < b ? steps : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            steps += __shfl_xor_sync(0xffffffffu, steps, o);
+            earlier += __shfl_xor_sync(0xffffffffu, earlier, o);
+        }
+        if (lane == 0) sums[tid >> 5][0] = steps, sums[tid >> 5][1] = earlier;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kCombineWarps; ++w) per_run += sums[w][0], before += sums[w][1];
+        per_run = run_steps(per_run, p.gangs);
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
+    if (!early) before = p.first[b], per_run = p.first[p.batch];
     if (node >= rq.rows) return;
     const int heads = min(kRows, p.group - g0), h0 = kvh * p.group + g0;
     const int mt = node / p.npt, r0 = (node - mt * p.npt) * p.group + g0;
     // The row tile's steps [u0, u1) lie in the runs c0 .. c1.
-    const long long per_run = p.first[p.batch];
-    const long long u0 = p.first[b] + (long long)mt * rq.ntiles, u1 = u0 + rq.ntiles;
+    const long long u0 = before + (long long)mt * rq.ntiles, u1 = u0 + rq.ntiles;
     const int c0 = (int)(u0 / per_run), c1 = rq.ntiles > 0 ? (int)((u1 - 1) / per_run) : c0 - 1;
     if (c0 == c1) return;  // one run had all of it and wrote the output
     // A run's first segment has the first place, any other the second.
     auto place = [&](int c) { return (((size_t)c * p.hkv + kvh) * 2 + (c == c0 && u0 > c * per_run)) * BM + r0; };
-    // Lane k of the first 8 keeps the statistics of row k.
+    // Lane k of the first 8 keeps the statistics of row k: the running reference and
+    // the sum relative to it, the sink's share included.  An infinite sink takes all.
     const bool has = lane < heads;
     const float sg = has && p.sink ? p.sink[h0 + lane] * ATTN_LOG2E : -INFINITY;
-    float M = sg;
-#pragma unroll 8
-    for (int c = c0; c <= c1; ++c)
-        if (has) M = fmaxf(M, p.part_ml[place(c) + lane].x);
-    const bool some = M != INFINITY && M != -INFINITY;
-    float Z = some ? fast_exp2(sg - M) : 1.f;
+    float M = sg, Z = sg == -INFINITY ? 0.f : 1.f;
     float o[kRows][V] = {};
-#pragma unroll(kRows == 1 ? 8 : 1)
+#pragma unroll(kRows == 1 ? 8 : 2)
     for (int c = c0; c <= c1; ++c) {
         const size_t at = place(c);
         const float2 x = has ? p.part_ml[at + lane] : make_float2(0.f, 0.f);
-        const float w = some && x.y != 0.f ? fast_exp2(x.x - M) : 0.f;  // 0: nothing seen in this segment
-        if (w != 0.f) Z += x.y * w;
         Vec u[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k)
             if (k < heads) u[k] = reinterpret_cast<const Vec*>(p.part_o + (at + k) * D)[lane];
+        float keep = 1.f, w = 0.f;  // factors of what there is and of this segment
+        if (x.y != 0.f && sg != INFINITY) {  // else nothing seen in this segment
+            const float m = fmaxf(M, x.x);
+            keep = Z != 0.f ? fast_exp2(M - m) : 0.f;
+            w = fast_exp2(x.x - m);
+            Z = Z * keep + x.y * w;
+            M = m;
+        }
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            const float f = __shfl_sync(0xffffffffu, w, k);
-            if (k >= heads || f == 0.f) continue;
+            const float fk = __shfl_sync(0xffffffffu, keep, k), fw = __shfl_sync(0xffffffffu, w, k);
+            if (k >= heads) continue;
             const float* v = reinterpret_cast<const float*>(&u[k]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) o[k][i] += v[i] * f;
+            for (int i = 0; i < V; ++i) o[k][i] = o[k][i] * fk + v[i] * fw;
         }
     }
-    const float inv = some ? 1.f / Z : 0.f;
+    const float inv = Z != 0.f && sg != INFINITY ? 1.f / Z : 0.f;
     const size_t row = (size_t)rq.q_start + node;
 #pragma unroll
     for (int k = 0; k < kRows; ++k) {
@@ -918,7 +950,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
 #pragma unroll
         for (int i = 0; i < V; i += 2) dst[i / 2] = f == 0.f ? 0u : pack_bf16x2(o[k][i] * f, o[k][i + 1] * f);
     }
-    if (has && p.lse) p.lse[(size_t)(h0 + lane) * p.total_q + row] = some ? (M + log2f(Z)) * ATTN_LN2 : M;
+    if (has && p.lse)
+        p.lse[(size_t)(h0 + lane) * p.total_q + row] = fabsf(M) == INFINITY ? M : (M + log2f(Z)) * ATTN_LN2;
 }
 
 // ---------------------------------------------------------------------------
@@ -986,6 +1019,7 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
     p.part_o = static_cast<float*>(scratch);
     p.part_ml = reinterpret_cast<float2*>(static_cast<char*>(scratch) + pl.part_o_bytes);
     p.first = reinterpret_cast<long long*>(static_cast<char*>(scratch) + pl.part_o_bytes + pl.part_ml_bytes);
+    p.gangs = pl.ctas / a.hkv;
     p.batch = a.batch;
     p.max_pages = a.max_pages;
     p.page_shift = 0;

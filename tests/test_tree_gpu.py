@@ -173,6 +173,24 @@ def test_large_scores(ext):
     assert np.all(np.abs(co.to_np(out) - O) <= 2.0 ** -8 * (A + np.abs(O)) + 2.1e-2 * A)
 
 
+def test_many_requests_of_one_node(ext):
+    """More requests than one block scans, of lengths that the runs cut anywhere."""
+    x = make([(37 * i) % 900 for i in range(300)], [1] * 300, 8, 1, 64, 16, seed=3)
+    out, lse = run(ext, x)
+    assert ext.device_status() == 0
+    check(x, out, lse)
+
+
+@pytest.mark.parametrize("prefix", [50, 2000])
+def test_infinite_scores_give_nan(ext, prefix):
+    """A visible token with a score of +inf leaves no finite softmax, however the keys are split."""
+    x = make([prefix], [5], 8, 2, 64, 16, seed=6)
+    x["q"] = x["q"].abs() + 0.5
+    x["k"].view(-1, 2, 64)[co.slot(x["table"][0].numpy(), 16, 20)] = float("inf")
+    out, lse = run(ext, x)
+    assert torch.all(torch.isnan(out)) and not torch.any(torch.isfinite(lse))
+
+
 def test_rows_of_other_requests_stay(ext):
     """Rows of out and lse behind the last request's keep what they held."""
     x = make([30], [5], 8, 2, 64, 16)
