@@ -204,6 +204,27 @@ def test_evict_matches_definition(ext, case, shared, in_place):
             assert same(got.cpu().view(-1, hkv, d)[rows], want.view(-1, hkv, d)[rows])
 
 
+@pytest.mark.parametrize("lens,budget,kind", [
+    ([200000, 150000], 70000, "random"),          # two rounds of keys in each CTA of a cluster
+    ([40000] + [50] * 79, 18000, "ties"),         # three rounds in one CTA
+    ([131073], 131072, "ties"), ([131073], 1, "random")])
+def test_evict_long_lists(ext, lens, budget, kind):
+    k, v, table, sl = paged(lens, 1, 64, 64, seed=budget)
+    first, last = (4, 1000) if budget > 1 else (0, 0)
+    w = weight_values(kind, (len(lens), 1, max(lens)), seed=2)
+    want_k, want_v, want_kept, want_w = evict_reference(k, v, table, lens, w, budget, first, last)
+    kc, vc, wc = k.cuda(), v.cuda(), w.cuda()
+    new, kept = ext.attn_sink_evict_paged(kc, vc, table.cuda(), sl.cuda(), wc, budget, first, last)
+    assert ext.device_status() == 0
+    assert torch.equal(new.cpu(), sl.clamp(max=budget)) and torch.equal(kept.cpu(), want_kept)
+    assert same(wc.cpu(), want_w)
+    kc, vc = kc.cpu(), vc.cpu()
+    for b, n in enumerate(lens):
+        rows = torch.from_numpy(co.slot(table[b].numpy(), 64, np.arange(min(n, budget))))
+        assert same(kc.view(-1, 64)[rows], want_k.view(-1, 64)[rows])
+        assert same(vc.view(-1, 64)[rows], want_v.view(-1, 64)[rows])
+
+
 def test_evict_refuses_nothing_it_documents(ext):
     """Lengths past the accumulator or the page table are cut there, with a status bit;
     pages of other requests stay as they were."""

@@ -185,3 +185,36 @@ def test_training_step_with_rotary_positions(ext):
         pair = np.concatenate([size[..., :32] + size[..., 32:]] * 2, -1)
         assert np.all(np.abs(co.to_np(got) - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -20 * pair)
     assert torch.all(torch.isfinite(gs)) and gs.abs().max() > 0
+
+
+def test_caches_whose_offsets_pass_32_bits(ext):
+    """The same calls on a small cache and on the same pages at the end of one of 2.4e9
+    elements give the same bits."""
+    from cache_ops import paged, same
+    k, v, table, sl = paged([700, 90], 8, 64, 16, seed=31)
+    pool, far = k.shape[0], 290000
+    g = torch.Generator().manual_seed(32)
+    q, nk, nv = (torch.randn(8, h, 64, generator=g).bfloat16().cuda() for h in (64, 8, 8))
+    cu_new, parents = cu([5, 3]).cuda(), torch.tensor([-1, 0, 0, 1, -1, -1, 0, 1]).int().cuda()
+    freqs, _ = ext.attn_sink_rope_freqs(64)
+    got = []
+    for at in (0, far):
+        kc, vc = (torch.empty(at + pool, 16, 8, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        kc[at:], vc[at:] = k.cuda(), v.cuda()
+        tc, n = (table + at * (table >= 0).int()).cuda(), sl.cuda()
+        qr = ext.attn_sink_rope_kv_append(q, nk, nv, kc, vc, tc, n, freqs, cu_new=cu_new, max_new=5)
+        out, lse = ext.attn_sink_tree_paged(qr, kc, vc, tc, cu_new, n, parents, 5, 700)
+        keep = torch.tensor([[0, 2, 4], [1, 2, 0]]).int().cuda() + (n - torch.tensor([5, 3], device="cuda").int())[:, None]
+        counts = torch.tensor([3, 2]).int().cuda()
+        ext.attn_sink_kv_compact(kc, vc, tc, keep, counts, base=n - torch.tensor([5, 3]).int().cuda())
+        n = n - torch.tensor([2, 1]).int().cuda()
+        w = torch.zeros(2, 8, 700, device="cuda")
+        out2, lse2 = ext.attn_sink_decode_paged_weights(q[:2], kc, vc, tc, n, w)
+        new, kept = ext.attn_sink_evict_paged(kc, vc, tc, n, w, 80, keep_first=4, keep_last=8)
+        torch.cuda.synchronize()
+        assert ext.device_status() == 0
+        got.append([t.cpu() for t in (qr, out, lse, out2, lse2, w, new, kept, kc[at:], vc[at:])])
+        del kc, vc
+        torch.cuda.empty_cache()
+    for a, b in zip(*got):
+        assert torch.equal(a, b) if a.dtype == torch.int32 else same(a, b)
