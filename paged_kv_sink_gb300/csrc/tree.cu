@@ -417,8 +417,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // segments past the last token and bad ones read slot 0
                     const int slot = bad || j >= L ? 0 : (pg << p.page_shift) | (j & ((1 << p.page_shift) - 1));
                     const uint32_t bad_segs = __ballot_sync(0xffffffffu, bad);
-                    const bool fix = !is_k && (j0 + BN > P || bad_segs != 0 || (j0 < gap1 && j0 + BN > gap0) ||
-                                               (j0 < some1 && j0 + BN > some0));
+                    const bool all = bad_segs != 0 || (j0 < gap1 && j0 + BN > gap0) || (j0 < some1 && j0 + BN > some0);
+                    const int from = all ? 0 : max(P - j0, 0);  // the first row to look at
+                    const bool fix = !is_k && from < BN;
                     uint64_t* bar = fix ? &S.v_fix : &full[st];
                     if (lane == 0) {
                         if (is_k) S.bad_segs[n % kTileRing] = bad_segs;
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         // Key row r of an atom is the 128 bytes at r * 128 (the swizzle
                         // permutes 16-byte chunks within a row).
-                        for (int e = lane; e < (int)(kTile / 16); e += 32) {
+                        for (int e = from * 8 + lane; e < (int)(kTile / 16); e += 32) {
                             const int r = (e >> 3) & (BN - 1), t = j0 + r;
                             uint4* cell = reinterpret_cast<uint4*>(dst0 + st * kTile) + e;
                             if (t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u)) {
