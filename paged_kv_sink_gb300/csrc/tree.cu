@@ -916,7 +916,7 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     const float sg = has && p.sink ? p.sink[h0 + lane] * ATTN_LOG2E : -INFINITY;
     float M = sg, Z = sg == -INFINITY ? 0.f : 1.f;
     float o[kRows][V] = {};
-#pragma unroll(kRows == 1 ? 8 : 2)
+#pragma unroll(kRows == 1 ? 4 : 2)
     for (int c = c0; c <= c1; ++c) {
         const size_t at = place(c);
         const float2 x = has ? p.part_ml[at + lane] : make_float2(0.f, 0.f);
