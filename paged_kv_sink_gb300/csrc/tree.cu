@@ -44,19 +44,22 @@
 //   * At d 128 (one row tile a request) the cache's reads.  32 requests of 8 to 32 nodes, 32
 //     heads over 8, 1024 + 7168 tokens visible: 190 - 197 us, 5.5 - 5.7 TB/s.  (One CTA per
 //     (request, row tile, KV head, range of keys), dispatched by the hardware: 222 us.)
-//   * At d 64 with several row tiles a request the slowest CTA.  16 requests of 1k to 16k
-//     tokens and 16 to 64 nodes, 64 heads over 8: 137 - 140 us for 87 steps a CTA.  The
-//     first S is ready after 7 us, a step takes 1.2 us (two CTAs an SM; 1.1 to 1.5, as an
-//     SM's two softmax phases fall together or apart; 1086 TFLOP/s at 1.175 us), the
-//     median CTA ends 10 us before the last, the merge takes 4.5 us.  Each row tile reads
-//     K and V for itself, 777 MB from HBM for 301 MB, and 81 % of the tiles' rows hold a node.
+//   * At d 64 with several row tiles a request HBM too, since each row tile reads K and V
+//     for itself.  16 requests of 1k to 16k tokens and 16 to 64 nodes, 64 heads over 8: 137
+//     - 140 us for 87 steps a CTA, 781 MB read for 301 MB (6.3 TB/s while the steps run).
+//     From L2 a step takes 1.175 us (two CTAs an SM, 1086 TFLOP/s: the exponentials' serial
+//     chain).  The first S is ready after 7 us, a masked tile with the drafted tokens costs
+//     4 us more than another, the merge 4.5 us, and 81 % of the tiles' rows hold a node.
 //   * One request: latency.  7 nodes over 2000 tokens 13.7 us: first S after 3.7 us, two
 //     steps and the epilogue 4.5, the merge 3.
 // With plain fp32 arithmetic, a CTA per node and KV head, the first two took 19.7 and 21.8
 // ms; without the runs the second 163 us.
-// Measured and left out: runs cut into rounds of shorter ones (slower), two gangs in
-// lockstep on neighbouring row tiles (465 MB instead of 777 in the second case, but no
-// faster: the slowest CTA stays), tensor memory allocated before the runs are known.
+// Measured and left out: runs cut into rounds of shorter ones (slower); two gangs on
+// neighbouring row tiles, which read 465 MB in the second case, with and without runs that
+// allow for the masked tiles: two row tiles a request at d 128 158 us instead of 176, all
+// else 2 - 5 % slower, for the longer schedule leaves the softmax short of registers;
+// tensor memory allocated before the runs are known; drafted tiles' rows cleaned by the
+// warp that issues P V, or a tile later (both slower at d 64).
 #include <cudaTypedefs.h>
 
 #include <type_traits>
