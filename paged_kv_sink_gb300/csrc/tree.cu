@@ -76,13 +76,13 @@ using namespace sm103;
 constexpr int BM = 128, BN = 128;
 constexpr int kStages = 3;  // K and V rings
 constexpr int kBadRing = 4;  // segments that the V producer may be ahead, + 1
-constexpr int kSegRing = 6;  // segments that the K producer may be ahead of the softmax, + 1
+constexpr int kSegRing = 5;  // segments that the K producer may be ahead of the softmax (S of 3 tiles on), + 1
 constexpr int kTileRing = 8;  // tiles that the K producer may be ahead of the softmax, + 1, and more
 constexpr int kMinSteps = 2;  // of a run
 constexpr int kThreads = 256;
 // 128 registers per thread at launch, moved from the control warps to the softmax
-// warps: 128 * 40 + 128 * 216 = 256 * 128.
-constexpr int kRegsCtrl = 40, kRegsSoftmax = 216;
+// warps: 128 * 48 + 128 * 208 = 256 * 128.
+constexpr int kRegsCtrl = 48, kRegsSoftmax = 208;
 constexpr uint32_t kAtom = 128 * 128;  // one 128-byte-swizzled atom column: 128 rows x 64 bf16
 constexpr float kRescaleThreshold = 64.0f;      // log2 units
 constexpr float kFastSumLimit = 1.8446744e19f;  // 2^64
@@ -167,31 +167,46 @@ __device__ __forceinline__ int some_end(const Params& p, const Request& r) {
     return p.win_last > 0 ? max(0, min(r.P, r.P + min(r.n, kMaxNodes) - p.win_last)) : 0;
 }
 
-// The key tiles [it0, it0 + ntiles) of one row tile: what a CTA works on at a time.
+// The steps [it0, it0 + ntiles) of one row tile: what a CTA works on at a time.  They take
+// its key tiles in turn, from `key0` on and round to the first behind the last.
 struct Segment {
     Request rq;
     int b, mt, it0, ntiles;  // request, row tile
-    __device__ __forceinline__ int tile(int it) const { return rq.tile(it0 + it); }
+    int key0;
+    __device__ __forceinline__ int tile(int it) const {
+        const int k = key0 + it;
+        return rq.tile(k < rq.ntiles ? k : k - rq.ntiles);
+    }
     __device__ __forceinline__ bool whole() const { return it0 == 0 && ntiles == rq.ntiles; }
 };
 
 // A gang's run of steps, segment by segment.  Warps 0 to 2 walk a cursor of their own,
-// kept in shared memory (it is read a few times per tile, and the warps have 40
+// kept in shared memory (it is read a few times per tile, and the warps have 48
 // registers); warp 0 hands its segments on to warp 3 and the softmax, which find them
 // there when its first tile arrives.
 struct Cursor : Segment {
     int left;  // steps of the run from this segment on
 
-    __device__ __forceinline__ void start(const Params& p, int b0, int step, int steps) {
+    __device__ __forceinline__ void start(const Params& p, int b0, int step, int steps, int per_run) {
         b = b0;
         left = steps;
         rq = request(p, b, false);
         mt = step / rq.ntiles;
         it0 = step - mt * rq.ntiles;
         ntiles = min(rq.ntiles - it0, left);
+        key0 = it0;
+        if (rq.mtiles > 1) turn(it0 > 0 ? (per_run - it0 % per_run) % per_run : 0, per_run);
+    }
+    // The gangs run side by side, and what one has read another finds in L2 if it comes
+    // soon.  So where a request has several row tiles, each begins with the key tile that
+    // its first step's place in the run (`at`) stands for, or, if more of its steps
+    // are in the next run, such that those begin there with the first key tile.
+    __device__ __forceinline__ void turn(int at, int per_run) {
+        const int nt = rq.ntiles, first = per_run - at;
+        key0 = (it0 + (nt < per_run && 2 * first < nt ? nt - first : at)) % nt;
     }
     // To the next segment; false at the run's end.  A converged warp calls it.
-    __device__ __forceinline__ bool next(const Params& p) {
+    __device__ __forceinline__ bool next(const Params& p, int run, int per_run) {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) {
             left -= ntiles;
@@ -203,6 +218,8 @@ struct Cursor : Segment {
                     while (steps_of(rq) == 0);
                 }
                 ntiles = min(rq.ntiles, left);
+                key0 = 0;
+                if (rq.mtiles > 1) turn(run - left, per_run);
             }
         }
         __syncwarp();
@@ -224,8 +241,9 @@ struct __align__(1024) Smem {
     uint32_t tmem_base;
     int abort;
     int start_b, start_step, run;  // the run's first request, step in it, and length
+    int per_run;                   // length of all runs but the last
     Cursor cursor[3];              // warps 0 to 2
-    uint32_t bad_segs[kTileRing];              // per tile: page segments read through a bad page id
+    int2 tiles[kTileRing];  // per tile: first token, page segments (bits) read through a bad page id
     // Per segment: tokens that some rows see and others do not whose V row holds an
     // infinity or a NaN; nodes, then prefix tokens at the window's start.
     uint32_t v_bad[kBadRing][2 * kMaxNodes / 32];
@@ -353,9 +371,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (blockIdx.x == 0 && tid == 0) p.first[p.batch] = per_run;
     if (total == 0) return;
-    if (tid == 0) S.run = (int)min(per_run, total - w0);
+    if (tid == 0) S.run = (int)min(per_run, total - w0), S.per_run = (int)per_run;
     __syncthreads();  // the run is known to all, and S.sums has been read
-    if (tid < 3) S.cursor[tid].start(p, S.start_b, S.start_step, S.run);
+    if (tid < 3) S.cursor[tid].start(p, S.start_b, S.start_step, S.run, S.per_run);
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, C::kTmemCols);
         tmem_relinquish();
@@ -425,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const bool fix = !is_k && from < BN;
                     uint64_t* bar = fix ? &S.v_fix : &full[st];
                     if (lane == 0) {
-                        if (is_k) S.bad_segs[n % kTileRing] = bad_segs;
+                        if (is_k) S.tiles[n % kTileRing] = make_int2(j0, (int)bad_segs);
                         mbar_expect_tx(bar, kTile);
                     }
                     __syncwarp();
@@ -466,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 ++segs;
-            } while (ok && c.next(p));
+            } while (ok && c.next(p, S.run, S.per_run));
             // Drain: every copy issued must have landed before the CTA exits.
             if (lane == 0) {
                 if (fixes > 0) drain_wait(&S.v_fix, (fixes - 1) & 1);
@@ -522,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     if (ok) umma_commit_e(&S.q_empty);
                     ++segs;
-                } while (ok && c.next(p));
+                } while (ok && c.next(p, S.run, S.per_run));
                 umma_commit_e(&S.final_bar);
                 drain_wait(&S.final_bar, 0);
             } else {
@@ -568,8 +586,6 @@ __global__ void __launch_bounds__(kThreads, 2)
             const Segment& c = S.segment[segs % kSegRing];  // arrived with its first tile
             const int P = c.rq.P, q_start = c.rq.q_start, ntiles = c.ntiles;
             const int32_t* const pages = p.page_table + (size_t)c.b * p.max_pages;
-            const int t_gap = c.rq.ta - c.it0, t0 = c.it0, t1 = c.rq.tb - c.rq.ta + c.it0;
-            auto tile_of = [&](int it) { return it < t_gap ? t0 + it : t1 + it; };
             const int node = c.mt * p.npt + row_node;
             const bool valid = r < p.npt * p.group && node < c.rq.rows;
             const bool work = __any_sync(0xffffffffu, valid);  // else only the barriers' arrivals
@@ -588,7 +604,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int a = up(node + 1); a > 0; a = up(a)) ++pos;
             const int pos_max = P + max(c.rq.n, 1) - 1;  // of any node
             for (int it = 0; it < ntiles; ++it, ++n) {
-                const int j0 = tile_of(it) * BN;
                 if (it > 0) {
                     ok = mbar_wait(&S.s_full, n & 1, abort);
                     if (!__all_sync(0xffffffffu, ok)) {
@@ -597,7 +612,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                 }
                 tc_fence_after();
-                const uint32_t bad_segs = S.bad_segs[n % kTileRing];
+                const int2 here = S.tiles[n % kTileRing];
+                const int j0 = here.x;
+                const uint32_t bad_segs = (uint32_t)here.y;
                 // The previous P V must be complete before P is overwritten or O rescaled.
                 auto wait_prev_pv = [&]() -> bool {
                     if (it == 0) return true;
