@@ -274,8 +274,10 @@ __device__ __forceinline__ bool group_all(bool x) {
     return y != 0;
 }
 
-__device__ __forceinline__ bool nonfinite_pair(uint32_t w) {
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+// Bits 15 and 31 of the result: whether the low / high bf16 of some word is an infinity or a NaN.
+__device__ __forceinline__ uint32_t nonfinite_in(const uint4& x) {
+    auto carry = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+    return (carry(x.x) | carry(x.y) | carry(x.z) | carry(x.w)) & 0x80008000u;
 }
 __device__ __forceinline__ uint32_t finite_pair(uint32_t w) {  // non-finite halves become 0
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
@@ -460,15 +462,45 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         // Key row r of an atom is the 128 bytes at r * 128 (the swizzle
                         // permutes 16-byte chunks within a row).
-                        for (int e = from * 8 + lane; e < (int)(kTile / 16); e += 32) {
+                        bool each = true;  // whether to go through the cells one by one
+                        if constexpr (!C::kTwoPerSm) {
+                            // 32 rows at a time: which are zeroed and which looked at, then 4
+                            // rows an instruction; the cells follow if there is something to
+                            // mend.  (32 KB in under 2 us; cell by cell 7.3, which held the V
+                            // ring up: 32 windowed requests 195 us instead of 187, two row
+                            // tiles a request 168 instead of 147.  At d 64 the SM's other CTA
+                            // hides it, and this form is 2 - 4 % slower there.)
+                            uint4* const cells = reinterpret_cast<uint4*>(dst0 + st * kTile) + lane;
+                            uint32_t found = 0;
+#pragma unroll 1
+                            for (int r0 = from & ~31; r0 < BN; r0 += 32) {
+                                const int r = r0 + lane, t = j0 + r;
+                                const bool zero =
+                                    t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u);
+                                const bool look = !zero && (t >= P || (t >= some0 && t < some1));
+                                const uint32_t zeros = __ballot_sync(0xffffffffu, zero) >> (lane >> 3);
+                                const uint32_t looks = __ballot_sync(0xffffffffu, look) >> (lane >> 3);
+#pragma unroll 1
+                                for (int a = 0; a < C::kAtoms; ++a) {
+                                    uint4* const x = cells + a * (BN * 8) + r0 * 8;
+#pragma unroll
+                                    for (int g = 0; g < 8; ++g)
+                                        if (zeros >> (4 * g) & 1u) x[g * 32] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                                    for (int g = 0; g < 8; ++g)
+                                        if (looks >> (4 * g) & 1u) found |= nonfinite_in(x[g * 32]);
+                                }
+                            }
+                            each = __any_sync(0xffffffffu, found != 0);
+                        }
+                        for (int e = each ? from * 8 + lane : (int)(kTile / 16); e < (int)(kTile / 16); e += 32) {
                             const int r = (e >> 3) & (BN - 1), t = j0 + r;
                             uint4* cell = reinterpret_cast<uint4*>(dst0 + st * kTile) + e;
                             if (t >= L || (t >= gap0 && t < gap1) || (bad_segs >> (r >> p.seg_shift) & 1u)) {
                                 *cell = make_uint4(0u, 0u, 0u, 0u);
                             } else if (t >= P || (t >= some0 && t < some1)) {
                                 const uint4 x = *cell;
-                                if (nonfinite_pair(x.x) || nonfinite_pair(x.y) || nonfinite_pair(x.z) ||
-                                    nonfinite_pair(x.w)) {
+                                if (nonfinite_in(x)) {
                                     *cell = make_uint4(finite_pair(x.x), finite_pair(x.y), finite_pair(x.z),
                                                        finite_pair(x.w));
                                     const int i = t >= P ? t - P : kMaxNodes + t - some0;
