@@ -42,24 +42,24 @@
 //
 // What bounds it, with the times measured:
 //   * At d 128 (one row tile a request) the cache's reads.  32 requests of 8 to 32 nodes, 32
-//     heads over 8, 1024 + 7168 tokens visible: 190 - 197 us, 5.5 - 5.7 TB/s.  (One CTA per
-//     (request, row tile, KV head, range of keys), dispatched by the hardware: 222 us.)
-//   * At d 64 with several row tiles a request HBM too, since each row tile reads K and V
-//     for itself.  16 requests of 1k to 16k tokens and 16 to 64 nodes, 64 heads over 8: 137
-//     - 140 us for 87 steps a CTA, 781 MB read for 301 MB (6.3 TB/s while the steps run).
-//     From L2 a step takes 1.175 us (two CTAs an SM, 1086 TFLOP/s: the exponentials' serial
-//     chain).  The first S is ready after 7 us, a masked tile with the drafted tokens costs
-//     4 us more than another, the merge 4.5 us, and 81 % of the tiles' rows hold a node.
-//   * One request: latency.  7 nodes over 2000 tokens 13.7 us: first S after 3.7 us, two
+//     heads over 8, 1024 + 7168 tokens visible: 187 us, 5.8 TB/s (7 TB/s while the steps
+//     run).  (One CTA per (request, row tile, KV head, range of keys), dispatched by the
+//     hardware: 222 us.)
+//   * At d 64 with several row tiles a request the softmax.  16 requests of 1k to 16k tokens
+//     and 16 to 64 nodes, 64 heads over 8: 131 us for 87 steps a CTA of 1.2 us each (two
+//     CTAs an SM; 1086 TFLOP/s at 1.175 us: the exponentials' serial chain).  The first S
+//     is ready after 6 us, a masked tile with the drafted tokens costs 2 us more than
+//     another, the last gang ends 7 us after the median one, the merge takes 4.5 us, and 81
+//     % of the tiles' rows hold a node.  HBM is read for 474 MB (301 MB of cache; 781 MB
+//     and 138 us while each row tile took its keys from the first on).
+//   * One request: latency.  7 nodes over 2000 tokens 13.8 us: first S after 3.7 us, two
 //     steps and the epilogue 4.5, the merge 3.
 // With plain fp32 arithmetic, a CTA per node and KV head, the first two took 19.7 and 21.8
 // ms; without the runs the second 163 us.
-// Measured and left out: runs cut into rounds of shorter ones (slower); two gangs on
-// neighbouring row tiles, which read 465 MB in the second case, with and without runs that
-// allow for the masked tiles: two row tiles a request at d 128 158 us instead of 176, all
-// else 2 - 5 % slower, for the longer schedule leaves the softmax short of registers;
-// tensor memory allocated before the runs are known; drafted tiles' rows cleaned by the
-// warp that issues P V, or a tile later (both slower at d 64).
+// Measured and left out: runs cut into rounds of shorter ones (slower); two gangs a run, on
+// neighbouring row tiles, and runs that allow for the masked tiles (each leaves the softmax
+// short of registers: all else 2 - 5 % slower); tensor memory allocated before the runs are
+// known; drafted tiles' rows cleaned by the warp that issues P V, or a tile later.
 #include <cudaTypedefs.h>
 
 #include <type_traits>
