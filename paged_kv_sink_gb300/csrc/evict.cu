@@ -422,6 +422,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const MoveArgs p, in
 // ---------------------------------------------------------------------------
 // Host side.
 
+constexpr int kPlainSmem = 24 * 1024;  // dynamic, beside the static part, that a launch may have without asking
+
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     if (a.batch == 0) return cudaSuccess;
     // Several CTAs per (request, head) while the GPU has SMs left and each has 8192
@@ -438,8 +440,10 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     const long long stretch = (cap + parts - 1) / parts;
     const int capacity = (int)(stretch < kRound ? stretch : kRound);
     cfg.dynamicSmemBytes = (size_t)capacity * 6;  // keys and offsets
-    cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRound * 6);
-    if (e != cudaSuccess) return e;
+    if (cfg.dynamicSmemBytes > kPlainSmem) {
+        cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRound * 6);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = parts;
@@ -465,8 +469,10 @@ cudaError_t launch_move(const MoveArgs& a, cudaStream_t s) {
         if ((1 << sh) == a.page_size) page_shift = sh;
     const dim3 grid(head_bytes / (16 * lanes), a.heads * (a.weights ? 3 : 2), a.batch);
     auto launch = [&](auto kernel, int smem) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
+        if (smem > kPlainSmem) {
+            cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
+        }
         kernel<<<grid, kMoveThreads, smem, s>>>(a, lanes, head_bytes, row_bytes, page_shift);
         return cudaGetLastError();
     };

@@ -76,7 +76,7 @@ using namespace sm103;
 constexpr int BM = 128, BN = 128;
 constexpr int kStages = 3;  // K and V rings
 constexpr int kBadRing = 4;  // segments that the V producer may be ahead, + 1
-constexpr int kSegRing = 5;  // segments that the K producer may be ahead of the softmax (S of 3 tiles on), + 1
+constexpr int kSegRing = 5;  // segments that the K producer (kStages tiles ahead of S) may be ahead of the softmax, + 1
 constexpr int kTileRing = 8;  // tiles that the K producer may be ahead of the softmax, + 1, and more
 constexpr int kMinSteps = 2;  // of a run
 constexpr int kThreads = 256;

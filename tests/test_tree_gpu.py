@@ -181,6 +181,19 @@ def test_many_requests_of_one_node(ext):
     check(x, out, lse)
 
 
+@pytest.mark.parametrize("prefix,nodes,hq,d,page,first,last", [
+    ([1000 + 7 * i for i in range(30)], [20 + i % 13 for i in range(30)], 64, 64, 16, 0, 0),   # short row tiles
+    ([9000, 3000], [100, 60], 64, 64, 16, 0, 0),                                               # over many runs
+    ([2000 + 50 * i for i in range(12)], [40] * 12, 32, 128, 64, 64, 900),
+    ([300 + 90 * i for i in range(24)], [70] * 24, 32, 128, 16, 0, 0)])
+def test_row_tiles_that_runs_cut(ext, prefix, nodes, hq, d, page, first, last):
+    """Several row tiles a request, cut by the GPU's runs at many places: each takes every key tile once."""
+    x = make(prefix, nodes, hq, 8, d, page, seed=14)
+    out, lse = run(ext, x, first, last)
+    assert ext.device_status() == 0
+    check(x, out, lse, first, last)
+
+
 @pytest.mark.parametrize("prefix", [50, 2000])
 def test_infinite_scores_give_nan(ext, prefix):
     """A visible token with a score of +inf leaves no finite softmax, however the keys are split."""
