@@ -260,8 +260,14 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
     mbar_wait(bar, parity, &dummy);
 }
 
+// The .aligned instructions below -- TMEM loads, stores and their waits, barriers of a
+// warpgroup -- are defined for a converged warp only, and nothing but a warp-wide
+// synchronisation promises that lanes are together again behind a loop or branch of
+// their own.  So a __syncwarp() stands before each that follows one.
+
 // Whether x holds in all 128 threads of the softmax warpgroup (also a barrier of theirs).
 __device__ __forceinline__ bool group_all(bool x) {
+    __syncwarp();
     uint32_t y;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
@@ -555,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     __syncwarp();
                     if (!(ok = wait_all(&S.q_full, segs & 1))) {
                         if (lane == 0) drain_wait(&S.q_full, segs & 1);  // the copy lands before the CTA exits
+                        __syncwarp();
                         break;
                     }
                     for (int it = 0; it < c.ntiles; ++it, ++n) {
@@ -662,6 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     continue;
                 }
                 uint32_t s[4][32];
+                __syncwarp();  // a segment's rows have walked to their roots one by one
                 tmem_ld32(tS, s[0]);
                 tmem_ld32(tS + 32, s[1]);
                 tmem_ld_wait();
@@ -712,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                     if ((c >> 5) <= w && (c + len - 1) >> 5 >= w) vis[w] &= ~(seg << (c & 31));
                             }
                     }
+                    __syncwarp();  // the rows have walked to their roots
                 }
                 auto mask_half = [&](auto hfc) {
                     constexpr int hf = decltype(hfc)::value;
@@ -802,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                     rs = exps_half(H0{}, m_use) + exps_half(H1{}, m_use);
+                    __syncwarp();
                     if (it > 0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
                         for (int ch = 0; ch < D / 32; ++ch) {
@@ -854,6 +864,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int ch = 0; ch < D / 32; ++ch) {
                 float u[32];
                 uint32_t raw[32];
+                __syncwarp();  // each row has added its own infinities to the last 32 columns
                 tmem_ld32(tO + ch * 32, raw);
                 tmem_ld_wait();
 #pragma unroll
@@ -897,6 +908,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             if (valid && direct && p.lse) p.lse[(size_t)h * p.total_q + row] = lse_v;
             if (valid && !direct) p.part_ml[part] = make_float2(l != 0.f ? m_ref : -INFINITY, l);
+            __syncwarp();
             if (any_bad) {  // the place is free for a later segment
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 if (r < 2 * kMaxNodes / 32) v_bad[r] = 0;

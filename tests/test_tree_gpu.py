@@ -326,3 +326,35 @@ def test_two_graphs_and_two_streams(ext):
         for x, o in zip(xs, outs):
             check(x, o[0].cpu(), o[1].cpu())
         assert same(eager[0], outs[0][0]) and same(eager[1], outs[0][1])
+
+
+@pytest.mark.parametrize("hq,hkv,d,page", [(8, 2, 64, 16), (8, 2, 128, 64), (24, 8, 64, 8)])
+def test_rows_of_a_warp_with_walks_of_different_lengths(ext, hq, hkv, d, page):
+    """Neighbouring nodes at depths from 0 to 60: each row walks its own number of steps to
+    its root, before a segment's first tile (positions, under a window), in masked tiles,
+    and again between the pieces of the output where V holds infinities."""
+    nodes, prefix = [90, 33, 120, 7], [400, 10, 129, 0]
+    x = make(prefix, nodes, hq, hkv, d, page, seed=23)
+    parents = []
+    for n in nodes:  # even nodes are a chain, every second odd one is a root, the others hang on the chain's start
+        parents += [i - 2 if i % 2 == 0 and i else -1 if i % 4 != 3 else 0 for i in range(n)]
+    x["parents"] = torch.tensor(parents).int()
+    first, last = 6, 40
+    out, lse = run(ext, x, first, last)
+    assert ext.device_status() == 0
+    check(x, out, lse, first, last)
+    # an infinity in every 32 columns of the V rows of a chain's node and of a root
+    v, row = x["v"].view(-1, hkv, d), 0
+    for b, n in enumerate(nodes):
+        for i in (4, 5):
+            v[int(co.slot(x["table"][b].numpy(), page, prefix[b] + i)), :, i::32] = float("inf")
+    got, got_lse = run(ext, x, first, last)
+    assert ext.device_status() == 0 and same(got_lse, lse)
+    for b, n in enumerate(nodes):
+        seen = co.tree_seen(parents[row:row + n], prefix[b], first, last)
+        want = out[row:row + n].clone()
+        for i in (4, 5):
+            sees = torch.from_numpy(np.nonzero(seen[:, prefix[b] + i])[0])
+            want[sees[:, None], :, torch.arange(i, d, 32)[None]] = float("inf")
+        assert same(got[row:row + n], want), b
+        row += n
