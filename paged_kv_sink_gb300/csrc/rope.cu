@@ -152,11 +152,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const Args p, int tile, 
     }
     const int r0 = blockIdx.x * tile;
     if constexpr (kAppend) {
-        // rows past the grid or past the tensors' end stay untouched
-        const bool over = n > (long long)gridDim.x * tile || n0 < 0 || (long long)n0 + n > p.rows;
+        // rows past max_new (the grid covers it rounded up to a tile) or past the tensors' end
+        // stay untouched
+        const bool over = n > p.max_new || n0 < 0 || (long long)n0 + n > p.rows;
         if (over && blockIdx.x == 0 && threadIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
         if (n0 < 0) return;
-        n = (int)min((long long)n, (long long)p.rows - n0);
+        n = (int)min((long long)min(n, p.max_new), (long long)p.rows - n0);
     }
     const int m = min(tile, n - r0);
     if (m <= 0) return;

@@ -263,3 +263,28 @@ def test_rope_in_a_graph_and_on_another_stream(ext):
     g.replay()
     want = ext.attn_sink_rope(q, k, pos, f)
     assert same(out[0], want[0]) and same(out[1], want[1])
+
+
+@pytest.mark.parametrize("most", [3, 3001])
+def test_rope_append_leaves_rows_past_max_new(ext, most):
+    """A request with one row more than max_new: that row is left out, in the caches and in
+    q_out, and the status says so, however many rows the batch has in all (a block takes 1
+    row of a small batch, 8 of a large one)."""
+    new = [most + 1, most, most, most]
+    k_cache, v_cache, table, sl = paged(new, 2, 64, 16, seed=16)
+    q, k = rows(sum(new), 4, 2, 64, seed=17)
+    f, _ = ext.attn_sink_rope_freqs(64)
+    ext.device_status()
+    got = []
+    for bound in (most, most + 1):
+        kc, vc, q_out = k_cache.clone().cuda(), v_cache.clone().cuda(), torch.full_like(q, 7.0).cuda()
+        ext.attn_sink_rope_kv_append(q.cuda(), k.cuda(), k.cuda(), kc, vc, table.cuda(), sl.cuda(), f,
+                                     cu_new=cu(new).cuda(), max_new=bound, q_out=q_out)
+        got.append((kc.cpu().view(-1, 2, 64), vc.cpu().view(-1, 2, 64), q_out.cpu(), ext.device_status()))
+    (kc, vc, q_out, status), (want_k, want_v, want_q, fine) = got
+    assert fine == 0 and status == ext._lib.DEV_SEQLEN_OOB
+    last = int(co.slot(table[0].numpy(), 16, most))
+    for g, want, before, at in ((kc, want_k, k_cache.view(-1, 2, 64), last), (vc, want_v, v_cache.view(-1, 2, 64), last),
+                                (q_out, want_q, torch.full_like(q, 7.0), most)):
+        assert same(g[at], before[at])
+        assert same(torch.cat([g[:at], g[at + 1:]]), torch.cat([want[:at], want[at + 1:]]))
