@@ -100,6 +100,19 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _made(stream, make, *args, **kw):
+    """An output that a call allocates.  It belongs to the stream that the call launches on
+    (None: the current one), so that its memory is not handed on while a kernel there
+    still writes it, even when the caller drops it at once, and it is recorded on the current
+    stream, where the caller goes on with it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _check(name, rc):
     if rc != OK:
         msg = lib().attn_sink_last_error().decode()
@@ -129,9 +142,9 @@ def attn_sink_fwd(q, k, v, sink, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_s
     tq, hq, d = q.shape
     hkv = k.shape[1]
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if lse is None and return_lse:
-        lse = torch.empty((hq, tq), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty, (hq, tq), dtype=torch.float32, device=q.device)
     rc = lib().attn_sink_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(sink), _ptr(cu_seqlens_q),
                              _ptr(cu_seqlens_k), cu_seqlens_q.numel() - 1, tq, k.shape[0], hq, hkv,
                              d, int(max_seqlen_q), int(max_seqlen_k), int(win_first), int(win_last),
@@ -180,9 +193,9 @@ def attn_sink_decode_paged(q, k_cache, v_cache, page_table, seqlens, sink=None, 
     B, hq, d = q.shape
     npages, ps, hkv, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if lse is None and return_lse:
-        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty, (B, hq), dtype=torch.float32, device=q.device)
     rc = getattr(lib(), _entry)(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table),
                                 page_table.shape[1], _ptr(seqlens), B, hq, hkv, d, ps, npages,
                                 _ptr(sink), int(win_first), int(win_last), float(scale),
@@ -224,9 +237,9 @@ def attn_sink_fwd_qkvpacked(qkv, hkv, sink, cu_seqlens_q, max_seqlen_q, win_firs
     kp, _ = _row_view(qkv, hq, hkv, d)
     vp, _ = _row_view(qkv, hq + hkv, hkv, d)
     if out is None:
-        out = torch.empty((T, hq, d), dtype=qkv.dtype, device=qkv.device)
+        out = _made(stream, torch.empty, (T, hq, d), dtype=qkv.dtype, device=qkv.device)
     if lse is None and return_lse:
-        lse = torch.empty((hq, T), dtype=torch.float32, device=qkv.device)
+        lse = _made(stream, torch.empty, (hq, T), dtype=torch.float32, device=qkv.device)
     rc = lib().attn_sink_fwd_strided(qp, kp, vp, rs, rs, rs, _ptr(sink), _ptr(cu_seqlens_q), _ptr(cu_seqlens_q),
                                      cu_seqlens_q.numel() - 1, T, T, hq, hkv, d, int(max_seqlen_q),
                                      int(max_seqlen_q), int(win_first), int(win_last), 1 if causal else 0,
@@ -248,9 +261,9 @@ def attn_sink_fwd_kvpacked(q, kv, sink, cu_seqlens_q, cu_seqlens_k, max_seqlen_q
     kp, rs = _row_view(kv3, 0, hkv, d)
     vp, _ = _row_view(kv3, hkv, hkv, d)
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if lse is None and return_lse:
-        lse = torch.empty((hq, tq), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty, (hq, tq), dtype=torch.float32, device=q.device)
     rc = lib().attn_sink_fwd_strided(_ptr(q), kp, vp, 0, rs, rs, _ptr(sink), _ptr(cu_seqlens_q),
                                      _ptr(cu_seqlens_k), cu_seqlens_q.numel() - 1, tq, tk, hq, hkv, d,
                                      int(max_seqlen_q), int(max_seqlen_k), int(win_first), int(win_last),
@@ -272,9 +285,9 @@ def attn_sink_bwd_qkvpacked(qkv, hkv, sink, out, lse, dout, cu_seqlens_q, max_se
     _need(lse, torch.float32, "lse")
     T, C, d = qkv.shape
     hq = C - 2 * hkv
-    dqkv = torch.empty_like(qkv) if dqkv is None else dqkv.reshape(T, C, d)
+    dqkv = _made(stream, torch.empty_like, qkv) if dqkv is None else dqkv.reshape(T, C, d)
     if sink is not None and dsink is None:
-        dsink = torch.empty_like(sink)
+        dsink = _made(stream, torch.empty_like, sink)
     qp, rs = _row_view(qkv, 0, hq, d)
     kp, _ = _row_view(qkv, hq, hkv, d)
     vp, _ = _row_view(qkv, hq + hkv, hkv, d)
@@ -302,11 +315,11 @@ def attn_sink_bwd_kvpacked(q, kv, sink, out, lse, dout, cu_seqlens_q, cu_seqlens
     _need(lse, torch.float32, "lse")
     tq, hq, d = q.shape
     tk, _, hkv, _ = kv.shape
-    dq = torch.empty_like(q) if dq is None else dq
-    dkv = torch.empty_like(kv) if dkv is None else dkv
+    dq = _made(stream, torch.empty_like, q) if dq is None else dq
+    dkv = _made(stream, torch.empty_like, kv) if dkv is None else dkv
     _need(dkv, torch.bfloat16, "dkv")
     if sink is not None and dsink is None:
-        dsink = torch.empty_like(sink)
+        dsink = _made(stream, torch.empty_like, sink)
     kp, rs = _row_view(kv.reshape(tk, 2 * hkv, d), 0, hkv, d)
     vp, _ = _row_view(kv.reshape(tk, 2 * hkv, d), hkv, hkv, d)
     dkp, drs = _row_view(dkv.reshape(tk, 2 * hkv, d), 0, hkv, d)
@@ -352,9 +365,9 @@ def attn_sink_decode_paged_append(q, k_new, v_new, k_cache, v_cache, page_table,
     B, hq, d = q.shape
     npages, ps, hkv, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if lse is None and return_lse:
-        lse = torch.empty((B, hq), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty, (B, hq), dtype=torch.float32, device=q.device)
     rc = lib().attn_sink_decode_paged_append(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                              _ptr(page_table), page_table.shape[1], _ptr(seqlens), B, hq, hkv, d,
                                              ps, npages, _ptr(sink), int(win_first), int(win_last), float(scale),
@@ -377,9 +390,9 @@ def attn_sink_fwd_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_k
     tq, hq, d = q.shape
     npages, ps, hkv, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     if lse is None and return_lse:
-        lse = torch.empty((hq, tq), dtype=torch.float32, device=q.device)
+        lse = _made(stream, torch.empty, (hq, tq), dtype=torch.float32, device=q.device)
     rc = lib().attn_sink_fwd_paged(_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
                                    _ptr(page_table), page_table.shape[1], _ptr(cu_seqlens_q), _ptr(seqlens_k),
                                    cu_seqlens_q.numel() - 1, tq, hq, hkv, d, ps, npages, int(max_seqlen_q),
@@ -399,11 +412,11 @@ def attn_sink_bwd(q, k, v, sink, out, lse, dout, cu_seqlens_q, cu_seqlens_k, max
     _need(lse, torch.float32, "lse")
     tq, hq, d = q.shape
     hkv = k.shape[1]
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _made(stream, torch.empty_like, q) if dq is None else dq
+    dk = _made(stream, torch.empty_like, k) if dk is None else dk
+    dv = _made(stream, torch.empty_like, v) if dv is None else dv
     if sink is not None and dsink is None:
-        dsink = torch.empty_like(sink)
+        dsink = _made(stream, torch.empty_like, sink)
     rc = lib().attn_sink_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(sink), _ptr(out), _ptr(lse), _ptr(dout),
                              _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), cu_seqlens_q.numel() - 1, tq,
                              k.shape[0], hq, hkv, d, int(max_seqlen_q), int(max_seqlen_k), int(win_first),
@@ -522,7 +535,7 @@ def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0,
         _expect("positions", positions, _I32, dev, (T,))
     r = _expect_inv_freq(inv_freq, dev, d)
     if q_out is None:
-        q_out, qo_rs = torch.empty_like(q, memory_format=torch.contiguous_format), 0
+        q_out, qo_rs = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format), 0
     else:
         qo_rs = _expect_rows("q_out", q_out, dev, q.shape)
     hkv = k_rs = ko_rs = 0
@@ -531,7 +544,7 @@ def attn_sink_rope(q, k, positions, inv_freq, interleaved=False, attn_scale=1.0,
         k_rs = _expect_rows("k", k, dev, (T, None if k.dim() != 3 else k.shape[1], d))
         hkv = k.shape[1]
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = _made(stream, torch.empty_like, k, memory_format=torch.contiguous_format)
         else:
             ko_rs = _expect_rows("k_out", k_out, dev, k.shape)
         kp, kop = k.data_ptr(), k_out.data_ptr()
@@ -595,7 +608,7 @@ def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seql
             _expect("positions", positions, _I32, dev, (T,))
         pos = positions.data_ptr()
     if q_out is None:
-        q_out, qo_rs = torch.empty_like(q, memory_format=torch.contiguous_format), 0
+        q_out, qo_rs = _made(stream, torch.empty_like, q, memory_format=torch.contiguous_format), 0
     else:
         qo_rs = _expect_rows("q_out", q_out, dev, q.shape)
     _run("attn_sink_rope_kv_append", dev, stream, q.data_ptr(), q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
@@ -605,21 +618,21 @@ def attn_sink_rope_kv_append(q, k_new, v_new, k_cache, v_cache, page_table, seql
     return q_out
 
 
-def _outputs(q, dev, lse_shape, sink, out, lse, return_lse):
+def _outputs(q, dev, lse_shape, sink, out, lse, return_lse, stream):
     """Checks or makes the outputs of an attention call; returns them and the pointers
     of sink, out and lse."""
     hq = q.shape[1]
     if sink is not None and not _is(sink, _F32, dev, (hq,)):
         _expect("sink", sink, _F32, dev, (hq,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _made(stream, torch.empty_like, q)
     elif not _is(out, _BF16, dev, q.shape):
         _expect("out", out, _BF16, dev, q.shape)
     if lse is not None:
         if not _is(lse, _F32, dev, lse_shape):
             _expect("lse", lse, _F32, dev, lse_shape)
     elif return_lse:
-        lse = torch.empty(lse_shape, dtype=_F32, device=q.device)
+        lse = _made(stream, torch.empty, lse_shape, dtype=_F32, device=q.device)
     return (out, lse, None if sink is None else sink.data_ptr(), out.data_ptr(),
             None if lse is None else lse.data_ptr())
 
@@ -642,7 +655,7 @@ def attn_sink_tree_paged(q, k_cache, v_cache, page_table, cu_seqlens_q, seqlens_
         _expect("cu_seqlens_q", cu_seqlens_q, _I32, dev, (B + 1,))
     if not _is(parents, _I32, dev, (T,)):
         _expect("parents", parents, _I32, dev, (T,))
-    out, lse, sp, op, lp = _outputs(q, dev, (hq, T), sink, out, lse, return_lse)
+    out, lse, sp, op, lp = _outputs(q, dev, (hq, T), sink, out, lse, return_lse, stream)
     _run("attn_sink_tree_paged", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          page_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), parents.data_ptr(), B, T, hq,
          hkv, d, ps, npages, int(max_seqlen_q), int(max_seqlen_k), sp, int(win_first), int(win_last), float(scale), op,
@@ -688,7 +701,7 @@ def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, wei
     shape = weights.shape
     if len(shape) != 3 or shape[0] != B or not _is(weights, _F32, dev, shape):
         _expect("weights", weights, _F32, dev, (B, None, None))
-    out, lse, sp, op, lp = _outputs(q, dev, (B, hq), sink, out, lse, return_lse)
+    out, lse, sp, op, lp = _outputs(q, dev, (B, hq), sink, out, lse, return_lse, stream)
     _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
          page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages, sp, int(win_first),
          int(win_last), float(scale), weights.data_ptr(), shape[1], shape[2], op, lp)
@@ -717,11 +730,11 @@ def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget
     elif not _is(weights_out, _F32, dev, shape):
         _expect("weights_out", weights_out, _F32, dev, shape)
     if kept is None:
-        kept = torch.empty((B, heads, max(budget, 0)), dtype=_I32, device=seqlens.device)
+        kept = _made(stream, torch.empty, (B, heads, max(budget, 0)), dtype=_I32, device=seqlens.device)
     elif not _is(kept, _I32, dev, (B, heads, budget)):
         _expect("kept", kept, _I32, dev, (B, heads, budget))
     if new_seqlens is None:
-        new_seqlens = torch.empty_like(seqlens)
+        new_seqlens = _made(stream, torch.empty_like, seqlens)
     elif not _is(new_seqlens, _I32, dev, (B,)):
         _expect("new_seqlens", new_seqlens, _I32, dev, (B,))
     _run("attn_sink_evict_paged", dev, stream, k_cache.data_ptr(), v_cache.data_ptr(), page_table.data_ptr(), max_pages,
@@ -733,7 +746,7 @@ def attn_sink_evict_paged(k_cache, v_cache, page_table, seqlens, weights, budget
 def attn_sink_visible_ranges(seqlens, win_first, win_last, stream=None):
     _need(seqlens, torch.int32, "seqlens")
     B = seqlens.numel()
-    ranges = torch.empty((B, 4), dtype=torch.int32, device=seqlens.device)
+    ranges = _made(stream, torch.empty, (B, 4), dtype=torch.int32, device=seqlens.device)
     rc = lib().attn_sink_visible_ranges(_ptr(seqlens), B, int(win_first), int(win_last),
                                         _ptr(ranges), _stream(stream))
     _check("attn_sink_visible_ranges", rc)
@@ -745,7 +758,7 @@ def attn_sink_visible_slots(seqlens, page_table, page_size, num_pages, win_first
     _need(seqlens, torch.int32, "seqlens")
     _need(page_table, torch.int32, "page_table")
     B = seqlens.numel()
-    slots = torch.empty((B, max_visible), dtype=torch.int32, device=seqlens.device)
+    slots = _made(stream, torch.empty, (B, max_visible), dtype=torch.int32, device=seqlens.device)
     rc = lib().attn_sink_visible_slots(_ptr(seqlens), _ptr(page_table), page_table.shape[1], B,
                                        int(page_size), int(num_pages), int(win_first),
                                        int(win_last), _ptr(slots), int(max_visible),
