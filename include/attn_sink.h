@@ -461,10 +461,11 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
  *   weights  (batch, weight_heads, weight_cap) fp32 device, updated in place; the
  *            caller sets new tokens' entries to 0 before their first call.  Tokens
  *            t >= weight_cap are left out and set ATTN_SINK_DEV_SEQLEN_OOB.
- * The sums have a fixed order (no atomics).  Scratch: 4 bytes per query head (those
- * of a KV head rounded up to 8, or to 16 above 8), request and token that the page
- * table can hold (or the window can show).  Everything else as in
- * attn_sink_decode_paged; hq at most 4096, and with weight_heads == 1 at most 6144
+ * The sums have a fixed order (no atomics).  Scratch for scores: 4 bytes per query head
+ * (those of a KV head rounded up to 8, or to 16 above 8), request and token that has an
+ * accumulator and that the page table can hold (or the window can show); at most 2 GiB
+ * at a time, or one request's: batches that need more are taken in rounds of requests.
+ * Everything else as in attn_sink_decode_paged; hq at most 4096, and with weight_heads == 1 at most 6144
  * query heads rounded up like that.
  */
 int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,

@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParam
                 // heads that do not exist: no weight, whatever 0 times the key is
                 const int hd = nt * 8 + 2 * (lane & 3);
                 const bool e0 = hd < nheads, e1 = hd + 1 < nheads;
-                if (v < v1)
+                const long long end = min((long long)v1, p.scores_cap);
+                if (v < end)
                     *reinterpret_cast<float2*>(dst) = make_float2(e0 ? x0 : -INFINITY, e1 ? x1 : -INFINITY);
-                if (v + 8 < v1)
+                if (v + 8 < end)
                     *reinterpret_cast<float2*>(dst + 8 * 8 * NT) =
                         make_float2(e0 ? x2 : -INFINITY, e1 ? x3 : -INFINITY);
             }
@@ -438,7 +439,10 @@ __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const Spl
         if (h < p.hq) merge_splits<D>(p, b, h, dd, nsplit, sink, out, lse);
         return;
     }
-    if ((long long)blockIdx.x * tokens >= nvis) return;
+    // the last visible token is the request's last
+    if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && nvis > 0 && r.b1 > cap) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    const long long scored = min((long long)nvis, p.scores_cap);
+    if ((long long)blockIdx.x * tokens >= scored) return;
     extern __shared__ float2 st[];  // (reference, 1 / denominator) of each query head, padded to H per head block
     const int head = blockIdx.y, hkv = p.hq / p.group;
     const int blocks = hkv * p.hblocks / heads;  // head blocks that this accumulator sums
@@ -461,17 +465,14 @@ __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const Spl
     };
     auto start = [&](long long v0) {
         v = (int)v0 + tid;
-        v1 = (int)min((long long)nvis, v0 + tokens);
+        v1 = (int)min(scored, v0 + tokens);
         load(0);
 #pragma unroll
         for (int k = 0; k < kT; ++k) {
             sum[k] = 0.f;
             if (v + k * kWeightThreads < v1) {
                 const int t = visible_token(r, v + k * kWeightThreads);
-                if (t < cap)
-                    sum[k] = w[t];
-                else
-                    raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+                if (t < cap) sum[k] = w[t];
             }
         }
     };
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const Spl
                 if (t < cap) w[t] = sum[k];
             }
         v0 += (long long)wblocks * tokens;
-        if (v0 >= nvis) break;
+        if (v0 >= scored) break;
         start(v0);
     }
 }
@@ -645,7 +646,7 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     sp.group = a.group;
     sp.scale_log2 = a.scale * ATTN_LOG2E;
     sp.scores = w ? w->scores : nullptr;
-    sp.scores_cap = pl.nvis_max;
+    sp.scores_cap = w ? w->scores_cap : 0;
     sp.page_shift = -1;
     for (int sh = 0; sh < 31; ++sh)
         if ((1 << sh) == a.page_size) sp.page_shift = sh;
@@ -683,8 +684,9 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
         // microsecond each (two fit an SM).
         const long long units = (long long)a.batch * w->heads;
         const int most = kWeightThreads * (pl.nt == 1 ? kWeightTokens<1> : kWeightTokens<2>);
-        const int tokens = (pl.nvis_max + most - 1) / most * units >= 4 * 152 ? most : 512;
-        int wblocks = (int)((pl.nvis_max + tokens - 1) / tokens);
+        const int tokens = (w->scores_cap + most - 1) / most * units >= 4 * 152 ? most : 512;
+        int wblocks = (int)((w->scores_cap + tokens - 1) / tokens);
+        if (wblocks < 1) wblocks = 1;
         if (wblocks * units >= 16 * 152) wblocks = (wblocks + 1) / 2;
         const int per_block = kWeightThreads / a.head_dim, merges = (a.hq + per_block - 1) / per_block;
         cfg.gridDim = dim3((unsigned)(wblocks + (merges + w->heads - 1) / w->heads), w->heads, a.batch);

@@ -26,7 +26,7 @@ struct SplitParams {
     float scale_log2;  // softmax scale * log2(e)
     // Accumulated attention weights only (else NULL):
     float* scores;         // (batch, hkv * hblocks, scores_cap, 8 nt) scores of the visible tokens, log2 units
-    long long scores_cap;  // visible tokens of the longest possible request
+    long long scores_cap;  // visible tokens of a request that have a place (a token past it has no accumulator)
 };
 
 // Validated arguments of attn_sink_decode_paged.
@@ -58,6 +58,7 @@ struct Weights {
     float* weights;  // (batch, heads, cap), heads 1 or hkv
     int heads, cap;
     float* scores;
+    long long scores_cap;
 };
 
 Plan make_plan(const Args& a);

@@ -113,6 +113,46 @@ def test_weights_with_bad_pages_infinite_sinks_and_a_short_accumulator(ext):
     assert status == ext._lib.DEV_PAGE_OOB and torch.all(w == 0)
 
 
+@pytest.mark.parametrize("cap,most", [(5200, 256), (262144, 2240)])
+@pytest.mark.parametrize("shared", [True, False])
+def test_weights_with_a_table_far_wider_than_the_requests(ext, cap, most, shared):
+    """64 requests, most of them short, behind a page table of 262144 tokens: the scratch stays
+    below `most` MiB (4 GiB for the table's width: 64 requests, 64 heads, 4 bytes a token), and
+    the results are the same as behind a table cut to the longest request."""
+    lens = [1 + 37 * b % 450 for b in range(64)]
+    lens[20], lens[63] = 5187, 3000
+    hkv, hq, heads = 8, 64, 1 if shared else 8
+    k, v, table, sl = paged(lens, hkv, 64, 16, seed=41)
+    wide = torch.full((64, 262144 // 16), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    g = torch.Generator().manual_seed(42)
+    q = torch.randn(64, hq, 64, generator=g).bfloat16()
+    dev = [t.cuda() for t in (q, k, v, wide, sl)]
+    cut = [*dev[:3], table.cuda(), dev[4]]
+    w, w2 = torch.ones(64, heads, cap, device="cuda"), torch.ones(64, heads, cap, device="cuda")
+    ref, ref_lse = ext.attn_sink_decode_paged(*dev)
+    ext.attn_sink_decode_paged_weights(*(t[:1] if t.shape[0] == 64 else t for t in cut), w2[:1].clone())
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    out, lse = ext.attn_sink_decode_paged_weights(*dev, w)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] <= most << 20
+    assert ext.device_status() == 0
+    assert same(out, ref) and same(lse, ref_lse)
+    ext.attn_sink_decode_paged_weights(*cut, w2)
+    # each weight is off by a factor of at most 3e-4, and one fp32 addition to 1
+    p, p2 = w.double() - 1.0, w2.double() - 1.0
+    assert torch.all((p - p2).abs() <= 6e-4 * p.abs() + 2.0 ** -22)
+    for b in (0, 20, 63):
+        n = lens[b]
+        kk, vv = (co.tokens(c, table[b], n) for c in (k, v))
+        _, _, P, _ = co.attend(q[b:b + 1], kk, vv, np.ones((1, n), bool), None, 0.125)
+        want = P[:, 0].reshape(heads, hq // heads, n).sum(1)
+        have = w[b].cpu().double().numpy()
+        assert np.all(np.abs(have[:, :n] - 1.0 - want) <= 3e-4 * want + 2.0 ** -23 * (1.0 + want))
+        assert np.all(have[:, n:] == 1.0)
+
+
 @pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (24, 2)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_weights_of_infinite_keys(ext, hq, hkv, shared):
