@@ -465,6 +465,8 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
  * (those of a KV head rounded up to 8, or to 16 above 8), request and token that has an
  * accumulator and that the page table can hold (or the window can show); at most 2 GiB
  * at a time, or one request's: batches that need more are taken in rounds of requests.
+ * (The lengths are on the device: a table much wider than they are costs scratch and
+ * time, unless attn_sink_decode_paged_weights_bounded is told the longest.)
  * Everything else as in attn_sink_decode_paged; hq at most 4096, and with weight_heads == 1 at most 6144
  * query heads rounded up like that.
  */
@@ -474,6 +476,19 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
                                    const float* sink, int win_first, int win_last, float scale,
                                    float* weights, int weight_heads, int weight_cap, attn_bf16* out,
                                    float* lse, void* stream);
+
+/*
+ * attn_sink_decode_paged_weights with a host bound of seqlens, max_seqlen >= 0.  Launches
+ * and scratch are sized by it instead of by the page table, which may be much wider
+ * than the requests are long; lengths past it are cut there (ATTN_SINK_DEV_SEQLEN_OOB).
+ */
+int attn_sink_decode_paged_weights_bounded(const attn_bf16* q, const attn_bf16* k_cache,
+                                           const attn_bf16* v_cache, const int32_t* page_table, int max_pages,
+                                           const int32_t* seqlens, int batch, int hq, int hkv, int head_dim,
+                                           int page_size, int num_pages, int max_seqlen, const float* sink,
+                                           int win_first, int win_last, float scale, float* weights,
+                                           int weight_heads, int weight_cap, attn_bf16* out, float* lse,
+                                           void* stream);
 
 /*
  * Eviction by accumulated weight.  A request with more than `budget` cached

@@ -51,6 +51,8 @@ _SIGS = {
     "attn_sink_kv_compact": [_P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _P],
     "attn_sink_decode_paged_weights": [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _I, _I, _F, _P, _I, _I,
                                        _P, _P, _P],
+    "attn_sink_decode_paged_weights_bounded": [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _I, _I, _F,
+                                               _P, _I, _I, _P, _P, _P],
     "attn_sink_evict_paged": [_P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P],
     "attn_sink_visible_ranges": [_P, _I, _I, _I, _P, _P],
     "attn_sink_visible_slots": [_P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P],
@@ -687,10 +689,12 @@ def attn_sink_kv_compact(k_cache, v_cache, page_table, src, counts, base=None, s
 
 
 def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, weights, sink=None, win_first=0,
-                                   win_last=0, scale=0.0, out=None, lse=None, return_lse=True, stream=None):
+                                   win_last=0, scale=0.0, out=None, lse=None, return_lse=True, stream=None,
+                                   max_seqlen=None):
     """attn_sink_decode_paged that also adds every visible token's attention weight to
     weights (B, Hkv or 1, cap) fp32, summed over the query heads of the KV head (or
-    all).  Returns (out, lse)."""
+    all).  max_seqlen: a host bound of seqlens, worth giving where page_table is much wider
+    than the requests are long (it sizes scratch and launches).  Returns (out, lse)."""
     dev = _device("q", q)
     if q.dim() != 3 or not _is(q, _BF16, dev, q.shape):
         _expect("q", q, _BF16, dev, (None, None, None))
@@ -702,9 +706,14 @@ def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, wei
     if len(shape) != 3 or shape[0] != B or not _is(weights, _F32, dev, shape):
         _expect("weights", weights, _F32, dev, (B, None, None))
     out, lse, sp, op, lp = _outputs(q, dev, (B, hq), sink, out, lse, return_lse, stream)
-    _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-         page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages, sp, int(win_first),
-         int(win_last), float(scale), weights.data_ptr(), shape[1], shape[2], op, lp)
+    rest = (sp, int(win_first), int(win_last), float(scale), weights.data_ptr(), shape[1], shape[2], op, lp)
+    sizes = (page_table.data_ptr(), max_pages, seqlens.data_ptr(), B, hq, hkv, d, ps, npages)
+    if max_seqlen is None:
+        _run("attn_sink_decode_paged_weights", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+             *sizes, *rest)
+    else:
+        _run("attn_sink_decode_paged_weights_bounded", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+             v_cache.data_ptr(), *sizes, int(max_seqlen), *rest)
     return out, lse
 
 

@@ -1,6 +1,7 @@
 // C ABI of the attention-with-sink library: argument validation, scratch
 // memory and kernel launches.  Every entry point is asynchronous on the
 // caller's stream and returns an ATTN_SINK_* status.
+#include <limits.h>
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -156,7 +157,7 @@ constexpr size_t kMaxScoreBytes = size_t(2) << 30;
 int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache, const int32_t* page_table,
                int max_pages, const int32_t* seqlens, int batch, int hq, int hkv, int head_dim, int page_size,
                int num_pages, const float* sink, int win_first, int win_last, float scale, attn_bf16* out,
-               float* lse, cudaStream_t s, attn::decode::Weights* w = nullptr) {
+               float* lse, cudaStream_t s, attn::decode::Weights* w = nullptr, int max_seqlen = -1) {
     if (batch == 0) return ATTN_SINK_OK;
     attn::decode::Args a;
     a.q = q;
@@ -178,6 +179,7 @@ int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_
     a.win_last = win_last;
     a.group = hq / hkv;
     a.scale = attn::resolve_scale(scale, head_dim);
+    a.max_seqlen = max_seqlen;
     const attn::decode::Plan pl = attn::decode::make_plan(a);
     // Partials, then (accumulated weights only) scores, of the requests of one round.
     size_t scores = 0;  // bytes, of a request
@@ -898,6 +900,17 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
                                    int hq, int hkv, int head_dim, int page_size, int num_pages, const float* sink,
                                    int win_first, int win_last, float scale, float* weights, int weight_heads,
                                    int weight_cap, attn_bf16* out, float* lse, void* stream) {
+    return attn_sink_decode_paged_weights_bounded(q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq, hkv,
+                                                  head_dim, page_size, num_pages, INT_MAX, sink, win_first, win_last,
+                                                  scale, weights, weight_heads, weight_cap, out, lse, stream);
+}
+
+int attn_sink_decode_paged_weights_bounded(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
+                                           const int32_t* page_table, int max_pages, const int32_t* seqlens,
+                                           int batch, int hq, int hkv, int head_dim, int page_size, int num_pages,
+                                           int max_seqlen, const float* sink, int win_first, int win_last,
+                                           float scale, float* weights, int weight_heads, int weight_cap,
+                                           attn_bf16* out, float* lse, void* stream) {
     t_last_error.clear();
     int rc = attn::validate_decode("decode_weights", q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq,
                                    hkv, head_dim, page_size, num_pages, win_first, out);
@@ -906,6 +919,7 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
     if (weight_heads != 1 && weight_heads != hkv)
         return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_heads %d must be 1 or hkv", weight_heads);
     if (weight_cap < 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: weight_cap must be >= 0");
+    if (max_seqlen < 0) return fail(ATTN_SINK_ERR_INVALID, "decode_weights: max_seqlen must be >= 0");
     if (hq > 4096) return fail(ATTN_SINK_ERR_UNSUPPORTED, "decode_weights: hq %d above 4096", hq);
     const int group = hq / hkv, padded = group <= 8 ? 8 : (group + 15) / 16 * 16;
     if ((long long)(hkv / weight_heads) * padded > kMaxWeightHeads)
@@ -918,7 +932,8 @@ int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache,
     w.heads = weight_heads;
     w.cap = weight_cap;
     return run_decode(q, k_cache, v_cache, page_table, max_pages, seqlens, batch, hq, hkv, head_dim, page_size,
-                      num_pages, sink, win_first, win_last, scale, out, lse, static_cast<cudaStream_t>(stream), &w);
+                      num_pages, sink, win_first, win_last, scale, out, lse, static_cast<cudaStream_t>(stream), &w,
+                      max_seqlen);
 }
 
 int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* page_table, int max_pages,

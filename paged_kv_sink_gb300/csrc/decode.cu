@@ -99,13 +99,12 @@ __device__ __forceinline__ uint32_t chunk_off(int row, int col) {
 }
 
 // Visible-token ranges of request b (decode query at position L-1), with L
-// clamped to the page table's capacity.
+// clamped to the longest possible request.
 __device__ __forceinline__ Ranges request_ranges(const SplitParams& p, int b, bool report) {
     int L = p.seqlens[b];
-    int cap = p.max_pages * p.page_size;
-    if (L > cap) {
+    if (L > p.max_tokens) {
         if (report) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-        L = cap;
+        L = p.max_tokens;
     }
     if (L < 0) L = 0;
     return visible_ranges(L - 1, p.win_first, p.win_last);
@@ -583,7 +582,7 @@ Plan make_plan(const Args& a) {
     Plan pl;
     pl.nt = a.group <= 8 ? 1 : 2;
     pl.hblocks = (a.group + 8 * pl.nt - 1) / (8 * pl.nt);
-    long long cap = (long long)a.max_pages * a.page_size;
+    const long long cap = a.max_tokens();
     long long nvis_max = cap;
     if (a.win_last > 0) {
         long long w = (long long)(a.win_first > 0 ? a.win_first : 0) + a.win_last;
@@ -634,6 +633,7 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     sp.part_o = part_o;
     sp.part_ml = part_ml;
     sp.max_pages = a.max_pages;
+    sp.max_tokens = a.max_tokens();
     sp.hq = a.hq;
     sp.hkv = a.hkv;
     sp.page_size = a.page_size;
@@ -719,6 +719,7 @@ cudaError_t launch_visible_slots(const int32_t* seqlens, const int32_t* page_tab
     sp.page_table = page_table;
     sp.seqlens = seqlens;
     sp.max_pages = max_pages;
+    sp.max_tokens = max_pages * page_size;
     sp.page_size = page_size;
     sp.page_shift = -1;
     sp.num_pages = num_pages;

@@ -21,6 +21,7 @@ struct SplitParams {
     float* part_o;    // (batch, hq, max_splits, head_dim) fp32, un-normalised
     float2* part_ml;  // (batch, hq, max_splits): (running max in log2 units, sum)
     int max_pages, hq, hkv, page_size, num_pages, win_first, win_last;
+    int max_tokens;    // longest possible request: lengths past it are cut there
     int split_tokens, max_splits, hblocks, group;
     int page_shift;    // log2(page_size) when it is a power of two, else -1
     float scale_log2;  // softmax scale * log2(e)
@@ -41,6 +42,12 @@ struct Args {
     float* lse;
     int max_pages, batch, hq, hkv, head_dim, page_size, num_pages, win_first, win_last, group;
     float scale;
+    int max_seqlen = -1;  // host bound of the lengths; -1: what the page table holds
+
+    int max_tokens() const {
+        const long long cap = (long long)max_pages * page_size;
+        return max_seqlen >= 0 && max_seqlen < cap ? max_seqlen : (int)cap;
+    }
 };
 
 // Split-KV work decomposition and scratch sizes.

@@ -88,6 +88,13 @@ def test_weights_refusals(lib, kw, rc, text):
     assert weights(lib, **kw) == rc and text in lib.attn_sink_last_error()
 
 
+@pytest.mark.parametrize("most,rc,text", [(-1, -1, b"max_seqlen"), (-2 ** 31, -1, b"max_seqlen"), (5, -1, b"weights")])
+def test_bounded_weights_refusals(lib, most, rc, text):
+    assert lib.attn_sink_decode_paged_weights_bounded(P, P, P, P, 4, P, 2, 8, 2, 64, 16, 8, most, None, 0, 0, 0.0, None, 2,
+                                                      64, P, None, None) == rc
+    assert text in lib.attn_sink_last_error()
+
+
 @pytest.mark.parametrize("kw,rc,text", [
     (dict(hq=1024, hkv=1024, heads=1), -2, b"6144"), (dict(hq=4000, hkv=400, heads=1), -2, b"6144"),
     (dict(hq=4096, hkv=512, heads=1, w=None), -1, b"NULL")])

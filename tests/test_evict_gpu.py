@@ -153,6 +153,30 @@ def test_weights_with_a_table_far_wider_than_the_requests(ext, cap, most, shared
         assert np.all(have[:, n:] == 1.0)
 
 
+@pytest.mark.parametrize("first,last", [(0, 0), (10, 50)])
+def test_weights_with_a_bound_of_the_lengths(ext, first, last):
+    """With max_seqlen the call behind a wide table is the one behind a table cut there, bit for
+    bit; a request past the bound is cut there and reported."""
+    lens, bound = [5000, 3, 640, 4096], 4096
+    k, v, table, sl = paged(lens, 2, 64, 16, seed=43)
+    wide = torch.full((4, 8192), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    q = torch.randn(4, 16, 64, generator=torch.Generator().manual_seed(44)).bfloat16()
+    sink = torch.zeros(16, device="cuda")
+    got = []
+    ext.device_status()
+    for t, n, kw in ((wide, sl, dict(max_seqlen=bound)), (table[:, :bound // 16].contiguous(), sl.clamp(max=bound), {})):
+        w = torch.zeros(4, 2, 8192 * 16, device="cuda")
+        got.append((*ext.attn_sink_decode_paged_weights(q.cuda(), k.cuda(), v.cuda(), t.cuda(), n.cuda(), w, sink, first,
+                                                        last, **kw), w))
+        assert ext.device_status() == (ext._lib.DEV_SEQLEN_OOB if kw else 0)
+    for a, b in zip(*got):
+        assert same(a, b)
+    got = [ext.attn_sink_decode_paged_weights(q.cuda(), k.cuda(), v.cuda(), wide.cuda(), sl.cuda(), w, max_seqlen=0)]
+    assert torch.all(got[0][0] == 0) and torch.all(torch.isneginf(got[0][1]))
+    assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
+
+
 @pytest.mark.parametrize("hq,hkv", [(2, 2), (6, 2), (24, 2)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_weights_of_infinite_keys(ext, hq, hkv, shared):
