@@ -462,13 +462,14 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
  *            caller sets new tokens' entries to 0 before their first call.  Tokens
  *            t >= weight_cap are left out and set ATTN_SINK_DEV_SEQLEN_OOB.
  * The sums have a fixed order (no atomics).  Scratch for scores: 4 bytes per query head
- * (those of a KV head rounded up to 8, or to 16 above 8), request and token that has an
- * accumulator and that the page table can hold (or the window can show); at most 2 GiB
- * at a time, or one request's: batches that need more are taken in rounds of requests.
- * (The lengths are on the device: a table much wider than they are costs scratch and
- * time, unless attn_sink_decode_paged_weights_bounded is told the longest.)
- * Everything else as in attn_sink_decode_paged; hq at most 4096, and with weight_heads == 1 at most 6144
- * query heads rounded up like that.
+ * (those of a KV head rounded up to 1, 2, 4, 8 or a multiple of 16), request and token
+ * that has an accumulator and that the page table can hold (or the window can show); at
+ * most 2 GiB at a time, or one request's: batches that need more are taken in rounds of
+ * requests.  (The lengths are on the device: a table much wider than they are costs
+ * scratch and time, unless attn_sink_decode_paged_weights_bounded is told the longest.)
+ * Everything else as in attn_sink_decode_paged; hq at most 4096, and with
+ * weight_heads == 1 at most 6144 query heads, those of a KV head rounded up to 8 or a
+ * multiple of 16.
  */
 int attn_sink_decode_paged_weights(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_cache,
                                    const int32_t* page_table, int max_pages, const int32_t* seqlens,

@@ -186,7 +186,7 @@ int run_decode(const attn_bf16* q, const attn_bf16* k_cache, const attn_bf16* v_
     int round = batch;
     if (w) {
         w->scores_cap = pl.nvis_max < w->cap ? pl.nvis_max : w->cap;
-        scores = (size_t)hkv * pl.hblocks * w->scores_cap * 8 * pl.nt * sizeof(float);
+        scores = (size_t)hkv * pl.hblocks * w->scores_cap * attn::decode::score_heads(a) * sizeof(float);
         const size_t most = scores ? kMaxScoreBytes / scores : (size_t)batch;
         const int rounds = most >= (size_t)batch ? 1 : most ? (int)((batch + most - 1) / most) : batch;
         round = (batch + rounds - 1) / rounds;

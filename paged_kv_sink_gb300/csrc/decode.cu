@@ -217,6 +217,14 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParam
             for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
     }
 
+    // kScores: this lane's place for the split's first token, and the tokens that have one
+    float* scores = nullptr;
+    int scored = 0;
+    if constexpr (kScores) {
+        scores = p.scores + (((long long)b * gridDim.y + blockIdx.y) * p.scores_cap + v0) * p.score_heads + 2 * (lane & 3);
+        scored = (int)min((long long)v1, p.scores_cap) - v0;
+    }
+
 #pragma unroll
     for (int s = 0; s < NSTAGE - 1; ++s) {
         if (s < nchunks) load_chunk(s, s);
@@ -260,19 +268,22 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const SplitParam
             const float x2 = ok1 ? sacc[nt][2] * p.scale_log2 : -INFINITY;
             const float x3 = ok1 ? sacc[nt][3] * p.scale_log2 : -INFINITY;
             if constexpr (kScores) {
-                // four lanes fill the 32 bytes of a token's 8 heads
-                const long long v = v0 + c * kChunk + crow;
-                float* dst = p.scores + ((((long long)b * gridDim.y + blockIdx.y) * p.scores_cap + v) * NT + nt) * 8 +
-                             2 * (lane & 3);
-                // heads that do not exist: no weight, whatever 0 times the key is
+                // four lanes have the scores of a token's 8 heads, two each
+                const int v = c * kChunk + crow;
                 const int hd = nt * 8 + 2 * (lane & 3);
+                float* dst = scores + v * p.score_heads + nt * 8;
+                // heads that do not exist: no weight, whatever 0 times the key is
                 const bool e0 = hd < nheads, e1 = hd + 1 < nheads;
-                const long long end = min((long long)v1, p.scores_cap);
-                if (v < end)
-                    *reinterpret_cast<float2*>(dst) = make_float2(e0 ? x0 : -INFINITY, e1 ? x1 : -INFINITY);
-                if (v + 8 < end)
-                    *reinterpret_cast<float2*>(dst + 8 * 8 * NT) =
-                        make_float2(e0 ? x2 : -INFINITY, e1 ? x3 : -INFINITY);
+                if (hd + 1 < p.score_heads) {
+                    if (v < scored)
+                        *reinterpret_cast<float2*>(dst) = make_float2(e0 ? x0 : -INFINITY, e1 ? x1 : -INFINITY);
+                    if (v + 8 < scored)
+                        *reinterpret_cast<float2*>(dst + 8 * p.score_heads) =
+                            make_float2(e0 ? x2 : -INFINITY, e1 ? x3 : -INFINITY);
+                } else if (hd < p.score_heads) {  // one head
+                    if (v < scored) dst[0] = x0;
+                    if (v + 8 < scored) dst[8] = x2;
+                }
             }
             const float mx0 = warp_max_g(fmaxf(x0, x2));
             const float mx1 = warp_max_g(fmaxf(x1, x3));
@@ -409,23 +420,29 @@ __global__ void __launch_bounds__(D) decode_combine_kernel(const SplitParams p, 
 // decode_combine_kernel does.
 // A weights block takes the statistics of its heads from the partials itself, so
 // nothing waits for the merge.  The scores that the split kernel stored (4 bytes per
-// query head and token, against 4 d for a KV head's K and V row) are read once, 8
-// tokens a thread in flight; the sums have a fixed order.  Requests are taken last
+// query head and token, those of a KV head rounded up to 1, 2, 4, 8 or a multiple of 16,
+// against 4 d for a KV head's K and V row) are read once, 8 tokens a thread in flight; the
+// sums have a fixed order.  Requests are taken last
 // first: the scores written last may still be in L2.
 // Bound by memory, as the split grid is.  64 requests of 1k to 32k tokens, 64 query heads
 // over 8 KV heads of 64: the call takes 484 - 496 us, of which the split grid, which
 // writes 285 MB of scores next to the 2.28 GB of K and V that it reads, has 400 (6.4
 // TB/s) and this launch 80 (356 MB, 4.4 TB/s).  Statistics, weights and merge as launches
 // of their own: 560 us.  4 requests of 256 to 2k tokens at head dim 128: 8.7 us against 10.4.
+// Scores of 8 heads a token whatever the group: one query head a KV head (64 requests of
+// 1k to 8k tokens, 12 heads of 64) 217 us instead of 180, four (32 windows of 8k tokens, 8 KV
+// heads of 128) 190 instead of 180.
 constexpr int kWeightThreads = 256;
-template <int NT>
-constexpr int kWeightTokens = NT == 1 ? 8 : 4;  // tokens per thread
+template <int H>
+constexpr int kWeightTokens = H <= 8 ? 8 : 4;  // tokens per thread
 
-template <int D, int NT>
+// H: heads whose scores lie side by side (score_heads).
+template <int D, int H>
 __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const SplitParams p, const float* sink,
                                                                        __nv_bfloat16* out, float* lse, float* weights,
                                                                        int heads, int cap, int wblocks, int tokens) {
-    constexpr int H = 8 * NT;
+    using Vec = typename std::conditional<H == 1, float, typename std::conditional<H == 2, float2, float4>::type>::type;
+    constexpr int kVec = sizeof(Vec) / sizeof(float);
     const int b = (int)(gridDim.z - 1 - blockIdx.z), tid = threadIdx.x;
     const Ranges r = request_ranges(p, b, false);
     const int nvis = visible_count(r);
@@ -447,19 +464,19 @@ __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const Spl
     const int blocks = hkv * p.hblocks / heads;  // head blocks that this accumulator sums
     // The first head block's scores and the accumulators are requested before the
     // statistics, which take two more loads in a row.
-    constexpr int kT = kWeightTokens<NT>;
+    constexpr int kT = kWeightTokens<H>;
     const float* xs = p.scores + ((long long)b * hkv * p.hblocks + head * blocks) * p.scores_cap * H;
     float* w = weights + ((size_t)b * heads + head) * cap;
     int v = 0, v1 = 0;  // this thread's first token, the chunk's end
-    float4 y[kT][H / 4];
+    Vec y[kT][H / kVec];
     float sum[kT];
     auto load = [&](int i) {
 #pragma unroll
         for (int k = 0; k < kT; ++k)
             if (v + k * kWeightThreads < v1) {
-                const float4* x = reinterpret_cast<const float4*>(xs + (i * p.scores_cap + v + k * kWeightThreads) * H);
+                const Vec* x = reinterpret_cast<const Vec*>(xs + (i * p.scores_cap + v + k * kWeightThreads) * H);
 #pragma unroll
-                for (int q = 0; q < H / 4; ++q) y[k][q] = __ldcs(x + q);
+                for (int q = 0; q < H / kVec; ++q) y[k][q] = __ldcs(x + q);
             }
     };
     auto start = [&](long long v0) {
@@ -506,12 +523,13 @@ __global__ void __launch_bounds__(kWeightThreads) decode_finish_kernel(const Spl
             for (int k = 0; k < kT; ++k) {
                 add[k] = 0.f;
 #pragma unroll
-                for (int q = 0; q < H / 4; ++q) {
-                    const float2* s4 = st + i * H + q * 4;
-                    add[k] += fast_exp2(y[k][q].x - s4[0].x) * s4[0].y;
-                    add[k] += fast_exp2(y[k][q].y - s4[1].x) * s4[1].y;
-                    add[k] += fast_exp2(y[k][q].z - s4[2].x) * s4[2].y;
-                    add[k] += fast_exp2(y[k][q].w - s4[3].x) * s4[3].y;
+                for (int q = 0; q < H / kVec; ++q) {
+                    const float* x = reinterpret_cast<const float*>(&y[k][q]);
+#pragma unroll
+                    for (int j = 0; j < kVec; ++j) {
+                        const float2 s = st[i * H + q * kVec + j];
+                        add[k] += fast_exp2(x[j] - s.x) * s.y;
+                    }
                 }
             }
             if (i + 1 < blocks) load(i + 1);
@@ -646,6 +664,7 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
     sp.group = a.group;
     sp.scale_log2 = a.scale * ATTN_LOG2E;
     sp.scores = w ? w->scores : nullptr;
+    sp.score_heads = score_heads(a);
     sp.scores_cap = w ? w->scores_cap : 0;
     sp.page_shift = -1;
     for (int sh = 0; sh < 31; ++sh)
@@ -683,7 +702,7 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
         // the longest request: blocks of shorter requests that find nothing to do cost a
         // microsecond each (two fit an SM).
         const long long units = (long long)a.batch * w->heads;
-        const int most = kWeightThreads * (pl.nt == 1 ? kWeightTokens<1> : kWeightTokens<2>);
+        const int most = kWeightThreads * (sp.score_heads <= 8 ? kWeightTokens<8> : kWeightTokens<16>);
         const int tokens = (w->scores_cap + most - 1) / most * units >= 4 * 152 ? most : 512;
         int wblocks = (int)((w->scores_cap + tokens - 1) / tokens);
         if (wblocks < 1) wblocks = 1;
@@ -691,10 +710,20 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
         const int per_block = kWeightThreads / a.head_dim, merges = (a.hq + per_block - 1) / per_block;
         cfg.gridDim = dim3((unsigned)(wblocks + (merges + w->heads - 1) / w->heads), w->heads, a.batch);
         cfg.blockDim = dim3(kWeightThreads);
-        cfg.dynamicSmemBytes = (size_t)a.hkv / w->heads * pl.hblocks * 8 * pl.nt * sizeof(float2);
-        auto finish = a.head_dim == 64 ? (pl.nt == 1 ? decode_finish_kernel<64, 1> : decode_finish_kernel<64, 2>)
-                                       : (pl.nt == 1 ? decode_finish_kernel<128, 1> : decode_finish_kernel<128, 2>);
-        e = cudaLaunchKernelEx(&cfg, finish, sp, sink, out, lse, w->weights, w->heads, w->cap, wblocks, tokens);
+        cfg.dynamicSmemBytes = (size_t)a.hkv / w->heads * pl.hblocks * sp.score_heads * sizeof(float2);
+        auto finish = [&](auto dim) {
+            constexpr int kD = decltype(dim)::value;
+            switch (sp.score_heads) {
+                case 1: return decode_finish_kernel<kD, 1>;
+                case 2: return decode_finish_kernel<kD, 2>;
+                case 4: return decode_finish_kernel<kD, 4>;
+                case 8: return decode_finish_kernel<kD, 8>;
+                default: return decode_finish_kernel<kD, 16>;
+            }
+        };
+        auto kernel = a.head_dim == 64 ? finish(std::integral_constant<int, 64>{})
+                                       : finish(std::integral_constant<int, 128>{});
+        e = cudaLaunchKernelEx(&cfg, kernel, sp, sink, out, lse, w->weights, w->heads, w->cap, wblocks, tokens);
     } else if (a.head_dim == 64) {
         e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<64>, sp, sink, out, lse);
     } else {

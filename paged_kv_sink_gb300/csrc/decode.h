@@ -26,7 +26,8 @@ struct SplitParams {
     int page_shift;    // log2(page_size) when it is a power of two, else -1
     float scale_log2;  // softmax scale * log2(e)
     // Accumulated attention weights only (else NULL):
-    float* scores;         // (batch, hkv * hblocks, scores_cap, 8 nt) scores of the visible tokens, log2 units
+    float* scores;         // (batch, hkv * hblocks, scores_cap, score_heads) scores of the visible tokens, log2 units
+    int score_heads;       // 16, or the group rounded up to 1, 2, 4 or 8
     long long scores_cap;  // visible tokens of a request that have a place (a token past it has no accumulator)
 };
 
@@ -67,6 +68,13 @@ struct Weights {
     float* scores;
     long long scores_cap;
 };
+
+// Heads of a head block whose scores are kept side by side.
+inline int score_heads(const Args& a) {
+    int n = 1;
+    while (n < a.group && n < 16) n *= 2;
+    return n;
+}
 
 Plan make_plan(const Args& a);
 // w != NULL: also adds every visible token's attention weight to w->weights.

@@ -153,6 +153,43 @@ def test_weights_with_a_table_far_wider_than_the_requests(ext, cap, most, shared
         assert np.all(have[:, n:] == 1.0)
 
 
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (6, 3), (9, 3), (12, 3), (5, 1), (12, 2), (7, 1), (8, 1), (9, 1), (32, 2), (34, 2)])
+def test_weights_of_every_group_size(ext, hq, hkv, shared):
+    """1 to 8 query heads a KV head, one tile of heads, and more."""
+    lens = [130, 1, 700]
+    k, v, table, sl = paged(lens, hkv, 64, 16, seed=hq)
+    q = torch.randn(3, hq, 64, generator=torch.Generator().manual_seed(45)).bfloat16()
+    heads = 1 if shared else hkv
+    dev = [t.cuda() for t in (q, k, v, table, sl)]
+    w = torch.zeros(3, heads, 701, device="cuda")
+    out, lse = ext.attn_sink_decode_paged_weights(*dev, w)
+    ref, ref_lse = ext.attn_sink_decode_paged(*dev)
+    assert ext.device_status() == 0 and same(out, ref) and same(lse, ref_lse)
+    for b, n in enumerate(lens):
+        kk, vv = (co.tokens(c, table[b], n) for c in (k, v))
+        _, _, P, _ = co.attend(q[b:b + 1], kk, vv, np.ones((1, n), bool), None, 0.125)
+        want = P[:, 0].reshape(heads, hq // heads, n).sum(1)
+        assert np.all(np.abs(w[b, :, :n].cpu().numpy() - want) <= 3e-4 * want) and not w[b, :, n:].any()
+
+
+def test_scores_take_no_more_room_than_the_heads_need(ext):
+    """64 requests, 8 query heads over 8 KV heads, accumulators of 65536 tokens: 134 MB of scores."""
+    lens = [40] * 64
+    k, v, table, sl = paged(lens, 8, 64, 16, seed=46)
+    wide = torch.full((64, 4096), -1, dtype=torch.int32)
+    wide[:, :table.shape[1]] = table
+    dev = [t.cuda() for t in (torch.ones(64, 8, 64).bfloat16(), k, v, wide, sl)]
+    w = torch.zeros(64, 8, 65536, device="cuda")
+    ext.attn_sink_decode_paged(*dev)
+    torch.cuda.synchronize()
+    free = torch.cuda.mem_get_info()[0]
+    ext.attn_sink_decode_paged_weights(*dev, w)
+    torch.cuda.synchronize()
+    assert free - torch.cuda.mem_get_info()[0] <= 256 << 20
+    np.testing.assert_allclose(w.sum(-1).cpu().numpy(), 1.0, rtol=3e-4)
+
+
 @pytest.mark.parametrize("first,last", [(0, 0), (10, 50)])
 def test_weights_with_a_bound_of_the_lengths(ext, first, last):
     """With max_seqlen the call behind a wide table is the one behind a table cut there, bit for
