@@ -419,6 +419,8 @@ int attn_sink_rope_kv_append(const attn_bf16* q, attn_bf16* q_out, const attn_bf
  * page id take no weight.  Rows of out and lse behind the last request's are
  * left as they were.  Cache slots that a request does not own never reach its results,
  * and a cached token's infinities and NaNs only the nodes that see it.
+ * As in every attention call here, scores, sums and lse are fp32, and the weights are
+ * rounded to bf16 where they meet V (out is off by at most 2^-8 of sum p |v| for it).
  * Supported: head_dim 64 or 128; hq % hkv == 0, hq / hkv <= 128; page_size a
  * power of two >= 8.  No gradient.
  */
@@ -455,7 +457,8 @@ int attn_sink_kv_compact(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t* 
  * cached token:
  *     weights[b][h][t] += sum_{g in h} exp(s_gt - LSE_g)
  * over the query heads g of KV head h (weight_heads == hkv) or over all query
- * heads (weight_heads == 1), for the visible tokens t of request b.  A token's
+ * heads (weight_heads == 1), for the visible tokens t of request b, from fp32 scores
+ * and sums (only where they meet V are the weights rounded to bf16).  A token's
  * weights of one call and query head sum to 1 less the sink's share.
  *
  *   weights  (batch, weight_heads, weight_cap) fp32 device, updated in place; the
