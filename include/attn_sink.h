@@ -348,8 +348,8 @@ int attn_sink_bwd_strided(const attn_bf16* q, const attn_bf16* k, const attn_bf1
  *     (x cos a - y sin a, y cos a + x sin a) * attn_scale,
  *     a = positions[row] * inv_freq[i]   (-a when inverse != 0),
  * and dimensions rotary_dim .. head_dim - 1 are copied bit for bit.  The gradient
- * of the rotation is the same call with inverse = 1.  Angles are reduced to
- * 2^-32 of a turn for every int32 position (negative ones included).
+ * of the rotation is the same call with inverse = 1.  The angle of any int32 position
+ * (negative ones included) is off by at most 1e-7 + |position| inv_freq 2^-52 radians.
  *
  *   q, q_out     (rows, hq, head_dim) bf16; q_out may be q
  *   k, k_out     (rows, hkv, head_dim) bf16, or both NULL (then hkv is ignored);

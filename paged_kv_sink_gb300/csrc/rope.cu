@@ -10,10 +10,12 @@
 // -a with the same factor (`inverse`).
 //
 // The angle: f_i / 2 pi is kept as a 64-bit fixed-point fraction of a turn, so
-// that p f_i modulo one turn is one wrapping 64-bit integer product, exact for
-// every int32 position (a fp32 product is 0.06 rad off at position 10^6), and
-// the range reduction of sine and cosine is the wrap itself.  The top 32 bits
-// (1.5e-9 rad) go to sincospif.
+// that p f_i modulo one turn is one wrapping 64-bit integer product that loses
+// nothing (a fp32 product is 0.06 rad off at position 10^6), and the range
+// reduction of sine and cosine is the wrap itself.  Two roundings are left: f_i / 2 pi is
+// formed in fp64, which p multiplies to |p| f_i 2^-52 rad (5e-7 at 2^31 for f_i = 1), and
+// the product's top 32 bits become the fp32 argument of sincospif, 24 bits of a half turn or
+// 1e-7 rad.  Both lie far below the 2^-8 of the bf16 outputs.
 //
 // It is bound by memory: every input element is read once and every output
 // element written once.  A block takes a few rows: it computes their r/2 sines

@@ -74,6 +74,33 @@ def test_rope_at_the_ends_of_int32(ext):
     assert same(yq[2].cpu(), q[2])  # position 0: no turn
 
 
+def test_rope_angles_keep_their_documented_accuracy(ext):
+    """An angle is off by at most 1e-7 + |p| f 2^-52 rad.  A head of ones and zeros turns into its
+    cosines and sines; at positions where one of them nearly vanishes the bf16 output shows
+    the angle's error itself.  Beside it: bf16 rounding (2^-8 of the value) and sincospif (2 ulp,
+    2^-22 of the value).  The exact angles are reduced with 50 digits."""
+    from decimal import Decimal, getcontext
+    getcontext().prec = 60
+    turn = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582")
+    f, _ = ext.attn_sink_rope_freqs(64)
+    near = []   # positions whose first pairs come closest to a multiple of a quarter turn
+    p = np.concatenate([np.arange(1, 300000), 2 ** 31 - 1 - np.arange(300000)])
+    for fi in f.cpu().tolist()[:4]:
+        quarters = p.astype(np.longdouble) * np.longdouble(fi) / np.longdouble(np.pi / 2)
+        near += p[np.argsort(np.abs(quarters - np.rint(quarters)))[:20]].tolist()
+    pos = near + [-x for x in near] + [0, 1, -1, 2 ** 31 - 1, -2 ** 31]
+    x = torch.zeros(len(pos), 1, 64).bfloat16()
+    x[..., :32] = 1.0
+    y, _ = ext.attn_sink_rope(x.cuda(), None, torch.tensor(pos).int().cuda(), f)
+    y = co.to_np(y)[:, 0]
+    for row, t in enumerate(pos):
+        for i, fi in enumerate(f.cpu().tolist()):
+            a = float((Decimal(t) * Decimal(fi)).remainder_near(turn))
+            slack = 1e-7 + abs(t) * fi * 2.0 ** -52
+            for got, want in ((y[row, i], np.cos(a)), (y[row, 32 + i], np.sin(a))):
+                assert abs(got - want) <= (2.0 ** -8 + 2.0 ** -22) * (abs(want) + slack) + slack, (t, i)
+
+
 @pytest.mark.parametrize("interleaved,r", [(False, 64), (True, 64), (False, 22), (True, 22)])
 def test_rope_in_place_on_a_packed_buffer(ext, interleaved, r):
     """Column ranges of a packed (T, hq + 2 hkv, d) buffer, rotated in place, equal the
