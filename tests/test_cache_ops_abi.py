@@ -63,6 +63,11 @@ def test_tree_refusals(lib, kw, rc, text):
     assert tree(lib, **kw) == rc and text in lib.attn_sink_last_error()
 
 
+def test_tree_refuses_a_negative_length_bound(lib):
+    assert tree(lib, mk=-1) == -1 and b"sizes" in lib.attn_sink_last_error()
+    assert tree(lib, mk=-2 ** 31) == -1 and tree(lib, mk=0, total=0) == 0
+
+
 def compact(lib, kc=P, vc=Q, src=P, batch=2, heads=1, rows=4, hkv=2, d=64, ps=16, np_=8, mp=4):
     return lib.attn_sink_kv_compact(kc, vc, P, mp, src, P, None, batch, heads, rows, hkv, d, ps, np_, None)
 

@@ -358,3 +358,18 @@ def test_rows_of_a_warp_with_walks_of_different_lengths(ext, hq, hkv, d, page):
             want[sees[:, None], :, torch.arange(i, d, 32)[None]] = float("inf")
         assert same(got[row:row + n], want), b
         row += n
+
+
+def test_length_estimates_change_nothing(ext):
+    """max_seqlen_k is checked for its sign alone: the keys are split by the lengths on the
+    device, so any estimate gives the same bits."""
+    x = make([300, 2500, 77], [4, 19, 8], 8, 2, 64, 16)
+    want, want_lse = run(ext, x, max_k=2519)
+    check(x, want, want_lse)
+    dev = {n: x[n].cuda() for n in ("q", "k", "v", "table", "sl", "cu", "parents", "sink")}
+    args = [dev[n] for n in ("q", "k", "v", "table", "cu", "sl", "parents")]
+    for max_k in (0, 1, 100000, 2 ** 31 - 1):
+        out, lse = ext.attn_sink_tree_paged(*args, 19, max_k, sink=dev["sink"])
+        assert same(out.cpu(), want) and same(lse.cpu(), want_lse)
+    with pytest.raises(ext.AttnSinkError, match="sizes"):
+        ext.attn_sink_tree_paged(*args, 19, -1, sink=dev["sink"])
