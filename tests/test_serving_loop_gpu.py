@@ -218,3 +218,62 @@ def test_caches_whose_offsets_pass_32_bits(ext):
         torch.cuda.empty_cache()
     for a, b in zip(*got):
         assert torch.equal(a, b) if a.dtype == torch.int32 else same(a, b)
+
+
+def test_a_captured_loop_equals_the_eager_one(ext):
+    """A decode step with its weights, an eviction, a draft and the move of its accepted path,
+    captured in one CUDA graph, give the eager calls' bits on every replay."""
+    from cache_ops import same
+    sl = torch.tensor([180, 95]).int()
+    table = torch.randperm(32, generator=torch.Generator().manual_seed(51)).int().view(2, 16)
+    g = torch.Generator().manual_seed(52)
+    k, v = (torch.randn(32, PAGE, HKV, D, generator=g).bfloat16() for _ in range(2))
+    T = [1, 1], [6, 3]
+    parents = torch.tensor([-1, 0, 0, 1, 3, -1] + [-1, 0, 1]).int().cuda()
+    depth = torch.tensor([0, 1, 1, 2, 3, 0] + [0, 1, 2]).int().cuda()
+    owner = torch.tensor([0] * 6 + [1] * 3).cuda()
+    path = torch.tensor([[0, 1, 3], [0, 1, 0]]).int().cuda()
+    accepted, drafted = torch.tensor([3, 2]).int().cuda(), torch.tensor([6, 3]).int().cuda()
+    table, c2 = table.cuda(), cu(T[1]).cuda()
+    f, m = ext.attn_sink_rope_freqs(D, scaling="bands", factor=4.0, original_len=128)
+    sink = torch.linspace(-1, 2, HQ).cuda()
+    kc, vc, lens = k.cuda(), v.cuda(), sl.cuda()
+    w = torch.zeros(2, HKV, table.shape[1] * PAGE, device="cuda")
+    rows = [torch.empty(sum(n), h, D, dtype=torch.bfloat16, device="cuda") for n in T for h in (HQ, HKV, HKV)]
+
+    def reset(seed):
+        g = torch.Generator().manual_seed(seed)
+        kc.copy_(k), vc.copy_(v), lens.copy_(sl), w.zero_()
+        for r in rows:
+            r.copy_(torch.randn(r.shape, generator=g))
+
+    def step():
+        lens.add_(1)
+        q = ext.attn_sink_rope_kv_append(*rows[:3], kc, vc, table, lens, f, attn_scale=m)
+        out, lse = ext.attn_sink_decode_paged_weights(q, kc, vc, table, lens, w, sink, 4, 100)
+        new, kept = ext.attn_sink_evict_paged(kc, vc, table, lens, w, 96, keep_first=4, keep_last=32)
+        n = new + drafted
+        pos = new[owner] + depth
+        q2 = ext.attn_sink_rope_kv_append(*rows[3:], kc, vc, table, n, f, cu_new=c2, max_new=6, positions=pos, attn_scale=m)
+        out2, lse2 = ext.attn_sink_tree_paged(q2, kc, vc, table, c2, n, parents, 6, 110, sink=sink)
+        ext.attn_sink_kv_compact(kc, vc, table, new[:, None] + path, accepted, base=new)
+        after = new + accepted
+        out3, lse3 = ext.attn_sink_decode_paged(q, kc, vc, table, after, sink)
+        return [q, out, lse, new, kept, q2, out2, lse2, after, out3, lse3]
+
+    want = []
+    for seed in (1, 2):
+        reset(seed)
+        want.append([t.clone() for t in step() + [kc, vc, w]])
+    torch.cuda.synchronize()
+    assert not same(want[0][1], want[1][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (2, 1, 2):
+        reset(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got + [kc, vc, w], want[seed - 1]):
+            assert torch.equal(a, b) if a.dtype == torch.int32 else same(a, b)
+    assert ext.device_status() == 0
