@@ -11,7 +11,7 @@ __all__ = ["attn_sink_rope_freqs"]
 
 
 def attn_sink_rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, low=1.0, high=None,
-                         attn_factor=None, device="cuda"):
+                         attn_factor=None, round_ends=True, device="cuda"):
     """(inv_freq, attn_scale): the rotary_dim / 2 inverse frequencies
     base^(-2i / rotary_dim) in radians per position as an fp64 tensor on ``device``,
     and the factor on the rotated part, changed by ``scaling`` to stretch a context
@@ -25,8 +25,9 @@ def attn_sink_rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, ori
       original context: below ``low`` (1) divided by ``factor``, above ``high`` (4)
       kept, between them blended linearly in n_i.
     * "yarn": as "bands" but with the blend linear in the pair index i, between the
-      indices (rounded outwards) of pairs with ``high`` (32) and ``low`` (1) turns,
-      and an attention factor of 0.1 ln(factor) + 1.
+      indices of pairs with ``high`` (32) and ``low`` (1) turns (rounded outwards, or as
+      they are where ``round_ends`` is false), and an attention factor of
+      0.1 ln(factor) + 1.
 
     ``attn_factor`` replaces the attention factor (1, or that of "yarn")."""
     r = int(rotary_dim)
@@ -55,7 +56,10 @@ def attn_sink_rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, ori
         else:
             def index(turns):  # of the pair that makes so many turns
                 return r * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
-            first, last = max(math.floor(index(high)), 0), min(math.ceil(index(low)), r - 1)
+            first, last = index(high), index(low)
+            if round_ends:
+                first, last = math.floor(first), math.ceil(last)
+            first, last = max(first, 0), min(last, r - 1)
             keep = [1.0 - (i - first) / max(last - first, 0.001) for i in range(r // 2)]
             scale = 0.1 * math.log(factor) + 1.0
         keep = [min(max(x, 0.0), 1.0) for x in keep]

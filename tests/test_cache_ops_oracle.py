@@ -63,6 +63,23 @@ def test_rope_frequencies():
     assert float(s[i]) == pytest.approx(float(f[i]) * (t + (1 - t) / 8)) and m == 1.5
 
 
+def test_rope_frequencies_with_an_unrounded_ramp():
+    """The blend starts and ends at fractional pair indices, where a pair would make exactly 32
+    and 1 turns of the original context; by default it is rounded outwards."""
+    r, base, old, factor = 64, 150000.0, 4096, 32.0
+    f, _ = attn_sink_rope_freqs(r, base=base, device="cpu")
+    got, m = attn_sink_rope_freqs(r, base=base, scaling="yarn", factor=factor, original_len=old, round_ends=False,
+                                  device="cpu")
+    rounded, _ = attn_sink_rope_freqs(r, base=base, scaling="yarn", factor=factor, original_len=old, device="cpu")
+    # base^(-2 i / r) old / (2 pi) = turns, solved for i
+    first, last = (r / 2 * math.log(old / (2 * math.pi * n)) / math.log(base) for n in (32.0, 1.0))
+    assert first != round(first) and last != round(last)
+    for got_f, a, b in ((got, first, last), (rounded, math.floor(first), math.ceil(last))):
+        stretched = np.clip((np.arange(32) - a) / (b - a), 0.0, 1.0)
+        np.testing.assert_allclose(got_f.numpy(), f.numpy() * (1 - stretched + stretched / factor), rtol=1e-13)
+    assert m == pytest.approx(0.1 * math.log(factor) + 1) and not torch.equal(got, rounded)
+
+
 @pytest.mark.parametrize("kw", [dict(rotary_dim=7), dict(rotary_dim=0), dict(rotary_dim=64, scaling="other"),
                                 dict(rotary_dim=64, base=1.0), dict(rotary_dim=64, scaling="linear", factor=0.5),
                                 dict(rotary_dim=2, scaling="base", factor=2.0), dict(rotary_dim=64, scaling="yarn"),
