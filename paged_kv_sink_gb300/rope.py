@@ -11,7 +11,7 @@ __all__ = ["attn_sink_rope_freqs"]
 
 
 def attn_sink_rope_freqs(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_len=None, low=1.0, high=None,
-                         attn_factor=None, round_ends=True, device="cuda"):
+                         attn_factor=None, device="cuda", round_ends=True):
     """(inv_freq, attn_scale): the rotary_dim / 2 inverse frequencies
     base^(-2i / rotary_dim) in radians per position as an fp64 tensor on ``device``,
     and the factor on the rotated part, changed by ``scaling`` to stretch a context
