@@ -37,6 +37,20 @@ __device__ __forceinline__ void raise_status(int bits) { atomicOr(&g_dev_status,
         return (int)e;                                                               \
     }
 
+// SMs of the current device (152 on GB300), asked for once per device and unit.
+static inline int num_sms() {
+    static int sms[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64) return 152;
+    if (!sms[dev]) {
+        int v = 0;
+        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+        sms[dev] = v > 0 ? v : 152;
+    }
+    return sms[dev];
+}
+
 // Nanosecond wall clock of the GPU.
 __device__ __forceinline__ uint64_t globaltimer_ns() {
     uint64_t t;

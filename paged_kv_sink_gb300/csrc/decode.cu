@@ -586,19 +586,6 @@ __global__ void visible_slots_kernel(SplitParams p, int32_t* slots, int max_visi
 // ---------------------------------------------------------------------------
 // Host side.
 
-static int num_sms_cached() {
-    static int sms[64] = {0};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64) return 152;
-    if (!sms[dev]) {
-        int v = 0;
-        cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        sms[dev] = v > 0 ? v : 152;
-    }
-    return sms[dev];
-}
-
 Plan make_plan(const Args& a) {
     Plan pl;
     pl.nt = a.group <= 8 ? 1 : 2;
@@ -616,7 +603,7 @@ Plan make_plan(const Args& a) {
     // split streams at least 256 tokens (the ring's fill and drain amortised)
     // and at most 256 KB of K per split (2048 tokens at d 64, 1024 at d 128):
     // longer splits leave too few CTAs, shorter ones are latency-bound waves.
-    const long long slots = (long long)num_sms_cached() * (a.head_dim == 64 ? 4 : 2);
+    const long long slots = (long long)num_sms() * (a.head_dim == 64 ? 4 : 2);
     const long long per_unit = (2 * slots + units - 1) / units;  // splits wanted per (request, head block)
     long long sp = (nvis_max + per_unit - 1) / per_unit;
     sp = (sp + kChunk - 1) / kChunk * kChunk;
@@ -706,10 +693,10 @@ cudaError_t launch(const Args& a, const Plan& pl, float* part_o, float2* part_ml
         // microsecond each (two fit an SM).
         const long long units = (long long)a.batch * w->heads;
         const int most = kWeightThreads * (sp.score_heads <= 8 ? kWeightTokens<8> : kWeightTokens<16>);
-        const int tokens = (w->scores_cap + most - 1) / most * units >= 4 * 152 ? most : 512;
+        const int tokens = (w->scores_cap + most - 1) / most * units >= 4 * num_sms() ? most : 512;
         int wblocks = (int)((w->scores_cap + tokens - 1) / tokens);
         if (wblocks < 1) wblocks = 1;
-        if (wblocks * units >= 16 * 152) wblocks = (wblocks + 1) / 2;
+        if (wblocks * units >= 16 * num_sms()) wblocks = (wblocks + 1) / 2;
         const int per_block = kWeightThreads / a.head_dim, merges = (a.hq + per_block - 1) / per_block;
         cfg.gridDim = dim3((unsigned)(wblocks + (merges + w->heads - 1) / w->heads), w->heads, a.batch);
         cfg.blockDim = dim3(kWeightThreads);

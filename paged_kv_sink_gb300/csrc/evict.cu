@@ -433,7 +433,7 @@ cudaError_t launch_select(const SelectArgs& a, cudaStream_t s) {
     // 8192 tokens do (2 us a digit).
     const long long cap = a.cap < a.token_cap ? a.cap : a.token_cap;
     int parts = 1;
-    while (parts < kMaxCluster && (long long)a.batch * a.heads * parts * 2 <= 152 && cap / (2 * parts) >= 8192)
+    while (parts < kMaxCluster && (long long)a.batch * a.heads * parts * 2 <= num_sms() && cap / (2 * parts) >= 8192)
         parts *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.heads * parts), a.batch);
@@ -465,7 +465,7 @@ cudaError_t launch_move(const MoveArgs& a, cudaStream_t s) {
     // 181 us; one request of 100k tokens: 32 88 us, 64 173 us, 256 700 us).
     int lanes = 1;
     while (lanes < 128 && head_bytes % (32 * lanes) == 0) lanes *= 2;
-    while (lanes > 2 && (long long)head_bytes / (16 * lanes) * a.heads * 2 * a.batch < 2 * 152) lanes /= 2;
+    while (lanes > 2 && (long long)head_bytes / (16 * lanes) * a.heads * 2 * a.batch < 2 * num_sms()) lanes /= 2;
     int page_shift = -1;
     for (int sh = 0; sh < 31; ++sh)
         if ((1 << sh) == a.page_size) page_shift = sh;
@@ -485,8 +485,8 @@ cudaError_t launch_move(const MoveArgs& a, cudaStream_t s) {
     auto choose = [&](auto check) {
         constexpr bool kC = decltype(check)::value;
         if (a.max_rows <= 2 * (kMoveThreads / lanes)) return launch(move_kernel<kC, 2, 2>, kMoveSmem<2, 2>);
-        if (ctas <= 152) return launch(move_kernel<kC, 8, 4>, kMoveSmem<8, 4>);
-        if (ctas <= 2 * 152) return launch(move_kernel<kC, 4, 4>, kMoveSmem<4, 4>);
+        if (ctas <= num_sms()) return launch(move_kernel<kC, 8, 4>, kMoveSmem<8, 4>);
+        if (ctas <= 2 * num_sms()) return launch(move_kernel<kC, 4, 4>, kMoveSmem<4, 4>);
         return launch(move_kernel<kC, 2, 4>, kMoveSmem<2, 4>);
     };
     return a.first_moved ? choose(std::false_type{}) : choose(std::true_type{});

@@ -268,7 +268,7 @@ static cudaError_t launch_d(const Args& a, cudaStream_t s) {
     const int heads = a.hq + (a.k ? a.hkv : 0) + (append ? a.hkv : 0);
     const long long longest = append ? a.max_new : a.rows;
     // Rows per block: one until every SM has several blocks, then up to eight.
-    int tile = a.rows / (152 * 8);
+    int tile = a.rows / (num_sms() * 8);
     tile = tile < 1 ? 1 : tile > kMaxRows ? kMaxRows : tile;
     const dim3 grid((unsigned)((longest + tile - 1) / tile), append ? a.batch : 1);
     const size_t smem = (size_t)tile * (D / 2) * sizeof(float2);

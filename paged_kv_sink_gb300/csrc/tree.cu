@@ -1068,7 +1068,7 @@ static cudaError_t make_map(CUtensorMap* m, const void* base, int D, int heads, 
 
 Plan make_plan(const Args& a) {
     Plan pl;
-    const int slots = 152 * (a.head_dim == 64 ? 2 : 1);
+    const int slots = num_sms() * (a.head_dim == 64 ? 2 : 1);
     pl.ctas = slots >= a.hkv ? slots / a.hkv * a.hkv : a.hkv;
     pl.part_o_bytes = (size_t)pl.ctas * 2 * BM * a.head_dim * sizeof(float);
     pl.part_ml_bytes = (size_t)pl.ctas * 2 * BM * sizeof(float2);
@@ -1126,7 +1126,7 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
         return e;
     }
     cudaLaunchConfig_t cfg = {};
-    const int rows = (long long)a.batch * a.max_seqlen_q * a.hq <= 152 * 32 ? 1 : 8;
+    const int rows = (long long)a.batch * a.max_seqlen_q * a.hq <= num_sms() * 32 ? 1 : 8;
     const long long warps = (long long)a.max_seqlen_q * a.hkv * ((p.group + rows - 1) / rows);
     cfg.gridDim = dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps), a.batch);
     cfg.blockDim = dim3(kCombineWarps * 32);
