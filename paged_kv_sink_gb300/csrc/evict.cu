@@ -82,7 +82,7 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* scratch, ui
 // or not, and with a list of the candidates after the first digit.)
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs p, int capacity) {
     extern __shared__ uint32_t keys[];  // of a round, `capacity`; then the kept tokens of a round as 16-bit offsets
-    __shared__ uint32_t hist[2][kBins];
+    __shared__ __align__(16) uint32_t hist[2][kBins];  // read four bins at a time
     __shared__ uint32_t warp_sum[4][kSelWarps];
     __shared__ uint32_t s_prefix, s_rank, s_ties, s_totals[2];
     __shared__ int s_first;
