@@ -713,7 +713,7 @@ def attn_sink_decode_paged_weights(q, k_cache, v_cache, page_table, seqlens, wei
              *sizes, *rest)
     else:
         _run("attn_sink_decode_paged_weights_bounded", dev, stream, q.data_ptr(), k_cache.data_ptr(),
-             v_cache.data_ptr(), *sizes, int(max_seqlen), *rest)
+             v_cache.data_ptr(), *sizes, min(int(max_seqlen), 2 ** 31 - 1), *rest)
     return out, lse
 
 

@@ -209,6 +209,9 @@ def test_weights_with_a_bound_of_the_lengths(ext, first, last):
         assert ext.device_status() == (ext._lib.DEV_SEQLEN_OOB if kw else 0)
     for a, b in zip(*got):
         assert same(a, b)
+    dev = [t.cuda() for t in (q, k, v, wide, sl)]
+    a, b = (ext.attn_sink_decode_paged_weights(*dev, w.clone(), **kw) for kw in ({}, dict(max_seqlen=2 ** 32 + 7)))
+    assert same(a[0], b[0]) and same(a[1], b[1]) and ext.device_status() == 0
     got = [ext.attn_sink_decode_paged_weights(q.cuda(), k.cuda(), v.cuda(), wide.cuda(), sl.cuda(), w, max_seqlen=0)]
     assert torch.all(got[0][0] == 0) and torch.all(torch.isneginf(got[0][1]))
     assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
