@@ -26,7 +26,7 @@
 // pipes never limit the gather rate.  They take bf16: the weights e^{s - M} are rounded
 // to it for P V (at most 2^-8 of each; the sums, the scores and what accumulates are
 // fp32, of unrounded weights), which takes the error of O, as a 2-norm over that of O, from
-// the 1.7e-3 of its own rounding to 2.2e-3 - 2.5e-3.
+// the 1.7e-3 of its own rounding to 2.0e-3 - 2.5e-3.
 #include "common.cuh"
 #include "decode.h"
 

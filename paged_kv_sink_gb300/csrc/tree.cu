@@ -41,7 +41,7 @@
 // divides them is that of the unrounded ones), because P V takes P in V's type: P as two
 // bf16 parts would take twice the tensor work and, at d 64, more tensor memory than two
 // CTAs an SM have.  Next to the output's own rounding it takes the error of O, as a
-// 2-norm over that of O, from 1.7e-3 to 2.2e-3 - 2.5e-3, as in every attention call of
+// 2-norm over that of O, from 1.7e-3 to 2.0e-3 - 2.5e-3, as in every attention call of
 // this library; LSE does not see it.
 //
 // Masks: prefix tiles that every row sees whole are not masked at all.  In the
@@ -54,13 +54,13 @@
 //     run).  (One CTA per (request, row tile, KV head, range of keys), dispatched by the
 //     hardware: 222 us.)
 //   * At d 64 with several row tiles a request the softmax.  16 requests of 1k to 16k tokens
-//     and 16 to 64 nodes, 64 heads over 8: 131 us for 87 steps a CTA of 1.2 us each (two
+//     and 16 to 64 nodes, 64 heads over 8: 132 us for 87 steps a CTA of 1.2 us each (two
 //     CTAs an SM; 1086 TFLOP/s at 1.175 us: the exponentials' serial chain).  The first S
 //     is ready after 6 us, a masked tile with the drafted tokens costs 2 us more than
 //     another, the last gang ends 7 us after the median one, the merge takes 4.5 us, and 81
 //     % of the tiles' rows hold a node.  HBM is read for 474 MB (301 MB of cache; 781 MB
 //     and 138 us while each row tile took its keys from the first on).
-//   * One request: latency.  7 nodes over 2000 tokens 13.8 us: first S after 3.7 us, two
+//   * One request: latency.  7 nodes over 2000 tokens 13.9 us: first S after 3.7 us, two
 //     steps and the epilogue 4.5, the merge 3.
 // With plain fp32 arithmetic, a CTA per node and KV head, the first two took 19.7 and 21.8
 // ms; without the runs the second 163 us.
@@ -89,7 +89,8 @@ constexpr int kTileRing = 8;  // tiles that the K producer may be ahead of the s
 constexpr int kMinSteps = 2;  // of a run
 constexpr int kThreads = 256;
 // 128 registers per thread at launch, moved from the control warps to the softmax
-// warps: 128 * 48 + 128 * 208 = 256 * 128.
+// warps: 128 * 48 + 128 * 208 = 256 * 128.  At d 128 they leave 13 words of a thread in
+// local memory (written once and read 28 times in the code), at d 64 one.
 constexpr int kRegsCtrl = 48, kRegsSoftmax = 208;
 constexpr uint32_t kAtom = 128 * 128;  // one 128-byte-swizzled atom column: 128 rows x 64 bf16
 constexpr float kRescaleThreshold = 64.0f;      // log2 units

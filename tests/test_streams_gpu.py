@@ -88,3 +88,25 @@ def test_outputs_dropped_while_the_current_stream_still_reads_them(ext, name):
     for a, b in zip(copies, want):
         assert torch.equal(a, b) if a.dtype == torch.int32 else same(a, b)
     del again
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_forked_stream_inside_a_capture(ext, name):
+    """A call on a stream that the capture forked to, its outputs made inside the capture."""
+    call, state = case(ext, name, 4)
+    before = [t.clone() for t in state]
+    want = [t.clone() for t in call(None)] + [t.clone() for t in state]
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = list(call(side))
+        torch.cuda.current_stream().wait_stream(side)
+        got = [t.clone() for t in got]
+    for _ in range(2):
+        for t, b in zip(state, before):
+            t.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got + list(state), want):
+            assert torch.equal(a, b) if a.dtype == torch.int32 else same(a, b)
