@@ -52,9 +52,9 @@ NCU_TRAFFIC = {
     # bwd_main128_kernel on the head-dim-128 training step: 1.910 GB + 0.946 GB
     "bwd_main128_kernel/train_d128": {"src": "8450e18315e5943f", "bytes": 2_856_080_128},
     # decode_split_kernel: 1.943 GB + 0.010 GB
-    "decode/decode_sink": {"src": "4b4888ba36de7c3d", "bytes": 1_953_487_872},
+    "decode/decode_sink": {"src": "37c5115fc316ae42", "bytes": 1_953_938_176},
     # decode_split_kernel: 1.074 GB + 0.007 GB
-    "decode/decode_window": {"src": "4b4888ba36de7c3d", "bytes": 1_080_692_480},
+    "decode/decode_window": {"src": "37c5115fc316ae42", "bytes": 1_080_723_200},
 }
 
 
