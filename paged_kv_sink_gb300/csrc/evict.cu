@@ -74,12 +74,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* scratch, ui
 // shared memory.  With one round the weights are read once: up to 131072 tokens while a
 // cluster of 8 is given to each list (at most 19 lists), down to 16384 where the lists
 // fill the GPU by themselves (more than 76).  With more, every digit and the ordered pass
-// load all rounds again, one after the other.  For the ordered pass a thread owns a run of consecutive tokens (an odd
-// number, so that a warp's reads fall into different banks); a scan of the runs' kept
-// counts gives every kept token its rank, and the list leaves through shared memory.
+// load all rounds again, one after the other.  For the ordered pass a thread owns a run of
+// consecutive tokens (an odd number, so that a warp's reads fall into different banks); a
+// scan of the runs' kept counts gives every kept token its rank, and the list leaves
+// through shared memory.
 // It is bound by the latency of its steps: 256 lists of 8k to 16k tokens take 22 us, one
-// of 2k 6.8 us; 256 of 16384 tokens 24 us, of 16385 (two rounds) 41, of 65536 124.  (24 us with ballots over 32 tokens at a time, with keys in registers
-// or not, and with a list of the candidates after the first digit.)
+// of 2k 6.8 us.  (24 us with ballots over 32 tokens at a time, with keys in registers or
+// not, and with a list of the candidates after the first digit.)  256 lists of 16384
+// tokens take 24 us, of 16385 (two rounds) 41, of 65536 124.
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectArgs p, int capacity) {
     extern __shared__ uint32_t keys[];  // of a round, `capacity`; then the kept tokens of a round as 16-bit offsets
     __shared__ __align__(16) uint32_t hist[2][kBins];  // read four bins at a time
