@@ -48,7 +48,7 @@
  *    are caught on the device: the offending load is skipped and a sticky
  *    device status is set, which attn_sink_device_status() reports.
  *  - One call takes at most 65535 requests (batch) in the forward, paged
- *    forward, decode, append, tree, compaction and eviction entry points, and at most 65535 * 128 query
+ *    forward, decode, append, tree, compaction, eviction, verification and page entry points, and at most 65535 * 128 query
  *    rows per request in the forward ones (each is one grid dimension of the
  *    launch); larger calls return ATTN_SINK_ERR_UNSUPPORTED.
  */
@@ -80,7 +80,13 @@ enum {
                                         aligned; the forward kernel did nothing            */
     ATTN_SINK_DEV_ORDER = 16,        /* attn_sink_kv_compact: a source token that is not after
                                         the one before it, or lies before its destination  */
-    ATTN_SINK_DEV_TREE = 32          /* attn_sink_tree_paged: a parent outside [-1, own index) */
+    ATTN_SINK_DEV_TREE = 32,         /* attn_sink_tree_paged: a parent outside [-1, own index);
+                                        attn_sink_verify_draft: outside [0, own index)     */
+    ATTN_SINK_DEV_VALUE = 64,        /* attn_sink_kv_append_q8: an infinity or NaN was replaced */
+    ATTN_SINK_DEV_PROB = 128,        /* attn_sink_verify_draft: a drafted token outside the
+                                        vocabulary, or a row without any probability       */
+    ATTN_SINK_DEV_POOL = 256         /* attn_sink_pages_*: too few free pages, or a table,
+                                        lengths and counts that contradict each other      */
 };
 
 /*
@@ -520,6 +526,186 @@ int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t*
                           int weight_cap, int hkv, int head_dim, int page_size, int num_pages, int budget,
                           int keep_first, int keep_last, float* weights_out, int32_t* kept,
                           int32_t* new_seqlens, void* stream);
+
+/* Formats of an 8-bit cache and types of probabilities. */
+enum { ATTN_SINK_E4M3 = 0, ATTN_SINK_INT8 = 1 };
+enum { ATTN_SINK_F32 = 0, ATTN_SINK_BF16 = 1, ATTN_SINK_F16 = 2 };
+
+/*
+ * The 8-bit paged cache.  k_cache and v_cache are (num_pages, page_size, hkv, head_dim)
+ * codes, e4m3 or int8; k_scale and v_scale are (num_pages, page_size / block, hkv) fp32,
+ * one scale for `block` tokens of a KV head.  block divides page_size.  A code c stands for
+ * c * scale.
+ *
+ * attn_sink_kv_append_q8 writes new K/V rows into it (attn_sink_kv_append's slots, checks
+ * and status bits).  For every block of tokens that receives rows, and each KV head of K
+ * and of V, with qmax = 448 (e4m3) or 127 (int8):
+ *   - needed = the least power of two s >= 2^-64 with max|x| <= qmax s over the new rows;
+ *   - scale = needed where the block's first token is new, else max(old scale, needed);
+ *   - codes = x / scale, rounded to nearest, ties to even.  If the scale grew, the codes of
+ *     the tokens that the block has are scaled down by the quotient and rounded again.
+ * Infinities become the largest code of their sign, NaN 0; both set
+ * ATTN_SINK_DEV_VALUE and do not count for the scale.  Codes behind the last token of a
+ * block are left as they were.  Pages that two requests share must not be written by either
+ * (attn_sink_pages_reserve copies them).
+ *
+ *   k_new, v_new    (total_new, hkv, head_dim) bf16; *_row_stride as in attn_sink_rope
+ *   cu_new          (batch+1,) int32 device, or NULL: request b's one new row is row b
+ *   seqlens         (batch,) int32 device, the new rows included
+ *   total_new       host row count of k_new and v_new; rows past it are left out
+ *   max_new         host upper bound of the new rows of a request; rows past it are left out
+ * Supported: head_dim 64 or 128; any page size.
+ */
+int attn_sink_kv_append_q8(const attn_bf16* k_new, const attn_bf16* v_new, long long k_row_stride,
+                           long long v_row_stride, const int32_t* cu_new, const int32_t* seqlens,
+                           const int32_t* page_table, int max_pages, int batch, int total_new, int hkv,
+                           int head_dim, int page_size, int num_pages, int max_new, int block, int format,
+                           void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* stream);
+
+/*
+ * attn_sink_decode_paged over the 8-bit cache.  Scales may be any positive numbers (those
+ * of V count as at least 2^-64), not only those that the append writes.  The products are
+ * fp16 with fp32 accumulation, in which both formats are exact: q enters them off by at
+ * most 2^-25 of its row's largest magnitude, the weights by at most 2^-11 of each, and
+ * weights below 2^-39 of the largest (times its V scale) are lost; scores, sums and
+ * lse are fp32.
+ *
+ *   max_seqlen  host bound of seqlens (INT_MAX: none); sizes launches and scratch.  Lengths
+ *               past it are cut there (ATTN_SINK_DEV_SEQLEN_OOB)
+ *   lse         (batch, hq) fp32; may be NULL
+ * Supported: head_dim 64 or 128; hq % hkv == 0; any page size.
+ */
+int attn_sink_decode_paged_q8(const attn_bf16* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale, int block, int format,
+                              const int32_t* page_table, int max_pages, const int32_t* seqlens, int batch,
+                              int hq, int hkv, int head_dim, int page_size, int num_pages, int max_seqlen,
+                              const float* sink, int win_first, int win_last, float scale, attn_bf16* out,
+                              float* lse, void* stream);
+
+/*
+ * attn_sink_fwd_paged over the 8-bit cache (which has the chunk's tokens already:
+ * attn_sink_kv_append_q8).  Few rows (max_seqlen_q * hq / hkv small: drafts in a row) are
+ * computed from the codes as in attn_sink_decode_paged_q8.  For more, the visible tokens
+ * are expanded to bf16, exactly, in scratch of 4 hkv head_dim bytes per request and token
+ * of max_seqlen_k, at most 2 GiB at a time (or one request's; larger batches in rounds of
+ * requests), and read by the forward's kernel.  What rows that see a token behind an out-of-range
+ * page id get is not defined; nothing outside the cache is read.
+ *   max_seqlen_k  host upper bound of seqlens_k, which must hold
+ *   lse           (hq, total_q) fp32; may be NULL
+ * Supported: head_dim 64 or 128; hq % hkv == 0; any page size.
+ */
+int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale, int block, int format,
+                           const int32_t* page_table, int max_pages, const int32_t* cu_seqlens_q,
+                           const int32_t* seqlens_k, int batch, int total_q, int hq, int hkv, int head_dim,
+                           int page_size, int num_pages, int max_seqlen_q, int max_seqlen_k, const float* sink,
+                           int win_first, int win_last, int causal, float scale, attn_bf16* out, float* lse,
+                           void* stream);
+
+/*
+ * Verification of drafted tokens by given random numbers.  Request b's rows [cu[b], cu[b+1])
+ * are its nodes: node 0 is its last token, which stands; the others are drafted, each hangs
+ * on an earlier one, its parent.  p_i and q_i are the target's and the draft model's
+ * probabilities of the token that follows node i.  From node 0 on, the children of the node
+ * reached are tested in their order; child number r, with token x and random number u, is
+ * taken if
+ *     u q_i(x) Z_r < max(p_i(x) - S_r q_i(x), 0),      S_0 = 0, Z_0 = 1,
+ * and refused otherwise, with
+ *     S_{r+1} = S_r + Z_r,   Z_{r+1} = sum_y max(p_i(y) - S_{r+1} q_i(y), 0).
+ * With draft == NULL it is taken if u Z_r < p_i(x) with Z_r = 1 less p_i of the refused
+ * siblings' tokens (each token once; a token that was refused is refused again).  Where no
+ * child is taken (or there is none), the next token is the least x with
+ *     sum_{y <= x} w(y) > u_next sum_y w(y),
+ * w(y) = max(p_i(y) - S q_i(y), 0), or p_i without the refused tokens; p_i itself where that
+ * leaves nothing.  The tokens are distributed as the target's where siblings are drawn
+ * independently from q_i (draft given) or are chosen without regard to the random numbers.
+ * Probabilities count as clamped to [0, 1] (NaN: 0) and enter sums as multiples of 2^-44;
+ * u_next is clamped to [0, 1) (NaN: 0), u is taken as it is (NaN: refused).
+ *
+ *   target, draft  (total, vocab) of type dtype (ATTN_SINK_F32, BF16 or F16); row i of a
+ *                  request: after its node i.  *_row_stride in elements (0: vocab)
+ *   tokens         (total,) int32; node 0's is not read.  One outside the vocabulary is refused
+ *                  and sets ATTN_SINK_DEV_PROB
+ *   parents        (total,) int32, or NULL: each node hangs on the one before it.  Node 0's is
+ *                  not looked at; another's must be in [0, own index), else the node is left out
+ *                  and sets ATTN_SINK_DEV_TREE
+ *   u, u_next      (total,) and (batch,) fp32; node 0's u is not used
+ *   base           (batch,) int32, or NULL: 0
+ *   max_nodes      host upper bound of a request's nodes, at most 256; further ones are left out
+ *                  and set ATTN_SINK_DEV_SEQLEN_OOB
+ *   src            (batch, max_nodes) int32: base[b] + index of the nodes that stand, node 0
+ *                  first, then -1 (attn_sink_kv_compact's src, with base the prefix's length)
+ *   counts         (batch,) int32: how many stand (0 for a request without nodes)
+ *   next_tokens    (batch,) int32: the next token; -1 for a request without nodes, and where
+ *                  the row has no probability at all (ATTN_SINK_DEV_PROB)
+ * Deterministic.  Supported: vocab below 2^20.
+ */
+int attn_sink_verify_draft(const void* target, const void* draft, long long target_row_stride,
+                           long long draft_row_stride, int dtype, const int32_t* tokens,
+                           const int32_t* parents, const int32_t* cu_seqlens, const float* u,
+                           const float* u_next, const int32_t* base, int batch, int total, int max_nodes,
+                           int vocab, int32_t* src, int32_t* counts, int32_t* next_tokens, void* stream);
+
+/*
+ * Bookkeeping of a paged cache's pages.  refs (num_pages,) int32 device counts, for every
+ * page, the page-table entries that hold it (0: the page is free).  A request of L tokens holds
+ * the first ceil(L / page_size) entries of its row.  `pools` is a host array of num_pools (at
+ * most 8) device tensors whose pages move together (K, V, their scales), tensor i with
+ * page_bytes[i] bytes a page; any alignment, fastest where both are multiples of 16.  All
+ * results are the same in every run.  Entries outside [0, num_pages) set
+ * ATTN_SINK_DEV_PAGE_OOB, lengths below 0 or above max_pages * page_size
+ * ATTN_SINK_DEV_SEQLEN_OOB; what contradicts the counts sets ATTN_SINK_DEV_POOL.
+ *
+ * attn_sink_pages_copy: page src[i] of every tensor to page dst[i], i < n (device arrays;
+ * -1 for both: no copy).  No page may be written twice, or be written and read.
+ */
+int attn_sink_pages_copy(void* const* pools, const long long* page_bytes, int num_pools, int num_pages,
+                         const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/*
+ * Row b of the new table (out_batch rows) is row src[b] of the old one (-1: a row without
+ * tokens), with its length; refs follow: the old rows' entries are given up, the new ones'
+ * are held.  Nothing else is copied: a row that then grows into a page that it shares calls
+ * attn_sink_pages_reserve first.  Entries behind a row's pages are -1.  out_table and
+ * out_seqlens must not be the inputs.
+ */
+int attn_sink_pages_fork(const int32_t* page_table, int32_t* refs, const int32_t* seqlens,
+                         const int32_t* src, int batch, int out_batch, int max_pages, int page_size,
+                         int num_pages, int32_t* out_table, int32_t* out_seqlens, void* stream);
+
+/*
+ * Gives back the pages of requests that shrink from seqlens[b] to new_seqlens[b] tokens (0: all
+ * of them): their entries become -1.  A new length above the old one sets ATTN_SINK_DEV_POOL
+ * and changes nothing.
+ */
+int attn_sink_pages_release(int32_t* page_table, int32_t* refs, const int32_t* seqlens,
+                            const int32_t* new_seqlens, int batch, int max_pages, int page_size, int num_pages,
+                            void* stream);
+
+/*
+ * Gives requests that grow from seqlens[b] to new_seqlens[b] tokens their pages, so that tokens
+ * seqlens[b] .. new_seqlens[b] - 1 can be written: free pages, lowest first, to the requests in
+ * order.  A request whose first new token goes into a page that others hold too gets a copy of
+ * it (in all tensors) instead, before its new pages; of several such requests of one page the
+ * last keeps the page, where they are all its holders.
+ *   missing  (1,) int32: 0, or the pages that are too few; then nothing is changed
+ *            (ATTN_SINK_DEV_POOL)
+ * A request whose lengths are out of range or fall is left alone.
+ */
+int attn_sink_pages_reserve(void* const* pools, const long long* page_bytes, int num_pools,
+                            int32_t* page_table, int32_t* refs, const int32_t* seqlens,
+                            const int32_t* new_seqlens, int batch, int max_pages, int page_size, int num_pages,
+                            int32_t* missing, void* stream);
+
+/*
+ * Brings the n held pages to the front: the i-th held page behind the first n goes to the i-th
+ * free page among them, in all tensors, in the rows' entries and in refs.  The pages from n on are
+ * free then.
+ *   held     (1,) int32: n
+ */
+int attn_sink_pages_compact(void* const* pools, const long long* page_bytes, int num_pools,
+                            int32_t* page_table, int32_t* refs, const int32_t* seqlens, int batch,
+                            int max_pages, int page_size, int num_pages, int32_t* held, void* stream);
 
 /*
  * The visible token ranges of each decode request, as the decode kernels

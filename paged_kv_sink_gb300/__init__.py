@@ -41,3 +41,14 @@ from .autograd import (  # noqa: F401
     attn_sink_varlen_qkvpacked_func,
 )
 from .rope import attn_sink_rope_freqs  # noqa: F401
+from .serving import (  # noqa: F401
+    attn_sink_decode_paged_q8,
+    attn_sink_fwd_paged_q8,
+    attn_sink_kv_append_q8,
+    attn_sink_pages_compact,
+    attn_sink_pages_copy,
+    attn_sink_pages_fork,
+    attn_sink_pages_release,
+    attn_sink_pages_reserve,
+    attn_sink_verify_draft,
+)

@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libattn_sink.so")
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE = 0, -1, -2, -3, -4
 DEV_PAGE_OOB, DEV_SEQLEN_OOB, DEV_TIMEOUT, DEV_LAYOUT = 1, 2, 4, 8
 DEV_ORDER, DEV_TREE = 16, 32
+DEV_VALUE, DEV_PROB, DEV_POOL = 64, 128, 256
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -57,6 +58,15 @@ _SIGS = {
     "attn_sink_visible_ranges": [_P, _I, _I, _I, _P, _P],
     "attn_sink_visible_slots": [_P, _P, _I, _I, _I, _I, _I, _I, _P, _I, _P],
     "attn_sink_device_status": [_P],
+    "attn_sink_kv_append_q8": [_P, _P, _L, _L, _P, _P, _P] + [_I] * 10 + [_P] * 5,
+    "attn_sink_decode_paged_q8": [_P] * 5 + [_I, _I, _P, _I, _P] + [_I] * 7 + [_P, _I, _I, _F, _P, _P, _P],
+    "attn_sink_fwd_paged_q8": [_P] * 5 + [_I, _I, _P, _I, _P, _P] + [_I] * 9 + [_P, _I, _I, _I, _F, _P, _P, _P],
+    "attn_sink_verify_draft": [_P, _P, _L, _L, _I] + [_P] * 6 + [_I] * 4 + [_P] * 4,
+    "attn_sink_pages_copy": [_P, _P, _I, _I, _P, _P, _I, _P],
+    "attn_sink_pages_fork": [_P] * 4 + [_I] * 5 + [_P] * 3,
+    "attn_sink_pages_release": [_P] * 4 + [_I] * 4 + [_P],
+    "attn_sink_pages_reserve": [_P, _P, _I] + [_P] * 4 + [_I] * 4 + [_P, _P],
+    "attn_sink_pages_compact": [_P, _P, _I] + [_P] * 3 + [_I] * 4 + [_P, _P],
     "attn_sink_selftest_wait": [_I, _P],
     "attn_sink_last_error": [],
     "attn_sink_version": [],

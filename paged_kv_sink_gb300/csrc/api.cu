@@ -16,10 +16,13 @@
 #include "evict.h"
 #include "host_io.h"
 #include "kv_append.h"
+#include "pages.h"
 #include "selftest.h"
 #include "prefill.h"
+#include "q8.h"
 #include "rope.h"
 #include "tree.h"
+#include "verify.h"
 
 namespace {
 
@@ -997,6 +1000,411 @@ int attn_sink_evict_paged(attn_bf16* k_cache, attn_bf16* v_cache, const int32_t*
     return ATTN_SINK_OK;
 }
 
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The 8-bit cache.
+
+namespace {
+
+// Sizes and pointers of an 8-bit cache; fills `c`.
+int check_q8(const char* who, void* k, void* v, float* ks, float* vs, const int32_t* page_table, int max_pages, int batch,
+             int hkv, int head_dim, int page_size, int num_pages, int block, int format, attn::q8::Cache* c) {
+    if (hkv <= 0) return fail(ATTN_SINK_ERR_INVALID, "%s: sizes must be positive", who);
+    int rc = check_cache(who, batch, max_pages, page_size, num_pages);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (head_dim != 64 && head_dim != 128)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: head_dim %d not supported (64, 128)", who, head_dim);
+    if (block <= 0 || page_size % block)
+        return fail(ATTN_SINK_ERR_INVALID, "%s: block %d must divide page_size %d", who, block, page_size);
+    if (format != ATTN_SINK_E4M3 && format != ATTN_SINK_INT8)
+        return fail(ATTN_SINK_ERR_INVALID, "%s: format %d is neither ATTN_SINK_E4M3 nor ATTN_SINK_INT8", who, format);
+    if (hkv > kMaxGridDim) return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: hkv %d above %d", who, hkv, kMaxGridDim);
+    if (batch == 0) return ATTN_SINK_OK;
+    if (!k || !v || !ks || !vs || !page_table) return fail(ATTN_SINK_ERR_INVALID, "%s: NULL tensor pointer", who);
+    if (!aligned16(k) || !aligned16(v)) return fail(ATTN_SINK_ERR_INVALID, "%s: caches must be 16-byte aligned", who);
+    if (k == v || ks == vs) return fail(ATTN_SINK_ERR_INVALID, "%s: the caches and their scales must differ", who);
+    c->k = static_cast<uint8_t*>(k);
+    c->v = static_cast<uint8_t*>(v);
+    c->k_scale = ks;
+    c->v_scale = vs;
+    c->page_table = page_table;
+    c->max_pages = max_pages;
+    c->hkv = hkv;
+    c->head_dim = head_dim;
+    c->page_size = page_size;
+    c->num_pages = num_pages;
+    c->block = block;
+    c->format = format;
+    return check_grid(who, batch, 0);
+}
+
+int run_attend_q8(const char* who, attn::q8::AttendArgs& a, cudaStream_t s) {
+    const attn::q8::AttendPlan pl = attn::q8::make_plan(a);
+    if ((long long)a.c.hkv * pl.tiles > kMaxGridDim)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: too many heads", who);
+    Scratch ws;
+    cudaError_t e = ws.alloc(pl.part_o_bytes + pl.part_ml_bytes, s);
+    if (e != cudaSuccess) return cuda_fail(e, "q8 attention: scratch allocation");
+    char* const base = static_cast<char*>(ws.ptr);
+    e = attn::q8::launch_attend(a, pl, reinterpret_cast<float*>(base), reinterpret_cast<float2*>(base + pl.part_o_bytes), s);
+    if (e != cudaSuccess) return cuda_fail(e, "q8 attention: launch");
+    return ATTN_SINK_OK;
+}
+
+// Rows (new tokens times query heads of a KV head) up to which a request's tokens are
+// read as codes by the row kernel; above, they are expanded for the tensor-core forward.
+constexpr long long kMaxAttendRows = 64;
+
+}  // namespace
+
+extern "C" {
+
+int attn_sink_kv_append_q8(const attn_bf16* k_new, const attn_bf16* v_new, long long k_row_stride, long long v_row_stride,
+                           const int32_t* cu_new, const int32_t* seqlens, const int32_t* page_table, int max_pages,
+                           int batch, int total_new, int hkv, int head_dim, int page_size, int num_pages, int max_new,
+                           int block, int format, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                           void* stream) {
+    t_last_error.clear();
+    if (total_new < 0 || max_new < 0) return fail(ATTN_SINK_ERR_INVALID, "kv_append_q8: sizes must be non-negative");
+    attn::q8::AppendArgs a = {};
+    int rc = check_q8("kv_append_q8", k_cache, v_cache, k_scale, v_scale, page_table, max_pages,
+                      max_new == 0 || total_new == 0 ? 0 : batch, hkv, head_dim, page_size, num_pages, block, format, &a.c);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (batch < 0) return fail(ATTN_SINK_ERR_INVALID, "kv_append_q8: sizes must be non-negative");
+    if ((rc = check_stride("kv_append_q8", "k_new", k_row_stride, hkv, head_dim)) != ATTN_SINK_OK ||
+        (rc = check_stride("kv_append_q8", "v_new", v_row_stride, hkv, head_dim)) != ATTN_SINK_OK)
+        return rc;
+    if (batch == 0 || max_new == 0 || total_new == 0) return ATTN_SINK_OK;
+    if (!k_new || !v_new || !seqlens) return fail(ATTN_SINK_ERR_INVALID, "kv_append_q8: NULL tensor pointer");
+    if (!aligned16(k_new) || !aligned16(v_new))
+        return fail(ATTN_SINK_ERR_INVALID, "kv_append_q8: tensors must be 16-byte aligned");
+    if (!cu_new && (max_new != 1 || total_new < batch))
+        return fail(ATTN_SINK_ERR_INVALID,
+                    "kv_append_q8: without cu_new every request appends one row (max_new 1, total_new = batch)");
+    a.k_new = as_bf16(k_new);
+    a.v_new = as_bf16(v_new);
+    a.k_rs = row_stride(k_row_stride, hkv, head_dim);
+    a.v_rs = row_stride(v_row_stride, hkv, head_dim);
+    a.cu_new = cu_new;
+    a.seqlens = seqlens;
+    a.batch = batch;
+    a.total_new = total_new;
+    a.max_new = max_new;
+    cudaError_t e = attn::q8::launch_append(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "kv_append_q8: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_decode_paged_q8(const attn_bf16* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                              const float* v_scale, int block, int format, const int32_t* page_table, int max_pages,
+                              const int32_t* seqlens, int batch, int hq, int hkv, int head_dim, int page_size,
+                              int num_pages, int max_seqlen, const float* sink, int win_first, int win_last, float scale,
+                              attn_bf16* out, float* lse, void* stream) {
+    t_last_error.clear();
+    attn::q8::AttendArgs a = {};
+    if (hq <= 0 || win_first < 0 || max_seqlen < 0)
+        return fail(ATTN_SINK_ERR_INVALID, "decode_q8: sizes must be non-negative (heads positive)");
+    int rc = check_q8("decode_q8", const_cast<void*>(k_cache), const_cast<void*>(v_cache), const_cast<float*>(k_scale),
+                      const_cast<float*>(v_scale), page_table, max_pages, batch, hkv, head_dim, page_size, num_pages, block,
+                      format, &a.c);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (hq % hkv) return fail(ATTN_SINK_ERR_UNSUPPORTED, "decode_q8: hq %% hkv != 0");
+    if (batch == 0) return ATTN_SINK_OK;
+    if (!q || !seqlens || !out) return fail(ATTN_SINK_ERR_INVALID, "decode_q8: NULL tensor pointer");
+    if (!aligned16(q) || !aligned16(out))
+        return fail(ATTN_SINK_ERR_INVALID, "decode_q8: q and out must be 16-byte aligned");
+    a.q = as_bf16(q);
+    a.seqlens = seqlens;
+    a.sink = sink;
+    a.out = as_bf16(out);
+    a.lse = lse;
+    a.batch = a.total_q = batch;
+    a.hq = hq;
+    a.max_q = 1;
+    a.max_seqlen = max_seqlen;
+    a.win_first = win_first;
+    a.win_last = win_last;
+    a.causal = 1;
+    a.scale = attn::resolve_scale(scale, head_dim);
+    return run_attend_q8("decode_q8", a, static_cast<cudaStream_t>(stream));
+}
+
+int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, int block, int format, const int32_t* page_table, int max_pages,
+                           const int32_t* cu_seqlens_q, const int32_t* seqlens_k, int batch, int total_q, int hq, int hkv,
+                           int head_dim, int page_size, int num_pages, int max_seqlen_q, int max_seqlen_k,
+                           const float* sink, int win_first, int win_last, int causal, float scale, attn_bf16* out,
+                           float* lse, void* stream) {
+    t_last_error.clear();
+    attn::q8::AttendArgs a = {};
+    if (batch < 0 || total_q < 0 || hq <= 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || win_first < 0)
+        return fail(ATTN_SINK_ERR_INVALID, "fwd_paged_q8: sizes must be non-negative (heads positive)");
+    if (win_last > 0 && !causal)
+        return fail(ATTN_SINK_ERR_INVALID, "fwd_paged_q8: first/last-window selection needs causal attention");
+    const bool none = batch == 0 || total_q == 0 || max_seqlen_q == 0;
+    int rc = check_q8("fwd_paged_q8", const_cast<void*>(k_cache), const_cast<void*>(v_cache), const_cast<float*>(k_scale),
+                      const_cast<float*>(v_scale), page_table, max_pages, none ? 0 : batch, hkv, head_dim, page_size,
+                      num_pages, block, format, &a.c);
+    if (rc != ATTN_SINK_OK) return rc;
+    if (hq % hkv) return fail(ATTN_SINK_ERR_UNSUPPORTED, "fwd_paged_q8: hq %% hkv != 0");
+    if (none) return ATTN_SINK_OK;
+    if (!q || !cu_seqlens_q || !seqlens_k || !out)
+        return fail(ATTN_SINK_ERR_INVALID, "fwd_paged_q8: NULL tensor pointer");
+    if (!aligned16(q) || !aligned16(out))
+        return fail(ATTN_SINK_ERR_INVALID, "fwd_paged_q8: q and out must be 16-byte aligned");
+    if ((rc = check_grid("fwd_paged_q8", batch, max_seqlen_q)) != ATTN_SINK_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (max_seqlen_q * (long long)(hq / hkv) <= kMaxAttendRows) {
+        a.q = as_bf16(q);
+        a.cu_q = cu_seqlens_q;
+        a.seqlens = seqlens_k;
+        a.sink = sink;
+        a.out = as_bf16(out);
+        a.lse = lse;
+        a.lse_by_head = 1;
+        a.batch = batch;
+        a.total_q = total_q;
+        a.hq = hq;
+        a.max_q = max_seqlen_q;
+        a.max_seqlen = max_seqlen_k;
+        a.win_first = win_first;
+        a.win_last = win_last;
+        a.causal = causal ? 1 : 0;
+        a.scale = attn::resolve_scale(scale, head_dim);
+        return run_attend_q8("fwd_paged_q8", a, s);
+    }
+    // Many rows: the tokens as bf16 in pages of their own, a round of requests at a time.
+    const long long cap = (long long)max_pages * page_size;
+    const long long keys = max_seqlen_k < cap ? max_seqlen_k : cap;
+    const int pages = keys > 0 ? (int)((keys + attn::q8::kExpandPage - 1) / attn::q8::kExpandPage) : 1;
+    const size_t cache = (size_t)pages * attn::q8::kExpandPage * hkv * head_dim * 2;  // bytes of a request's K or V
+    const size_t most = kMaxScoreBytes / (2 * cache);
+    int round = most >= (size_t)batch ? batch : most ? (int)most : 1;
+    round = (batch + (batch + round - 1) / round - 1) / ((batch + round - 1) / round);
+    Scratch ws;
+    cudaError_t e = ws.alloc(2 * cache * round + (size_t)pages * round * sizeof(int32_t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: scratch allocation");
+    char* const base = static_cast<char*>(ws.ptr);
+    for (int b0 = 0; b0 < batch; b0 += round) {
+        attn::q8::ExpandArgs x = {};
+        x.c = a.c;
+        x.c.page_table = page_table + (size_t)b0 * max_pages;
+        x.cu_q = cu_seqlens_q + b0;
+        x.seqlens = seqlens_k + b0;
+        x.batch = batch - b0 < round ? batch - b0 : round;
+        x.pages = pages;
+        x.win_first = win_first;
+        x.win_last = win_last;
+        x.k_out = reinterpret_cast<__nv_bfloat16*>(base);
+        x.v_out = reinterpret_cast<__nv_bfloat16*>(base + cache * round);
+        x.table_out = reinterpret_cast<int32_t*>(base + 2 * cache * round);
+        if ((e = attn::q8::launch_expand(x, s)) != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: launch");
+        attn::prefill::FwdArgs f = {};
+        f.q = q;
+        f.k = x.k_out;
+        f.v = x.v_out;
+        f.sink = sink;
+        f.cu_q = x.cu_q;
+        f.out = out;
+        f.lse = lse;
+        f.batch = x.batch;
+        f.total_q = total_q;
+        f.hq = hq;
+        f.hkv = hkv;
+        f.head_dim = head_dim;
+        f.max_seqlen_q = max_seqlen_q;
+        f.max_seqlen_k = max_seqlen_k;
+        f.win_first = win_first;
+        f.win_last = win_last;
+        f.causal = causal ? 1 : 0;
+        f.scale = attn::resolve_scale(scale, head_dim);
+        f.page_table = x.table_out;
+        f.seqlens_k = x.seqlens;
+        f.max_pages = pages;
+        f.page_size = attn::q8::kExpandPage;
+        f.num_pages = pages * x.batch;
+        std::string err;
+        if ((e = attn::prefill::launch_fwd(f, s, &err)) != cudaSuccess)
+            return fail(ATTN_SINK_ERR_CUDA, "fwd_paged_q8: %s: %s", err.c_str(), cudaGetErrorString(e));
+    }
+    return ATTN_SINK_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Verification of drafted tokens.
+
+int attn_sink_verify_draft(const void* target, const void* draft, long long target_row_stride, long long draft_row_stride,
+                           int dtype, const int32_t* tokens, const int32_t* parents, const int32_t* cu_seqlens,
+                           const float* u, const float* u_next, const int32_t* base, int batch, int total, int max_nodes,
+                           int vocab, int32_t* src, int32_t* counts, int32_t* next_tokens, void* stream) {
+    t_last_error.clear();
+    if (batch < 0 || total < 0 || max_nodes < 0 || vocab <= 0)
+        return fail(ATTN_SINK_ERR_INVALID, "verify_draft: sizes must be non-negative (vocab positive)");
+    if (dtype != ATTN_SINK_F32 && dtype != ATTN_SINK_BF16 && dtype != ATTN_SINK_F16)
+        return fail(ATTN_SINK_ERR_INVALID, "verify_draft: unknown dtype %d", dtype);
+    if (max_nodes > attn::verify::kMaxNodes)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "verify_draft: max_nodes %d above %d nodes per request", max_nodes,
+                    attn::verify::kMaxNodes);
+    if (vocab >= 1 << 20) return fail(ATTN_SINK_ERR_UNSUPPORTED, "verify_draft: vocab %d not below 2^20", vocab);
+    if (target_row_stride < 0 || (target_row_stride && target_row_stride < vocab) || draft_row_stride < 0 ||
+        (draft_row_stride && draft_row_stride < vocab))
+        return fail(ATTN_SINK_ERR_INVALID, "verify_draft: a row stride must be 0 or at least vocab");
+    if (batch == 0) return ATTN_SINK_OK;
+    if (!cu_seqlens || !u_next || !counts || !next_tokens || (max_nodes > 0 && !src) ||
+        (total > 0 && (!target || !tokens || !u)))
+        return fail(ATTN_SINK_ERR_INVALID, "verify_draft: NULL tensor pointer");
+    const uintptr_t size = dtype == ATTN_SINK_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(target) % size || reinterpret_cast<uintptr_t>(draft) % size)
+        return fail(ATTN_SINK_ERR_INVALID, "verify_draft: probabilities must be aligned to their type");
+    if (int rc = check_grid("verify_draft", batch, 0)) return rc;
+    attn::verify::Args a = {};
+    a.target = target;
+    a.draft = draft;
+    a.target_rs = target_row_stride ? target_row_stride : vocab;
+    a.draft_rs = draft_row_stride ? draft_row_stride : vocab;
+    a.tokens = tokens;
+    a.parents = parents;
+    a.cu = cu_seqlens;
+    a.u = u;
+    a.u_next = u_next;
+    a.base = base;
+    a.src = src;
+    a.counts = counts;
+    a.next = next_tokens;
+    a.batch = batch;
+    a.total = total;
+    a.max_nodes = max_nodes;
+    a.vocab = vocab;
+    a.dtype = dtype;
+    cudaError_t e = attn::verify::launch(a, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "verify_draft: launch");
+    return ATTN_SINK_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Pages.
+
+namespace {
+
+int check_pages(const char* who, int32_t* table, int32_t* refs, int batch, int max_pages, int page_size, int num_pages,
+                attn::pages::Table* t) {
+    int rc = check_cache(who, batch, max_pages, page_size, num_pages);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_grid(who, batch, 0)) != ATTN_SINK_OK) return rc;
+    if (!refs || (batch > 0 && !table)) return fail(ATTN_SINK_ERR_INVALID, "%s: NULL tensor pointer", who);
+    *t = {table, refs, batch, max_pages, page_size, num_pages};
+    return ATTN_SINK_OK;
+}
+
+int check_pools(const char* who, void* const* pools, const long long* page_bytes, int num_pools, attn::pages::Pools* p) {
+    if (num_pools < 0) return fail(ATTN_SINK_ERR_INVALID, "%s: sizes must be non-negative", who);
+    if (num_pools > attn::pages::kMaxPools)
+        return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: %d tensors above %d", who, num_pools, attn::pages::kMaxPools);
+    if (num_pools > 0 && (!pools || !page_bytes)) return fail(ATTN_SINK_ERR_INVALID, "%s: NULL tensor pointer", who);
+    p->count = num_pools;
+    for (int i = 0; i < num_pools; ++i) {
+        if (!pools[i]) return fail(ATTN_SINK_ERR_INVALID, "%s: NULL tensor pointer", who);
+        if (page_bytes[i] <= 0 || page_bytes[i] >= 1LL << 40)
+            return fail(ATTN_SINK_ERR_INVALID, "%s: page_bytes must be positive (and below 2^40)", who);
+        for (int j = 0; j < i; ++j)
+            if (pools[j] == pools[i]) return fail(ATTN_SINK_ERR_INVALID, "%s: the tensors must differ", who);
+        p->base[i] = pools[i];
+        p->bytes[i] = page_bytes[i];
+    }
+    return ATTN_SINK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_sink_pages_copy(void* const* pools, const long long* page_bytes, int num_pools, int num_pages,
+                         const int32_t* src, const int32_t* dst, int n, void* stream) {
+    t_last_error.clear();
+    attn::pages::Pools p = {};
+    if (n < 0 || num_pages <= 0) return fail(ATTN_SINK_ERR_INVALID, "pages_copy: sizes must be non-negative");
+    int rc = check_pools("pages_copy", pools, page_bytes, num_pools, &p);
+    if (rc != ATTN_SINK_OK || n == 0) return rc;
+    if (!src || !dst) return fail(ATTN_SINK_ERR_INVALID, "pages_copy: NULL tensor pointer");
+    cudaError_t e = attn::pages::launch_copy(p, src, dst, nullptr, n, num_pages, true, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pages_copy: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_pages_fork(const int32_t* page_table, int32_t* refs, const int32_t* seqlens, const int32_t* src, int batch,
+                         int out_batch, int max_pages, int page_size, int num_pages, int32_t* out_table,
+                         int32_t* out_seqlens, void* stream) {
+    t_last_error.clear();
+    attn::pages::Table t;
+    if (out_batch < 0) return fail(ATTN_SINK_ERR_INVALID, "pages_fork: sizes must be non-negative");
+    int rc = check_pages("pages_fork", const_cast<int32_t*>(page_table), refs, batch, max_pages, page_size, num_pages, &t);
+    if (rc != ATTN_SINK_OK || (rc = check_grid("pages_fork", out_batch, 0)) != ATTN_SINK_OK) return rc;
+    if ((batch > 0 && !seqlens) || (out_batch > 0 && (!src || !out_table || !out_seqlens)))
+        return fail(ATTN_SINK_ERR_INVALID, "pages_fork: NULL tensor pointer");
+    if (out_batch > 0 && (out_table == page_table || out_seqlens == seqlens))
+        return fail(ATTN_SINK_ERR_INVALID, "pages_fork: the outputs must not be the inputs (other rows read them)");
+    cudaError_t e = attn::pages::launch_fork(t, seqlens, src, out_batch, out_table, out_seqlens,
+                                             static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pages_fork: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_pages_release(int32_t* page_table, int32_t* refs, const int32_t* seqlens, const int32_t* new_seqlens,
+                            int batch, int max_pages, int page_size, int num_pages, void* stream) {
+    t_last_error.clear();
+    attn::pages::Table t;
+    int rc = check_pages("pages_release", page_table, refs, batch, max_pages, page_size, num_pages, &t);
+    if (rc != ATTN_SINK_OK || batch == 0) return rc;
+    if (!seqlens || !new_seqlens) return fail(ATTN_SINK_ERR_INVALID, "pages_release: NULL tensor pointer");
+    cudaError_t e = attn::pages::launch_release(t, seqlens, new_seqlens, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "pages_release: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_pages_reserve(void* const* pools, const long long* page_bytes, int num_pools, int32_t* page_table,
+                            int32_t* refs, const int32_t* seqlens, const int32_t* new_seqlens, int batch, int max_pages,
+                            int page_size, int num_pages, int32_t* missing, void* stream) {
+    t_last_error.clear();
+    attn::pages::Table t;
+    attn::pages::Pools p = {};
+    int rc = check_pools("pages_reserve", pools, page_bytes, num_pools, &p);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_pages("pages_reserve", page_table, refs, batch, max_pages, page_size, num_pages, &t)) != ATTN_SINK_OK)
+        return rc;
+    if (!missing || (batch > 0 && (!seqlens || !new_seqlens)))
+        return fail(ATTN_SINK_ERR_INVALID, "pages_reserve: NULL tensor pointer");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch ws;
+    cudaError_t e = ws.alloc(attn::pages::reserve_scratch(t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "pages_reserve: scratch allocation");
+    e = attn::pages::launch_reserve(p, t, seqlens, new_seqlens, missing, ws.ptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "pages_reserve: launch");
+    return ATTN_SINK_OK;
+}
+
+int attn_sink_pages_compact(void* const* pools, const long long* page_bytes, int num_pools, int32_t* page_table,
+                            int32_t* refs, const int32_t* seqlens, int batch, int max_pages, int page_size, int num_pages,
+                            int32_t* held, void* stream) {
+    t_last_error.clear();
+    attn::pages::Table t;
+    attn::pages::Pools p = {};
+    int rc = check_pools("pages_compact", pools, page_bytes, num_pools, &p);
+    if (rc != ATTN_SINK_OK) return rc;
+    if ((rc = check_pages("pages_compact", page_table, refs, batch, max_pages, page_size, num_pages, &t)) != ATTN_SINK_OK)
+        return rc;
+    if (!held || (batch > 0 && !seqlens)) return fail(ATTN_SINK_ERR_INVALID, "pages_compact: NULL tensor pointer");
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch ws;
+    cudaError_t e = ws.alloc(attn::pages::compact_scratch(t), s);
+    if (e != cudaSuccess) return cuda_fail(e, "pages_compact: scratch allocation");
+    e = attn::pages::launch_compact(p, t, seqlens, held, ws.ptr, s);
+    if (e != cudaSuccess) return cuda_fail(e, "pages_compact: launch");
+    return ATTN_SINK_OK;
+}
+
 int attn_sink_device_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int bits = 0;
@@ -1007,6 +1415,10 @@ int attn_sink_device_status(void* stream) {
     if (!e) e = attn::rope::status_exchange(s, &bits);
     if (!e) e = attn::tree::status_exchange(s, &bits);
     if (!e) e = attn::evict::status_exchange(s, &bits);
+    if (!e) e = attn::q8::append_status_exchange(s, &bits);
+    if (!e) e = attn::q8::attend_status_exchange(s, &bits);
+    if (!e) e = attn::verify::status_exchange(s, &bits);
+    if (!e) e = attn::pages::status_exchange(s, &bits);
     if (!e) e = attn::selftest::status_exchange(s, &bits);
     if (e) return cuda_fail(static_cast<cudaError_t>(e), "device_status");
     return bits;

@@ -1,0 +1,505 @@
+// Bookkeeping of a paged cache's pages on the device: forked page-table rows, pages for
+// growing requests, pages given back, pages moved together (sm_103a).
+//
+// A page is held by as many page-table entries as refs counts.  Everything that is decided
+// here is an integer and the same in every run: free pages are given lowest first, to
+// requests in their order; counts change by atomic additions, whose order does not show.
+//
+//  * fork: row b of the new table is row src[b] of the old one.  Entries that a row keeps
+//    cost nothing; the others take their old page's count down and their new one's up.
+//  * release: the entries of a request that shrinks.
+//  * reserve: the entries of requests that grow.  A request that writes into a partly filled
+//    page which others hold too gets a copy of it first; of several that all write into one
+//    page the last keeps it, where nobody else holds it (as if they came one after the
+//    other).  If the free pages do not suffice nothing is changed.
+//  * compact: the i-th held page behind the first n = (number of held pages) goes to the
+//    i-th free page among them.
+// reserve and compact decide in one cluster of CTAs, which scan the counts by slices and
+// meet at the cluster's barrier; the pages are then moved by a grid of its own, which reads the
+// list from the device.  The decisions are bound by latency, the moves by HBM.
+#include "pages.h"
+
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace attn {
+namespace pages {
+
+constexpr int kCtas = 8;        // of the deciding cluster
+constexpr int kThreads = 1024;  // of its CTAs
+constexpr int kPer = 4;         // pages of a thread in a step of a scan
+
+__device__ __forceinline__ int pages_of(int tokens, int page_size) {
+    return tokens / page_size + (tokens % page_size ? 1 : 0);
+}
+
+// A length as the row can hold it.
+__device__ __forceinline__ int length_of(const Table& t, const int32_t* seqlens, int b) {
+    const long long cap = (long long)t.max_pages * t.page_size;
+    const int L = seqlens[b];
+    if (L < 0 || L > cap) {
+        raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+        return L < 0 ? 0 : (int)cap;
+    }
+    return L;
+}
+
+__device__ __forceinline__ bool valid_page(const Table& t, int p) { return (unsigned)p < (unsigned)t.num_pages; }
+
+// One reference less.
+__device__ __forceinline__ void drop(const Table& t, int p) {
+    if (!valid_page(t, p)) {
+        raise_status(ATTN_SINK_DEV_PAGE_OOB);
+    } else if (atomicSub(t.refs + p, 1) <= 0) {
+        atomicAdd(t.refs + p, 1);
+        raise_status(ATTN_SINK_DEV_POOL);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Rows of the table: a warp each.
+
+constexpr int kRowWarps = 4;
+
+__global__ void __launch_bounds__(kRowWarps * 32) fork_kernel(const Table t, const int32_t* seqlens, const int32_t* src,
+                                                              int out_batch, int32_t* out_table, int32_t* out_seqlens) {
+    const int b = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const bool had = b < t.batch, has = b < out_batch;
+    if (!had && !has) return;
+    int from = has ? src[b] : -1;
+    if (from < -1 || from >= t.batch) {
+        if (lane == 0) raise_status(ATTN_SINK_DEV_POOL);
+        from = -1;
+    }
+    const int held = had ? pages_of(length_of(t, seqlens, b), t.page_size) : 0;
+    const int L = from >= 0 ? length_of(t, seqlens, from) : 0, want = pages_of(L, t.page_size);
+    const int32_t* const mine = t.table + (size_t)b * t.max_pages;
+    const int32_t* const other = t.table + (size_t)max(from, 0) * t.max_pages;
+    const int width = has ? t.max_pages : held;
+    for (int i = lane; i < width; i += 32) {
+        const int was = i < held ? mine[i] : -1, is = i < want ? other[i] : -1;
+        if (was != is || (i < held) != (i < want)) {
+            if (i < held) drop(t, was);
+            if (i < want) {
+                if (valid_page(t, is)) atomicAdd(t.refs + is, 1);
+                else raise_status(ATTN_SINK_DEV_PAGE_OOB);
+            }
+        }
+        if (has) out_table[(size_t)b * t.max_pages + i] = is;
+    }
+    if (has && lane == 0) out_seqlens[b] = L;
+}
+
+__global__ void __launch_bounds__(kRowWarps * 32) release_kernel(const Table t, const int32_t* seqlens,
+                                                                 const int32_t* new_seqlens) {
+    const int b = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= t.batch) return;
+    const int L = length_of(t, seqlens, b), to = length_of(t, new_seqlens, b);
+    if (to > L && lane == 0) raise_status(ATTN_SINK_DEV_POOL);
+    const int held = pages_of(L, t.page_size), keep = pages_of(to, t.page_size);
+    int32_t* const row = t.table + (size_t)b * t.max_pages;
+    for (int i = keep + lane; i < held; i += 32) {
+        drop(t, row[i]);
+        row[i] = -1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Scans inside the cluster.
+
+using u64 = unsigned long long;
+
+// Exclusive sum over the block's threads in order; the block's total in `all`.
+__device__ __forceinline__ u64 block_scan(u64 x, u64* warps, u64& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 run = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += y;
+    }
+    if (lane == 31) warps[warp] = run;
+    __syncthreads();
+    if (warp == 0) {
+        u64 w = warps[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const u64 y = __shfl_up_sync(0xffffffffu, w, o);
+            if (lane >= o) w += y;
+        }
+        warps[lane] = w;
+    }
+    __syncthreads();
+    const u64 before = warp ? warps[warp - 1] : 0;
+    all = warps[31];
+    __syncthreads();
+    return before + run - x;
+}
+
+// This CTA's slice of the pages, whole steps of a thread.
+__device__ __forceinline__ int2 slice_of(int num_pages, int rank) {
+    const int len = ((num_pages + kCtas - 1) / kCtas + kPer - 1) / kPer * kPer;
+    const int a = (int)min((long long)num_pages, (long long)rank * len);
+    return make_int2(a, (int)min((long long)num_pages, (long long)a + len));
+}
+
+// Number of pages in the slice for which f(page, refs) holds.
+template <class F>
+__device__ __forceinline__ int count_pages(const Table& t, int2 s, u64* warps, F f) {
+    int n = 0;
+    for (int p0 = s.x + (int)threadIdx.x; p0 < s.y; p0 += kThreads) n += f(p0, t.refs[p0]) ? 1 : 0;
+    u64 all;
+    block_scan(n, warps, all);
+    return (int)all;
+}
+
+// Calls emit(rank, page) for those pages, ranks from `base` on, while they are below `most`.
+template <class F, class G>
+__device__ __forceinline__ void rank_pages(const Table& t, int2 s, int base, int most, u64* warps, F f, G emit) {
+    for (int p0 = s.x; p0 < s.y && base < most; p0 += kThreads * kPer) {
+        const int p = p0 + (int)threadIdx.x * kPer;
+        bool is[kPer];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            is[i] = p + i < s.y && f(p + i, t.refs[p + i]);
+            n += is[i] ? 1 : 0;
+        }
+        u64 all;
+        int r = base + (int)block_scan(n, warps, all);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (is[i]) {
+                if (r < most) emit(r, p + i);
+                ++r;
+            }
+        base += (int)all;
+    }
+}
+
+// Scratch of reserve: per page the requests that are about to write into it and the last
+// of them; the free pages in order; per request its place in the free pages, and whether it
+// copies; the copies; totals.
+struct ReserveScratch {
+    int32_t *users, *last, *free, *offset, *src, *dst, *head;
+    __host__ __device__ ReserveScratch(void* at, const Table& t) {
+        int32_t* p = static_cast<int32_t*>(at);
+        head = p;  // [0] copies, [1] pages needed, [2..] free pages of each slice
+        users = head + 16;
+        last = users + t.num_pages;
+        free = last + t.num_pages;
+        offset = free + t.num_pages;  // top bit: copies
+        src = offset + t.batch;
+        dst = src + t.batch;
+    }
+};
+
+struct Growth {
+    int from, to;  // pages held, wanted
+    int shared;    // the page that the first new token goes into, or -1
+};
+
+__device__ __forceinline__ Growth growth_of(const Table& t, const int32_t* seqlens, const int32_t* new_seqlens, int b) {
+    const long long cap = (long long)t.max_pages * t.page_size;
+    const int L0 = seqlens[b], L1 = new_seqlens[b];
+    Growth g = {0, 0, -1};
+    if (L0 < 0 || L1 > cap || L1 < L0) return g;  // reported once, below
+    g.from = pages_of(L0, t.page_size);
+    g.to = pages_of(L1, t.page_size);
+    if (L1 > L0 && L0 % t.page_size) {
+        const int p = t.table[(size_t)b * t.max_pages + L0 / t.page_size];
+        g.shared = valid_page(t, p) ? p : -1;
+    }
+    return g;
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    reserve_kernel(const Table t, const int32_t* seqlens, const int32_t* new_seqlens, int32_t* missing, void* scratch) {
+    __shared__ u64 warps[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
+    const ReserveScratch s(scratch, t);
+    const int2 slice = slice_of(t.num_pages, rank);
+    for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
+        const int L0 = seqlens[b], L1 = new_seqlens[b];
+        const long long cap = (long long)t.max_pages * t.page_size;
+        if (L0 < 0 || L1 > cap) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+        else if (L1 < L0) raise_status(ATTN_SINK_DEV_POOL);
+        else if (L1 > L0 && L0 % t.page_size && !valid_page(t, t.table[(size_t)b * t.max_pages + L0 / t.page_size]))
+            raise_status(ATTN_SINK_DEV_PAGE_OOB);
+        const Growth g = growth_of(t, seqlens, new_seqlens, b);
+        if (g.shared >= 0) {
+            s.users[g.shared] = 0;
+            s.last[g.shared] = -1;
+        }
+    }
+    const int mine = count_pages(t, slice, warps, [](int, int r) { return r <= 0; });
+    if (tid == 0) s.head[2 + rank] = mine;
+    cluster.sync();
+    for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
+        const Growth g = growth_of(t, seqlens, new_seqlens, b);
+        if (g.shared >= 0) {
+            atomicAdd(s.users + g.shared, 1);
+            atomicMax(s.last + g.shared, b);
+        }
+    }
+    cluster.sync();
+    if (rank == 0) {
+        // the requests' places: pages in the low bits of a sum (65535 requests of less than
+        // 2^31 stay below 2^47), copies in the high ones
+        constexpr int kCopyBit = 47;
+        constexpr u64 kNeedMask = (1ull << kCopyBit) - 1;
+        u64 base = 0;
+        for (int b0 = 0; b0 < t.batch; b0 += kThreads) {
+            const int b = b0 + tid;
+            bool copy = false;
+            u64 n = 0;
+            Growth g = {0, 0, -1};
+            if (b < t.batch) {
+                g = growth_of(t, seqlens, new_seqlens, b);
+                if (g.shared >= 0) {
+                    const int refs = t.refs[g.shared], users = s.users[g.shared];
+                    if (users > refs) raise_status(ATTN_SINK_DEV_POOL);
+                    copy = refs > 1 && users <= refs && !(users == refs && s.last[g.shared] == b);
+                }
+                n = (u64)(g.to - g.from + (copy ? 1 : 0)) | (u64)(copy ? 1 : 0) << kCopyBit;
+            }
+            u64 all;
+            const u64 at = base + block_scan(n, warps, all);
+            base += all;
+            if (b < t.batch) {
+                s.offset[b] = (int)min(at & kNeedMask, 0x7fffffffull) | (copy ? (int)0x80000000 : 0);
+                const int c = (int)(at >> kCopyBit);
+                if (copy) {
+                    s.src[c] = g.shared;
+                    s.dst[c] = -1 - b;  // the page is not known yet
+                }
+            }
+        }
+        if (tid == 0) {
+            s.head[0] = (int)(base >> kCopyBit);
+            s.head[1] = (int)min(base & kNeedMask, 0x7fffffffull);
+        }
+    }
+    cluster.sync();
+    const int need = s.head[1], copies = s.head[0];
+    long long before = 0, have = 0;
+    for (int c = 0; c < kCtas; ++c) {
+        if (c < rank) before += s.head[2 + c];
+        have += s.head[2 + c];
+    }
+    const bool fits = need <= have;
+    if (rank == 0 && tid == 0) {
+        missing[0] = fits ? 0 : (int)(need - have);
+        if (!fits) raise_status(ATTN_SINK_DEV_POOL);
+    }
+    if (fits)
+        rank_pages(t, slice, (int)before, need, warps, [](int, int r) { return r <= 0; },
+                   [&](int r, int p) { s.free[r] = p; });
+    cluster.sync();
+    if (!fits) {
+        if (rank == 0 && tid == 0) s.head[0] = 0;  // nothing is copied
+        return;
+    }
+    const int lane = tid & 31;
+    for (int b = rank * (kThreads / 32) + (tid >> 5); b < t.batch; b += all_threads / 32) {
+        const Growth g = growth_of(t, seqlens, new_seqlens, b);
+        __syncwarp();  // all lanes have read the row before it changes
+        const int o = s.offset[b] & 0x7fffffff;
+        const int copy = s.offset[b] < 0 ? 1 : 0;
+        int32_t* const row = t.table + (size_t)b * t.max_pages;
+        for (int i = g.from - copy + lane; i < g.to; i += 32) {
+            const int p = s.free[o + i - (g.from - copy)];
+            row[i] = p;
+            t.refs[p] = 1;
+        }
+        if (copy && lane == 0) atomicSub(t.refs + g.shared, 1);
+    }
+    for (int c = rank * kThreads + tid; c < copies; c += all_threads) {
+        const int b = -1 - s.dst[c];
+        s.dst[c] = s.free[s.offset[b] & 0x7fffffff];
+    }
+}
+
+// Scratch of compact: where held pages go, the moves, totals.
+struct CompactScratch {
+    int32_t *to, *src, *dst, *head;
+    __host__ __device__ CompactScratch(void* at, const Table& t) {
+        int32_t* p = static_cast<int32_t*>(at);
+        head = p;  // [0] moves, [2..] held pages of each slice, [10..] free ones in front, [18..] held ones behind
+        to = head + 32;
+        src = to + t.num_pages;
+        dst = src + t.num_pages;
+    }
+};
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    compact_kernel(const Table t, const int32_t* seqlens, int32_t* held, void* scratch) {
+    __shared__ u64 warps[32];
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
+    const CompactScratch s(scratch, t);
+    const int2 slice = slice_of(t.num_pages, rank);
+    int n = count_pages(t, slice, warps, [](int, int r) { return r > 0; });
+    if (tid == 0) s.head[2 + rank] = n;
+    cluster.sync();
+    n = 0;
+    for (int c = 0; c < kCtas; ++c) n += s.head[2 + c];
+    const auto gap = [n](int p, int r) { return p < n && r <= 0; };
+    const auto out = [n](int p, int r) { return p >= n && r > 0; };
+    const int gaps = count_pages(t, slice, warps, gap), outs = count_pages(t, slice, warps, out);
+    if (tid == 0) {
+        s.head[10 + rank] = gaps;
+        s.head[18 + rank] = outs;
+    }
+    cluster.sync();
+    int gap0 = 0, out0 = 0, moves = 0;
+    for (int c = 0; c < kCtas; ++c) {
+        if (c < rank) {
+            gap0 += s.head[10 + c];
+            out0 += s.head[18 + c];
+        }
+        moves += s.head[18 + c];
+    }
+    rank_pages(t, slice, gap0, t.num_pages, warps, gap, [&](int r, int p) { s.dst[r] = p; });
+    rank_pages(t, slice, out0, t.num_pages, warps, out, [&](int r, int p) { s.src[r] = p; });
+    for (int p = max(slice.x, n) + tid; p < slice.y; p += kThreads) s.to[p] = -1;
+    if (rank == 0 && tid == 0) {
+        s.head[0] = moves;
+        held[0] = n;
+    }
+    cluster.sync();
+    for (int r = rank * kThreads + tid; r < moves; r += all_threads) {
+        const int from = s.src[r], to = s.dst[r];
+        s.to[from] = to;
+        t.refs[to] = t.refs[from];
+        t.refs[from] = 0;
+    }
+    cluster.sync();
+    const int lane = tid & 31;
+    for (int b = rank * (kThreads / 32) + (tid >> 5); b < t.batch; b += all_threads / 32) {
+        const int pages = pages_of(length_of(t, seqlens, b), t.page_size);
+        int32_t* const row = t.table + (size_t)b * t.max_pages;
+        for (int i = lane; i < pages; i += 32) {
+            const int p = row[i];
+            if (!valid_page(t, p)) {
+                raise_status(ATTN_SINK_DEV_PAGE_OOB);
+            } else if (p >= n) {
+                if (s.to[p] >= 0) row[i] = s.to[p];
+                else raise_status(ATTN_SINK_DEV_POOL);  // held by a row, but not counted
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Page copies: work items of kPiece bytes, (copy, tensor, piece) in that order.
+
+constexpr int kCopyThreads = 256;
+constexpr int kAhead = 4;  // 16-byte loads of a thread in flight
+constexpr long long kPiece = 16LL * kCopyThreads * kAhead;
+
+template <class V>
+__device__ __forceinline__ void copy_piece(const char* from, char* to, long long bytes) {
+    const V* const a = reinterpret_cast<const V*>(from);
+    V* const b = reinterpret_cast<V*>(to);
+    const int n = (int)(bytes / (long long)sizeof(V));
+    for (int i = threadIdx.x; i < n; i += kCopyThreads * kAhead) {
+        V x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k * kCopyThreads < n) x[k] = a[i + k * kCopyThreads];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i + k * kCopyThreads < n) b[i + k * kCopyThreads] = x[k];
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const int32_t* src, const int32_t* dst,
+                                                            const int32_t* count, int n, int num_pages, bool report) {
+    if (count) n = min(n, *count);
+    long long pieces = 0;  // of one copy
+    for (int i = 0; i < p.count; ++i) pieces += (p.bytes[i] + kPiece - 1) / kPiece;
+    for (long long w = blockIdx.x; w < n * pieces; w += gridDim.x) {
+        const int c = (int)(w / pieces);
+        long long k = w - c * pieces;
+        int i = 0;
+        for (; i < p.count; ++i) {
+            const long long own = (p.bytes[i] + kPiece - 1) / kPiece;
+            if (k < own) break;
+            k -= own;
+        }
+        const int from = src[c], to = dst[c];
+        if ((unsigned)from >= (unsigned)num_pages || (unsigned)to >= (unsigned)num_pages) {
+            if (report && threadIdx.x == 0 && (from != -1 || to != -1)) raise_status(ATTN_SINK_DEV_PAGE_OOB);
+            continue;
+        }
+        if (from == to) continue;
+        const long long at = k * kPiece, len = min(kPiece, p.bytes[i] - at);
+        char* const base = static_cast<char*>(p.base[i]);
+        const char* const a = base + (long long)from * p.bytes[i] + at;
+        char* const b = base + (long long)to * p.bytes[i] + at;
+        const unsigned long long odd = (unsigned long long)p.bytes[i] | (unsigned long long)base;
+        if (!(odd & 15)) copy_piece<uint4>(a, b, len);
+        else if (!(odd & 3)) copy_piece<uint32_t>(a, b, len);
+        else copy_piece<uint8_t>(a, b, len);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+size_t reserve_scratch(const Table& t) { return (16 + 3 * (size_t)t.num_pages + 3 * (size_t)t.batch) * 4; }
+size_t compact_scratch(const Table& t) { return (32 + 3 * (size_t)t.num_pages) * 4; }
+
+cudaError_t launch_copy(const Pools& p, const int32_t* src, const int32_t* dst, const int32_t* count, int n, int num_pages,
+                        bool report, cudaStream_t s) {
+    long long pieces = 0;
+    for (int i = 0; i < p.count; ++i) pieces += (p.bytes[i] + kPiece - 1) / kPiece;
+    if (n <= 0 || pieces == 0) return cudaSuccess;
+    // all resident at once: 8 CTAs of 256 threads an SM
+    const long long want = n * pieces, most = 8LL * num_sms();
+    copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, s>>>(p, src, dst, count, n, num_pages, report);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fork(const Table& t, const int32_t* seqlens, const int32_t* src, int out_batch, int32_t* out_table,
+                        int32_t* out_seqlens, cudaStream_t s) {
+    const int rows = t.batch > out_batch ? t.batch : out_batch;
+    if (rows == 0) return cudaSuccess;
+    fork_kernel<<<(rows + kRowWarps - 1) / kRowWarps, kRowWarps * 32, 0, s>>>(t, seqlens, src, out_batch, out_table,
+                                                                            out_seqlens);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_release(const Table& t, const int32_t* seqlens, const int32_t* new_seqlens, cudaStream_t s) {
+    if (t.batch == 0) return cudaSuccess;
+    release_kernel<<<(t.batch + kRowWarps - 1) / kRowWarps, kRowWarps * 32, 0, s>>>(t, seqlens, new_seqlens);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_reserve(const Pools& p, const Table& t, const int32_t* seqlens, const int32_t* new_seqlens,
+                           int32_t* missing, void* scratch, cudaStream_t s) {
+    reserve_kernel<<<kCtas, kThreads, 0, s>>>(t, seqlens, new_seqlens, missing, scratch);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const ReserveScratch r(scratch, t);
+    return launch_copy(p, r.src, r.dst, r.head, t.batch, t.num_pages, false, s);
+}
+
+cudaError_t launch_compact(const Pools& p, const Table& t, const int32_t* seqlens, int32_t* held, void* scratch,
+                           cudaStream_t s) {
+    compact_kernel<<<kCtas, kThreads, 0, s>>>(t, seqlens, held, scratch);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const CompactScratch c(scratch, t);
+    return launch_copy(p, c.src, c.dst, c.head, t.num_pages, t.num_pages, false, s);
+}
+
+ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+
+}  // namespace pages
+}  // namespace attn

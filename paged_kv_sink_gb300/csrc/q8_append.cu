@@ -1,0 +1,308 @@
+// The 8-bit cache's other side: new rows into codes and scales, and codes back into
+// bf16 pages (sm_103a).
+//
+// Append.  A block of tokens and a KV head share one scale, a power of two:
+//     e = the least exponent >= -64 with max|x| <= qmax 2^e   (qmax 448 or 127)
+//     code = round(x 2^-e), to nearest, ties to even.
+// A power of two costs e4m3 nothing (a floating-point format has the same digits at
+// every scale) and int8 less than one bit, and it lets a block that is filled a few
+// tokens at a time keep its digits: when a new row needs a larger scale, the rows
+// that the block has are brought to it by a shift, which for e4m3 is exact but in its
+// subnormals and for int8 rounds by at most one step of the final scale in all
+// (half a step of every scale on the way, each half the next).  The block's scale never
+// falls while it has tokens, so that codes do not depend on how many calls filled
+// it, but for those roundings.
+//
+// One warp per (block of tokens, KV head, K or V): the largest magnitude and the codes
+// come from one read, its rows kept in registers.  Bound by memory: 35k rows of 8 heads
+// of 128 (int8, blocks of 32).
+#include "q8.cuh"
+
+#include <cuda_fp8.h>
+
+namespace attn {
+namespace q8 {
+
+constexpr int kAppendWarps = 8;
+constexpr int kHeld = 8;  // 16-byte pieces of rows that a lane keeps
+
+// 8 fp32 in units of the scale as 8 codes.
+template <int F>
+__device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
+    uint2 r;
+    if constexpr (F == kE4M3) {
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // cvt's first operand is the upper half
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+        r.x = h[0] | (uint32_t)h[1] << 16;
+        r.y = h[2] | (uint32_t)h[3] << 16;
+    } else {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(x[i] + 12582912.f);  // 1.5 2^23: the low byte is round(x)
+        r.x = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+        r.y = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
+    }
+    return r;
+}
+
+template <int F>
+__device__ __forceinline__ void decode8(uint2 w, float (&x)[8]) {
+    uint32_t h[4];
+    quad_to_f16<F>(w.x, h[0], h[1]);
+    quad_to_f16<F>(w.y, h[2], h[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = f16_to_float2(h[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t x) {  // NaN wins
+    const uint32_t y = x & 0x7fff7fffu;
+    const __nv_bfloat162 m =
+        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&m);
+}
+
+// Exponent of the scale for a largest magnitude `top` (finite, >= 0).
+template <int F>
+__device__ __forceinline__ int needed_exp(float top) {
+    if (!(top > 0.f)) return kMinExp;
+    int k;
+    const float f = frexpf(top, &k);  // top = f 2^k, 0.5 <= f < 1
+    // 448 = 0.875 2^9, 127 = (127/128) 2^7
+    const int e = F == kE4M3 ? k - 9 + (f > 0.875f ? 1 : 0) : k - 7 + (f > 0.9921875f ? 1 : 0);
+    return e < kMinExp ? kMinExp : e;
+}
+
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+template <int D, int F>
+__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a, int page_shift) {
+    constexpr int kLanes = D / 8;          // lanes of a row
+    constexpr int kRows = 32 / kLanes;     // rows of a warp's instruction
+    const Cache& c = a.c;
+    const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane / kLanes, seg = lane % kLanes;
+    const long long task = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const bool is_v = task & 1;
+    const int head = (int)((task >> 1) % c.hkv);
+    const int n0 = a.cu_new ? a.cu_new[b] : b;
+    int n = a.cu_new ? a.cu_new[b + 1] - n0 : 1;
+    const int L = a.seqlens[b];
+    const bool first = task == 0 && lane == 0;
+    if (first && n > a.max_new) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    if (n0 < 0 || n <= 0) return;
+    const int start = L - n;  // token of the first new row
+    // as in the bf16 append, rows of negative tokens and behind the page table are left out
+    const long long cap = (long long)c.max_pages * c.page_size;
+    if (first && (start < 0 || L > cap || n0 + (long long)n > a.total_new)) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    const int from = max(start, 0);
+    int end = L < cap ? L : (int)cap;
+    if (n0 + (long long)n > a.total_new) end = min(end, start + max(0, a.total_new - n0));
+    if (n > a.max_new) end = min(end, start + a.max_new);
+    if (end <= from) return;
+    const long long t0l = (from / c.block + (task >> 1) / c.hkv) * (long long)c.block;
+    if (t0l >= end) return;
+    const int t0 = (int)t0l;
+    const Place pl = place_of(t0, c.page_size, page_shift);
+    const int page = c.page_table[(size_t)b * c.max_pages + pl.page];
+    if ((unsigned)page >= (unsigned)c.num_pages) {
+        if (lane == 0) raise_status(ATTN_SINK_DEV_PAGE_OOB);
+        return;
+    }
+    const int lo = max(t0, from), hi = min(t0 + c.block, end);
+    const __nv_bfloat16* src =
+        (is_v ? a.v_new : a.k_new) + (n0 + (long long)(lo - start)) * (is_v ? a.v_rs : a.k_rs) + head * D + seg * 8;
+    const long long rs = is_v ? a.v_rs : a.k_rs;
+    uint8_t* dst = (is_v ? c.v : c.k) + (((size_t)page * c.page_size + pl.in_page) * c.hkv + head) * D + seg * 8;
+    const size_t ds = (size_t)c.hkv * D;
+    float* scale = (is_v ? c.v_scale : c.k_scale) +
+                   ((size_t)page * (c.page_size / c.block) + pl.in_page / c.block) * c.hkv + head;
+
+    uint4 held[kHeld];
+    uint32_t top2 = 0;
+    const int rows = hi - lo;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = i * kRows + sub;
+        held[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + r * rs)) : make_uint4(0, 0, 0, 0);
+    }
+    const float old = lo > t0 ? *scale : 0.f;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+        top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, held[i].x), held[i].y), held[i].z), held[i].w);
+    for (int r = kHeld * kRows + sub; r < rows; r += kRows) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + r * rs));
+        top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, x.x), x.y), x.z), x.w);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) top2 = max_abs2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
+    // bf16 magnitudes as integers keep their order: infinities and NaNs are 0x7f80 and above
+    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+    const bool odd = top >= 0x7f80u;
+    if (odd) {  // the largest finite one
+        if (lane == 0) raise_status(ATTN_SINK_DEV_VALUE);
+        top = 0;
+        for (int r = sub; r < rows; r += kRows) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + r * rs));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t p = w[i] & 0x7fffu, q = (w[i] >> 16) & 0x7fffu;
+                if (p < 0x7f80u) top = max(top, p);
+                if (q < 0x7f80u) top = max(top, q);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    const int e = needed_exp<F>(__uint_as_float(top << 16));
+    float sc = exp2i(e), inv = exp2i(-e);
+    if (lo > t0) {
+        if (old >= sc) {
+            sc = old;
+            inv = 1.f / old;
+        } else {  // the rows that the block has, brought to the larger scale
+            const float ratio = old > 0.f ? old / sc : 0.f;
+            for (int r = sub; r < lo - t0; r += kRows) {
+                uint2* at = reinterpret_cast<uint2*>(dst + r * ds);
+                float x[8];
+                decode8<F>(*at, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] *= ratio;
+                *at = encode8<F>(x);
+            }
+        }
+    }
+    auto put = [&](int r, const uint4& x) {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = bf16_lo(w[i]) * inv;
+            f[2 * i + 1] = bf16_hi(w[i]) * inv;
+        }
+        if (odd) {  // infinities: the largest code of their sign; NaN: 0
+            constexpr float kMax = F == kE4M3 ? 448.f : 127.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i], -kMax), kMax);
+        }
+        *reinterpret_cast<uint2*>(dst + (size_t)(lo - t0 + r) * ds) = encode8<F>(f);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int r = i * kRows + sub;
+        if (r < rows) put(r, held[i]);
+    }
+    for (int r = kHeld * kRows + sub; r < rows; r += kRows) put(r, __ldg(reinterpret_cast<const uint4*>(src + r * rs)));
+    if (lane == 0) *scale = sc;
+}
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
+    if (a.batch == 0 || a.max_new <= 0) return cudaSuccess;
+    // blocks that max_new tokens can touch, wherever they start
+    const long long blocks = ((long long)a.max_new + a.c.block - 2) / a.c.block + 1;
+    const long long tasks = blocks * a.c.hkv * 2;
+    const long long grid_x = (tasks + kAppendWarps - 1) / kAppendWarps;
+    if (grid_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    dim3 grid((unsigned)grid_x, a.batch);
+    const int sh = shift_of(a.c.page_size);
+    if (a.c.head_dim == 64) {
+        if (a.c.format == kE4M3) append_kernel<64, kE4M3><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
+        else append_kernel<64, kInt8><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
+    } else {
+        if (a.c.format == kE4M3) append_kernel<128, kE4M3><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
+        else append_kernel<128, kInt8><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
+    }
+    return cudaGetLastError();
+}
+
+// Codes back into bf16, which holds every c 2^e of either format: the forward's
+// tensor-core kernel reads the result as a paged cache of its own.  Only the 128-key
+// tiles that the windows show are written.
+constexpr int kExpandThreads = 256;
+constexpr int kExpandTokens = 32;  // tokens of a block
+
+template <int F>
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs a, int page_shift) {
+    const Cache& c = a.c;
+    const int b = blockIdx.y;
+    const int Lq = max(0, a.cu_q[b + 1] - a.cu_q[b]);
+    const long long cap = min((long long)c.max_pages * c.page_size, (long long)a.pages * kExpandPage);
+    int L = a.seqlens[b];
+    if (L > cap) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+        L = (int)cap;
+    }
+    const int t0 = blockIdx.x * kExpandTokens;
+    if (Lq == 0 || t0 >= L) return;
+    if (a.win_last > 0) {  // no row sees tokens between the first window and the first row's last one
+        const long long lo = max(0LL, (long long)L - Lq + 1 - a.win_last);
+        if (t0 >= (a.win_first + 127LL) / 128 * 128 && t0 + kExpandTokens <= lo / 128 * 128) return;
+    }
+    if (threadIdx.x == 0) a.table_out[(size_t)b * a.pages + t0 / kExpandPage] = b * a.pages + t0 / kExpandPage;
+    __shared__ int page_of[kExpandTokens], in_of[kExpandTokens];
+    if (threadIdx.x < kExpandTokens) {
+        const int t = t0 + threadIdx.x;
+        int page = -1, in = 0;
+        if (t < L) {
+            const Place pl = place_of(t, c.page_size, page_shift);
+            page = c.page_table[(size_t)b * c.max_pages + pl.page];
+            in = pl.in_page;
+            if ((unsigned)page >= (unsigned)c.num_pages) {
+                raise_status(ATTN_SINK_DEV_PAGE_OOB);
+                page = -2;
+            }
+        }
+        page_of[threadIdx.x] = page;
+        in_of[threadIdx.x] = in;
+    }
+    __syncthreads();
+    const int vec = c.hkv * c.head_dim / 16, dv = c.head_dim / 16;  // 16-code pieces of a row, of a head
+    for (int i = threadIdx.x; i < kExpandTokens * vec; i += kExpandThreads) {
+        const int r = i / vec, x = i - r * vec, page = page_of[r];
+        if (page == -1) break;  // behind the request's end
+        const size_t to = ((size_t)b * a.pages * kExpandPage + t0 + r) * vec + x;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            uint4* out = reinterpret_cast<uint4*>(kv ? a.v_out : a.k_out) + to * 2;
+            if (page < 0) {
+                out[0] = out[1] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const float sc = (kv ? c.v_scale : c.k_scale)[((size_t)page * (c.page_size / c.block) + in_of[r] / c.block) *
+                                                              c.hkv + x / dv];
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(kv ? c.v : c.k) +
+                                   ((size_t)page * c.page_size + in_of[r]) * vec + x);
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t p, q;
+                quad_to_f16<F>(in[j], p, q);
+                const float2 f = f16_to_float2(p), g = f16_to_float2(q);
+                y[2 * j] = pack_bf16x2(f.x * sc, f.y * sc);
+                y[2 * j + 1] = pack_bf16x2(g.x * sc, g.y * sc);
+            }
+            out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+            out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+    }
+}
+
+cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t s) {
+    if (a.batch == 0 || a.pages == 0) return cudaSuccess;
+    dim3 grid((unsigned)a.pages * (kExpandPage / kExpandTokens), a.batch);
+    const int sh = shift_of(a.c.page_size);
+    if (a.c.format == kE4M3) expand_kernel<kE4M3><<<grid, kExpandThreads, 0, s>>>(a, sh);
+    else expand_kernel<kInt8><<<grid, kExpandThreads, 0, s>>>(a, sh);
+    return cudaGetLastError();
+}
+
+ATTN_DEFINE_STATUS_ACCESSOR(append_status_exchange)
+
+}  // namespace q8
+}  // namespace attn

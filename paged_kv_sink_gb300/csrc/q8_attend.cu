@@ -1,0 +1,620 @@
+// Attention over the 8-bit paged cache: one new token a request (decode) or a few
+// (drafts in a row), with the sink and the first/last windows (sm_103a).
+//
+// What it computes, for a query row i with head h of a request:
+//     s_t = scale (q_i . kc_t) ks_t,   O = sum_t e^{s_t - M} vs_t vc_t / Z,
+//     Z = e^{sink - M} + sum_t e^{s_t - M}
+// over the tokens t that the row sees; kc, vc are codes and ks, vs the scales of
+// their block of tokens and KV head.
+//
+// Structure: one CTA per (split of visible tokens, KV head and row tile, request); the
+// rows of a tile are (new token, query head of the KV group) pairs, 8 to 32 of them.
+//  * Each of the four warps streams 32-token chunks of its own through a ring of
+//    shared-memory stages (16-byte cp.async gathers through the page table), so that
+//    nothing but the end of the split brings the warps together.
+//  * S^T = K q^T and O^T += V^T P^T are small tensor-core products whose A operands
+//    are made from the codes in registers: both formats are exact in fp16, and the
+//    order of the head dimensions in a product is free, so that a lane takes 16
+//    bytes of a token's row as they lie.  q enters as fp16 of a row scaled by a power of
+//    two to a largest magnitude in [1, 2): what fp16 loses there is 2^-25 of that.
+//  * Scales stay out of the products: ks multiplies the scores; vs is folded into the
+//    weights as log2(vs) in the exponent, with the running maximum taken over
+//    s_t + log2 vs_t, so that P = e^{s - M} vs never leaves fp16's range: it is at most
+//    2^14 there, and what falls below 2^-39 of the largest weight is lost.  Its
+//    rounding to fp16 is off by at most 2^-11 of each weight (bf16: 2^-8).  The
+//    denominator sums P / vs, unrounded, in fp32.
+//  * attend_combine_kernel merges the splits in the log-sum-exp sense and folds the
+//    sink in once; with a single split the CTA does it itself.
+// Bound by HBM: half the bytes of the bf16 cache.
+#include "q8.cuh"
+
+#include <math.h>
+
+namespace attn {
+namespace q8 {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTokens = 32;        // tokens of a warp's chunk
+constexpr float kHead = 14.f;      // P is at most 2^kHead
+constexpr float kMinScale = 5.421010862427522e-20f;  // 2^-64
+
+struct Params {
+    Cache c;
+    const __nv_bfloat16* q;
+    const int32_t* cu_q;
+    const int32_t* seqlens;
+    const float* sink;
+    __nv_bfloat16* out;
+    float* lse;
+    float* part_o;    // (rows, hq, max_splits, d), un-normalised
+    float2* part_ml;  // (rows, hq, max_splits): (reference in log2 units, sum)
+    int total_q, hq, group, max_q, max_tokens, win_first, win_last, causal, lse_by_head;
+    int page_shift, tiles, split_tokens, max_splits;
+    float scale_log2;
+};
+
+// One request as the kernels see it.
+struct Request {
+    int q_start, Lq, L, off;  // off: position of its first row
+};
+
+__device__ __forceinline__ Request request_of(const Params& p, int b, bool report) {
+    Request r;
+    r.q_start = p.cu_q ? p.cu_q[b] : b;
+    r.Lq = p.cu_q ? p.cu_q[b + 1] - r.q_start : 1;
+    r.L = p.seqlens[b];
+    bool bad = r.L > p.max_tokens || r.Lq > p.max_q || r.q_start + (long long)r.Lq > p.total_q || r.q_start < 0;
+    r.L = max(0, min(r.L, p.max_tokens));
+    // rows past the host's bounds are left alone; the others keep their positions
+    r.off = r.L - r.Lq;
+    if (r.q_start < 0) r.Lq = 0;
+    r.Lq = max(0, min(min(r.Lq, p.max_q), p.total_q - r.q_start));
+    if (bad && report) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    return r;
+}
+
+// Tokens that some row of the tile's new tokens [tok0, tok1] sees.
+__device__ __forceinline__ Ranges tile_ranges(const Params& p, const Request& r, int tok0, int tok1) {
+    Ranges v;
+    const int n = p.causal ? max(0, r.off + tok1 + 1) : r.L;
+    v.a0 = 0;
+    v.b0 = n;
+    v.a1 = n;
+    v.b1 = n;
+    if (p.win_last > 0) {
+        v.b0 = min(p.win_first, n);
+        v.a1 = (int)max((long long)v.b0, (long long)r.off + tok0 + 1 - p.win_last);
+        v.a1 = min(v.a1, n);
+    }
+    return v;
+}
+
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+// Byte offset of 16-byte piece `seg` of staged token row t (of a warp's 32).  The pieces
+// are permuted so that both readers are free of bank conflicts: 8 rows x 4 pieces (K) and
+// 4 rows x 8 lanes (V), with the token order of row_of below.
+template <int D>
+__device__ __forceinline__ uint32_t stage_off(int t, int seg) {
+    if constexpr (D == 64) return t * 64 + ((seg ^ (((t >> 2) & 1) << 1)) << 4);
+    return t * 128 + ((seg ^ ((t & 1) << 2) ^ (((t >> 1) & 3) << 1)) << 4);
+}
+
+// Staged row (of 8) that row g of a product stands for.
+template <int D>
+__device__ __forceinline__ int row_of(int g) {
+    return D == 64 ? g ^ ((g >> 1) & 1) : g;
+}
+
+__device__ __forceinline__ float max_g(float x) {  // over lanes with equal lane % 4
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+__device__ __forceinline__ float sum_g(float x) {
+    x += __shfl_xor_sync(0xffffffffu, x, 4);
+    x += __shfl_xor_sync(0xffffffffu, x, 8);
+    return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// The root of the factor 2^x that brings a partial sum to a common reference.  The sums are
+// taken against references that kHead and the V scales put below the scores' maximum, so that
+// they are large where 2^x may be below fp32's range: it is multiplied in twice.
+__device__ __forceinline__ float half_factor(float x) { return fast_exp2(0.5f * x); }
+
+// A row's output from the merged reference, sum and accumulator (an infinite
+// reference: nothing seen and no sink, or an infinite sink that takes all the mass).
+__device__ __forceinline__ float finish(float M, float Z, float acc, float& lse) {
+    if (M == -INFINITY || M == INFINITY) {
+        lse = M;
+        return 0.f;
+    }
+    lse = (M + log2f(Z)) * ATTN_LN2;
+    return acc / Z;
+}
+
+template <int D, int STAGES>
+struct Smem {
+    static constexpr int kData = 2 * kTokens * D;        // K and V codes of a warp's chunk
+    static constexpr int kStage = kData + 3 * kTokens * 4;  // and its tokens' scales and positions
+    static constexpr int kBytes = kWarps * STAGES * kStage;
+};
+
+// kRows: several new tokens, so that rows see different tokens.
+template <int D, int NT, int STAGES, int F, bool kRows>
+__global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
+    using SM = Smem<D, STAGES>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    constexpr int H = 8 * NT;
+    constexpr int kSegs = D / 16;          // 16-byte pieces of a row
+    constexpr int kRowsPer = 32 / kSegs;   // rows of a warp's copy instruction
+    constexpr int KK = D / 16;             // k steps of S
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    const Cache& c = p.c;
+    const int split = blockIdx.x, b = blockIdx.z;
+    const int kvh = blockIdx.y / p.tiles, tile = blockIdx.y % p.tiles;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, cc = lane & 3;
+
+    const Request r = request_of(p, b, tid == 0 && split == 0 && blockIdx.y == 0);
+    const int row0 = tile * H, nrows = min(H, r.Lq * p.group - row0);
+    if (nrows <= 0) return;
+    const int tok0 = kRows ? row0 / p.group : 0, tok1 = kRows ? (row0 + nrows - 1) / p.group : 0;
+    const Ranges vis = tile_ranges(p, r, tok0, tok1);
+    const int nvis = visible_count(vis);
+    const long long v0l = (long long)split * p.split_tokens;
+    if (v0l >= nvis && p.max_splits > 1) return;
+    const int v0 = (int)v0l, v1 = (int)min((long long)nvis, v0l + p.split_tokens);
+    const int nchunks = (v1 - v0 - warp * kTokens + kWarps * kTokens - 1) / (kWarps * kTokens);  // of this warp
+
+    // Query row, head of tile row j.
+    auto row_at = [&](int j, int& tok, int& head) {
+        const int x = row0 + j;
+        tok = kRows ? x / p.group : 0;
+        head = kvh * p.group + (kRows ? x - tok * p.group : x);
+    };
+
+    uint8_t* const ring = smem + warp * STAGES * SM::kStage;
+    auto load = [&](int chunk, int st) {
+        uint8_t* const base = ring + st * SM::kStage;
+        const int v = v0 + (chunk * kWarps + warp) * kTokens + lane;
+        int page = -1, slot = 0, t = -1;
+        size_t sc = 0;
+        if (v < v1) {
+            t = visible_token(vis, v);
+            const Place pl = place_of(t, c.page_size, p.page_shift);
+            page = c.page_table[(size_t)b * c.max_pages + pl.page];
+            if ((unsigned)page < (unsigned)c.num_pages) {
+                slot = page * c.page_size + pl.in_page;
+                sc = ((size_t)page * (c.page_size / c.block) + pl.in_page / c.block) * c.hkv + kvh;
+            } else {
+                raise_status(ATTN_SINK_DEV_PAGE_OOB);
+                page = t = -1;
+            }
+        }
+        float* const meta = reinterpret_cast<float*>(base + SM::kData);
+        reinterpret_cast<int*>(meta + 2 * kTokens)[lane] = t;  // -1: takes no weight
+        copy4(smem_u32(meta + lane), c.k_scale + sc, page >= 0 ? 4 : 0);
+        copy4(smem_u32(meta + kTokens + lane), c.v_scale + sc, page >= 0 ? 4 : 0);
+        if (page < 0) slot = -1;
+#pragma unroll
+        for (int i = 0; i < kTokens / kRowsPer; ++i) {
+            const int row = i * kRowsPer + lane / kSegs, seg = lane % kSegs;
+            const int sl = __shfl_sync(0xffffffffu, slot, row);
+            const size_t off = ((size_t)max(sl, 0) * c.hkv + kvh) * D + seg * 16;
+            const uint32_t to = smem_u32(base) + stage_off<D>(row, seg);
+            copy16(to, c.k + off, sl >= 0 ? 16 : 0);
+            copy16(to + kTokens * D, c.v + off, sl >= 0 ? 16 : 0);
+        }
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+        if (s < nchunks) load(s, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    // q as the B operand of S^T = K q^T: lane (g, cc) has row g's dims 16 cc .. 16 cc + 15
+    // (d 128: and 64 further), k step kk of them 4 kk .. 4 kk + 3.
+    uint32_t qf[NT][KK][2];
+    float factor[NT][2];  // of this lane's two score columns: softmax scale, q's scale
+    int seen_to[NT][2];   // last position that the column's row sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        int tok, head;
+        row_at(nt * 8 + g, tok, head);
+        const bool ok = nt * 8 + g < nrows;
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + ((size_t)(r.q_start + (ok ? tok : 0)) * p.hq + (ok ? head : 0)) * D);
+        uint32_t w[KK * 2];
+#pragma unroll
+        for (int i = 0; i < KK / 2; ++i) {  // 8 dims each
+            const int at = (i >> 1) * 8 + cc * 2 + (i & 1);
+            const uint4 x = ok ? src[at] : make_uint4(0, 0, 0, 0);
+            w[4 * i] = x.x;
+            w[4 * i + 1] = x.y;
+            w[4 * i + 2] = x.z;
+            w[4 * i + 3] = x.w;
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < KK * 2; ++i) top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // exponent of top; rows that are zero or not finite are taken as they are
+        int e = (__float_as_int(top) >> 23) - 127;
+        if (e == -127 || e == 128) e = 0;
+        e = max(-126, min(e, 126));
+        const float down = __int_as_float((127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < KK * 2; ++i)
+            qf[nt][i >> 1][i & 1] = pack_f16x2(bf16_lo(w[i]) * down, bf16_hi(w[i]) * down);
+        const float up = p.scale_log2 * __int_as_float((127 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            factor[nt][i] = __shfl_sync(0xffffffffu, up, (2 * cc + i) * 4);
+            if constexpr (kRows) {
+                int tk, hd;
+                row_at(nt * 8 + 2 * cc + i, tk, hd);
+                seen_to[nt][i] = nt * 8 + 2 * cc + i < nrows ? (p.causal ? r.off + tk : r.L - 1) : -1;
+            }
+        }
+    }
+
+    float m_run[NT][2], l_run[NT][2], o[KK][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        m_run[nt][0] = m_run[nt][1] = -INFINITY;
+        l_run[nt][0] = l_run[nt][1] = 0.f;
+#pragma unroll
+        for (int mt = 0; mt < KK; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
+    }
+
+    for (int chunk = 0; chunk < nchunks; ++chunk) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();  // the chunk's bytes, copied by all lanes; the stage read last is free
+        if (chunk + STAGES - 1 < nchunks) load(chunk + STAGES - 1, (chunk + STAGES - 1) % STAGES);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint8_t* const sK = ring + (chunk % STAGES) * SM::kStage;
+        const uint8_t* const sV = sK + kTokens * D;
+        const float* const meta = reinterpret_cast<const float*>(sK + SM::kData);
+
+        float x[2][NT][4];
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[tt][nt][i] = 0.f;
+            const int ra = tt * 16 + row_of<D>(g);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) {
+                const uint4 a = *reinterpret_cast<const uint4*>(sK + stage_off<D>(ra, h * 4 + cc));
+                const uint4 d = *reinterpret_cast<const uint4*>(sK + stage_off<D>(ra + 8, h * 4 + cc));
+                const uint32_t wa[4] = {a.x, a.y, a.z, a.w}, wd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    uint32_t f[4];
+                    quad_to_f16<F>(wa[kk], f[0], f[2]);
+                    quad_to_f16<F>(wd[kk], f[1], f[3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(x[tt][nt], f, qf[nt][h * 4 + kk]);
+                }
+            }
+        }
+        // this lane's tokens: rows ra and ra + 8 of both tiles
+        float ks[4], lv[4], iv[4];
+        int pos[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = (i >> 1) * 16 + (i & 1) * 8 + row_of<D>(g);
+            ks[i] = meta[t];
+            const float vs = fmaxf(meta[kTokens + t], kMinScale);
+            pos[i] = reinterpret_cast<const int*>(meta + 2 * kTokens)[t];
+            lv[i] = pos[i] >= 0 ? __log2f(vs) : -INFINITY;
+            iv[i] = __fdividef(1.f, vs);
+        }
+        uint32_t pf[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float mn[2] = {m_run[nt][0], m_run[nt][1]};
+            float y[2][4];
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float s = x[i >> 1][nt][(i & 1) * 2 + col];
+                    float v = s * (ks[i] * factor[nt][col]) + lv[i];
+                    bool hide = pos[i] < 0;
+                    if constexpr (kRows) {
+                        hide |= pos[i] > seen_to[nt][col];
+                        if (p.win_last > 0) hide |= pos[i] >= p.win_first && pos[i] <= seen_to[nt][col] - p.win_last;
+                    }
+                    y[col][i] = hide ? -INFINITY : v;
+                }
+                const float top = max_g(fmaxf(fmaxf(y[col][0], y[col][1]), fmaxf(y[col][2], y[col][3])));
+                mn[col] = fmaxf(mn[col], top);
+            }
+            // what came before is rescaled where some row of the warp has a new maximum
+            if (__any_sync(0xffffffffu, mn[0] != m_run[nt][0] || mn[1] != m_run[nt][1])) {
+#pragma unroll
+                for (int col = 0; col < 2; ++col) {
+                    const float al = mn[col] == -INFINITY ? 1.f : fast_exp2(m_run[nt][col] - mn[col]);
+                    l_run[nt][col] *= al;
+                    m_run[nt][col] = mn[col];
+#pragma unroll
+                    for (int mt = 0; mt < KK; ++mt) {
+                        o[mt][nt][col] *= al;
+                        o[mt][nt][2 + col] *= al;
+                    }
+                }
+            }
+            float w[2][4];
+#pragma unroll
+            for (int col = 0; col < 2; ++col) {
+                const float ref = mn[col] == -INFINITY ? 0.f : mn[col] - kHead;
+                float l = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[col][i] = fast_exp2(y[col][i] - ref);
+                    l += w[col][i] * iv[i];
+                }
+                l_run[nt][col] += l;
+            }
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                pf[tt][nt][0] = transpose8(pack_f16x2(w[0][tt * 2], w[1][tt * 2]));
+                pf[tt][nt][1] = transpose8(pack_f16x2(w[0][tt * 2 + 1], w[1][tt * 2 + 1]));
+            }
+        }
+        // O^T (dims x rows) += V^T P^T: lane (g, cc) has dims g D/8 .. of tokens 2cc, 2cc + 1,
+        // 2cc + 8, 2cc + 9; product row g of step mt is its dim 2 mt, row g + 8 the next.
+#pragma unroll
+        for (int tt = 0; tt < 2; ++tt) {
+            uint32_t w[4][D / 32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = tt * 16 + (i >> 1) * 8 + row_of<D>(2 * cc + (i & 1));
+                if constexpr (D == 64) {
+                    const uint2 d = *reinterpret_cast<const uint2*>(sV + stage_off<D>(t, g >> 1) + (g & 1) * 8);
+                    w[i][0] = d.x;
+                    w[i][1] = d.y;
+                } else {
+                    const uint4 d = *reinterpret_cast<const uint4*>(sV + stage_off<D>(t, g));
+                    w[i][0] = d.x;
+                    w[i][1] = d.y;
+                    w[i][2] = d.z;
+                    w[i][3] = d.w;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j) {  // 4 dims each, two steps
+                uint32_t f[2][4];
+                quad_to_f16<F>(__byte_perm(w[0][j], w[1][j], 0x5140), f[0][0], f[0][1]);
+                quad_to_f16<F>(__byte_perm(w[0][j], w[1][j], 0x7362), f[1][0], f[1][1]);
+                quad_to_f16<F>(__byte_perm(w[2][j], w[3][j], 0x5140), f[0][2], f[0][3]);
+                quad_to_f16<F>(__byte_perm(w[2][j], w[3][j], 0x7362), f[1][2], f[1][3]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * j + k][nt], f[k], pf[tt][nt]);
+            }
+        }
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+
+    // Merge the four warps through shared memory.
+    float* const sm_m = reinterpret_cast<float*>(smem);  // [warp][H]
+    float* const sm_l = sm_m + kWarps * H;
+    float* const sm_o = sm_l + kWarps * H;               // [warp][H][D]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int col = 0; col < 2; ++col) {
+            const float l = sum_g(l_run[nt][col]);
+            const int j = nt * 8 + 2 * cc + col;
+            if (g == 0) {
+                sm_m[warp * H + j] = m_run[nt][col] - kHead;
+                sm_l[warp * H + j] = l;
+            }
+            float* const dst = sm_o + (warp * H + j) * D + g * (D / 8);
+#pragma unroll
+            for (int mt = 0; mt < KK; mt += 2)
+                *reinterpret_cast<float4*>(dst + 2 * mt) = make_float4(o[mt][nt][col], o[mt][nt][2 + col],
+                                                                       o[mt + 1][nt][col], o[mt + 1][nt][2 + col]);
+        }
+    __syncthreads();
+    for (int e = tid; e < nrows * D; e += kThreads) {
+        const int j = e / D, dd = e % D;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * H + j]);
+        int tok, head;
+        row_at(j, tok, head);
+        const size_t row = (size_t)(r.q_start + tok) * p.hq + head;
+        const bool direct = p.max_splits == 1;
+        const float sg = direct && p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
+        M = fmaxf(M, sg);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float acc = 0.f, l = direct ? fast_exp2(sg - ref) : 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = half_factor(sm_m[w * H + j] - ref);
+            acc += sm_o[(w * H + j) * D + dd] * f * f;
+            l += sm_l[w * H + j] * f * f;
+        }
+        if (direct) {
+            float lse;
+            p.out[row * D + dd] = __float2bfloat16_rn(finish(M, l, acc, lse));
+            if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
+        } else {
+            const size_t at = row * p.max_splits + split;
+            p.part_o[at * D + dd] = acc;
+            if (dd == 0) p.part_ml[at] = make_float2(M, l);
+        }
+    }
+}
+
+// One block per (query head, new token, request).
+template <int D, int NT>
+__global__ void __launch_bounds__(D) attend_combine_kernel(const Params p) {
+    const int head = blockIdx.x, tok = blockIdx.y, b = blockIdx.z, dd = threadIdx.x;
+    const Request r = request_of(p, b, false);
+    if (tok >= r.Lq) return;
+    // the splits of the row's tile
+    const int x = tok * p.group + head % p.group, row0 = x / (8 * NT) * (8 * NT);
+    const int last = min(row0 + 8 * NT, r.Lq * p.group) - 1;
+    const int nvis = visible_count(tile_ranges(p, r, row0 / p.group, last / p.group));
+    const int nsplit = (int)(((long long)nvis + p.split_tokens - 1) / p.split_tokens);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const size_t row = (size_t)(r.q_start + tok) * p.hq + head, base = row * p.max_splits;
+    const float sg = p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
+    float M = sg;
+    for (int s = 0; s < nsplit; ++s) M = fmaxf(M, p.part_ml[base + s].x);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float Z = fast_exp2(sg - ref), acc = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < nsplit; ++s) {
+        const float2 ml = p.part_ml[base + s];
+        const float f = half_factor(ml.x - ref);
+        Z += ml.y * f * f;
+        acc += p.part_o[(base + s) * D + dd] * f * f;
+    }
+    float lse;
+    p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, acc, lse));
+    if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+
+static int max_tokens(const AttendArgs& a) {
+    const long long cap = (long long)a.c.max_pages * a.c.page_size;
+    return a.max_seqlen < cap ? a.max_seqlen : (int)cap;
+}
+
+AttendPlan make_plan(const AttendArgs& a) {
+    AttendPlan pl;
+    const int group = a.hq / a.c.hkv;
+    const long long rows = (long long)group * a.max_q;
+    // 32 rows a tile at d 64; at d 128 their accumulators would not fit the registers
+    pl.nt = rows <= 8 ? 1 : rows <= 16 || a.c.head_dim == 128 ? 2 : 4;
+    pl.tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+    long long nvis = max_tokens(a);
+    if (a.win_last > 0) {  // a tile's rows are at most 8 nt tokens apart
+        const long long w = (long long)a.win_first + a.win_last + (a.max_q > 1 ? 8 * pl.nt : 0);
+        nvis = w < nvis ? w : nvis;
+    }
+    if (nvis < 1) nvis = 1;
+    // As in the bf16 decode: about two waves of resident CTAs, splits of 256 tokens at
+    // least and 128 KB of K at most.
+    const long long units = (long long)a.batch * a.c.hkv * pl.tiles;
+    const long long slots = (long long)num_sms() * (a.c.head_dim == 64 ? 4 : 2);
+    const long long per_unit = (2 * slots + units - 1) / units;
+    long long sp = (nvis + per_unit - 1) / per_unit;
+    sp = (sp + kWarps * kTokens - 1) / (kWarps * kTokens) * (kWarps * kTokens);
+    const long long most = 2048LL * 64 / a.c.head_dim;
+    if (sp > most) sp = most;
+    if (sp < 256) sp = 256;
+    pl.split_tokens = (int)sp;
+    pl.max_splits = (int)((nvis + sp - 1) / sp);
+    const size_t parts = pl.max_splits > 1 ? (size_t)a.total_q * a.hq * pl.max_splits : 0;
+    pl.part_o_bytes = parts * a.c.head_dim * sizeof(float);
+    pl.part_ml_bytes = parts * sizeof(float2);
+    return pl;
+}
+
+template <int D, int NT, int F, bool kRows>
+static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
+    constexpr int STAGES = 3;
+    int smem = Smem<D, STAGES>::kBytes;
+    const int merge = kWarps * 8 * NT * (D + 2) * 4;
+    if (smem < merge) smem = merge;
+    auto kern = attend_kernel<D, NT, STAGES, F, kRows>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(pl.max_splits, a.c.hkv * pl.tiles, a.batch), kThreads, smem, s>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || pl.max_splits == 1) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.hq, a.max_q, a.batch);
+    cfg.blockDim = dim3(D);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT>, p)) != cudaSuccess) return e;
+    return cudaGetLastError();
+}
+
+template <int D, int F>
+static cudaError_t pick(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
+    const bool rows = a.max_q > 1 || !a.causal;
+    if (pl.nt == 1) return rows ? run<D, 1, F, true>(p, a, pl, s) : run<D, 1, F, false>(p, a, pl, s);
+    if constexpr (D == 64)
+        if (pl.nt == 4) return rows ? run<D, 4, F, true>(p, a, pl, s) : run<D, 4, F, false>(p, a, pl, s);
+    return rows ? run<D, 2, F, true>(p, a, pl, s) : run<D, 2, F, false>(p, a, pl, s);
+}
+
+cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part_o, float2* part_ml, cudaStream_t s) {
+    if (a.batch == 0 || a.max_q == 0 || a.total_q == 0) return cudaSuccess;
+    Params p;
+    p.c = a.c;
+    p.q = a.q;
+    p.cu_q = a.cu_q;
+    p.seqlens = a.seqlens;
+    p.sink = a.sink;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.part_o = part_o;
+    p.part_ml = part_ml;
+    p.total_q = a.total_q;
+    p.hq = a.hq;
+    p.group = a.hq / a.c.hkv;
+    p.max_q = a.max_q;
+    p.max_tokens = max_tokens(a);
+    p.win_first = a.win_first;
+    p.win_last = a.win_last;
+    p.causal = a.causal;
+    p.lse_by_head = a.lse_by_head;
+    p.page_shift = shift_of(a.c.page_size);
+    p.tiles = pl.tiles;
+    p.split_tokens = pl.split_tokens;
+    p.max_splits = pl.max_splits;
+    p.scale_log2 = a.scale * ATTN_LOG2E;
+    if (a.c.head_dim == 64) return a.c.format == kE4M3 ? pick<64, kE4M3>(p, a, pl, s) : pick<64, kInt8>(p, a, pl, s);
+    return a.c.format == kE4M3 ? pick<128, kE4M3>(p, a, pl, s) : pick<128, kInt8>(p, a, pl, s);
+}
+
+ATTN_DEFINE_STATUS_ACCESSOR(attend_status_exchange)
+
+}  // namespace q8
+}  // namespace attn
