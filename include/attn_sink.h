@@ -567,7 +567,7 @@ int attn_sink_kv_append_q8(const attn_bf16* k_new, const attn_bf16* v_new, long 
  * of V count as at least 2^-64), not only those that the append writes.  The products are
  * fp16 with fp32 accumulation, in which both formats are exact: q enters them off by at
  * most 2^-25 of its row's largest magnitude, the weights by at most 2^-11 of each, and
- * weights below 2^-39 of the largest (times its V scale) are lost; scores, sums and
+ * weights below 2^-31 of the largest (times its V scale) are lost; scores, sums and
  * lse are fp32.
  *
  *   max_seqlen  host bound of seqlens (INT_MAX: none); sizes launches and scratch.  Lengths

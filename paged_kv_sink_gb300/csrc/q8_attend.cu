@@ -18,16 +18,18 @@
 //    bytes of a token's row as they lie.  q enters as fp16 of a row scaled by a power of
 //    two to a largest magnitude in [1, 2): what fp16 loses there is 2^-25 of that.
 //  * Scales stay out of the products: ks multiplies the scores; vs is folded into the
-//    weights as log2(vs) in the exponent, with the running maximum taken over
-//    s_t + log2 vs_t, so that P = e^{s - M} vs never leaves fp16's range: it is at most
-//    2^14 there, and what falls below 2^-39 of the largest weight is lost.  Its
-//    rounding to fp16 is off by at most 2^-11 of each weight (bf16: 2^-8).  The
-//    denominator sums P / vs, unrounded, in fp32.
+//    weights as log2(vs) in the exponent, P = 2^(s log2 e + log2 vs - ref), with the
+//    reference kept 7 to 15 below the running maximum of the exponents (it moves, and what came
+//    before is rescaled, only where a weight would pass 2^15): P never leaves fp16's range,
+//    and what falls below 2^-31 of the largest weight is lost.  Its rounding to fp16 is off by
+//    at most 2^-11 of each weight (bf16: 2^-8).  The denominator sums P / vs, unrounded, in
+//    fp32.
 //  * attend_combine_kernel merges the splits in the log-sum-exp sense and folds the
 //    sink in once; with a single split the CTA does it itself.
 // Bound by HBM: half the bytes of the bf16 cache.
 #include "q8.cuh"
 
+#include <limits.h>
 #include <math.h>
 
 namespace attn {
@@ -36,7 +38,9 @@ namespace q8 {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTokens = 32;        // tokens of a warp's chunk
-constexpr float kHead = 14.f;      // P is at most 2^kHead
+// P is at most 2^(kHead + kSlack), and its row's largest at least about 2^kHead.
+constexpr float kHead = 7.f, kSlack = 8.f;
+constexpr float kNoRef = -1e30f;   // nothing seen yet
 constexpr float kMinScale = 5.421010862427522e-20f;  // 2^-64
 
 struct Params {
@@ -50,7 +54,7 @@ struct Params {
     float* part_o;    // (rows, hq, max_splits, d), un-normalised
     float2* part_ml;  // (rows, hq, max_splits): (reference in log2 units, sum)
     int total_q, hq, group, max_q, max_tokens, win_first, win_last, causal, lse_by_head;
-    int page_shift, tiles, split_tokens, max_splits;
+    int page_shift, block_shift, blocks, tiles, split_tokens, max_splits;  // blocks: of a page
     float scale_log2;
 };
 
@@ -132,6 +136,17 @@ __device__ __forceinline__ int row_of(int g) {
     return D == 64 ? g ^ ((g >> 1) & 1) : g;
 }
 
+__device__ __forceinline__ float lg2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float max_g(float x) {  // over lanes with equal lane % 4
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
@@ -163,7 +178,7 @@ template <int D, int STAGES>
 struct Smem {
     static constexpr int kData = 2 * kTokens * D;        // K and V codes of a warp's chunk
     static constexpr int kStage = kData + 3 * kTokens * 4;  // and its tokens' scales and positions
-    static constexpr int kBytes = kWarps * STAGES * kStage;
+    static constexpr int kBytes = kWarps * (STAGES * kStage + kTokens * 16);
 };
 
 // kRows: several new tokens, so that rows see different tokens.
@@ -200,42 +215,63 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
         head = kvh * p.group + (kRows ? x - tok * p.group : x);
     };
 
+    // Tokens up to full_to, and of the last window from full_from on, are seen by every row.
+    const int full_to = !p.causal ? INT_MAX : r.off + tok0;
+    const int full_from = p.win_last > 0 ? (int)max(0LL, (long long)r.off + tok1 + 1 - p.win_last) : 0;
+
     uint8_t* const ring = smem + warp * STAGES * SM::kStage;
-    auto load = [&](int chunk, int st) {
-        uint8_t* const base = ring + st * SM::kStage;
+    const uint32_t ring_at = smem_u32(ring);
+    // Copies: lane (row, seg) of an instruction.
+    const int my_row = lane / kSegs, my_seg = lane % kSegs;
+    const uint8_t* const kb = c.k + (size_t)kvh * D + my_seg * 16;
+    const uint8_t* const vb = c.v + (size_t)kvh * D + my_seg * 16;
+    const uint32_t row_bytes = (uint32_t)c.hkv * D;
+    const int32_t* const pages = c.page_table + (size_t)b * c.max_pages;
+    const int n0 = vis.b0, gap = vis.a1 - vis.b0;  // visible token v is token v, behind the first window v + gap
+    // Page of this lane's token of a chunk (-1: behind the split's end), one chunk ahead of its
+    // copies; and the token's place in the page.
+    auto token_at = [&](int chunk) {
         const int v = v0 + (chunk * kWarps + warp) * kTokens + lane;
-        int page = -1, slot = 0, t = -1;
-        size_t sc = 0;
-        if (v < v1) {
-            t = visible_token(vis, v);
-            const Place pl = place_of(t, c.page_size, p.page_shift);
-            page = c.page_table[(size_t)b * c.max_pages + pl.page];
-            if ((unsigned)page < (unsigned)c.num_pages) {
-                slot = page * c.page_size + pl.in_page;
-                sc = ((size_t)page * (c.page_size / c.block) + pl.in_page / c.block) * c.hkv + kvh;
-            } else {
-                raise_status(ATTN_SINK_DEV_PAGE_OOB);
-                page = t = -1;
-            }
+        return v < v1 ? v + (v >= n0 ? gap : 0) : -1;
+    };
+    auto page_at = [&](int t) { return t >= 0 ? pages[place_of(t, c.page_size, p.page_shift).page] : -1; };
+    auto load = [&](int t, int page, int st) {
+        const uint32_t at = ring_at + st * SM::kStage;
+        uint32_t slot = 0, sc = kvh;
+        bool ok = (unsigned)page < (unsigned)c.num_pages;
+        if (ok) {
+            const int in = place_of(t, c.page_size, p.page_shift).in_page;
+            slot = (uint32_t)page * c.page_size + in;
+            sc = p.block_shift >= 0 ? in >> p.block_shift : in / c.block;
+        } else if (t >= 0) {
+            raise_status(ATTN_SINK_DEV_PAGE_OOB);
+            t = -1;
         }
-        float* const meta = reinterpret_cast<float*>(base + SM::kData);
-        reinterpret_cast<int*>(meta + 2 * kTokens)[lane] = t;  // -1: takes no weight
-        copy4(smem_u32(meta + lane), c.k_scale + sc, page >= 0 ? 4 : 0);
-        copy4(smem_u32(meta + kTokens + lane), c.v_scale + sc, page >= 0 ? 4 : 0);
-        if (page < 0) slot = -1;
+        const size_t so = ok ? ((size_t)page * p.blocks + sc) * c.hkv + kvh : 0;
+        const uint32_t meta = at + SM::kData + lane * 4;
+        asm volatile("st.shared.s32 [%0], %1;" ::"r"(meta + 2 * kTokens * 4), "r"(t) : "memory");  // -1: takes no weight
+        copy4(meta, c.k_scale + so, ok ? 4 : 0);
+        copy4(meta + kTokens * 4, c.v_scale + so, ok ? 4 : 0);
+        // (the permutation repeats after 8 rows: two instructions at d 128)
+        const uint32_t to[2] = {at + stage_off<D>(my_row, my_seg),
+                                at + stage_off<D>(my_row + kRowsPer, my_seg) - kRowsPer * D};
+        const uint32_t some = __ballot_sync(0xffffffffu, ok);
 #pragma unroll
         for (int i = 0; i < kTokens / kRowsPer; ++i) {
-            const int row = i * kRowsPer + lane / kSegs, seg = lane % kSegs;
-            const int sl = __shfl_sync(0xffffffffu, slot, row);
-            const size_t off = ((size_t)max(sl, 0) * c.hkv + kvh) * D + seg * 16;
-            const uint32_t to = smem_u32(base) + stage_off<D>(row, seg);
-            copy16(to, c.k + off, sl >= 0 ? 16 : 0);
-            copy16(to + kTokens * D, c.v + off, sl >= 0 ? 16 : 0);
+            const uint32_t sl = __shfl_sync(0xffffffffu, slot, i * kRowsPer + my_row);
+            const int bytes = some == 0xffffffffu || (some >> (i * kRowsPer + my_row) & 1) ? 16 : 0;  // 0: zeros
+            const size_t off = (size_t)sl * row_bytes;
+            copy16(to[i & 1] + i * kRowsPer * D, kb + off, bytes);
+            copy16(to[i & 1] + i * kRowsPer * D + kTokens * D, vb + off, bytes);
         }
     };
+    int t_next = token_at(0), page_next = page_at(t_next);
 #pragma unroll
     for (int s = 0; s < STAGES - 1; ++s) {
-        if (s < nchunks) load(s, s);
+        const int t = t_next, page = page_next;
+        t_next = token_at(s + 1);
+        page_next = page_at(t_next);
+        if (s < nchunks) load(t, page, s);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
@@ -285,10 +321,11 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
         }
     }
 
-    float m_run[NT][2], l_run[NT][2], o[KK][NT][4];
+    // ref: what the exponents are taken against, kept kHead to kHead + kSlack below the running maximum
+    float ref[NT][2], l_run[NT][2], o[KK][NT][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        m_run[nt][0] = m_run[nt][1] = -INFINITY;
+        ref[nt][0] = ref[nt][1] = kNoRef;
         l_run[nt][0] = l_run[nt][1] = 0.f;
 #pragma unroll
         for (int mt = 0; mt < KK; ++mt)
@@ -296,14 +333,31 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
             for (int i = 0; i < 4; ++i) o[mt][nt][i] = 0.f;
     }
 
-    for (int chunk = 0; chunk < nchunks; ++chunk) {
+    // this warp's tokens as the products need them: (ks, log2 vs, 1 / vs, position)
+    float4* const ready = reinterpret_cast<float4*>(smem + kWarps * STAGES * SM::kStage) + warp * kTokens;
+    for (int chunk = 0, st = 0; chunk < nchunks; ++chunk) {
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
         __syncwarp();  // the chunk's bytes, copied by all lanes; the stage read last is free
-        if (chunk + STAGES - 1 < nchunks) load(chunk + STAGES - 1, (chunk + STAGES - 1) % STAGES);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const uint8_t* const sK = ring + (chunk % STAGES) * SM::kStage;
+        const uint8_t* const sK = ring + st * SM::kStage;
         const uint8_t* const sV = sK + kTokens * D;
-        const float* const meta = reinterpret_cast<const float*>(sK + SM::kData);
+        bool full = true;  // every row sees every token of the chunk
+        {
+            const float* const meta = reinterpret_cast<const float*>(sK + SM::kData) + lane;
+            const float vs = fmaxf(meta[kTokens], kMinScale);
+            const int t = __float_as_int(meta[2 * kTokens]);
+            ready[lane] = make_float4(meta[0], t >= 0 ? lg2_approx(vs) : -INFINITY, rcp_approx(vs), __int_as_float(t));
+            if constexpr (kRows)
+                full = __all_sync(0xffffffffu, t <= full_to && (t < p.win_first || t >= full_from));
+        }
+        {
+            const int t = t_next, page = page_next;
+            t_next = token_at(chunk + STAGES);
+            page_next = page_at(t_next);
+            if (chunk + STAGES - 1 < nchunks) load(t, page, st == 0 ? STAGES - 1 : st - 1);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        __syncwarp();  // `ready` is written
+        st = st + 1 == STAGES ? 0 : st + 1;
 
         float x[2][NT][4];
 #pragma unroll
@@ -329,45 +383,37 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
             }
         }
         // this lane's tokens: rows ra and ra + 8 of both tiles
-        float ks[4], lv[4], iv[4];
-        int pos[4];
+        float4 tk[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = (i >> 1) * 16 + (i & 1) * 8 + row_of<D>(g);
-            ks[i] = meta[t];
-            const float vs = fmaxf(meta[kTokens + t], kMinScale);
-            pos[i] = reinterpret_cast<const int*>(meta + 2 * kTokens)[t];
-            lv[i] = pos[i] >= 0 ? __log2f(vs) : -INFINITY;
-            iv[i] = __fdividef(1.f, vs);
-        }
+        for (int i = 0; i < 4; ++i) tk[i] = ready[(i >> 1) * 16 + (i & 1) * 8 + row_of<D>(g)];
         uint32_t pf[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float mn[2] = {m_run[nt][0], m_run[nt][1]};
             float y[2][4];
+            bool over = false;
 #pragma unroll
             for (int col = 0; col < 2; ++col) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float s = x[i >> 1][nt][(i & 1) * 2 + col];
-                    float v = s * (ks[i] * factor[nt][col]) + lv[i];
-                    bool hide = pos[i] < 0;
-                    if constexpr (kRows) {
-                        hide |= pos[i] > seen_to[nt][col];
-                        if (p.win_last > 0) hide |= pos[i] >= p.win_first && pos[i] <= seen_to[nt][col] - p.win_last;
-                    }
-                    y[col][i] = hide ? -INFINITY : v;
+                    // (tokens without weight have codes of 0 and a log2 vs of -inf)
+                    y[col][i] = fmaf(x[i >> 1][nt][(i & 1) * 2 + col], tk[i].x * factor[nt][col], tk[i].y);
+                    if constexpr (kRows)
+                        if (!full) {
+                            const int t = __float_as_int(tk[i].w), last = seen_to[nt][col];
+                            if (t > last || (p.win_last > 0 && t >= p.win_first && t <= last - p.win_last))
+                                y[col][i] = -INFINITY;
+                        }
                 }
-                const float top = max_g(fmaxf(fmaxf(y[col][0], y[col][1]), fmaxf(y[col][2], y[col][3])));
-                mn[col] = fmaxf(mn[col], top);
+                over |= fmaxf(fmaxf(y[col][0], y[col][1]), fmaxf(y[col][2], y[col][3])) > ref[nt][col] + (kHead + kSlack);
             }
-            // what came before is rescaled where some row of the warp has a new maximum
-            if (__any_sync(0xffffffffu, mn[0] != m_run[nt][0] || mn[1] != m_run[nt][1])) {
+            // the reference follows the maximum where a weight would pass 2^(kHead + kSlack)
+            if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
                 for (int col = 0; col < 2; ++col) {
-                    const float al = mn[col] == -INFINITY ? 1.f : fast_exp2(m_run[nt][col] - mn[col]);
+                    const float top = max_g(fmaxf(fmaxf(y[col][0], y[col][1]), fmaxf(y[col][2], y[col][3])));
+                    const float r1 = fmaxf(ref[nt][col], top - kHead), al = fast_exp2(ref[nt][col] - r1);
+                    ref[nt][col] = r1;
                     l_run[nt][col] *= al;
-                    m_run[nt][col] = mn[col];
 #pragma unroll
                     for (int mt = 0; mt < KK; ++mt) {
                         o[mt][nt][col] *= al;
@@ -377,16 +423,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
             }
             float w[2][4];
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
-                const float ref = mn[col] == -INFINITY ? 0.f : mn[col] - kHead;
-                float l = 0.f;
+            for (int col = 0; col < 2; ++col)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    w[col][i] = fast_exp2(y[col][i] - ref);
-                    l += w[col][i] * iv[i];
+                    w[col][i] = fast_exp2(y[col][i] - ref[nt][col]);
+                    l_run[nt][col] = fmaf(w[col][i], tk[i].z, l_run[nt][col]);
                 }
-                l_run[nt][col] += l;
-            }
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
                 pf[tt][nt][0] = transpose8(pack_f16x2(w[0][tt * 2], w[1][tt * 2]));
@@ -441,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
             const float l = sum_g(l_run[nt][col]);
             const int j = nt * 8 + 2 * cc + col;
             if (g == 0) {
-                sm_m[warp * H + j] = m_run[nt][col] - kHead;
+                sm_m[warp * H + j] = ref[nt][col] == kNoRef ? -INFINITY : ref[nt][col];
                 sm_l[warp * H + j] = l;
             }
             float* const dst = sm_o + (warp * H + j) * D + g * (D / 8);
@@ -606,6 +648,8 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part
     p.causal = a.causal;
     p.lse_by_head = a.lse_by_head;
     p.page_shift = shift_of(a.c.page_size);
+    p.block_shift = shift_of(a.c.block);
+    p.blocks = a.c.page_size / a.c.block;
     p.tiles = pl.tiles;
     p.split_tokens = pl.split_tokens;
     p.max_splits = pl.max_splits;
