@@ -36,6 +36,7 @@ struct AppendArgs {
     const int32_t* cu_new;       // (batch+1), or NULL: one row per request
     const int32_t* seqlens;
     int batch, total_new, max_new;
+    int page_shift, block_shift, blocks;  // (set by the launch) log2 or -1; blocks of a page
 };
 
 // The visible tokens of every request as bf16 pages of a cache of their own, of

@@ -18,29 +18,30 @@
 // of 128 (int8, blocks of 32).
 #include "q8.cuh"
 
-#include <cuda_fp8.h>
+#include <limits.h>
+
+#include <type_traits>
 
 namespace attn {
 namespace q8 {
 
-constexpr int kAppendWarps = 8;
-constexpr int kHeld = 8;  // 16-byte pieces of rows that a lane keeps
+constexpr int kAppendWarps = 4;
 
-// 8 fp32 in units of the scale as 8 codes.
+// 8 fp32 times `inv` as 8 codes.
 template <int F>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8]) {
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
     uint2 r;
     if constexpr (F == kE4M3) {
         uint16_t h[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)  // cvt's first operand is the upper half
-            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h[i]) : "f"(x[2 * i + 1] * inv), "f"(x[2 * i] * inv));
         r.x = h[0] | (uint32_t)h[1] << 16;
         r.y = h[2] | (uint32_t)h[3] << 16;
     } else {
         uint32_t u[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(x[i] + 12582912.f);  // 1.5 2^23: the low byte is round(x)
+        for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(fmaf(x[i], inv, 12582912.f));  // 1.5 2^23: the low byte is round(x inv)
         r.x = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
         r.y = __byte_perm(__byte_perm(u[4], u[5], 0x0040), __byte_perm(u[6], u[7], 0x0040), 0x5410);
     }
@@ -60,13 +61,6 @@ __device__ __forceinline__ void decode8(uint2 w, float (&x)[8]) {
     }
 }
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t x) {  // NaN wins
-    const uint32_t y = x & 0x7fff7fffu;
-    const __nv_bfloat162 m =
-        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&m);
-}
-
 // Exponent of the scale for a largest magnitude `top` (finite, >= 0).
 template <int F>
 __device__ __forceinline__ int needed_exp(float top) {
@@ -80,144 +74,199 @@ __device__ __forceinline__ int needed_exp(float top) {
 
 __device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
 
+// Request b's new rows as the kernels see them: tokens [from, end), row of token t n0 + t - start.
+struct NewRows {
+    int n0, start, from, end;
+    bool some;
+};
+
+__device__ __forceinline__ NewRows new_rows(const AppendArgs& a, int b, bool report) {
+    NewRows r;
+    r.n0 = a.cu_new ? a.cu_new[b] : b;
+    const int n = a.cu_new ? a.cu_new[b + 1] - r.n0 : 1;
+    const int L = a.seqlens[b];
+    r.start = L - n;
+    // as in the bf16 append, rows of negative tokens and behind the page table are left out
+    const long long cap = (long long)a.c.max_pages * a.c.page_size;
+    if (report && n > 0 && (n > a.max_new || r.start < 0 || L > cap || r.n0 + (long long)n > a.total_new))
+        raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    r.from = max(r.start, 0);
+    r.end = L < cap ? L : (int)cap;
+    if (r.n0 + (long long)n > a.total_new) r.end = min(r.end, r.start + max(0, a.total_new - r.n0));
+    if (n > a.max_new) r.end = min(r.end, r.start + a.max_new);
+    r.some = r.n0 >= 0 && n > 0 && r.end > r.from;
+    return r;
+}
+
+// What a block of one head's K or V has in the cache.
+template <int D>
+struct Block {
+    uint8_t* codes;  // of its first token, at this lane's 8 dims
+    size_t step;     // from token to token
+    float* scale;
+    __device__ __forceinline__ Block(const AppendArgs& a, bool is_v, int page, int in_page, int head, int seg) {
+        const Cache& c = a.c;
+        codes = (is_v ? c.v : c.k) + (((size_t)page * c.page_size + in_page) * c.hkv + head) * D + seg * 8;
+        step = (size_t)c.hkv * D;
+        scale = (is_v ? c.v_scale : c.k_scale) +
+                ((size_t)page * a.blocks + (a.block_shift >= 0 ? in_page >> a.block_shift : in_page / c.block)) * c.hkv + head;
+    }
+};
+
+// The block's scale and its reciprocal for new rows of largest magnitude `top`, `have` tokens being
+// there with scale `old`; if it grows, their codes (rows r0, r0 + step, ..) are brought to it.
 template <int D, int F>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendArgs a, int page_shift) {
+__device__ __forceinline__ float2 settle_scale(const Block<D>& k, uint32_t top, int have, float old, int r0, int step) {
+    const int e = needed_exp<F>(__uint_as_float(top << 16));
+    float2 s = make_float2(exp2i(e), exp2i(-e));
+    if (have > 0) {
+        if (old >= s.x) {
+            s = make_float2(old, 1.f / old);
+        } else {
+            const float ratio = old > 0.f ? old / s.x : 0.f;
+            for (int r = r0; r < have; r += step) {
+                uint2* at = reinterpret_cast<uint2*>(k.codes + r * k.step);
+                float x[8];
+                decode8<F>(*at, x);
+                *at = encode8<F>(x, ratio);
+            }
+        }
+    }
+    return s;
+}
+
+// Codes of 8 bf16.  odd: there may be infinities (the largest code of their sign) and NaNs (0).
+template <int F>
+__device__ __forceinline__ uint2 codes_of(const uint4& x, float inv, bool odd) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = bf16_lo(w[i]);
+        f[2 * i + 1] = bf16_hi(w[i]);
+    }
+    if (odd) {
+        constexpr float kMax = F == kE4M3 ? 448.f : 127.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i] * inv, -kMax), kMax);
+        inv = 1.f;
+    }
+    return encode8<F>(f, inv);
+}
+
+// The largest magnitudes of the even and the odd of 8 bf16 and of `top`'s, as integers: they keep
+// the values' order, infinities and NaNs are kOdd and above.
+constexpr uint32_t kOdd = 0x7f80u;
+__device__ __forceinline__ uint32_t max_abs8(uint32_t top, const uint4& x) {
+    top = __vimax3_u16x2(top, x.x & 0x7fff7fffu, x.y & 0x7fff7fffu);
+    return __vimax3_u16x2(top, x.z & 0x7fff7fffu, x.w & 0x7fff7fffu);
+}
+// The largest finite magnitude of 8 bf16 and `top`.
+__device__ __forceinline__ uint32_t max_finite8(uint32_t top, const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t p = w[i] & 0x7fffu, q = (w[i] >> 16) & 0x7fffu;
+        if (p < 0x7f80u) top = max(top, p);
+        if (q < 0x7f80u) top = max(top, q);
+    }
+    return top;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t x) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// A warp per (block, head, K or V).  kHeld: 16-byte pieces of the rows that a lane keeps in
+// registers (those of longer blocks are read again).
+template <int D, int F, int kHeld>
+__global__ void __launch_bounds__(kAppendWarps * 32, kHeld == 4 ? 8 : kHeld == 8 ? 6 : 4) append_kernel(const AppendArgs a) {
     constexpr int kLanes = D / 8;          // lanes of a row
     constexpr int kRows = 32 / kLanes;     // rows of a warp's instruction
     const Cache& c = a.c;
     const int b = blockIdx.y, lane = threadIdx.x & 31, sub = lane / kLanes, seg = lane % kLanes;
-    const long long task = (long long)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    const uint32_t task = blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     const bool is_v = task & 1;
-    const int head = (int)((task >> 1) % c.hkv);
-    const int n0 = a.cu_new ? a.cu_new[b] : b;
-    int n = a.cu_new ? a.cu_new[b + 1] - n0 : 1;
-    const int L = a.seqlens[b];
-    const bool first = task == 0 && lane == 0;
-    if (first && n > a.max_new) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-    if (n0 < 0 || n <= 0) return;
-    const int start = L - n;  // token of the first new row
-    // as in the bf16 append, rows of negative tokens and behind the page table are left out
-    const long long cap = (long long)c.max_pages * c.page_size;
-    if (first && (start < 0 || L > cap || n0 + (long long)n > a.total_new)) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-    const int from = max(start, 0);
-    int end = L < cap ? L : (int)cap;
-    if (n0 + (long long)n > a.total_new) end = min(end, start + max(0, a.total_new - n0));
-    if (n > a.max_new) end = min(end, start + a.max_new);
-    if (end <= from) return;
-    const long long t0l = (from / c.block + (task >> 1) / c.hkv) * (long long)c.block;
-    if (t0l >= end) return;
+    const uint32_t index = (task >> 1) / (uint32_t)c.hkv;
+    const int head = (int)((task >> 1) - index * c.hkv);
+    const NewRows n = new_rows(a, b, task == 0 && lane == 0);
+    const long long t0l = ((a.block_shift >= 0 ? n.from >> a.block_shift : n.from / c.block) + (long long)index) * c.block;
+    if (!n.some || t0l >= n.end) return;
     const int t0 = (int)t0l;
-    const Place pl = place_of(t0, c.page_size, page_shift);
+    const Place pl = place_of(t0, c.page_size, a.page_shift);
     const int page = c.page_table[(size_t)b * c.max_pages + pl.page];
+    const int lo = max(t0, n.from), rows = min(t0 + c.block, n.end) - lo;
+    const long long rs = is_v ? a.v_rs : a.k_rs;
+    const __nv_bfloat16* src = (is_v ? a.v_new : a.k_new) + (n.n0 + (long long)(lo - n.start)) * rs + head * D + seg * 8;
+    src += sub * rs;  // this lane's rows: sub, sub + kRows, ..
+    const long long far = kRows * rs;
+    uint4 held[kHeld];
+    {
+        const __nv_bfloat16* x = src;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i, x += far)
+            held[i] = i * kRows + sub < rows ? __ldcs(reinterpret_cast<const uint4*>(x)) : make_uint4(0, 0, 0, 0);
+    }
+    auto row = [&](int r) { return __ldg(reinterpret_cast<const uint4*>(src + (r - sub) * rs)); };
+    // (the rows are on their way; where they go)
     if ((unsigned)page >= (unsigned)c.num_pages) {
         if (lane == 0) raise_status(ATTN_SINK_DEV_PAGE_OOB);
         return;
     }
-    const int lo = max(t0, from), hi = min(t0 + c.block, end);
-    const __nv_bfloat16* src =
-        (is_v ? a.v_new : a.k_new) + (n0 + (long long)(lo - start)) * (is_v ? a.v_rs : a.k_rs) + head * D + seg * 8;
-    const long long rs = is_v ? a.v_rs : a.k_rs;
-    uint8_t* dst = (is_v ? c.v : c.k) + (((size_t)page * c.page_size + pl.in_page) * c.hkv + head) * D + seg * 8;
-    const size_t ds = (size_t)c.hkv * D;
-    float* scale = (is_v ? c.v_scale : c.k_scale) +
-                   ((size_t)page * (c.page_size / c.block) + pl.in_page / c.block) * c.hkv + head;
-
-    uint4 held[kHeld];
+    const Block<D> k(a, is_v, page, pl.in_page, head, seg);
+    const float old = lo > t0 ? *k.scale : 0.f;
     uint32_t top2 = 0;
-    const int rows = hi - lo;
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int r = i * kRows + sub;
-        held[i] = r < rows ? __ldg(reinterpret_cast<const uint4*>(src + r * rs)) : make_uint4(0, 0, 0, 0);
-    }
-    const float old = lo > t0 ? *scale : 0.f;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, held[i].x), held[i].y), held[i].z), held[i].w);
-    for (int r = kHeld * kRows + sub; r < rows; r += kRows) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + r * rs));
-        top2 = max_abs2(max_abs2(max_abs2(max_abs2(top2, x.x), x.y), x.z), x.w);
-    }
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) top2 = max_abs2(top2, __shfl_xor_sync(0xffffffffu, top2, o));
-    // bf16 magnitudes as integers keep their order: infinities and NaNs are 0x7f80 and above
-    uint32_t top = max(top2 & 0xffffu, top2 >> 16);
-    const bool odd = top >= 0x7f80u;
-    if (odd) {  // the largest finite one
+    for (int i = 0; i < kHeld; ++i) top2 = max_abs8(top2, held[i]);
+    for (int r = kHeld * kRows + sub; r < rows; r += kRows) top2 = max_abs8(top2, row(r));
+    uint32_t top = warp_max(max(top2 & 0xffffu, top2 >> 16));
+    const bool odd = top >= kOdd;
+    if (odd) {
         if (lane == 0) raise_status(ATTN_SINK_DEV_VALUE);
         top = 0;
-        for (int r = sub; r < rows; r += kRows) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + r * rs));
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t p = w[i] & 0x7fffu, q = (w[i] >> 16) & 0x7fffu;
-                if (p < 0x7f80u) top = max(top, p);
-                if (q < 0x7f80u) top = max(top, q);
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int r = sub; r < rows; r += kRows) top = max_finite8(top, row(r));
+        top = warp_max(top);
     }
-    const int e = needed_exp<F>(__uint_as_float(top << 16));
-    float sc = exp2i(e), inv = exp2i(-e);
-    if (lo > t0) {
-        if (old >= sc) {
-            sc = old;
-            inv = 1.f / old;
-        } else {  // the rows that the block has, brought to the larger scale
-            const float ratio = old > 0.f ? old / sc : 0.f;
-            for (int r = sub; r < lo - t0; r += kRows) {
-                uint2* at = reinterpret_cast<uint2*>(dst + r * ds);
-                float x[8];
-                decode8<F>(*at, x);
+    const float2 s = settle_scale<D, F>(k, top, lo - t0, old, sub, kRows);
+    uint8_t* to = k.codes + (size_t)(lo - t0 + sub) * k.step;
+    const size_t pace = kRows * k.step;
+    int r = sub;
+    if (!odd) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= ratio;
-                *at = encode8<F>(x);
-            }
-        }
+        for (int i = 0; i < kHeld; ++i, r += kRows, to += pace)
+            if (i * kRows + sub < rows) *reinterpret_cast<uint2*>(to) = codes_of<F>(held[i], s.y, false);
     }
-    auto put = [&](int r, const uint4& x) {
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float f[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = bf16_lo(w[i]) * inv;
-            f[2 * i + 1] = bf16_hi(w[i]) * inv;
-        }
-        if (odd) {  // infinities: the largest code of their sign; NaN: 0
-            constexpr float kMax = F == kE4M3 ? 448.f : 127.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = isnan(f[i]) ? 0.f : fminf(fmaxf(f[i], -kMax), kMax);
-        }
-        *reinterpret_cast<uint2*>(dst + (size_t)(lo - t0 + r) * ds) = encode8<F>(f);
-    };
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int r = i * kRows + sub;
-        if (r < rows) put(r, held[i]);
-    }
-    for (int r = kHeld * kRows + sub; r < rows; r += kRows) put(r, __ldg(reinterpret_cast<const uint4*>(src + r * rs)));
-    if (lane == 0) *scale = sc;
+    for (; r < rows; r += kRows, to += pace) *reinterpret_cast<uint2*>(to) = codes_of<F>(row(r), s.y, odd);
+    __syncwarp();  // every lane has read the old one
+    if (lane == 0) *k.scale = s.x;
 }
 
-cudaError_t launch_append(const AppendArgs& a, cudaStream_t s) {
-    if (a.batch == 0 || a.max_new <= 0) return cudaSuccess;
+cudaError_t launch_append(const AppendArgs& args, cudaStream_t s) {
+    if (args.batch == 0 || args.max_new <= 0) return cudaSuccess;
+    AppendArgs a = args;
+    a.page_shift = shift_of(a.c.page_size);
+    a.block_shift = shift_of(a.c.block);
+    a.blocks = a.c.page_size / a.c.block;
     // blocks that max_new tokens can touch, wherever they start
     const long long blocks = ((long long)a.max_new + a.c.block - 2) / a.c.block + 1;
-    const long long tasks = blocks * a.c.hkv * 2;
-    const long long grid_x = (tasks + kAppendWarps - 1) / kAppendWarps;
-    if (grid_x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    dim3 grid((unsigned)grid_x, a.batch);
-    const int sh = shift_of(a.c.page_size);
-    if (a.c.head_dim == 64) {
-        if (a.c.format == kE4M3) append_kernel<64, kE4M3><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
-        else append_kernel<64, kInt8><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
-    } else {
-        if (a.c.format == kE4M3) append_kernel<128, kE4M3><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
-        else append_kernel<128, kInt8><<<grid, kAppendWarps * 32, 0, s>>>(a, sh);
-    }
-    return cudaGetLastError();
+    const long long x = (blocks * a.c.hkv * 2 + kAppendWarps - 1) / kAppendWarps;
+    if (x > (1LL << 28)) return cudaErrorInvalidConfiguration;  // (its warps are counted in 32 bits)
+    const dim3 grid((unsigned)x, a.batch);
+    const int rows = a.max_new < a.c.block ? a.max_new : a.c.block, pieces = (rows + 256 / a.c.head_dim - 1) / (256 / a.c.head_dim);
+    auto go = [&](auto d, auto f) {
+        constexpr int kD = decltype(d)::value, kF = decltype(f)::value;
+        if (pieces <= 4) append_kernel<kD, kF, 4><<<grid, kAppendWarps * 32, 0, s>>>(a);
+        else if (pieces <= 8) append_kernel<kD, kF, 8><<<grid, kAppendWarps * 32, 0, s>>>(a);
+        else append_kernel<kD, kF, 16><<<grid, kAppendWarps * 32, 0, s>>>(a);
+        return cudaGetLastError();
+    };
+    using std::integral_constant;
+    if (a.c.head_dim == 64)
+        return a.c.format == kE4M3 ? go(integral_constant<int, 64>{}, integral_constant<int, kE4M3>{})
+                                   : go(integral_constant<int, 64>{}, integral_constant<int, kInt8>{});
+    return a.c.format == kE4M3 ? go(integral_constant<int, 128>{}, integral_constant<int, kE4M3>{})
+                               : go(integral_constant<int, 128>{}, integral_constant<int, kInt8>{});
 }
 
 // Codes back into bf16, which holds every c 2^e of either format: the forward's
