@@ -620,7 +620,7 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
  * leaves nothing.  The tokens are distributed as the target's where siblings are drawn
  * independently from q_i (draft given) or are chosen without regard to the random numbers.
  * Probabilities count as clamped to [0, 1] (NaN: 0) and enter sums as multiples of 2^-44;
- * u_next is clamped to [0, 1) (NaN: 0), u is taken as it is (NaN: refused).
+ * u_next is clamped to [0, 1) (NaN: 0); a negative u counts as 0 (NaN: refused).
  *
  *   target, draft  (total, vocab) of type dtype (ATTN_SINK_F32, BF16 or F16); row i of a
  *                  request: after its node i.  *_row_stride in elements (0: vocab)

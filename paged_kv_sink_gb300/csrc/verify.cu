@@ -32,6 +32,8 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace cg = cooperative_groups;
@@ -39,7 +41,7 @@ namespace cg = cooperative_groups;
 namespace attn {
 namespace verify {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
@@ -81,127 +83,147 @@ __device__ __forceinline__ Fixed to_fixed(float hi, float lo) {
 }
 __device__ __forceinline__ u64 units(u64 high, long long low) { return (high << 22) + (u64)low; }
 
-// What a pass sums: p (k = 0), p - q (k = 1), p - S q (k = 2), each cut at 0.
-struct Weight {
+// What a pass sums: p (K = 0), p - q (K = 1) or p - S q (K = 2), cut at 0.
+struct Cover {
     int k;
     float s_hi, s_lo;
-    __device__ __forceinline__ Fixed operator()(float p, float q) const {
-        p = clamp01(p);
-        if (k == 0) return to_fixed(p, 0.f);
-        q = clamp01(q);
-        float hi, lo;
-        if (k == 1) {
-            hi = p - q;
-            lo = -q - (hi - p);  // exact where p >= q
-        } else {
-            const float m = s_hi * q, e = fmaf(s_hi, q, -m) + s_lo * q;
-            const float d = p - m, z = d - p;
-            const float rest = ((p - (d - z)) - (m + z)) - e;
-            hi = d + rest;
-            lo = rest - (hi - d);
-        }
-        if (!(hi > 0.f)) hi = lo = 0.f;
-        return to_fixed(hi, lo);
-    }
 };
 
-// A row of probabilities, read as vectors of N elements from the last N-element border
-// at or before it (`skew` elements; those before and behind the row read as 0).
-template <int T, int N>
-struct Row {
-    using E = typename Elem<T>::type;
-    const E* at;  // element 0 of the row
-    int skew, vocab;
-    __device__ __forceinline__ void get(int v, float (&x)[N]) const {
-        const int e = v - skew;
-        if (N > 1 && e >= 0 && e + N <= vocab) {
-            struct alignas(sizeof(E) * N) V {
-                E x[N];
-            };
-            const V y = *reinterpret_cast<const V*>(at + e);
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = Elem<T>::get(y.x[i]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = e + i >= 0 && e + i < vocab ? Elem<T>::get(at[e + i]) : 0.f;
-        }
+template <int K>
+__device__ __forceinline__ Fixed weight(const Cover& s, float p, float q) {
+    p = clamp01(p);
+    if constexpr (K == 0) return to_fixed(p, 0.f);
+    q = clamp01(q);
+    float hi, lo;
+    if constexpr (K == 1) {
+        hi = p - q;
+        lo = -q - (hi - p);  // exact where p >= q
+    } else {
+        const float m = s.s_hi * q, e = fmaf(s.s_hi, q, -m) + s.s_lo * q;
+        const float d = p - m, z = d - p;
+        const float rest = ((p - (d - z)) - (m + z)) - e;
+        hi = d + rest;
+        lo = rest - (hi - d);
     }
-};
+    if (!(hi > 0.f)) hi = lo = 0.f;
+    return to_fixed(hi, lo);
+}
+
+// A warp takes its slice in batches of kBatch elements, as kBatch / 32 / N vectors of N a lane,
+// the a-th of them 32 N a elements in.
+constexpr int kBatch = 512;
+constexpr int kMaxBatches = (1 << 20) / (kMaxCluster * kWarps * kBatch) + 2;  // of a warp
+
+// Elements [v, v + kBatch) of the row from `skew` elements before it; those outside the row
+// are 0.
+template <int T, int N>
+__device__ __forceinline__ void load_batch(const typename Elem<T>::type* row, int skew, int vocab, int v,
+                                           float (&x)[kBatch / 32]) {
+    using E = typename Elem<T>::type;
+    const int lane = threadIdx.x & 31, e0 = v - skew;
+    const E* const at = row + (e0 + lane * N);
+    if (e0 >= 0 && e0 + kBatch <= vocab) {
+        struct alignas(sizeof(E) * N) V {
+            E x[N];
+        };
+        V y[kBatch / 32 / N];
+#pragma unroll
+        for (int a = 0; a < kBatch / 32 / N; ++a) y[a] = *reinterpret_cast<const V*>(at + a * 32 * N);
+#pragma unroll
+        for (int a = 0; a < kBatch / 32 / N; ++a)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[a * N + i] = Elem<T>::get(y[a].x[i]);
+    } else {
+#pragma unroll
+        for (int a = 0; a < kBatch / 32 / N; ++a)
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int e = e0 + lane * N + a * 32 * N + i;
+                x[a * N + i] = e >= 0 && e < vocab ? Elem<T>::get(at[a * 32 * N + i]) : 0.f;
+            }
+    }
+}
 
 struct Shared {
     int token[kMaxNodes];
     int parent[kMaxNodes];
     float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
     int path[kMaxNodes];
-    int gone[kMaxNodes];      // refused siblings' tokens (without draft probabilities)
-    u64 part[kWarps];         // the warps' sums of the last pass
-    u64 total[2][kMaxCluster];  // the CTAs'
+    int gone[kMaxNodes];        // refused siblings' tokens (without draft probabilities)
+    bool first[kMaxNodes];      // taken, if no sibling was refused before
+    u64 part[kWarps][kMaxBatches];  // the batches' sums of the last pass
+    u64 warp[kWarps];               // the warps'
+    u64 total[2][kMaxCluster];      // the CTAs'
     // what the walk stands at
     int node, count, refused, ngone, more;
     float s_hi, s_lo;
 };
 
-__device__ __forceinline__ u64 warp_sum(u64 x) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+// A warp's elements of a row, counted from the row's last vector border: whole batches.
+// wide: p and q lie alike to such a border, so that both are read as vectors.
+struct Slice {
+    int v0, v1, skew;
+    bool wide;
+};
+
+template <class E>
+__device__ __forceinline__ Slice slice_of(const E* p, const E* q, int vocab, int ctas, int who) {
+    constexpr int kVec = 16 / sizeof(E);
+    Slice s;
+    const int sp = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(E) % kVec);
+    s.wide = sp == (int)(reinterpret_cast<uintptr_t>(q) / sizeof(E) % kVec);
+    s.skew = s.wide ? sp : 0;
+    const int span = vocab + s.skew, warps = ctas * kWarps;
+    const int len = ((span + warps - 1) / warps + kBatch - 1) / kBatch * kBatch;
+    s.v0 = min(span, who * len);
+    s.v1 = min(span, s.v0 + len);
+    return s;
 }
 
-// Sum of this warp's slice [v0, v1) of the (shifted) row.
-template <int T, int N>
-__device__ u64 slice_sum(const Row<T, N>& p, const Row<T, N>& q, const Weight& w, int v0, int v1) {
-    const int lane = threadIdx.x & 31;
-    constexpr int kAhead = 4;  // vectors in flight
+// Sums of this warp's batches into part[]; returns their sum (lane 0).
+template <int T, int N, int K>
+__device__ __forceinline__ u64 sum_slice(const typename Elem<T>::type* p, const typename Elem<T>::type* q, const Cover& s,
+                                         const Slice& sl, int vocab, u64* part) {
     u64 sum = 0;
-    for (int v = v0 + lane * N; v < v1; v += 32 * N * kAhead) {
-        float x[kAhead][N], y[kAhead][N];
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) {
-            const int at = v + a * 32 * N;
-            if (at < v1) {
-                p.get(at, x[a]);
-                if (w.k) q.get(at, y[a]);
-            }
-        }
-        uint32_t high = 0;
+    for (int v = sl.v0, j = 0; v < sl.v1; v += kBatch, ++j) {
+        float x[kBatch / 32], y[kBatch / 32];
+        load_batch<T, N>(p, sl.skew, vocab, v, x);
+        if (K) load_batch<T, N>(q, sl.skew, vocab, v, y);
+        uint32_t high = 0;  // at most kBatch 2^22 over the warp
         int low = 0;
 #pragma unroll
-        for (int a = 0; a < kAhead; ++a)
-            if (v + a * 32 * N < v1) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const Fixed f = w(x[a][i], w.k ? y[a][i] : 0.f);
-                    high += f.high;
-                    low += f.low;
-                }
-            }
-        sum += units(high, low);
+        for (int i = 0; i < kBatch / 32; ++i) {
+            const Fixed f = weight<K>(s, x[i], K ? y[i] : 0.f);
+            high += f.high;
+            low += f.low;
+        }
+        high = __reduce_add_sync(0xffffffffu, high);
+        low = __reduce_add_sync(0xffffffffu, low);
+        const u64 one = units(high, low);
+        sum += one;
+        if ((threadIdx.x & 31) == 0) part[j] = one;
     }
-    return warp_sum(sum);
+    return sum;
 }
 
-// The element of this warp's slice at which the running sum first exceeds `left`.
-template <int T, int N>
-__device__ int slice_find(const Row<T, N>& p, const Row<T, N>& q, const Weight& w, int v0, int v1, u64 left,
-                          const int* gone, int ngone) {
+// The element of the batch at v at which the running sum first exceeds `left`.
+template <int T, int N, int K>
+__device__ __forceinline__ int find_in_batch(const typename Elem<T>::type* p, const typename Elem<T>::type* q, const Cover& s,
+                                             int skew, int vocab, int v, u64 left, const int* gone, int ngone) {
     const int lane = threadIdx.x & 31;
-    for (int v = v0; v < v1; v += 32 * N) {
-        const int at = v + lane * N;
-        float x[N], y[N];
+    float x[kBatch / 32], y[kBatch / 32];
+    load_batch<T, N>(p, skew, vocab, v, x);
+    if (K) load_batch<T, N>(q, skew, vocab, v, y);
+#pragma unroll
+    for (int a = 0; a < kBatch / 32 / N; ++a) {
+        const int e = v - skew + (a * 32 + lane) * N;
         u64 f[N], mine = 0;
-        if (at < v1) {
-            p.get(at, x);
-            if (w.k) q.get(at, y);
-        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            f[i] = 0;
-            if (at < v1) {
-                const Fixed z = w(x[i], w.k ? y[i] : 0.f);
-                f[i] = units(z.high, z.low);
-                for (int j = 0; j < ngone; ++j)
-                    if (gone[j] == at + i - p.skew) f[i] = 0;
-            }
+            const Fixed z = weight<K>(s, x[a * N + i], K ? y[a * N + i] : 0.f);
+            f[i] = units(z.high, z.low);
+            for (int j = 0; j < ngone; ++j)
+                if (gone[j] == e + i) f[i] = 0;
             mine += f[i];
         }
         u64 run = mine;  // inclusive over lanes
@@ -212,18 +234,18 @@ __device__ int slice_find(const Row<T, N>& p, const Row<T, N>& q, const Weight& 
         }
         const uint32_t past = __ballot_sync(0xffffffffu, run > left);
         if (past) {
-            const int who = __ffs(past) - 1;
             int found = 0;
             u64 z = run - mine;
+            bool open = true;
 #pragma unroll
-            for (int i = N - 1; i >= 0; --i) {
-                // the least i whose sum exceeds `left`
-                u64 s = z;
-#pragma unroll
-                for (int j = 0; j <= i; ++j) s += f[j];
-                if (s > left) found = at + i - p.skew;
+            for (int i = 0; i < N; ++i) {
+                z += f[i];
+                if (open && z > left) {
+                    found = e + i;
+                    open = false;
+                }
             }
-            return __shfl_sync(0xffffffffu, found, who);
+            return __shfl_sync(0xffffffffu, found, __ffs(past) - 1);
         }
         left -= __shfl_sync(0xffffffffu, run, 31);
     }
@@ -243,29 +265,8 @@ __device__ __forceinline__ u64 part_of(float u, u64 x) {
     return down < 64 ? y >> down : 0;
 }
 
-// A warp's elements of a row, counted from the row's last vector border: whole vectors of
-// all lanes.  wide: p and q lie alike to such a border, so that both are read as vectors.
-struct Slice {
-    int v0, v1, skew;
-    bool wide;
-};
-
-template <class E>
-__device__ __forceinline__ Slice slice_of(const E* p, const E* q, int vocab, int ctas, int who) {
-    constexpr int kVec = 16 / sizeof(E);
-    Slice s;
-    const int sp = (int)(reinterpret_cast<uintptr_t>(p) / sizeof(E) % kVec);
-    s.wide = sp == (int)(reinterpret_cast<uintptr_t>(q) / sizeof(E) % kVec);
-    s.skew = s.wide ? sp : 0;
-    const int span = vocab + s.skew, warps = ctas * kWarps, step = 32 * kVec;
-    const int len = ((span + warps - 1) / warps + step - 1) / step * step;
-    s.v0 = min(span, who * len);
-    s.v1 = min(span, s.v0 + len);
-    return s;
-}
-
 template <int T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
     using E = typename Elem<T>::type;
     constexpr int kVec = 16 / sizeof(E);
     __shared__ Shared S;
@@ -312,35 +313,52 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
         }
         S.parent[i] = i > 0 ? par : -1;
         S.token[i] = x;
-        S.u[i] = a.u[r0 + i];
+        const float u = a.u[r0 + i];
+        S.u[i] = u < 0.f ? 0.f : u;
         S.px[i] = px;
         S.qx[i] = qx;
+        S.first[i] = (draft ? (double)S.u[i] * qx : (double)S.u[i]) < px;
     }
     __syncthreads();
 
     // One pass over the slices: the sum over the cluster of what `w` leaves of a node's row,
-    // less the tokens in S.gone; the warps' parts stay in S.part, the CTAs' in S.total.
+    // less the tokens in S.gone; the batches' and warps' sums stay in S.part and S.warp, the CTAs'
+    // in S.total.
     int passes = 0;
     auto row_at = [&](const E* base, long long rs, int i) { return base + i * rs; };
-    auto sum_row = [&](int node, const Weight& w, int ngone) {
+    auto each_form = [&](bool wide, const Cover& w, auto f) {  // f(vector length, kind of weight)
+        using std::integral_constant;
+        if (wide) {
+            if (w.k == 0) return f(integral_constant<int, kVec>{}, integral_constant<int, 0>{});
+            if (w.k == 1) return f(integral_constant<int, kVec>{}, integral_constant<int, 1>{});
+            return f(integral_constant<int, kVec>{}, integral_constant<int, 2>{});
+        }
+        // (p and q that lie differently: few callers, one form)
+        return f(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+    };
+    auto sum_row = [&](int node, const Cover& w, int ngone) {
         const E* const pr = row_at(target, a.target_rs, node);
         const E* const qr = w.k ? row_at(draft, a.draft_rs, node) : pr;
         const Slice sl = slice_of<E>(pr, qr, a.vocab, ctas, rank * kWarps + warp);
-        u64 part = sl.wide ? slice_sum<T, kVec>({pr, sl.skew, a.vocab}, {qr, sl.skew, a.vocab}, w, sl.v0, sl.v1)
-                           : slice_sum<T, 1>({pr, 0, a.vocab}, {qr, 0, a.vocab}, w, sl.v0, sl.v1);
+        u64 part = each_form(sl.wide, w, [&](auto n, auto k) {
+            return sum_slice<T, decltype(n)::value, decltype(k)::value>(pr, qr, w, sl, a.vocab, S.part[warp]);
+        });
+        if (ngone) __syncwarp();
         for (int j = 0; j < ngone; ++j) {
             const int v = S.gone[j] + sl.skew;
             if (v >= sl.v0 && v < sl.v1) {
-                const Fixed f = w(Elem<T>::get(pr[S.gone[j]]), 0.f);
+                const Fixed f = to_fixed(clamp01(Elem<T>::get(pr[S.gone[j]])), 0.f);
                 part -= units(f.high, f.low);
+                if (lane == 0) S.part[warp][(v - sl.v0) / kBatch] -= units(f.high, f.low);
             }
         }
-        if (lane == 0) S.part[warp] = part;
+        if (lane == 0) S.warp[warp] = part;
         __syncthreads();
         u64* const totals = S.total[passes++ & 1];
-        if (warp == 0) {
-            const u64 mine = warp_sum(lane < kWarps ? S.part[lane] : 0);
-            if (lane < ctas) *cluster.map_shared_rank(totals + rank, lane) = mine;
+        if (tid < ctas) {
+            u64 mine = 0;
+            for (int i = 0; i < kWarps; ++i) mine += S.warp[i];
+            *cluster.map_shared_rank(totals + rank, tid) = mine;
         }
         cluster.sync();
         u64 sum = 0;
@@ -352,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
     int node = 0, count = 1, scanned = 1, refused = 0, ngone = 0;
     double cover = 0.0, mass = 1.0;
     u64 sum = 0;
-    Weight w = {0, 0.f, 0.f};
+    Cover w = {0, 0.f, 0.f};
     cluster.sync();  // every CTA of the cluster runs before its shared memory is written
     for (;;) {
         if (warp == 0) {
@@ -369,7 +387,9 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
                 scanned = c + 1;
                 const double px = S.px[c], u = S.u[c];
                 bool take, again = false;
-                if (draft) {
+                if (refused + ngone == 0) {
+                    take = S.first[c];
+                } else if (draft) {
                     const double qx = S.qx[c];
                     take = u * qx * mass < fmax(px - cover * qx, 0.0);
                 } else {  // a token that a sibling has lost is not there again
@@ -439,16 +459,20 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const Args a) {
         if (left < totals[c]) return;
         left -= totals[c];
     }
-    for (int v = 0; v < warp; ++v) {
-        if (left < S.part[v]) return;
-        left -= S.part[v];
+    for (int i = 0; i < warp; ++i) {
+        if (left < S.warp[i]) return;
+        left -= S.warp[i];
     }
-    if (left >= S.part[warp]) return;
+    if (left >= S.warp[warp]) return;
     const E* const pr = row_at(target, a.target_rs, S.node);
     const E* const qr = w.k ? row_at(draft, a.draft_rs, S.node) : pr;
     const Slice sl = slice_of<E>(pr, qr, a.vocab, ctas, rank * kWarps + warp);
-    const int x = sl.wide ? slice_find<T, kVec>({pr, sl.skew, a.vocab}, {qr, sl.skew, a.vocab}, w, sl.v0, sl.v1, left, S.gone, nout)
-                          : slice_find<T, 1>({pr, 0, a.vocab}, {qr, 0, a.vocab}, w, sl.v0, sl.v1, left, S.gone, nout);
+    int j = 0;
+    for (; left >= S.part[warp][j]; ++j) left -= S.part[warp][j];
+    const int x = each_form(sl.wide, w, [&](auto n, auto k) {
+        return find_in_batch<T, decltype(n)::value, decltype(k)::value>(pr, qr, w, sl.skew, a.vocab, sl.v0 + j * kBatch, left,
+                                                                        S.gone, nout);
+    });
     if (lane == 0) a.next[b] = x;
 }
 
