@@ -20,6 +20,7 @@
 #include "pages.h"
 
 #include <cooperative_groups.h>
+#include <limits.h>
 
 #include "common.cuh"
 
@@ -30,7 +31,8 @@ namespace pages {
 
 constexpr int kCtas = 8;        // of the deciding cluster
 constexpr int kThreads = 1024;  // of its CTAs
-constexpr int kPer = 4;         // pages of a thread in a step of a scan
+constexpr int kRowParts = 4;    // warps that share a row of the table when its entries change
+constexpr int kPer = 4;         // counts that a thread reads at once
 
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
     return tokens / page_size + (tokens % page_size ? 1 : 0);
@@ -139,44 +141,36 @@ __device__ __forceinline__ u64 block_scan(u64 x, u64* warps, u64& all) {
     return before + run - x;
 }
 
-// This CTA's slice of the pages, whole steps of a thread.
-__device__ __forceinline__ int2 slice_of(int num_pages, int rank) {
-    const int len = ((num_pages + kCtas - 1) / kCtas + kPer - 1) / kPer * kPer;
-    const int a = (int)min((long long)num_pages, (long long)rank * len);
-    return make_int2(a, (int)min((long long)num_pages, (long long)a + len));
+// Pages of this thread: contiguous, in the order of the cluster's threads, whole int4 of counts.
+struct Span {
+    int p0, p1;
+};
+
+__device__ __forceinline__ Span span_of(int num_pages, int rank) {
+    const long long threads = kCtas * kThreads;
+    const int len = (int)((num_pages + threads - 1) / threads + kPer - 1) / kPer * kPer;
+    const long long at = ((long long)rank * kThreads + threadIdx.x) * len;
+    Span s;
+    s.p0 = (int)min((long long)num_pages, at);
+    s.p1 = (int)min((long long)num_pages, at + len);
+    return s;
 }
 
-// Number of pages in the slice for which f(page, refs) holds.
+// f(page, count) for the span's pages, in order.
 template <class F>
-__device__ __forceinline__ int count_pages(const Table& t, int2 s, u64* warps, F f) {
-    int n = 0;
-    for (int p0 = s.x + (int)threadIdx.x; p0 < s.y; p0 += kThreads) n += f(p0, t.refs[p0]) ? 1 : 0;
-    u64 all;
-    block_scan(n, warps, all);
-    return (int)all;
-}
-
-// Calls emit(rank, page) for those pages, ranks from `base` on, while they are below `most`.
-template <class F, class G>
-__device__ __forceinline__ void rank_pages(const Table& t, int2 s, int base, int most, u64* warps, F f, G emit) {
-    for (int p0 = s.x; p0 < s.y && base < most; p0 += kThreads * kPer) {
-        const int p = p0 + (int)threadIdx.x * kPer;
-        bool is[kPer];
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            is[i] = p + i < s.y && f(p + i, t.refs[p + i]);
-            n += is[i] ? 1 : 0;
+__device__ __forceinline__ void each_page(const Table& t, Span s, F f) {
+    if (reinterpret_cast<uintptr_t>(t.refs) % 16 == 0) {
+        int p = s.p0;
+        for (; p + kPer <= s.p1; p += kPer) {
+            const int4 r = *reinterpret_cast<const int4*>(t.refs + p);
+            f(p, r.x);
+            f(p + 1, r.y);
+            f(p + 2, r.z);
+            f(p + 3, r.w);
         }
-        u64 all;
-        int r = base + (int)block_scan(n, warps, all);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (is[i]) {
-                if (r < most) emit(r, p + i);
-                ++r;
-            }
-        base += (int)all;
+        for (; p < s.p1; ++p) f(p, t.refs[p]);
+    } else {
+        for (int p = s.p0; p < s.p1; ++p) f(p, t.refs[p]);
     }
 }
 
@@ -222,7 +216,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
     const ReserveScratch s(scratch, t);
-    const int2 slice = slice_of(t.num_pages, rank);
+    const Span span = span_of(t.num_pages, rank);
     for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
         const int L0 = seqlens[b], L1 = new_seqlens[b];
         const long long cap = (long long)t.max_pages * t.page_size;
@@ -236,8 +230,10 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             s.last[g.shared] = -1;
         }
     }
-    const int mine = count_pages(t, slice, warps, [](int, int r) { return r <= 0; });
-    if (tid == 0) s.head[2 + rank] = mine;
+    u64 mine = 0, all;
+    each_page(t, span, [&](int, int r) { mine += r <= 0 ? 1 : 0; });
+    mine = block_scan(mine, warps, all);  // this thread's first free page in the CTA's order
+    if (tid == 0) s.head[2 + rank] = (int)all;
     cluster.sync();
     for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
         const Growth g = growth_of(t, seqlens, new_seqlens, b);
@@ -296,9 +292,16 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         missing[0] = fits ? 0 : (int)(need - have);
         if (!fits) raise_status(ATTN_SINK_DEV_POOL);
     }
-    if (fits)
-        rank_pages(t, slice, (int)before, need, warps, [](int, int r) { return r <= 0; },
-                   [&](int r, int p) { s.free[r] = p; });
+    if (fits) {
+        long long r = before + (long long)mine;
+        if (r < need)
+            each_page(t, span, [&](int p, int refs) {
+                if (refs <= 0) {
+                    if (r < need) s.free[r] = p;
+                    ++r;
+                }
+            });
+    }
     cluster.sync();
     if (!fits) {
         if (rank == 0 && tid == 0) s.head[0] = 0;  // nothing is copied
@@ -329,7 +332,7 @@ struct CompactScratch {
     int32_t *to, *src, *dst, *head;
     __host__ __device__ CompactScratch(void* at, const Table& t) {
         int32_t* p = static_cast<int32_t*>(at);
-        head = p;  // [0] moves, [2..] held pages of each slice, [10..] free ones in front, [18..] held ones behind
+        head = p;  // [0] moves, [1] held pages, [2..] those of each CTA, [10..] free ones in front, [18..] held ones behind
         to = head + 32;
         src = to + t.num_pages;
         dst = src + t.num_pages;
@@ -337,38 +340,47 @@ struct CompactScratch {
 };
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
-    compact_kernel(const Table t, const int32_t* seqlens, int32_t* held, void* scratch) {
+    compact_kernel(const Table t, int32_t* held, void* scratch) {
     __shared__ u64 warps[32];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
     const CompactScratch s(scratch, t);
-    const int2 slice = slice_of(t.num_pages, rank);
-    int n = count_pages(t, slice, warps, [](int, int r) { return r > 0; });
-    if (tid == 0) s.head[2 + rank] = n;
+    const Span span = span_of(t.num_pages, rank);
+    // held pages
+    u64 x = 0, all;
+    each_page(t, span, [&](int, int r) { x += r > 0 ? 1 : 0; });
+    block_scan(x, warps, all);
+    if (tid == 0) s.head[2 + rank] = (int)all;
     cluster.sync();
-    n = 0;
+    int n = 0;
     for (int c = 0; c < kCtas; ++c) n += s.head[2 + c];
-    const auto gap = [n](int p, int r) { return p < n && r <= 0; };
-    const auto out = [n](int p, int r) { return p >= n && r > 0; };
-    const int gaps = count_pages(t, slice, warps, gap), outs = count_pages(t, slice, warps, out);
+    // free ones among the first n (low half), held ones behind (high half), and their ranks
+    x = 0;
+    each_page(t, span, [&](int p, int r) { x += p < n ? (r <= 0 ? 1ull : 0) : r > 0 ? 1ull << 32 : 0; });
+    u64 at = block_scan(x, warps, all);
     if (tid == 0) {
-        s.head[10 + rank] = gaps;
-        s.head[18 + rank] = outs;
+        s.head[10 + rank] = (int)(uint32_t)all;
+        s.head[18 + rank] = (int)(all >> 32);
     }
     cluster.sync();
-    int gap0 = 0, out0 = 0, moves = 0;
+    int moves = 0;
     for (int c = 0; c < kCtas; ++c) {
-        if (c < rank) {
-            gap0 += s.head[10 + c];
-            out0 += s.head[18 + c];
-        }
+        if (c < rank) at += (u64)(uint32_t)s.head[10 + c] | (u64)(uint32_t)s.head[18 + c] << 32;
         moves += s.head[18 + c];
     }
-    rank_pages(t, slice, gap0, t.num_pages, warps, gap, [&](int r, int p) { s.dst[r] = p; });
-    rank_pages(t, slice, out0, t.num_pages, warps, out, [&](int r, int p) { s.src[r] = p; });
-    for (int p = max(slice.x, n) + tid; p < slice.y; p += kThreads) s.to[p] = -1;
+    uint32_t gap = (uint32_t)at, out = (uint32_t)(at >> 32);
+    each_page(t, span, [&](int p, int r) {
+        if (p < n) {
+            if (r <= 0) s.dst[gap++] = p;
+        } else if (r > 0) {
+            s.src[out++] = p;
+        } else {
+            s.to[p] = -1;
+        }
+    });
     if (rank == 0 && tid == 0) {
         s.head[0] = moves;
+        s.head[1] = n;
         held[0] = n;
     }
     cluster.sync();
@@ -378,17 +390,21 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         t.refs[to] = t.refs[from];
         t.refs[from] = 0;
     }
-    cluster.sync();
-    const int lane = tid & 31;
-    for (int b = rank * (kThreads / 32) + (tid >> 5); b < t.batch; b += all_threads / 32) {
+}
+
+// The rows' entries of pages that move.
+__device__ void retarget(const Table& t, const int32_t* seqlens, const int32_t* to, int n) {
+    const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
+    for (int w = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); w < t.batch * kRowParts; w += warps) {
+        const int b = w / kRowParts, part = w % kRowParts;
         const int pages = pages_of(length_of(t, seqlens, b), t.page_size);
         int32_t* const row = t.table + (size_t)b * t.max_pages;
-        for (int i = lane; i < pages; i += 32) {
+        for (int i = part * 32 + lane; i < pages; i += 32 * kRowParts) {
             const int p = row[i];
             if (!valid_page(t, p)) {
                 raise_status(ATTN_SINK_DEV_PAGE_OOB);
             } else if (p >= n) {
-                if (s.to[p] >= 0) row[i] = s.to[p];
+                if (to[p] >= 0) row[i] = to[p];
                 else raise_status(ATTN_SINK_DEV_POOL);  // held by a row, but not counted
             }
         }
@@ -418,20 +434,22 @@ __device__ __forceinline__ void copy_piece(const char* from, char* to, long long
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const int32_t* src, const int32_t* dst,
-                                                            const int32_t* count, int n, int num_pages, bool report) {
-    if (count) n = min(n, *count);
-    long long pieces = 0;  // of one copy
-    for (int i = 0; i < p.count; ++i) pieces += (p.bytes[i] + kPiece - 1) / kPiece;
-    for (long long w = blockIdx.x; w < n * pieces; w += gridDim.x) {
-        const int c = (int)(w / pieces);
-        long long k = w - c * pieces;
-        int i = 0;
-        for (; i < p.count; ++i) {
-            const long long own = (p.bytes[i] + kPiece - 1) / kPiece;
-            if (k < own) break;
-            k -= own;
+// Copies by all CTAs of the grid.
+__device__ __forceinline__ void copy_pages(const Pools& p, const int32_t* src, const int32_t* dst, int n, int num_pages,
+                                           bool report) {
+    int pieces = 0;  // of one copy
+    for (int i = 0; i < p.count; ++i) pieces += p.pieces[i];
+    // this CTA's items, gridDim.x apart: copy c, piece k
+    long long c = blockIdx.x / pieces;
+    int k0 = blockIdx.x % pieces;
+    const int dc = gridDim.x / pieces, dk = gridDim.x - dc * pieces;
+    for (; c < n; c += dc, k0 += dk) {
+        if (k0 >= pieces) {
+            k0 -= pieces;
+            if (++c >= n) break;
         }
+        int k = k0, i = 0;
+        for (; k >= p.pieces[i]; ++i) k -= p.pieces[i];
         const int from = src[c], to = dst[c];
         if ((unsigned)from >= (unsigned)num_pages || (unsigned)to >= (unsigned)num_pages) {
             if (report && threadIdx.x == 0 && (from != -1 || to != -1)) raise_status(ATTN_SINK_DEV_PAGE_OOB);
@@ -449,20 +467,43 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const
     }
 }
 
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const int32_t* src, const int32_t* dst,
+                                                            const int32_t* count, int n, int num_pages, bool report) {
+    copy_pages(p, src, dst, count ? min(n, *count) : n, num_pages, report);
+}
+
+// What follows compact_kernel: the table's entries and the pages.
+__global__ void __launch_bounds__(kCopyThreads) move_kernel(const Pools p, const Table t, const int32_t* seqlens, void* scratch) {
+    const CompactScratch s(scratch, t);
+    retarget(t, seqlens, s.to, s.head[1]);
+    if (p.count) copy_pages(p, s.src, s.dst, s.head[0], t.num_pages, false);
+}
+
 // ---------------------------------------------------------------------------
 // Host side.
 
 size_t reserve_scratch(const Table& t) { return (16 + 3 * (size_t)t.num_pages + 3 * (size_t)t.batch) * 4; }
 size_t compact_scratch(const Table& t) { return (32 + 3 * (size_t)t.num_pages) * 4; }
 
+// Pieces that copies are cut into.
+static Pools with_pieces(const Pools& p) {
+    Pools q = p;
+    for (int i = 0; i < q.count; ++i) q.pieces[i] = (int)((q.bytes[i] + kPiece - 1) / kPiece);
+    return q;
+}
+
+// 8 CTAs of 256 threads an SM: all that are resident at once.
+static int resident_ctas() { return 8 * num_sms(); }
+
 cudaError_t launch_copy(const Pools& p, const int32_t* src, const int32_t* dst, const int32_t* count, int n, int num_pages,
                         bool report, cudaStream_t s) {
+    const Pools q = with_pieces(p);
     long long pieces = 0;
-    for (int i = 0; i < p.count; ++i) pieces += (p.bytes[i] + kPiece - 1) / kPiece;
+    for (int i = 0; i < q.count; ++i) pieces += q.pieces[i];
     if (n <= 0 || pieces == 0) return cudaSuccess;
-    // all resident at once: 8 CTAs of 256 threads an SM
-    const long long want = n * pieces, most = 8LL * num_sms();
-    copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, s>>>(p, src, dst, count, n, num_pages, report);
+    if (pieces > INT_MAX / 2) return cudaErrorInvalidConfiguration;
+    const long long want = n * pieces, most = resident_ctas();
+    copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, s>>>(q, src, dst, count, n, num_pages, report);
     return cudaGetLastError();
 }
 
@@ -492,11 +533,18 @@ cudaError_t launch_reserve(const Pools& p, const Table& t, const int32_t* seqlen
 
 cudaError_t launch_compact(const Pools& p, const Table& t, const int32_t* seqlens, int32_t* held, void* scratch,
                            cudaStream_t s) {
-    compact_kernel<<<kCtas, kThreads, 0, s>>>(t, seqlens, held, scratch);
+    const Pools q = with_pieces(p);
+    long long pieces = 0;
+    for (int i = 0; i < q.count; ++i) pieces += q.pieces[i];
+    if (pieces > INT_MAX / 2) return cudaErrorInvalidConfiguration;
+    compact_kernel<<<kCtas, kThreads, 0, s>>>(t, held, scratch);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const CompactScratch c(scratch, t);
-    return launch_copy(p, c.src, c.dst, c.head, t.num_pages, t.num_pages, false, s);
+    const long long want = t.num_pages * (pieces > 0 ? pieces : 1), rows = ((long long)t.batch * kRowParts + 7) / 8;
+    long long grid = want > rows ? want : rows;
+    if (grid > resident_ctas()) grid = resident_ctas();
+    move_kernel<<<(unsigned)grid, kCopyThreads, 0, s>>>(q, t, seqlens, scratch);
+    return cudaGetLastError();
 }
 
 ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)

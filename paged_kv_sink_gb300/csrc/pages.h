@@ -17,6 +17,7 @@ constexpr int kMaxPools = 8;
 struct Pools {
     void* base[kMaxPools];
     long long bytes[kMaxPools];  // of a page
+    int pieces[kMaxPools];       // (set by the launches) work items of a page
     int count;
 };
 
