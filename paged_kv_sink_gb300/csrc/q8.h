@@ -70,6 +70,7 @@ struct AttendPlan {
     int tiles;         // row tiles of a KV head
     int split_tokens;  // visible tokens per split
     int max_splits;
+    bool gather;       // a row's splits are one cluster, which merges them
     size_t part_o_bytes, part_ml_bytes;  // of all rows
 };
 

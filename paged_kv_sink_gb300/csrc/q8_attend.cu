@@ -24,13 +24,19 @@
 //    and what falls below 2^-31 of the largest weight is lost.  Its rounding to fp16 is off by
 //    at most 2^-11 of each weight (bf16: 2^-8).  The denominator sums P / vs, unrounded, in
 //    fp32.
-//  * attend_combine_kernel merges the splits in the log-sum-exp sense and folds the
-//    sink in once; with a single split the CTA does it itself.
+//  * The splits are merged in the log-sum-exp sense and the sink is folded in once: by the
+//    cluster that they form, through distributed shared memory, where a row has at most 8,
+//    by attend_combine_kernel where it has more.
 // Bound by HBM: half the bytes of the bf16 cache.
 #include "q8.cuh"
 
+#include <cooperative_groups.h>
 #include <limits.h>
 #include <math.h>
+
+#include <atomic>
+
+namespace cg = cooperative_groups;
 
 namespace attn {
 namespace q8 {
@@ -38,6 +44,7 @@ namespace q8 {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kTokens = 32;        // tokens of a warp's chunk
+constexpr int kGather = 8;         // splits that one cluster holds
 // P is at most 2^(kHead + kSlack), and its row's largest at least about 2^kHead.
 constexpr float kHead = 7.f, kSlack = 8.f;
 constexpr float kNoRef = -1e30f;   // nothing seen yet
@@ -181,9 +188,10 @@ struct Smem {
     static constexpr int kBytes = kWarps * (STAGES * kStage + kTokens * 16);
 };
 
-// kRows: several new tokens, so that rows see different tokens.
-template <int D, int NT, int STAGES, int F, bool kRows>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
+// kRows: several new tokens, so that rows see different tokens.  gather: the splits are one
+// cluster, which merges them itself.
+template <int D, int NT, int STAGES, int F, bool kRows, bool gather>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : 2) attend_kernel(const Params p) {
     using SM = Smem<D, STAGES>;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int H = 8 * NT;
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
     const Ranges vis = tile_ranges(p, r, tok0, tok1);
     const int nvis = visible_count(vis);
     const long long v0l = (long long)split * p.split_tokens;
-    if (v0l >= nvis && p.max_splits > 1) return;
+    if (v0l >= nvis && !gather) return;
     const int v0 = (int)v0l, v1 = (int)min((long long)nvis, v0l + p.split_tokens);
     const int nchunks = (v1 - v0 - warp * kTokens + kWarps * kTokens - 1) / (kWarps * kTokens);  // of this warp
 
@@ -493,34 +501,70 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const Params p) {
                                                                        o[mt + 1][nt][col], o[mt + 1][nt][2 + col]);
         }
     __syncthreads();
+    float* const all_m = sm_o + kWarps * H * D;  // the CTA's: [H], [H], [H][D]
+    float* const all_l = all_m + H;
+    float* const all_o = all_l + H;
     for (int e = tid; e < nrows * D; e += kThreads) {
         const int j = e / D, dd = e % D;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * H + j]);
-        int tok, head;
-        row_at(j, tok, head);
-        const size_t row = (size_t)(r.q_start + tok) * p.hq + head;
-        const bool direct = p.max_splits == 1;
-        const float sg = direct && p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
-        M = fmaxf(M, sg);
         const float ref = M == -INFINITY ? 0.f : M;
-        float acc = 0.f, l = direct ? fast_exp2(sg - ref) : 0.f;
+        float acc = 0.f, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = half_factor(sm_m[w * H + j] - ref);
             acc += sm_o[(w * H + j) * D + dd] * f * f;
             l += sm_l[w * H + j] * f * f;
         }
-        if (direct) {
-            float lse;
-            p.out[row * D + dd] = __float2bfloat16_rn(finish(M, l, acc, lse));
-            if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
+        if constexpr (gather) {
+            all_o[e] = acc;
+            if (dd == 0) {
+                all_m[j] = M;
+                all_l[j] = l;
+            }
         } else {
-            const size_t at = row * p.max_splits + split;
+            int tok, head;
+            row_at(j, tok, head);
+            const size_t at = ((size_t)(r.q_start + tok) * p.hq + head) * p.max_splits + split;
             p.part_o[at * D + dd] = acc;
             if (dd == 0) p.part_ml[at] = make_float2(M, l);
         }
+    }
+    if constexpr (gather) {
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        for (int e = split * kThreads + tid; e < nrows * D; e += p.max_splits * kThreads) {
+            const int j = e / D, dd = e % D;
+            int tok, head;
+            row_at(j, tok, head);
+            const size_t row = (size_t)(r.q_start + tok) * p.hq + head;
+            const float sg = p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
+            float M = sg, m[kGather], l[kGather], x[kGather];
+#pragma unroll
+            for (int c = 0; c < kGather; ++c) {
+                m[c] = -INFINITY;
+                if (c < p.max_splits) {
+                    m[c] = *cluster.map_shared_rank(all_m + j, c);
+                    l[c] = *cluster.map_shared_rank(all_l + j, c);
+                    x[c] = *cluster.map_shared_rank(all_o + e, c);
+                }
+                M = fmaxf(M, m[c]);
+            }
+            const float ref = M == -INFINITY ? 0.f : M;
+            float acc = 0.f, Z = fast_exp2(sg - ref);
+#pragma unroll
+            for (int c = 0; c < kGather; ++c)
+                if (c < p.max_splits) {
+                    const float f = half_factor(m[c] - ref);
+                    acc += x[c] * f * f;
+                    Z += l[c] * f * f;
+                }
+            float lse;
+            p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, acc, lse));
+            if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
+        }
+        cluster.sync();  // the others may still read this CTA's sums
     }
 }
 
@@ -587,36 +631,72 @@ AttendPlan make_plan(const AttendArgs& a) {
     if (sp < 256) sp = 256;
     pl.split_tokens = (int)sp;
     pl.max_splits = (int)((nvis + sp - 1) / sp);
-    const size_t parts = pl.max_splits > 1 ? (size_t)a.total_q * a.hq * pl.max_splits : 0;
+    // Few splits that are all resident at once merge as clusters (one launch, no scratch; 5 new tokens
+    // of one request of 2000 18.6 -> 14.4 us).  In a batch of several waves the CTAs that end early
+    // would wait for their cluster (64 requests of 1k to 16k tokens, 12 heads 162 -> 258 us).
+    pl.gather = pl.max_splits == 1 || (pl.max_splits <= kGather && units * pl.max_splits <= slots);
+    const size_t parts = !pl.gather ? (size_t)a.total_q * a.hq * pl.max_splits : 0;
     pl.part_o_bytes = parts * a.c.head_dim * sizeof(float);
     pl.part_ml_bytes = parts * sizeof(float2);
     return pl;
 }
 
-template <int D, int NT, int F, bool kRows>
-static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
+// Shared memory above 48 KB is asked for once per kernel and device.
+template <class Kernel>
+static cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& allowed) {
+    if (bytes <= 48 << 10) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (bit & allowed.load(std::memory_order_relaxed)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
+template <int D, int NT, int F, bool kRows, bool gather>
+static cudaError_t run_form(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
     // Two stages and more CTAs rather than three (d 64: 6 of 38 KB instead of 4, 222 -> 212 us on 64
     // requests of 1k to 32k tokens; d 128: 3 instead of 2, 426 -> 406).
     constexpr int STAGES = 2;
     int smem = Smem<D, STAGES>::kBytes;
-    const int merge = kWarps * 8 * NT * (D + 2) * 4;
+    const int merge = (kWarps + (gather ? 1 : 0)) * 8 * NT * (D + 2) * 4;
     if (smem < merge) smem = merge;
-    auto kern = attend_kernel<D, NT, STAGES, F, kRows>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    auto kern = attend_kernel<D, NT, STAGES, F, kRows, gather>;
+    static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have its shared memory
+    cudaError_t e = allow_smem(kern, smem, allowed);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(pl.max_splits, a.c.hkv * pl.tiles, a.batch), kThreads, smem, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || pl.max_splits == 1) return e;
+    cudaLaunchAttribute attr[1];
+    {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(pl.max_splits, a.c.hkv * pl.tiles, a.batch);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = gather ? pl.max_splits : 1;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+    }
+    if constexpr (gather) return cudaGetLastError();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.hq, a.max_q, a.batch);
     cfg.blockDim = dim3(D);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if ((e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT>, p)) != cudaSuccess) return e;
     return cudaGetLastError();
+}
+
+template <int D, int NT, int F, bool kRows>
+static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
+    return pl.gather ? run_form<D, NT, F, kRows, true>(p, a, pl, s) : run_form<D, NT, F, kRows, false>(p, a, pl, s);
 }
 
 template <int D, int F>
