@@ -1039,8 +1039,7 @@ int check_q8(const char* who, void* k, void* v, float* ks, float* vs, const int3
     return check_grid(who, batch, 0);
 }
 
-int run_attend_q8(const char* who, attn::q8::AttendArgs& a, cudaStream_t s) {
-    const attn::q8::AttendPlan pl = attn::q8::make_plan(a);
+int run_attend_q8(const char* who, const attn::q8::AttendArgs& a, const attn::q8::AttendPlan& pl, cudaStream_t s) {
     if ((long long)a.c.hkv * pl.tiles > kMaxGridDim)
         return fail(ATTN_SINK_ERR_UNSUPPORTED, "%s: too many heads", who);
     Scratch ws;
@@ -1052,9 +1051,23 @@ int run_attend_q8(const char* who, attn::q8::AttendArgs& a, cudaStream_t s) {
     return ATTN_SINK_OK;
 }
 
-// Rows (new tokens times query heads of a KV head) up to which a request's tokens are
-// read as codes by the row kernel; above, they are expanded for the tensor-core forward.
-constexpr long long kMaxAttendRows = 64;
+// Which kernels compute new tokens over an 8-bit cache, by what a request has at most (n new tokens,
+// g query heads of a KV head; times of 16 requests of 1k to 16k tokens, 8 KV heads):
+//  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 144 us, chain
+//    149; 16: 266, chain 155), 32 at 128 (16 rows: 90, chain 260; 64: 319, chain 270), and up
+//    to four times as many where its CTAs are all resident at once (one request of 2000 tokens,
+//    128 rows: 16.5 us, chain 27; 256: 28.8, chain 31);
+//  * else, on the tokens expanded to bf16, the kernel of drafted trees on a chain, whose tiles hold
+//    (token, head) rows, up to 48 tokens at head dim 64 (32 tokens: 190 us, forward 403; 64 of 4
+//    requests: 79, forward 74), 96 at 128 (64: 89, forward 122; 128: 137, forward 127), g > 1;
+//  * else the forward's, whose tiles hold 128 tokens of one head.
+bool few_rows(const attn::q8::AttendArgs& a, const attn::q8::AttendPlan& pl) {
+    const long long rows = a.max_q * (long long)(a.hq / a.c.hkv), most = a.c.head_dim == 64 ? 64 : 32;
+    return rows <= most || (rows <= 4 * most && pl.gather);
+}
+bool as_chain(int max_q, int group, int head_dim, int causal) {
+    return causal && max_q <= (head_dim == 64 ? 48 : 96) && group > 1 && group <= 128;
+}
 
 }  // namespace
 
@@ -1127,7 +1140,7 @@ int attn_sink_decode_paged_q8(const attn_bf16* q, const void* k_cache, const voi
     a.win_last = win_last;
     a.causal = 1;
     a.scale = attn::resolve_scale(scale, head_dim);
-    return run_attend_q8("decode_q8", a, static_cast<cudaStream_t>(stream));
+    return run_attend_q8("decode_q8", a, attn::q8::make_plan(a), static_cast<cudaStream_t>(stream));
 }
 
 int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -1155,25 +1168,24 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         return fail(ATTN_SINK_ERR_INVALID, "fwd_paged_q8: q and out must be 16-byte aligned");
     if ((rc = check_grid("fwd_paged_q8", batch, max_seqlen_q)) != ATTN_SINK_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (max_seqlen_q * (long long)(hq / hkv) <= kMaxAttendRows) {
-        a.q = as_bf16(q);
-        a.cu_q = cu_seqlens_q;
-        a.seqlens = seqlens_k;
-        a.sink = sink;
-        a.out = as_bf16(out);
-        a.lse = lse;
-        a.lse_by_head = 1;
-        a.batch = batch;
-        a.total_q = total_q;
-        a.hq = hq;
-        a.max_q = max_seqlen_q;
-        a.max_seqlen = max_seqlen_k;
-        a.win_first = win_first;
-        a.win_last = win_last;
-        a.causal = causal ? 1 : 0;
-        a.scale = attn::resolve_scale(scale, head_dim);
-        return run_attend_q8("fwd_paged_q8", a, s);
-    }
+    a.q = as_bf16(q);
+    a.cu_q = cu_seqlens_q;
+    a.seqlens = seqlens_k;
+    a.sink = sink;
+    a.out = as_bf16(out);
+    a.lse = lse;
+    a.lse_by_head = 1;
+    a.batch = batch;
+    a.total_q = total_q;
+    a.hq = hq;
+    a.max_q = max_seqlen_q;
+    a.max_seqlen = max_seqlen_k;
+    a.win_first = win_first;
+    a.win_last = win_last;
+    a.causal = causal ? 1 : 0;
+    a.scale = attn::resolve_scale(scale, head_dim);
+    const attn::q8::AttendPlan pl = attn::q8::make_plan(a);
+    if (few_rows(a, pl)) return run_attend_q8("fwd_paged_q8", a, pl, s);
     // Many rows: the tokens as bf16 in pages of their own, a round of requests at a time.
     const long long cap = (long long)max_pages * page_size;
     const long long keys = max_seqlen_k < cap ? max_seqlen_k : cap;
@@ -1182,8 +1194,10 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
     const size_t most = kMaxScoreBytes / (2 * cache);
     int round = most >= (size_t)batch ? batch : most ? (int)most : 1;
     round = (batch + (batch + round - 1) / round - 1) / ((batch + round - 1) / round);
+    const bool chain = as_chain(max_seqlen_q, hq / hkv, head_dim, causal);
+    const size_t table = ((size_t)pages * round * sizeof(int32_t) + 15) & ~size_t(15);
     Scratch ws;
-    cudaError_t e = ws.alloc(2 * cache * round + (size_t)pages * round * sizeof(int32_t), s);
+    cudaError_t e = ws.alloc(2 * cache * round + table + (chain ? (size_t)total_q * sizeof(int32_t) : 0), s);
     if (e != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: scratch allocation");
     char* const base = static_cast<char*>(ws.ptr);
     for (int b0 = 0; b0 < batch; b0 += round) {
@@ -1199,7 +1213,43 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         x.k_out = reinterpret_cast<__nv_bfloat16*>(base);
         x.v_out = reinterpret_cast<__nv_bfloat16*>(base + cache * round);
         x.table_out = reinterpret_cast<int32_t*>(base + 2 * cache * round);
+        x.parents = chain ? reinterpret_cast<int32_t*>(base + 2 * cache * round + table) : nullptr;
+        x.total_q = total_q;
         if ((e = attn::q8::launch_expand(x, s)) != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: launch");
+        std::string err;
+        if (chain) {
+            attn::tree::Args t = {};
+            t.q = q;
+            t.k_cache = x.k_out;
+            t.v_cache = x.v_out;
+            t.page_table = x.table_out;
+            t.cu_q = x.cu_q;
+            t.seqlens_k = x.seqlens;
+            t.parents = x.parents;
+            t.sink = sink;
+            t.out = out;
+            t.lse = lse;
+            t.max_pages = pages;
+            t.batch = x.batch;
+            t.total_q = total_q;
+            t.hq = hq;
+            t.hkv = hkv;
+            t.head_dim = head_dim;
+            t.page_size = attn::q8::kExpandPage;
+            t.num_pages = pages * x.batch;
+            t.max_seqlen_q = max_seqlen_q;
+            t.win_first = win_first;
+            t.win_last = win_last;
+            t.scale = attn::resolve_scale(scale, head_dim);
+            t.chain = true;
+            const attn::tree::Plan tp = attn::tree::make_plan(t);
+            Scratch parts;
+            if ((e = parts.alloc(tp.part_o_bytes + tp.part_ml_bytes + tp.first_bytes, s)) != cudaSuccess)
+                return cuda_fail(e, "fwd_paged_q8: scratch allocation");
+            if ((e = attn::tree::launch(t, tp, parts.ptr, s, &err)) != cudaSuccess)
+                return fail(ATTN_SINK_ERR_CUDA, "fwd_paged_q8: %s: %s", err.c_str(), cudaGetErrorString(e));
+            continue;
+        }
         attn::prefill::FwdArgs f = {};
         f.q = q;
         f.k = x.k_out;
@@ -1224,7 +1274,6 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         f.max_pages = pages;
         f.page_size = attn::q8::kExpandPage;
         f.num_pages = pages * x.batch;
-        std::string err;
         if ((e = attn::prefill::launch_fwd(f, s, &err)) != cudaSuccess)
             return fail(ATTN_SINK_ERR_CUDA, "fwd_paged_q8: %s: %s", err.c_str(), cudaGetErrorString(e));
     }

@@ -51,6 +51,8 @@ struct ExpandArgs {
     __nv_bfloat16* k_out;
     __nv_bfloat16* v_out;
     int32_t* table_out;  // (batch, pages)
+    int32_t* parents;    // (total_q,), or NULL: each row's predecessor in its request
+    int total_q;
 };
 
 struct AttendArgs {

@@ -276,10 +276,13 @@ constexpr int kExpandThreads = 256;
 constexpr int kExpandTokens = 32;  // tokens of a block
 
 template <int F>
-__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs a, int page_shift) {
+__global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs a, int page_shift, int block_shift, int blocks) {
     const Cache& c = a.c;
     const int b = blockIdx.y;
-    const int Lq = max(0, a.cu_q[b + 1] - a.cu_q[b]);
+    const int q_start = a.cu_q[b], Lq = max(0, a.cu_q[b + 1] - q_start);
+    if (a.parents && blockIdx.x == 0)
+        for (int i = threadIdx.x; i < Lq; i += kExpandThreads)
+            if ((unsigned)(q_start + i) < (unsigned)a.total_q) a.parents[q_start + i] = i - 1;
     const long long cap = min((long long)c.max_pages * c.page_size, (long long)a.pages * kExpandPage);
     int L = a.seqlens[b];
     if (L > cap) {
@@ -310,35 +313,55 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs
         in_of[threadIdx.x] = in;
     }
     __syncthreads();
-    const int vec = c.hkv * c.head_dim / 16, dv = c.head_dim / 16;  // 16-code pieces of a row, of a head
-    for (int i = threadIdx.x; i < kExpandTokens * vec; i += kExpandThreads) {
-        const int r = i / vec, x = i - r * vec, page = page_of[r];
-        if (page == -1) break;  // behind the request's end
-        const size_t to = ((size_t)b * a.pages * kExpandPage + t0 + r) * vec + x;
+    // 8 codes of K and of V a step, kAhead steps' loads in flight.
+    constexpr int kAhead = 4;
+    const int vec = c.hkv * c.head_dim / 8, shift = c.head_dim == 64 ? 3 : 4;  // 8-code pieces of a row, log2 of a head's
+    const int dr = kExpandThreads / vec, dx = kExpandThreads - dr * vec;
+    int r = threadIdx.x / vec, x = threadIdx.x - r * vec;
+    const int rows = min(kExpandTokens, L - t0);
+    uint4* const ko = reinterpret_cast<uint4*>(a.k_out) + ((size_t)b * a.pages * kExpandPage + t0) * vec;
+    uint4* const vo = reinterpret_cast<uint4*>(a.v_out) + ((size_t)b * a.pages * kExpandPage + t0) * vec;
+    while (r < rows) {
+        uint2 w[kAhead][2];
+        float sc[kAhead][2];
+        int to[kAhead];
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-            uint4* out = reinterpret_cast<uint4*>(kv ? a.v_out : a.k_out) + to * 2;
-            if (page < 0) {
-                out[0] = out[1] = make_uint4(0, 0, 0, 0);
-                continue;
+        for (int i = 0; i < kAhead; ++i) {
+            to[i] = r < rows ? r * vec + x : -1;
+            w[i][0] = w[i][1] = make_uint2(0, 0);
+            sc[i][0] = sc[i][1] = 0.f;
+            const int page = r < rows ? page_of[r] : -1;
+            if (page >= 0) {  // (a bad page: zeros)
+                const size_t at = ((size_t)page * c.page_size + in_of[r]) * vec + x;
+                const size_t so = ((size_t)page * blocks + (block_shift >= 0 ? in_of[r] >> block_shift : in_of[r] / c.block)) * c.hkv +
+                                  (x >> shift);
+                w[i][0] = __ldcs(reinterpret_cast<const uint2*>(c.k) + at);
+                w[i][1] = __ldcs(reinterpret_cast<const uint2*>(c.v) + at);
+                sc[i][0] = c.k_scale[so];
+                sc[i][1] = c.v_scale[so];
             }
-            const float sc = (kv ? c.v_scale : c.k_scale)[((size_t)page * (c.page_size / c.block) + in_of[r] / c.block) *
-                                                              c.hkv + x / dv];
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(kv ? c.v : c.k) +
-                                   ((size_t)page * c.page_size + in_of[r]) * vec + x);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t y[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t p, q;
-                quad_to_f16<F>(in[j], p, q);
-                const float2 f = f16_to_float2(p), g = f16_to_float2(q);
-                y[2 * j] = pack_bf16x2(f.x * sc, f.y * sc);
-                y[2 * j + 1] = pack_bf16x2(g.x * sc, g.y * sc);
+            r += dr;
+            x += dx;
+            if (x >= vec) {
+                x -= vec;
+                ++r;
             }
-            out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-            out[1] = make_uint4(y[4], y[5], y[6], y[7]);
         }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (to[i] >= 0) {
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    float f[8];
+                    decode8<F>(w[i][kv], f);
+                    uint4 y;
+                    y.x = pack_bf16x2(f[0] * sc[i][kv], f[1] * sc[i][kv]);
+                    y.y = pack_bf16x2(f[2] * sc[i][kv], f[3] * sc[i][kv]);
+                    y.z = pack_bf16x2(f[4] * sc[i][kv], f[5] * sc[i][kv]);
+                    y.w = pack_bf16x2(f[6] * sc[i][kv], f[7] * sc[i][kv]);
+                    (kv ? vo : ko)[to[i]] = y;
+                }
+            }
     }
 }
 
@@ -346,8 +369,8 @@ cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t s) {
     if (a.batch == 0 || a.pages == 0) return cudaSuccess;
     dim3 grid((unsigned)a.pages * (kExpandPage / kExpandTokens), a.batch);
     const int sh = shift_of(a.c.page_size);
-    if (a.c.format == kE4M3) expand_kernel<kE4M3><<<grid, kExpandThreads, 0, s>>>(a, sh);
-    else expand_kernel<kInt8><<<grid, kExpandThreads, 0, s>>>(a, sh);
+    if (a.c.format == kE4M3) expand_kernel<kE4M3><<<grid, kExpandThreads, 0, s>>>(a, sh, shift_of(a.c.block), a.c.page_size / a.c.block);
+    else expand_kernel<kInt8><<<grid, kExpandThreads, 0, s>>>(a, sh, shift_of(a.c.block), a.c.page_size / a.c.block);
     return cudaGetLastError();
 }
 

@@ -122,6 +122,7 @@ struct Params {
     int gangs, batch, max_pages, page_shift, seg_shift, num_pages;
     int hq, hkv, group, total_q, max_q;
     int npt;  // nodes per row tile
+    int chain;  // a request may have fewer tokens than nodes (its prefix is negative then)
     int win_first, win_last;
     float scale_log2;
 };
@@ -141,14 +142,14 @@ __device__ __forceinline__ Request request(const Params& p, int b, bool report) 
     r.L = p.seqlens_k[b];
     const long long cap = (long long)p.max_pages << p.page_shift;
     const bool over = r.n > p.max_q || r.q_start < 0 || (long long)r.q_start + r.n > p.total_q;
-    if (over || (r.n > 0 && (r.L > cap || r.L < r.n))) {
+    if (over || (r.n > 0 && (r.L > cap || (r.L < r.n && !(p.chain && r.L >= 0))))) {
         if (report) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
         if (r.L > cap) r.L = (int)cap;
     }
     r.rows = r.q_start < 0 ? 0 : max(0, min(min(r.n, p.max_q), p.total_q - r.q_start));
     r.mtiles = (r.rows + p.npt - 1) / p.npt;
-    if (r.L < r.n) r.L = 0;  // the nodes are not in the cache: nothing is seen
-    r.P = max(0, r.L - r.n);
+    if (r.L < 0 || (r.L < r.n && !p.chain)) r.L = 0;  // the nodes are not in the cache: nothing is seen
+    r.P = p.chain ? r.L - r.n : max(0, r.L - r.n);
     const int t_end = (r.L + BN - 1) / BN;
     r.ta = r.tb = t_end;
     if (p.win_last > 0) {
@@ -1086,6 +1087,7 @@ static cudaError_t launch_d(const Args& a, const Plan& pl, void* scratch, cudaSt
     p.cu_q = a.cu_q;
     p.seqlens_k = a.seqlens_k;
     p.parents = a.parents;
+    p.chain = a.chain ? 1 : 0;
     p.page_table = a.page_table;
     p.v_cache = static_cast<const __nv_bfloat16*>(a.v_cache);
     p.out = static_cast<__nv_bfloat16*>(a.out);

@@ -27,6 +27,9 @@ struct Args {
     int max_pages, batch, total_q, hq, hkv, head_dim, page_size, num_pages, max_seqlen_q;
     int win_first, win_last;
     float scale;
+    // The nodes are a chain and stand at L - n, L - n + 1, .. also where a request has fewer
+    // tokens than nodes: those before position 0 see nothing.
+    bool chain = false;
 };
 
 // Grid and scratch sizes.

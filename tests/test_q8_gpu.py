@@ -329,7 +329,11 @@ EXTEND = [
     ([500, 40], [16, 9], 8, 2, 64, 16, 8, 0, 6, True, True),      # windows shorter than the draft
     ([300, 20], [30, 2], 2, 2, 64, 16, 4, 0, 0, False, False),    # not causal
     ([600, 0, 33], [64, 64, 1], 1, 1, 128, 8, 8, 0, 0, True, True),
-    ([130], [100], 12, 12, 64, 32, 16, 0, 0, True, True),         # expanded from here on
+    ([130], [100], 12, 12, 64, 32, 16, 0, 0, True, True),
+    ([1000, 3, 0, 200], [40, 33, 48, 0], 64, 8, 64, 16, 16, 0, 0, True, True),  # expanded from here on: chains
+    ([700, 90], [37, 48], 16, 1, 64, 24, 8, 20, 61, False, True),
+    ([500, 0, 33], [90, 96, 1], 32, 8, 128, 64, 32, 0, 0, True, True),
+    ([900, 300], [80, 33], 24, 4, 128, 7, 7, 100, 30, True, True),
     ([1000, 3, 0, 200], [300, 129, 128, 0], 8, 2, 64, 16, 16, 0, 0, True, True),
     ([1000, 0], [200, 500], 8, 4, 128, 24, 8, 0, 0, False, True),
     ([2000, 700], [150, 400], 16, 4, 64, 16, 16, 100, 300, True, True),
@@ -359,14 +363,14 @@ def test_extend_matches_definition(ext, case, fmt):
         at += n
 
 
-@pytest.mark.parametrize("n", [5, 200])
-def test_extend_leaves_other_rows_alone(ext, n):
+@pytest.mark.parametrize("n,hq", [(5, 4), (40, 32), (200, 4)])
+def test_extend_leaves_other_rows_alone(ext, n, hq):
     """Rows behind the last request's and rows past max_seqlen_q stay; requests with fewer tokens
-    than rows see none in the first ones."""
+    than rows see none in the first ones.  (5 and 4: the row kernel, 40 and 32: chains, 200: the forward.)"""
     c = Cache([300, 3], 2, 64, 16, 16, "int8", seed=12)
-    q = torch.randn(n + 5 + 4, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    q = torch.randn(n + 5 + 4, hq, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
     out = torch.full_like(q, 7).cuda()
-    lse = torch.full((4, q.shape[0]), 7.0).cuda()
+    lse = torch.full((hq, q.shape[0]), 7.0).cuda()
     ext.device_status()
     ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu([n, 5]).cuda(), torch.tensor([300, 3]).int().cuda(), n, 300, out=out, lse=lse)
     assert ext.device_status() == 0
@@ -379,18 +383,19 @@ def test_extend_leaves_other_rows_alone(ext, n):
 
 
 def test_expanded_batches_go_in_rounds(ext):
-    """A length bound far above the lengths: scratch stays at 2 GiB and a little, results the same."""
+    """A length bound far above the lengths: scratch stays at 2 GiB and a little, results the same.
+    (140 rows a request: the expanding form whatever the bound; fewer may go either way by it.)"""
     lens = [200 + 31 * b for b in range(24)]
     c = Cache(lens, 8, 128, 16, 16, "e4m3", seed=13)
     wide = torch.full((24, 65536 // 16), -1, dtype=torch.int32)
     wide[:, :c.table.shape[1]] = c.table
-    q = torch.randn(24 * 100, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
-    dev, sl, cq = c.dev(), torch.tensor(lens).int().cuda(), cu([100] * 24).cuda()
-    out, lse = ext.attn_sink_fwd_paged_q8(q, *dev, cq, sl, 100, max(lens))
+    q = torch.randn(24 * 140, 8, 128, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    dev, sl, cq = c.dev(), torch.tensor(lens).int().cuda(), cu([140] * 24).cuda()
+    out, lse = ext.attn_sink_fwd_paged_q8(q, *dev, cq, sl, 140, max(lens))
     torch.cuda.synchronize()
     free = torch.cuda.mem_get_info()[0]
     dev[4] = wide.cuda()
-    out2, lse2 = ext.attn_sink_fwd_paged_q8(q, *dev, cq, sl, 100, 65536)
+    out2, lse2 = ext.attn_sink_fwd_paged_q8(q, *dev, cq, sl, 140, 65536)
     torch.cuda.synchronize()
     assert free - torch.cuda.mem_get_info()[0] <= 2400 << 20
     assert same(out, out2) and same(lse, lse2) and ext.device_status() == 0
