@@ -20,31 +20,32 @@ _NO_BOUND = 2 ** 31 - 1
 
 def _expect_q8(k_cache, v_cache, k_scale, v_scale, page_table, dev, batch, d=None):
     """Returns (num_pages, page_size, hkv, d, max_pages, block, format)."""
-    fmt, shape = _FORMATS.get(k_cache.dtype), k_cache.shape
-    if fmt is None:
-        raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {k_cache.dtype}")
-    if len(shape) != 4 or (d is not None and shape[3] != d) or not _is(k_cache, k_cache.dtype, dev, shape):
-        _expect("k_cache", k_cache, k_cache.dtype, dev, (None, None, None, d))
-    if not _is(v_cache, k_cache.dtype, dev, shape):
-        _expect("v_cache", v_cache, k_cache.dtype, dev, shape)
-    npages, ps, hkv, d = shape
-    blocks = k_scale.shape[1] if k_scale.dim() == 3 else 0
-    want = (npages, blocks, hkv)
-    if not _is(k_scale, _F32, dev, want):
-        _expect("k_scale", k_scale, _F32, dev, (npages, None, hkv))
-    if not _is(v_scale, _F32, dev, want):
-        _expect("v_scale", v_scale, _F32, dev, want)
+    kind, shape, scales, table = k_cache.dtype, k_cache.shape, k_scale.shape, page_table.shape
+    fmt = _FORMATS.get(kind)
+    usual = (fmt is not None and len(shape) == 4 and len(scales) == 3 and len(table) == 2
+             and (d is None or shape[3] == d) and _is(k_cache, kind, dev, shape) and _is(v_cache, kind, dev, shape)
+             and scales[0] == shape[0] and scales[2] == shape[2] and _is(k_scale, _F32, dev, scales)
+             and _is(v_scale, _F32, dev, scales) and table[0] == batch and _is(page_table, _I32, dev, table))
+    if not usual:
+        if fmt is None:
+            raise TypeError(f"k_cache must be torch.float8_e4m3fn or torch.int8, got {kind}")
+        _expect("k_cache", k_cache, kind, dev, (None, None, None, d))
+        _expect("v_cache", v_cache, kind, dev, shape)
+        _expect("k_scale", k_scale, _F32, dev, (shape[0], None, shape[2]))
+        _expect("v_scale", v_scale, _F32, dev, scales)
+        _expect("page_table", page_table, _I32, dev, (batch, None))
+    blocks, ps = scales[1], shape[1]
     if blocks < 1 or ps % blocks:
         raise TypeError(f"k_scale has {blocks} blocks a page, which must divide its {ps} tokens")
-    if page_table.dim() != 2 or not _is(page_table, _I32, dev, (batch, page_table.shape[1])):
-        _expect("page_table", page_table, _I32, dev, (batch, None))
-    return npages, ps, hkv, d, page_table.shape[1], ps // blocks, fmt
+    return shape[0], ps, shape[2], shape[3], table[1], ps // blocks, fmt
 
 
 def _expect_i32(name, t, dev, n=None):
-    if t.dim() != 1 or not _is(t, _I32, dev, (t.shape[0] if n is None else n,)):
+    """A (n,) int32 tensor (n None: of any length); returns its length."""
+    shape = t.shape
+    if len(shape) != 1 or (n is not None and shape[0] != n) or not _is(t, _I32, dev, shape):
         _expect(name, t, _I32, dev, (n,))
-    return t.shape[0]
+    return shape[0]
 
 
 def attn_sink_kv_append_q8(k_new, v_new, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, cu_new=None,
@@ -115,14 +116,23 @@ def attn_sink_fwd_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu
     return out, lse
 
 
-def _expect_probs(name, t, dtype, dev, shape):
-    """A (rows, vocab) matrix with contiguous rows; returns its row stride."""
-    if t.dtype != dtype or t.get_device() != dev or t.dim() != 2 or t.shape != shape:
-        _expect(name, t, dtype, dev, shape, contiguous=False)
+def _row_stride(name, t):
+    """Row stride of a (rows, vocab) matrix with contiguous rows (0: contiguous)."""
+    if t.is_contiguous():
+        return 0
     rows, vocab = t.shape
     if vocab > 1 and t.stride(1) != 1 or rows > 1 and t.stride(0) < vocab:
         raise TypeError(f"{name}: a row's probabilities must be contiguous and rows must not overlap")
     return t.stride(0) if rows > 1 else 0
+
+
+def _output(name, t, like, shape, dev, stream):
+    """An int32 output: checked, or made on the device of `like`."""
+    if t is None:
+        return like.new_empty(shape) if stream is None else _made(stream, like.new_empty, shape)
+    if not _is(t, _I32, dev, shape):
+        _expect(name, t, _I32, dev, shape)
+    return t
 
 
 def attn_sink_verify_draft(target, tokens, parents, cu_seqlens, u, u_next, max_nodes, draft=None, base=None, src=None,
@@ -136,62 +146,74 @@ def attn_sink_verify_draft(target, tokens, parents, cu_seqlens, u, u_next, max_n
     stand as base[b] + index, -1 behind (attn_sink_kv_compact's src and counts, with base the
     prefix's length), their number, and the token that follows them."""
     dev = _device("target", target)
-    dtype = _TYPES.get(target.dtype)
+    kind, shape = target.dtype, target.shape
+    dtype = _TYPES.get(kind)
     if dtype is None:
-        raise TypeError(f"target must be torch.float32, torch.bfloat16 or torch.float16, got {target.dtype}")
-    shape = target.shape if target.dim() == 2 else (None, None)
-    p_rs = _expect_probs("target", target, target.dtype, dev, shape)
+        raise TypeError(f"target must be torch.float32, torch.bfloat16 or torch.float16, got {kind}")
+    if len(shape) != 2:
+        _expect("target", target, kind, dev, (None, None))
     T, vocab = shape
+    p_rs = _row_stride("target", target)
     q_rs, qp = 0, None
     if draft is not None:
-        q_rs, qp = _expect_probs("draft", draft, target.dtype, dev, shape), draft.data_ptr()
+        if draft.dtype != kind or draft.shape != shape or draft.get_device() != dev:
+            _expect("draft", draft, kind, dev, tuple(shape), contiguous=False)
+        q_rs, qp = _row_stride("draft", draft), draft.data_ptr()
     B = _expect_i32("cu_seqlens", cu_seqlens, dev) - 1
     if B < 0:
         raise TypeError("cu_seqlens must have a number more than there are requests")
     _expect_i32("tokens", tokens, dev, T)
+    up = bp = None
     if parents is not None:
         _expect_i32("parents", parents, dev, T)
+        up = parents.data_ptr()
     if base is not None:
         _expect_i32("base", base, dev, B)
-    for name, t, n in (("u", u, T), ("u_next", u_next, B)):
-        if not _is(t, _F32, dev, (n,)):
-            _expect(name, t, _F32, dev, (n,))
+        bp = base.data_ptr()
+    if not _is(u, _F32, dev, (T,)):
+        _expect("u", u, _F32, dev, (T,))
+    if not _is(u_next, _F32, dev, (B,)):
+        _expect("u_next", u_next, _F32, dev, (B,))
     max_nodes = int(max_nodes)
-    made = []
-    for name, t, want in (("src", src, (B, max(max_nodes, 0))), ("counts", counts, (B,)),
-                          ("next_tokens", next_tokens, (B,))):
-        if t is None:
-            t = _made(stream, torch.empty, want, dtype=_I32, device=target.device)
-        elif not _is(t, _I32, dev, want):
-            _expect(name, t, _I32, dev, want)
-        made.append(t)
-    _run("attn_sink_verify_draft", dev, stream, target.data_ptr(), qp, p_rs, q_rs, dtype, tokens.data_ptr(),
-         None if parents is None else parents.data_ptr(), cu_seqlens.data_ptr(), u.data_ptr(), u_next.data_ptr(),
-         None if base is None else base.data_ptr(), B, T, max_nodes, vocab, *(t.data_ptr() for t in made))
-    return tuple(made)
+    src = _output("src", src, tokens, (B, max(max_nodes, 0)), dev, stream)
+    counts = _output("counts", counts, tokens, (B,), dev, stream)
+    next_tokens = _output("next_tokens", next_tokens, tokens, (B,), dev, stream)
+    _run("attn_sink_verify_draft", dev, stream, target.data_ptr(), qp, p_rs, q_rs, dtype, tokens.data_ptr(), up,
+         cu_seqlens.data_ptr(), u.data_ptr(), u_next.data_ptr(), bp, B, T, max_nodes, vocab, src.data_ptr(),
+         counts.data_ptr(), next_tokens.data_ptr())
+    return src, counts, next_tokens
+
+
+_PTRS = [ctypes.c_void_p * n for n in range(9)]  # (a call has at most 8 tensors)
+_SIZES = [ctypes.c_longlong * n for n in range(9)]
 
 
 def _expect_pools(caches, dev, num_pages):
     """The host arrays of the tensors' addresses and page sizes."""
-    caches = (caches,) if isinstance(caches, torch.Tensor) else tuple(caches)
+    if isinstance(caches, torch.Tensor):
+        caches = (caches,)
+    ptrs, sizes = [], []
     for i, c in enumerate(caches):
-        if c.get_device() != dev or not c.is_contiguous() or c.dim() < 2 or c.shape[0] != num_pages:
-            _expect(f"caches[{i}]", c, c.dtype, dev, (num_pages,) + (None,) * max(1, c.dim() - 1))
-    n = len(caches)
-    ptrs = (ctypes.c_void_p * n)(*(c.data_ptr() for c in caches))
-    sizes = (ctypes.c_longlong * n)(*(c.nbytes // num_pages if num_pages else 0 for c in caches))
-    return ptrs, sizes, n
+        shape = c.shape
+        if len(shape) < 2 or shape[0] != num_pages or c.get_device() != dev or not c.is_contiguous():
+            _expect(f"caches[{i}]", c, c.dtype, dev, (num_pages,) + (None,) * max(1, len(shape) - 1))
+        ptrs.append(c.data_ptr())
+        sizes.append(c.nbytes // num_pages if num_pages else 0)
+    n = len(ptrs)
+    if n > 8:
+        return (ctypes.c_void_p * n)(*ptrs), (ctypes.c_longlong * n)(*sizes), n
+    return _PTRS[n](*ptrs), _SIZES[n](*sizes), n
 
 
 def _expect_table(page_table, refs, seqlens):
     """Returns (device, batch, max_pages, num_pages)."""
-    dev = _device("page_table", page_table)
-    if page_table.dim() != 2 or not _is(page_table, _I32, dev, page_table.shape):
+    dev, table, pool = _device("page_table", page_table), page_table.shape, refs.shape
+    if not (len(table) == 2 and len(pool) == 1 and _is(page_table, _I32, dev, table) and _is(refs, _I32, dev, pool)
+            and _is(seqlens, _I32, dev, table[:1])):
         _expect("page_table", page_table, _I32, dev, (None, None))
-    B, max_pages = page_table.shape
-    n = _expect_i32("refs", refs, dev)
-    _expect_i32("seqlens", seqlens, dev, B)
-    return dev, B, max_pages, n
+        _expect("refs", refs, _I32, dev, (None,))
+        _expect("seqlens", seqlens, _I32, dev, (table[0],))
+    return dev, table[0], table[1], pool[0]
 
 
 def attn_sink_pages_copy(caches, src, dst, stream=None):
@@ -215,14 +237,8 @@ def attn_sink_pages_fork(page_table, refs, seqlens, src, page_size, out_table=No
     (table (len(src), max_pages), seqlens (len(src),))."""
     dev, B, max_pages, pages = _expect_table(page_table, refs, seqlens)
     n = _expect_i32("src", src, dev)
-    if out_table is None:
-        out_table = _made(stream, torch.empty, (n, max_pages), dtype=_I32, device=page_table.device)
-    elif not _is(out_table, _I32, dev, (n, max_pages)):
-        _expect("out_table", out_table, _I32, dev, (n, max_pages))
-    if out_seqlens is None:
-        out_seqlens = _made(stream, torch.empty, (n,), dtype=_I32, device=page_table.device)
-    else:
-        _expect_i32("out_seqlens", out_seqlens, dev, n)
+    out_table = _output("out_table", out_table, page_table, (n, max_pages), dev, stream)
+    out_seqlens = _output("out_seqlens", out_seqlens, page_table, (n,), dev, stream)
     _run("attn_sink_pages_fork", dev, stream, page_table.data_ptr(), refs.data_ptr(), seqlens.data_ptr(), src.data_ptr(), B,
          n, max_pages, int(page_size), pages, out_table.data_ptr(), out_seqlens.data_ptr())
     return out_table, out_seqlens
@@ -244,10 +260,7 @@ def attn_sink_pages_reserve(caches, page_table, refs, seqlens, new_seqlens, page
     dev, B, max_pages, pages = _expect_table(page_table, refs, seqlens)
     _expect_i32("new_seqlens", new_seqlens, dev, B)
     ptrs, sizes, n = _expect_pools(caches, dev, pages)
-    if missing is None:
-        missing = _made(stream, torch.empty, (1,), dtype=_I32, device=page_table.device)
-    else:
-        _expect_i32("missing", missing, dev, 1)
+    missing = _output("missing", missing, page_table, (1,), dev, stream)
     _run("attn_sink_pages_reserve", dev, stream, ptrs, sizes, n, page_table.data_ptr(), refs.data_ptr(),
          seqlens.data_ptr(), new_seqlens.data_ptr(), B, max_pages, int(page_size), pages, missing.data_ptr())
     return missing
@@ -258,10 +271,7 @@ def attn_sink_pages_compact(caches, page_table, refs, seqlens, page_size, held=N
     Returns held (1,) int32, their number: the pages from there on are free."""
     dev, B, max_pages, pages = _expect_table(page_table, refs, seqlens)
     ptrs, sizes, n = _expect_pools(caches, dev, pages)
-    if held is None:
-        held = _made(stream, torch.empty, (1,), dtype=_I32, device=page_table.device)
-    else:
-        _expect_i32("held", held, dev, 1)
+    held = _output("held", held, page_table, (1,), dev, stream)
     _run("attn_sink_pages_compact", dev, stream, ptrs, sizes, n, page_table.data_ptr(), refs.data_ptr(),
          seqlens.data_ptr(), B, max_pages, int(page_size), pages, held.data_ptr())
     return held
