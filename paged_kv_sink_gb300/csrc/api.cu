@@ -1195,9 +1195,9 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
     int round = most >= (size_t)batch ? batch : most ? (int)most : 1;
     round = (batch + (batch + round - 1) / round - 1) / ((batch + round - 1) / round);
     const bool chain = as_chain(max_seqlen_q, hq / hkv, head_dim, causal);
-    const size_t table = ((size_t)pages * round * sizeof(int32_t) + 15) & ~size_t(15);
+    const size_t ints = (size_t)pages * round + round + (chain ? total_q : 0);  // table, lengths, parents
     Scratch ws;
-    cudaError_t e = ws.alloc(2 * cache * round + table + (chain ? (size_t)total_q * sizeof(int32_t) : 0), s);
+    cudaError_t e = ws.alloc(2 * cache * round + ints * sizeof(int32_t), s);
     if (e != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: scratch allocation");
     char* const base = static_cast<char*>(ws.ptr);
     for (int b0 = 0; b0 < batch; b0 += round) {
@@ -1213,7 +1213,8 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         x.k_out = reinterpret_cast<__nv_bfloat16*>(base);
         x.v_out = reinterpret_cast<__nv_bfloat16*>(base + cache * round);
         x.table_out = reinterpret_cast<int32_t*>(base + 2 * cache * round);
-        x.parents = chain ? reinterpret_cast<int32_t*>(base + 2 * cache * round + table) : nullptr;
+        x.lens_out = x.table_out + (size_t)pages * round;
+        x.parents = chain ? x.lens_out + round : nullptr;
         x.total_q = total_q;
         if ((e = attn::q8::launch_expand(x, s)) != cudaSuccess) return cuda_fail(e, "fwd_paged_q8: launch");
         std::string err;
@@ -1224,7 +1225,7 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
             t.v_cache = x.v_out;
             t.page_table = x.table_out;
             t.cu_q = x.cu_q;
-            t.seqlens_k = x.seqlens;
+            t.seqlens_k = x.lens_out;
             t.parents = x.parents;
             t.sink = sink;
             t.out = out;
@@ -1270,7 +1271,7 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         f.causal = causal ? 1 : 0;
         f.scale = attn::resolve_scale(scale, head_dim);
         f.page_table = x.table_out;
-        f.seqlens_k = x.seqlens;
+        f.seqlens_k = x.lens_out;
         f.max_pages = pages;
         f.page_size = attn::q8::kExpandPage;
         f.num_pages = pages * x.batch;

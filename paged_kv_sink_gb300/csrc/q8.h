@@ -51,6 +51,7 @@ struct ExpandArgs {
     __nv_bfloat16* k_out;
     __nv_bfloat16* v_out;
     int32_t* table_out;  // (batch, pages)
+    int32_t* lens_out;   // (batch,): the lengths, cut at what the table and `pages` hold
     int32_t* parents;    // (total_q,), or NULL: each row's predecessor in its request
     int total_q;
 };

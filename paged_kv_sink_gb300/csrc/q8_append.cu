@@ -289,6 +289,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs
         if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
         L = (int)cap;
     }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[b] = max(L, 0);
     const int t0 = blockIdx.x * kExpandTokens;
     if (Lq == 0 || t0 >= L) return;
     if (a.win_last > 0) {  // no row sees tokens between the first window and the first row's last one

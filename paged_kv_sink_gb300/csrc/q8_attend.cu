@@ -207,7 +207,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : 2) attend_kernel(const
 
     const Request r = request_of(p, b, tid == 0 && split == 0 && blockIdx.y == 0);
     const int row0 = tile * H, nrows = min(H, r.Lq * p.group - row0);
-    if (nrows <= 0) return;
+    if (nrows <= 0) {
+        if constexpr (gather) {  // as often as the others of the cluster
+            cg::this_cluster().sync();
+            cg::this_cluster().sync();
+        }
+        return;
+    }
     const int tok0 = kRows ? row0 / p.group : 0, tok1 = kRows ? (row0 + nrows - 1) / p.group : 0;
     const Ranges vis = tile_ranges(p, r, tok0, tok1);
     const int nvis = visible_count(vis);

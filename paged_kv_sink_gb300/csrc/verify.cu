@@ -23,7 +23,7 @@
 // Tests of single tokens are fp64.
 //
 // One cluster of CTAs per request.  Each CTA walks the tree itself (the nodes' two
-// probabilities are gathered up front) and the CTAs share the passes over a row, one
+// probabilities are gathered up front, by one of them) and the CTAs share the passes over a row, one
 // per refused child and one for the drawing, by contiguous slices of the vocabulary; the
 // slices' totals are exchanged through distributed shared memory.  Bound by the row's
 // bytes in a large batch, by latency in a small one.
@@ -44,6 +44,7 @@ namespace verify {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
+static_assert(kThreads >= kMaxNodes, "a thread per node");
 
 using u64 = unsigned long long;
 
@@ -144,18 +145,24 @@ __device__ __forceinline__ void load_batch(const typename Elem<T>::type* row, in
     }
 }
 
+// A drafted token: its parent, its number and its probabilities after the parent; first: taken, if
+// no sibling was refused before.
+struct Node {
+    int parent, token;
+    float u, px, qx;
+    int first;
+};
+
 struct Shared {
-    int token[kMaxNodes];
-    int parent[kMaxNodes];
-    float u[kMaxNodes], px[kMaxNodes], qx[kMaxNodes];
+    int n, r0;                  // nodes, the request's first row
+    Node node[kMaxNodes];
     int path[kMaxNodes];
     int gone[kMaxNodes];        // refused siblings' tokens (without draft probabilities)
-    bool first[kMaxNodes];      // taken, if no sibling was refused before
     u64 part[kWarps][kMaxBatches];  // the batches' sums of the last pass
     u64 warp[kWarps];               // the warps'
     u64 total[2][kMaxCluster];      // the CTAs'
     // what the walk stands at
-    int node, count, refused, ngone, more;
+    int at, count, refused, ngone, more;
     float s_hi, s_lo;
 };
 
@@ -274,13 +281,62 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
     const int ctas = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int b = blockIdx.x / ctas, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const int r0 = a.cu[b];
-    int n = a.cu[b + 1] - r0;
-    if (n > a.max_nodes || r0 < 0 || r0 + (long long)n > a.total) {
-        if (rank == 0 && tid == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-        n = r0 < 0 ? 0 : min(min(n, a.max_nodes), a.total - r0);
+    // What the walk goes by is read once, by the first CTA, and handed to the others: all take the
+    // same steps and meet at the same barriers, whatever else happens to the inputs meanwhile.
+    cluster.barrier_arrive();  // this CTA runs
+    if (rank == 0) {
+        const int r0 = a.cu[b];
+        int n = a.cu[b + 1] - r0;
+        if (n > a.max_nodes || r0 < 0 || r0 + (long long)n > a.total) {
+            if (tid == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+            n = r0 < 0 ? 0 : min(min(n, a.max_nodes), a.total - r0);
+        }
+        const E* const target = static_cast<const E*>(a.target) + (long long)r0 * a.target_rs;
+        const E* const draft = a.draft ? static_cast<const E*>(a.draft) + (long long)r0 * a.draft_rs : nullptr;
+        Node k = {};
+        if (tid < n) {  // (kThreads >= kMaxNodes)
+            const int i = tid;
+            int par = i - 1;
+            if (a.parents && i > 0) {
+                par = a.parents[r0 + i];
+                if (par < 0 || par >= i) {
+                    raise_status(ATTN_SINK_DEV_TREE);
+                    par = -1;
+                }
+            }
+            const int x = i > 0 ? a.tokens[r0 + i] : 0;
+            float px = 0.f, qx = 0.f;
+            if (i > 0 && par >= 0) {
+                if (x >= 0 && x < a.vocab) {
+                    px = clamp01(Elem<T>::get(target[par * a.target_rs + x]));
+                    if (draft) qx = clamp01(Elem<T>::get(draft[par * a.draft_rs + x]));
+                } else {
+                    raise_status(ATTN_SINK_DEV_PROB);
+                }
+            }
+            const float u = a.u[r0 + i];
+            k.parent = i > 0 ? par : -1;
+            k.token = x;
+            k.u = u < 0.f ? 0.f : u;
+            k.px = px;
+            k.qx = qx;
+            k.first = (draft ? (double)k.u * qx : (double)k.u) < px;
+        }
+        cluster.barrier_wait();  // and so do the others
+        for (int c = 0; c < ctas; ++c) {
+            Shared* const to = cluster.map_shared_rank(&S, c);
+            if (tid < n) to->node[tid] = k;
+            if (tid == 0) {
+                to->n = n;
+                to->r0 = r0;
+            }
+        }
+    } else {
+        cluster.barrier_wait();
     }
-    if (n <= 0) {  // the whole cluster
+    cluster.sync();
+    const int n = S.n, first_row = S.r0;
+    if (n <= 0) {
         if (rank == 0) {
             for (int j = tid; j < a.max_nodes; j += kThreads) a.src[(size_t)b * a.max_nodes + j] = -1;
             if (tid == 0) {
@@ -290,36 +346,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
         }
         return;
     }
-    const E* const target = static_cast<const E*>(a.target) + (long long)r0 * a.target_rs;
-    const E* const draft = a.draft ? static_cast<const E*>(a.draft) + (long long)r0 * a.draft_rs : nullptr;
-    for (int i = tid; i < n; i += kThreads) {
-        int par = i - 1;
-        if (a.parents && i > 0) {
-            par = a.parents[r0 + i];
-            if (par < 0 || par >= i) {
-                if (rank == 0) raise_status(ATTN_SINK_DEV_TREE);
-                par = -1;
-            }
-        }
-        const int x = i > 0 ? a.tokens[r0 + i] : 0;
-        float px = 0.f, qx = 0.f;
-        if (i > 0 && par >= 0) {
-            if (x >= 0 && x < a.vocab) {
-                px = clamp01(Elem<T>::get(target[par * a.target_rs + x]));
-                if (draft) qx = clamp01(Elem<T>::get(draft[par * a.draft_rs + x]));
-            } else if (rank == 0) {
-                raise_status(ATTN_SINK_DEV_PROB);
-            }
-        }
-        S.parent[i] = i > 0 ? par : -1;
-        S.token[i] = x;
-        const float u = a.u[r0 + i];
-        S.u[i] = u < 0.f ? 0.f : u;
-        S.px[i] = px;
-        S.qx[i] = qx;
-        S.first[i] = (draft ? (double)S.u[i] * qx : (double)S.u[i]) < px;
-    }
-    __syncthreads();
+    const E* const target = static_cast<const E*>(a.target) + (long long)first_row * a.target_rs;
+    const E* const draft = a.draft ? static_cast<const E*>(a.draft) + (long long)first_row * a.draft_rs : nullptr;
 
     // One pass over the slices: the sum over the cluster of what `w` leaves of a node's row,
     // less the tokens in S.gone; the batches' and warps' sums stay in S.part and S.warp, the CTAs'
@@ -371,29 +399,28 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
     double cover = 0.0, mass = 1.0;
     u64 sum = 0;
     Cover w = {0, 0.f, 0.f};
-    cluster.sync();  // every CTA of the cluster runs before its shared memory is written
     for (;;) {
         if (warp == 0) {
             if (lane == 0 && count == 1) S.path[0] = 0;
             bool more = false;  // a child was refused: what is left of the row has to be summed
             while (scanned < n && !more) {
                 const int i = scanned + lane;
-                const uint32_t kids = __ballot_sync(0xffffffffu, i < n && S.parent[i] == node);
+                const uint32_t kids = __ballot_sync(0xffffffffu, i < n && S.node[i].parent == node);
                 if (!kids) {
                     scanned += 32;
                     continue;
                 }
                 const int c = scanned + __ffs(kids) - 1;
                 scanned = c + 1;
-                const double px = S.px[c], u = S.u[c];
+                const double px = S.node[c].px, u = S.node[c].u;
                 bool take, again = false;
                 if (refused + ngone == 0) {
-                    take = S.first[c];
+                    take = S.node[c].first;
                 } else if (draft) {
-                    const double qx = S.qx[c];
+                    const double qx = S.node[c].qx;
                     take = u * qx * mass < fmax(px - cover * qx, 0.0);
                 } else {  // a token that a sibling has lost is not there again
-                    for (int j = lane; j < ngone; j += 32) again |= S.gone[j] == S.token[c];
+                    for (int j = lane; j < ngone; j += 32) again |= S.gone[j] == S.node[c].token;
                     again = __any_sync(0xffffffffu, again);
                     take = !again && u * mass < px;
                 }
@@ -408,15 +435,15 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
                     ++refused;
                     cover += mass;
                     more = true;
-                } else if (!again && S.token[c] >= 0 && S.token[c] < a.vocab) {
-                    if (lane == 0) S.gone[ngone] = S.token[c];
+                } else if (!again && S.node[c].token >= 0 && S.node[c].token < a.vocab) {
+                    if (lane == 0) S.gone[ngone] = S.node[c].token;
                     ++ngone;
                     mass = fmax(mass - px, 0.0);
                 }
                 __syncwarp();
             }
             if (lane == 0) {
-                S.node = node;
+                S.at = node;
                 S.count = count;
                 S.refused = refused;
                 S.ngone = ngone;
@@ -429,14 +456,14 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
         const bool more = S.more;
         if (!more && S.refused > 0) break;  // the last pass's weights are those to draw from
         w = {S.refused < 2 ? S.refused : 2, S.s_hi, S.s_lo};
-        sum = sum_row(S.node, w, S.ngone);
+        sum = sum_row(S.at, w, S.ngone);
         if (!more) break;
         mass = (double)sum * 0x1p-44;
     }
     int nout = S.ngone;
     if (sum == 0 && (w.k || nout)) {  // nothing is left: the target's own row
         w.k = nout = 0;
-        sum = sum_row(S.node, w, 0);
+        sum = sum_row(S.at, w, 0);
     }
 
     if (rank == 0) {
@@ -464,8 +491,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const Args a) {
         left -= S.warp[i];
     }
     if (left >= S.warp[warp]) return;
-    const E* const pr = row_at(target, a.target_rs, S.node);
-    const E* const qr = w.k ? row_at(draft, a.draft_rs, S.node) : pr;
+    const E* const pr = row_at(target, a.target_rs, S.at);
+    const E* const qr = w.k ? row_at(draft, a.draft_rs, S.at) : pr;
     const Slice sl = slice_of<E>(pr, qr, a.vocab, ctas, rank * kWarps + warp);
     int j = 0;
     for (; left >= S.part[warp][j]; ++j) left -= S.part[warp][j];

@@ -382,6 +382,25 @@ def test_extend_leaves_other_rows_alone(ext, n, hq):
     assert torch.all(out[n:n + 2] == 0) and torch.all(lse[:, n:n + 2] == float("-inf"))
 
 
+@pytest.mark.parametrize("n", [5, 40, 60])
+def test_extend_of_more_tokens_than_the_table_holds(ext, n):
+    """Lengths are cut at the table's 48 tokens (which end inside a tile) and reported, in all forms:
+    the row kernel, a chain and the forward."""
+    c = Cache([48, 48], 1, 64, 16, 16, "e4m3", seed=31)
+    c.table = c.table[:, :3].contiguous()
+    hq = 8
+    q = torch.randn(2 * n, hq, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    junk = torch.full((64 << 20,), float("nan"), device="cuda")  # (memory that a later allocation may find)
+    del junk
+    ext.device_status()
+    out, lse = ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu([n, n]).cuda(), torch.tensor([60, 48]).int().cuda(), n, 64)
+    assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
+    for b in range(2):
+        k, v = c.tokens(b)
+        rows = slice(b * n, (b + 1) * n)
+        check(out[rows].cpu(), lse[:, rows].cpu(), q[rows], k, v, so.chunk_seen(48, n), None, 2.0 ** -8)
+
+
 def test_expanded_batches_go_in_rounds(ext):
     """A length bound far above the lengths: scratch stays at 2 GiB and a little, results the same.
     (140 rows a request: the expanding form whatever the bound; fewer may go either way by it.)"""
