@@ -16,7 +16,9 @@
 //    i-th free page among them.
 // reserve and compact decide in one cluster of CTAs, which scan the counts by slices and
 // meet at the cluster's barrier; the pages are then moved by a grid of its own, which reads the
-// list from the device.  The decisions are bound by latency, the moves by HBM.
+// list from the device.  The decisions are bound by latency (reserve 10 to 16 us for 4 and 512
+// requests, compact 10 and 15 for pools of 826 and 47k pages), the moves by HBM (9.9k pages of 16 KB in K
+// and V, 650 MB read and written: 97 us, the copy's rate).
 #include "pages.h"
 
 #include <cooperative_groups.h>

@@ -27,7 +27,11 @@
 //  * The splits are merged in the log-sum-exp sense and the sink is folded in once: by the
 //    cluster that they form, through distributed shared memory, where a row has at most 8,
 //    by attend_combine_kernel where it has more.
-// Bound by HBM: half the bytes of the bf16 cache.
+// Bound by HBM: half the bytes of the bf16 cache.  64 requests of 1k to 32k tokens, 64 query
+// heads over 8 of 64 (1.2 GB): 207 us, of which the split grid has 200 (6.0 TB/s; the copy's rate is
+// 6.8); 32 windows of 8192 tokens, 32 over 8 of 128 (0.54 GB): 97 us.  24 warps an SM at d 64
+// (80 registers, 38 KB a CTA), 12 at d 128: more warps were worth more than more bytes in
+// flight (a third stage of the ring: 222 us).
 #include "q8.cuh"
 
 #include <cooperative_groups.h>
@@ -574,10 +578,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : 2) attend_kernel(const
     }
 }
 
-// One block per (query head, new token, request).
+// One block per (query head, new token, request): its warps take the splits in turn, 4 in flight, a lane
+// D / 32 dims.
 template <int D, int NT>
-__global__ void __launch_bounds__(D) attend_combine_kernel(const Params p) {
-    const int head = blockIdx.x, tok = blockIdx.y, b = blockIdx.z, dd = threadIdx.x;
+__global__ void __launch_bounds__(128) attend_combine_kernel(const Params p) {
+    constexpr int N = D / 32, kW = 4;
+    __shared__ float sm[kW][D + 2];
+    const int head = blockIdx.x, tok = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Request r = request_of(p, b, false);
     if (tok >= r.Lq) return;
     // the splits of the row's tile
@@ -587,20 +594,59 @@ __global__ void __launch_bounds__(D) attend_combine_kernel(const Params p) {
     const int nsplit = (int)(((long long)nvis + p.split_tokens - 1) / p.split_tokens);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t row = (size_t)(r.q_start + tok) * p.hq + head, base = row * p.max_splits;
+    float M = -INFINITY, Z = 0.f, acc[N] = {};
+    for (int s0 = warp; s0 < nsplit; s0 += 4 * kW) {
+        float2 ml[4];
+        float o[4][N];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s = s0 + i * kW;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (s < nsplit) {
+                ml[i] = p.part_ml[base + s];
+#pragma unroll
+                for (int k = 0; k < N; ++k) o[i][k] = p.part_o[(base + s) * D + lane * N + k];
+            }
+        }
+        const float m = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
+        const float ref = m == -INFINITY ? 0.f : m, g = half_factor(M - ref);
+        M = m;
+        Z *= g * g;
+#pragma unroll
+        for (int k = 0; k < N; ++k) acc[k] *= g * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (s0 + i * kW < nsplit) {
+                const float f = half_factor(ml[i].x - ref);
+                Z += ml[i].y * f * f;
+#pragma unroll
+                for (int k = 0; k < N; ++k) acc[k] += o[i][k] * f * f;
+            }
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) sm[warp][lane * N + k] = acc[k];
+    if (lane == 0) {
+        sm[warp][D] = M;
+        sm[warp][D + 1] = Z;
+    }
+    __syncthreads();
+    const int dd = threadIdx.x;
+    if (dd >= D) return;
     const float sg = p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
-    float M = sg;
-    for (int s = 0; s < nsplit; ++s) M = fmaxf(M, p.part_ml[base + s].x);
+    M = sg;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, sm[w][D]);
     const float ref = M == -INFINITY ? 0.f : M;
-    float Z = fast_exp2(sg - ref), acc = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < nsplit; ++s) {
-        const float2 ml = p.part_ml[base + s];
-        const float f = half_factor(ml.x - ref);
-        Z += ml.y * f * f;
-        acc += p.part_o[(base + s) * D + dd] * f * f;
+    Z = fast_exp2(sg - ref);
+    float a = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        const float f = half_factor(sm[w][D] - ref);
+        Z += sm[w][D + 1] * f * f;
+        a += sm[w][dd] * f * f;
     }
     float lse;
-    p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, acc, lse));
+    p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, a, lse));
     if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
 }
 
@@ -694,7 +740,7 @@ static cudaError_t run_form(const Params& p, const AttendArgs& a, const AttendPl
     if constexpr (gather) return cudaGetLastError();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.hq, a.max_q, a.batch);
-    cfg.blockDim = dim3(D);
+    cfg.blockDim = dim3(128);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
