@@ -1053,10 +1053,10 @@ int run_attend_q8(const char* who, const attn::q8::AttendArgs& a, const attn::q8
 
 // Which kernels compute new tokens over an 8-bit cache, by what a request has at most (n new tokens,
 // g query heads of a KV head; times of 16 requests of 1k to 16k tokens, 8 KV heads):
-//  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 144 us, chain
-//    149; 16: 266, chain 155), 32 at 128 (16 rows: 90, chain 260; 64: 319, chain 270), and up
+//  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 146 us, chain
+//    149; 16: 266, chain 152), 32 at 128 (16 rows: 88, chain 260; 64: 319, chain 285), and up
 //    to four times as many where its CTAs are all resident at once (one request of 2000 tokens,
-//    128 rows: 16.5 us, chain 27; 256: 28.8, chain 31);
+//    128 rows: 14.4 us, chain 27; 256: 18.5, chain 31);
 //  * else, on the tokens expanded to bf16, the kernel of drafted trees on a chain, whose tiles hold
 //    (token, head) rows, up to 48 tokens at head dim 64 (32 tokens: 190 us, forward 403; 64 of 4
 //    requests: 79, forward 74), 96 at 128 (64: 89, forward 122; 128: 137, forward 127), g > 1;

@@ -8,7 +8,7 @@
 // their block of tokens and KV head.
 //
 // Structure: one CTA per (split of visible tokens, KV head and row tile, request); the
-// rows of a tile are (new token, query head of the KV group) pairs, 8 to 32 of them.
+// rows of a tile are (new token, query head of the KV group) pairs, 8 or 16 of them.
 //  * Each of the four warps streams 32-token chunks of its own through a ring of
 //    shared-memory stages (16-byte cp.async gathers through the page table), so that
 //    nothing but the end of the split brings the warps together.
@@ -195,7 +195,7 @@ struct Smem {
 // kRows: several new tokens, so that rows see different tokens.  gather: the splits are one
 // cluster, which merges them itself.
 template <int D, int NT, int STAGES, int F, bool kRows, bool gather>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : 2) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : D == 64 ? 4 : 3) attend_kernel(const Params p) {
     using SM = Smem<D, STAGES>;
     extern __shared__ __align__(128) uint8_t smem[];
     constexpr int H = 8 * NT;
@@ -662,22 +662,26 @@ AttendPlan make_plan(const AttendArgs& a) {
     AttendPlan pl;
     const int group = a.hq / a.c.hkv;
     const long long rows = (long long)group * a.max_q;
-    // 32 rows a tile at d 64; at d 128 their accumulators would not fit the registers
-    pl.nt = rows <= 8 ? 1 : rows <= 16 || a.c.head_dim == 128 ? 2 : 4;
-    pl.tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
     long long nvis = max_tokens(a);
-    if (a.win_last > 0) {  // a tile's rows are at most 8 nt tokens apart
-        const long long w = (long long)a.win_first + a.win_last + (a.max_q > 1 ? 8 * pl.nt : 0);
+    if (a.win_last > 0) {  // a tile's rows are at most 16 tokens apart
+        const long long w = (long long)a.win_first + a.win_last + (a.max_q > 1 ? 16 : 0);
         nvis = w < nvis ? w : nvis;
     }
     if (nvis < 1) nvis = 1;
+    // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
+    // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
+    // 85 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92).
+    const long long kv = (long long)a.batch * a.c.hkv, most8 = (long long)num_sms() * (a.c.head_dim == 64 ? 6 : 3);
+    const long long least = (nvis + 255) / 256;
+    pl.nt = rows <= 8 || (rows <= 4096 && least <= kGather && kv * ((rows + 7) / 8) * least <= most8) ? 1 : 2;
+    pl.tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
     // Splits of 256 to 2048 tokens, in steps of what the CTA's warps take at once: those for which the
     // waves of resident CTAs are shortest, a CTA's start and end counted as kStart tokens
     // (64 requests of 1k to 32k tokens at d 128, 1024 a split: 402 us, 2048: 385; 32 windows of 8192,
     // 4 and 8 splits: 107 us, 5: 99).
     constexpr int kStep = kWarps * kTokens, kStart = 128, kLeast = 256, kMost = 2048;
-    const long long units = (long long)a.batch * a.c.hkv * pl.tiles;
-    const long long slots = (long long)num_sms() * (pl.nt > 1 ? 2 : a.c.head_dim == 64 ? 6 : 3);
+    const long long units = kv * pl.tiles;
+    const long long slots = pl.nt == 1 ? most8 : (long long)num_sms() * (a.c.head_dim == 64 ? 4 : 3);
     long long best = -1;
     for (int sp = kMost; sp >= kLeast; sp -= kStep) {
         const long long n = (nvis + sp - 1) / sp, waves = (units * n + slots - 1) / slots, cost = waves * (sp + kStart);
@@ -759,8 +763,6 @@ template <int D, int F>
 static cudaError_t pick(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
     const bool rows = a.max_q > 1 || !a.causal;
     if (pl.nt == 1) return rows ? run<D, 1, F, true>(p, a, pl, s) : run<D, 1, F, false>(p, a, pl, s);
-    if constexpr (D == 64)
-        if (pl.nt == 4) return rows ? run<D, 4, F, true>(p, a, pl, s) : run<D, 4, F, false>(p, a, pl, s);
     return rows ? run<D, 2, F, true>(p, a, pl, s) : run<D, 2, F, false>(p, a, pl, s);
 }
 
