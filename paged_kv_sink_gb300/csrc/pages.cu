@@ -215,6 +215,7 @@ __device__ __forceinline__ Growth growth_of(const Table& t, const int32_t* seqle
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     reserve_kernel(const Table t, const int32_t* seqlens, const int32_t* new_seqlens, int32_t* missing, void* scratch) {
     __shared__ u64 warps[32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
     const ReserveScratch s(scratch, t);
@@ -344,6 +345,7 @@ struct CompactScratch {
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     compact_kernel(const Table t, int32_t* held, void* scratch) {
     __shared__ u64 warps[32];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
     const CompactScratch s(scratch, t);
@@ -471,12 +473,14 @@ __device__ __forceinline__ void copy_pages(const Pools& p, const int32_t* src, c
 
 __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const int32_t* src, const int32_t* dst,
                                                             const int32_t* count, int n, int num_pages, bool report) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the list is complete (launched behind reserve_kernel)
     copy_pages(p, src, dst, count ? min(n, *count) : n, num_pages, report);
 }
 
 // What follows compact_kernel: the table's entries and the pages.
 __global__ void __launch_bounds__(kCopyThreads) move_kernel(const Pools p, const Table t, const int32_t* seqlens, void* scratch) {
     const CompactScratch s(scratch, t);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the decisions are complete
     retarget(t, seqlens, s.to, s.head[1]);
     if (p.count) copy_pages(p, s.src, s.dst, s.head[0], t.num_pages, false);
 }
@@ -497,6 +501,23 @@ static Pools with_pieces(const Pools& p) {
 // 8 CTAs of 256 threads an SM: all that are resident at once.
 static int resident_ctas() { return 8 * num_sms(); }
 
+// A grid of copies; `early`: as a programmatic dependent of the deciding kernel before it, whose
+// end it waits for itself.
+template <class Kernel, class... Args>
+static cudaError_t launch_behind(unsigned grid, bool early, cudaStream_t s, Kernel kernel, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 cudaError_t launch_copy(const Pools& p, const int32_t* src, const int32_t* dst, const int32_t* count, int n, int num_pages,
                         bool report, cudaStream_t s) {
     const Pools q = with_pieces(p);
@@ -505,8 +526,8 @@ cudaError_t launch_copy(const Pools& p, const int32_t* src, const int32_t* dst, 
     if (n <= 0 || pieces == 0) return cudaSuccess;
     if (pieces > INT_MAX / 2) return cudaErrorInvalidConfiguration;
     const long long want = n * pieces, most = resident_ctas();
-    copy_kernel<<<(unsigned)(want < most ? want : most), kCopyThreads, 0, s>>>(q, src, dst, count, n, num_pages, report);
-    return cudaGetLastError();
+    return launch_behind((unsigned)(want < most ? want : most), count != nullptr, s, copy_kernel, q, src, dst, count, n,
+                         num_pages, report);
 }
 
 cudaError_t launch_fork(const Table& t, const int32_t* seqlens, const int32_t* src, int out_batch, int32_t* out_table,
@@ -545,8 +566,7 @@ cudaError_t launch_compact(const Pools& p, const Table& t, const int32_t* seqlen
     const long long want = t.num_pages * (pieces > 0 ? pieces : 1), rows = ((long long)t.batch * kRowParts + 7) / 8;
     long long grid = want > rows ? want : rows;
     if (grid > resident_ctas()) grid = resident_ctas();
-    move_kernel<<<(unsigned)grid, kCopyThreads, 0, s>>>(q, t, seqlens, scratch);
-    return cudaGetLastError();
+    return launch_behind((unsigned)grid, true, s, move_kernel, q, t, seqlens, scratch);
 }
 
 ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
