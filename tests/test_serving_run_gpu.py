@@ -305,3 +305,57 @@ def test_a_forked_stream_inside_a_capture(ext, name):
         torch.cuda.synchronize()
         for a, b in zip(got + list(state), want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_calls_on_two_streams_at_once(ext, name):
+    """Calls that run side by side share nothing: each has the outputs and effects that it has alone."""
+    made = [one_call(ext, name, seed) for seed in (5, 6)]
+    before = [[t.clone() for t in state] for _, state in made]
+    want = []
+    for call, state in made:
+        want.append([t.clone() for t in call(None)] + [t.clone() for t in state])
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(10):
+        for (_, state), old in zip(made, before):
+            for t, b in zip(state, old):
+                t.view(torch.uint8).copy_(b.view(torch.uint8))
+        torch.cuda.synchronize()
+        got = []
+        for (call, state), st in zip(made, streams):
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(200_000)
+            got.append((call(st), state))
+        torch.cuda.synchronize()
+        for (out, state), w in zip(got, want):
+            for a, b in zip(list(out) + list(state), w):
+                assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    assert ext.device_status() == 0
+
+
+def test_two_graphs_replayed_side_by_side(ext):
+    """Graphs that were captured from the same calls have scratch of their own."""
+    made = [one_call(ext, name, seed) for seed, name in enumerate(("many", "decode", "reserve", "few"), 7)]
+    want = [[t.clone() for t in call(None)] for call, _ in made]
+    before = [[t.clone() for t in state] for _, state in made]
+    graphs = []
+    for (call, state), old in zip(made, before):
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(None)
+        graphs.append((g, out))
+    # (reserve gives pages once: what it finds the second time needs none)
+    for (_, state), old in zip(made, before):
+        for t, b in zip(state, old):
+            t.view(torch.uint8).copy_(b.view(torch.uint8))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (g, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, out), w in zip(graphs, want):
+        for a, b in zip(out, w):
+            assert torch.equal(a, b) or same(a, b)
