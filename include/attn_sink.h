@@ -48,7 +48,8 @@
  *    are caught on the device: the offending load is skipped and a sticky
  *    device status is set, which attn_sink_device_status() reports.
  *  - One call takes at most 65535 requests (batch) in the forward, paged
- *    forward, decode, append, tree, compaction, eviction, verification and page entry points, and at most 65535 * 128 query
+ *    forward, decode, append, tree, compaction, eviction, verification and page entry points,
+ *    and at most 65535 * 128 query
  *    rows per request in the forward ones (each is one grid dimension of the
  *    launch); larger calls return ATTN_SINK_ERR_UNSUPPORTED.
  */
@@ -546,8 +547,9 @@ enum { ATTN_SINK_F32 = 0, ATTN_SINK_BF16 = 1, ATTN_SINK_F16 = 2 };
  *     the tokens that the block has are scaled down by the quotient and rounded again.
  * Infinities become the largest code of their sign, NaN 0; both set
  * ATTN_SINK_DEV_VALUE and do not count for the scale.  Codes behind the last token of a
- * block are left as they were.  Pages that two requests share must not be written by either
- * (attn_sink_pages_reserve copies them).
+ * block are left as they were, and are rewritten with the block's scale when they are appended.
+ * Pages that two requests share must not be written by either (attn_sink_pages_reserve copies
+ * them).
  *
  *   k_new, v_new    (total_new, hkv, head_dim) bf16; *_row_stride as in attn_sink_rope
  *   cu_new          (batch+1,) int32 device, or NULL: request b's one new row is row b
@@ -563,8 +565,9 @@ int attn_sink_kv_append_q8(const attn_bf16* k_new, const attn_bf16* v_new, long 
                            void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* stream);
 
 /*
- * attn_sink_decode_paged over the 8-bit cache.  Scales may be any positive numbers (those
- * of V count as at least 2^-64), not only those that the append writes.  The products are
+ * attn_sink_decode_paged over the 8-bit cache.  Scales may be any positive finite numbers
+ * (those of V count as at least 2^-64), not only those that the append writes; the codes of a
+ * request's tokens have to be numbers (the append writes no NaN).  The products are
  * fp16 with fp32 accumulation, in which both formats are exact: q enters them off by at
  * most 2^-25 of its row's largest magnitude, the weights by at most 2^-11 of each, and
  * weights below 2^-31 of the largest (times its V scale) are lost; scores, sums and
@@ -586,11 +589,15 @@ int attn_sink_decode_paged_q8(const attn_bf16* q, const void* k_cache, const voi
  * attn_sink_fwd_paged over the 8-bit cache (which has the chunk's tokens already:
  * attn_sink_kv_append_q8).  Few rows (max_seqlen_q * hq / hkv small: drafts in a row) are
  * computed from the codes as in attn_sink_decode_paged_q8.  For more, the visible tokens
- * are expanded to bf16, exactly, in scratch of 4 hkv head_dim bytes per request and token
+ * are expanded to bf16 (exactly, where the scales are powers of two, as the append writes them;
+ * else rounded to it) in scratch of 4 hkv head_dim bytes per request and token
  * of max_seqlen_k, at most 2 GiB at a time (or one request's; larger batches in rounds of
- * requests), and read by the forward's kernel.  What rows that see a token behind an out-of-range
- * page id get is not defined; nothing outside the cache is read.
- *   max_seqlen_k  host upper bound of seqlens_k, which must hold
+ * requests), and read by the kernel of attn_sink_tree_paged (as a chain) or of
+ * attn_sink_fwd_paged, with their rounding of the weights to bf16 (2^-8).  Position i of a
+ * request's n rows is seqlens_k - n + i; rows before position 0 see nothing.  What rows that see
+ * a token behind an out-of-range page id get is not defined; nothing outside the cache is read.
+ *   max_seqlen_k  host upper bound of seqlens_k, which must hold (it sizes scratch and launches;
+ *                 no memory behind the page table or the scratch is read where it does not)
  *   lse           (hq, total_q) fp32; may be NULL
  * Supported: head_dim 64 or 128; hq % hkv == 0; any page size.
  */
@@ -700,7 +707,8 @@ int attn_sink_pages_reserve(void* const* pools, const long long* page_bytes, int
 /*
  * Brings the n held pages to the front: the i-th held page behind the first n goes to the i-th
  * free page among them, in all tensors, in the rows' entries and in refs.  The pages from n on are
- * free then.
+ * free then.  Every entry that holds a page has to be in the given table: a page that is only
+ * counted moves too, and who else remembers its number loses it.
  *   held     (1,) int32: n
  */
 int attn_sink_pages_compact(void* const* pools, const long long* page_bytes, int num_pools,

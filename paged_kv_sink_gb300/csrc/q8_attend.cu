@@ -105,7 +105,6 @@ __device__ __forceinline__ Ranges tile_ranges(const Params& p, const Request& r,
     return v;
 }
 
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
@@ -586,7 +585,10 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(const Params p) {
     __shared__ float sm[kW][D + 2];
     const int head = blockIdx.x, tok = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Request r = request_of(p, b, false);
-    if (tok >= r.Lq) return;
+    if (tok >= r.Lq) {  // (no grid behind this one starts before attend_kernel has ended)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     // the splits of the row's tile
     const int x = tok * p.group + head % p.group, row0 = x / (8 * NT) * (8 * NT);
     const int last = min(row0 + 8 * NT, r.Lq * p.group) - 1;
