@@ -407,22 +407,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : D == 64 ? 4 : 3) atten
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float y[2][4];
-            bool over = false;
 #pragma unroll
-            for (int col = 0; col < 2; ++col) {
+            for (int col = 0; col < 2; ++col)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    // (tokens without weight have codes of 0 and a log2 vs of -inf)
+                for (int i = 0; i < 4; ++i)  // (tokens without weight have codes of 0 and a log2 vs of -inf)
                     y[col][i] = fmaf(x[i >> 1][nt][(i & 1) * 2 + col], tk[i].x * factor[nt][col], tk[i].y);
-                    if constexpr (kRows)
-                        if (!full) {
+            if constexpr (kRows)
+                if (!full) {  // (apart: inside the loop above it would be carried as selects)
+#pragma unroll
+                    for (int col = 0; col < 2; ++col)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
                             const int t = __float_as_int(tk[i].w), last = seen_to[nt][col];
                             if (t > last || (p.win_last > 0 && t >= p.win_first && t <= last - p.win_last))
                                 y[col][i] = -INFINITY;
                         }
                 }
+            bool over = false;
+#pragma unroll
+            for (int col = 0; col < 2; ++col)
                 over |= fmaxf(fmaxf(y[col][0], y[col][1]), fmaxf(y[col][2], y[col][3])) > ref[nt][col] + (kHead + kSlack);
-            }
             // the reference follows the maximum where a weight would pass 2^(kHead + kSlack)
             if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -672,7 +676,8 @@ AttendPlan make_plan(const AttendArgs& a) {
     if (nvis < 1) nvis = 1;
     // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
     // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
-    // 85 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92).
+    // 81 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
+    // share chunks converted once in shared memory, 102, and of 64 rows, 8 tokens, 141 against 139).
     const long long kv = (long long)a.batch * a.c.hkv, most8 = (long long)num_sms() * (a.c.head_dim == 64 ? 6 : 3);
     const long long least = (nvis + 255) / 256;
     pl.nt = rows <= 8 || (rows <= 4096 && least <= kGather && kv * ((rows + 7) / 8) * least <= most8) ? 1 : 2;
