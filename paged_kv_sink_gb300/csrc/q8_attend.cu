@@ -677,7 +677,7 @@ AttendPlan make_plan(const AttendArgs& a) {
     // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
     // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
     // 81 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
-    // share chunks converted once in shared memory, 102, and of 64 rows, 8 tokens, 141 against 139).
+    // share chunks converted once in shared memory, 100).
     const long long kv = (long long)a.batch * a.c.hkv, most8 = (long long)num_sms() * (a.c.head_dim == 64 ? 6 : 3);
     const long long least = (nvis + 255) / 256;
     pl.nt = rows <= 8 || (rows <= 4096 && least <= kGather && kv * ((rows + 7) / 8) * least <= most8) ? 1 : 2;
