@@ -14,11 +14,11 @@
 //    other).  If the free pages do not suffice nothing is changed.
 //  * compact: the i-th held page behind the first n = (number of held pages) goes to the
 //    i-th free page among them.
-// reserve and compact decide in one cluster of CTAs, which scan the counts by slices and
-// meet at the cluster's barrier; the pages are then moved by a grid of its own, which reads the
-// list from the device.  The decisions are bound by latency (reserve 10 to 16 us for 4 and 512
-// requests, compact 10 and 15 for pools of 826 and 47k pages), the moves by HBM (9.9k pages of 16 KB in K
-// and V, 650 MB read and written: 97 us, the copy's rate).
+// reserve and compact decide in one cluster of CTAs, which scan the counts by slices, tell each
+// other their totals through distributed shared memory and meet at the cluster's barrier; the pages
+// are then moved by a grid of its own, which reads the list from the device.  The decisions are bound by latency
+// (reserve 8 and 12 us for 4 and 512 requests, compact 6 and 13 for pools of 826 and 47k pages), the moves by
+// HBM (9.9k pages of 16 KB in K and V, 650 MB read and written: 96 us, the copy's rate).
 #include "pages.h"
 
 #include <cooperative_groups.h>
@@ -158,37 +158,66 @@ __device__ __forceinline__ Span span_of(int num_pages, int rank) {
     return s;
 }
 
-// f(page, count) for the span's pages, in order.
+// f(page, whether it is held) for the span's pages, in order.
 template <class F>
-__device__ __forceinline__ void each_page(const Table& t, Span s, F f) {
+__device__ __forceinline__ void each_count(const Table& t, Span s, F f) {
     if (reinterpret_cast<uintptr_t>(t.refs) % 16 == 0) {
         int p = s.p0;
         for (; p + kPer <= s.p1; p += kPer) {
             const int4 r = *reinterpret_cast<const int4*>(t.refs + p);
-            f(p, r.x);
-            f(p + 1, r.y);
-            f(p + 2, r.z);
-            f(p + 3, r.w);
+            f(p, r.x > 0);
+            f(p + 1, r.y > 0);
+            f(p + 2, r.z > 0);
+            f(p + 3, r.w > 0);
         }
-        for (; p < s.p1; ++p) f(p, t.refs[p]);
+        for (; p < s.p1; ++p) f(p, t.refs[p] > 0);
     } else {
-        for (int p = s.p0; p < s.p1; ++p) f(p, t.refs[p]);
+        for (int p = s.p0; p < s.p1; ++p) f(p, t.refs[p] > 0);
     }
 }
 
+// The same as often as wanted: the counts of spans of up to 64 pages (pools of up to 524288)
+// are read once.
+struct Held {
+    Span span;
+    u64 mask;
+    __device__ __forceinline__ Held(const Table& t, Span s) : span(s), mask(0) {
+        if (s.p1 - s.p0 <= 64) each_count(t, s, [&](int p, bool held) { mask |= (u64)held << (p - s.p0); });
+    }
+    template <class F>
+    __device__ __forceinline__ void each(const Table& t, F f) const {
+        if (span.p1 - span.p0 <= 64) {
+            for (int p = span.p0; p < span.p1; ++p) f(p, mask >> (p - span.p0) & 1);
+        } else {
+            each_count(t, span, f);
+        }
+    }
+    __device__ __forceinline__ int count(const Table& t) const {
+        if (span.p1 - span.p0 <= 64) return __popcll(mask);
+        int n = 0;
+        each_count(t, span, [&](int, bool held) { n += held; });
+        return n;
+    }
+};
+
+// Totals of the cluster's CTAs, known to all of them after the next cluster barrier.
+__device__ __forceinline__ void tell(cg::cluster_group& cluster, u64* totals, u64 mine) {
+    if (threadIdx.x < kCtas) *cluster.map_shared_rank(totals + cluster.block_rank(), threadIdx.x) = mine;
+}
+
 // Scratch of reserve: per page the requests that are about to write into it and the last
-// of them; the free pages in order; per request its place in the free pages, and whether it
-// copies; the copies; totals.
+// of them; the free pages in order; what the requests get; the copies; totals.
 struct ReserveScratch {
-    int32_t *users, *last, *free, *offset, *src, *dst, *head;
+    int4* plan;  // per request: pages held, pages wanted, place in the free pages (top bit: copies), the page that is shared
+    int32_t *users, *last, *free, *src, *dst, *head;
     __host__ __device__ ReserveScratch(void* at, const Table& t) {
         int32_t* p = static_cast<int32_t*>(at);
-        head = p;  // [0] copies, [1] pages needed, [2..] free pages of each slice
-        users = head + 16;
+        head = p;  // [0] copies, [1] pages needed
+        plan = reinterpret_cast<int4*>(p + 16);
+        users = p + 16 + 4 * (size_t)t.batch;
         last = users + t.num_pages;
         free = last + t.num_pages;
-        offset = free + t.num_pages;  // top bit: copies
-        src = offset + t.batch;
+        src = free + t.num_pages;
         dst = src + t.batch;
     }
 };
@@ -214,13 +243,15 @@ __device__ __forceinline__ Growth growth_of(const Table& t, const int32_t* seqle
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     reserve_kernel(const Table t, const int32_t* seqlens, const int32_t* new_seqlens, int32_t* missing, void* scratch) {
-    __shared__ u64 warps[32];
+    __shared__ u64 warps[32], totals[kCtas];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
+    cluster.barrier_arrive();  // this CTA runs
     const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
     const ReserveScratch s(scratch, t);
-    const Span span = span_of(t.num_pages, rank);
-    for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
+    const int b_first = rank * kThreads + tid;
+    Growth first = {0, 0, -1};  // of request b_first; those further on are looked up again
+    for (int b = b_first; b < t.batch; b += all_threads) {
         const int L0 = seqlens[b], L1 = new_seqlens[b];
         const long long cap = (long long)t.max_pages * t.page_size;
         if (L0 < 0 || L1 > cap) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
@@ -228,18 +259,20 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         else if (L1 > L0 && L0 % t.page_size && !valid_page(t, t.table[(size_t)b * t.max_pages + L0 / t.page_size]))
             raise_status(ATTN_SINK_DEV_PAGE_OOB);
         const Growth g = growth_of(t, seqlens, new_seqlens, b);
+        if (b == b_first) first = g;
         if (g.shared >= 0) {
             s.users[g.shared] = 0;
             s.last[g.shared] = -1;
         }
     }
-    u64 mine = 0, all;
-    each_page(t, span, [&](int, int r) { mine += r <= 0 ? 1 : 0; });
-    mine = block_scan(mine, warps, all);  // this thread's first free page in the CTA's order
-    if (tid == 0) s.head[2 + rank] = (int)all;
+    const Held held(t, span_of(t.num_pages, rank));
+    u64 all;
+    const u64 mine = block_scan(held.span.p1 - held.span.p0 - held.count(t), warps, all);  // this thread's first free page in the CTA's order
+    cluster.barrier_wait();
+    tell(cluster, totals, all);
     cluster.sync();
-    for (int b = rank * kThreads + tid; b < t.batch; b += all_threads) {
-        const Growth g = growth_of(t, seqlens, new_seqlens, b);
+    for (int b = b_first; b < t.batch; b += all_threads) {
+        const Growth g = b == b_first ? first : growth_of(t, seqlens, new_seqlens, b);
         if (g.shared >= 0) {
             atomicAdd(s.users + g.shared, 1);
             atomicMax(s.last + g.shared, b);
@@ -258,11 +291,11 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             u64 n = 0;
             Growth g = {0, 0, -1};
             if (b < t.batch) {
-                g = growth_of(t, seqlens, new_seqlens, b);
+                g = b == b_first ? first : growth_of(t, seqlens, new_seqlens, b);
                 if (g.shared >= 0) {
-                    const int refs = t.refs[g.shared], users = s.users[g.shared];
+                    const int refs = t.refs[g.shared], users = s.users[g.shared], last = s.last[g.shared];
                     if (users > refs) raise_status(ATTN_SINK_DEV_POOL);
-                    copy = refs > 1 && users <= refs && !(users == refs && s.last[g.shared] == b);
+                    copy = refs > 1 && users <= refs && !(users == refs && last == b);
                 }
                 n = (u64)(g.to - g.from + (copy ? 1 : 0)) | (u64)(copy ? 1 : 0) << kCopyBit;
             }
@@ -270,7 +303,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             const u64 at = base + block_scan(n, warps, all);
             base += all;
             if (b < t.batch) {
-                s.offset[b] = (int)min(at & kNeedMask, 0x7fffffffull) | (copy ? (int)0x80000000 : 0);
+                s.plan[b] = make_int4(g.from, g.to, (int)min(at & kNeedMask, 0x7fffffffull) | (copy ? (int)0x80000000 : 0), g.shared);
                 const int c = (int)(at >> kCopyBit);
                 if (copy) {
                     s.src[c] = g.shared;
@@ -287,8 +320,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     const int need = s.head[1], copies = s.head[0];
     long long before = 0, have = 0;
     for (int c = 0; c < kCtas; ++c) {
-        if (c < rank) before += s.head[2 + c];
-        have += s.head[2 + c];
+        if (c < rank) before += (long long)totals[c];
+        have += (long long)totals[c];
     }
     const bool fits = need <= have;
     if (rank == 0 && tid == 0) {
@@ -298,8 +331,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     if (fits) {
         long long r = before + (long long)mine;
         if (r < need)
-            each_page(t, span, [&](int p, int refs) {
-                if (refs <= 0) {
+            held.each(t, [&](int p, bool is_held) {
+                if (!is_held) {
                     if (r < need) s.free[r] = p;
                     ++r;
                 }
@@ -312,92 +345,82 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     }
     const int lane = tid & 31;
     for (int b = rank * (kThreads / 32) + (tid >> 5); b < t.batch; b += all_threads / 32) {
-        const Growth g = growth_of(t, seqlens, new_seqlens, b);
-        __syncwarp();  // all lanes have read the row before it changes
-        const int o = s.offset[b] & 0x7fffffff;
-        const int copy = s.offset[b] < 0 ? 1 : 0;
+        const int4 plan = s.plan[b];
+        const int copy = plan.z < 0 ? 1 : 0, from = plan.x - copy;
+        const int32_t* const free = s.free + (plan.z & 0x7fffffff) - from;
         int32_t* const row = t.table + (size_t)b * t.max_pages;
-        for (int i = g.from - copy + lane; i < g.to; i += 32) {
-            const int p = s.free[o + i - (g.from - copy)];
+        for (int i = from + lane; i < plan.y; i += 32) {
+            const int p = free[i];
             row[i] = p;
             t.refs[p] = 1;
         }
-        if (copy && lane == 0) atomicSub(t.refs + g.shared, 1);
+        if (copy && lane == 0) atomicSub(t.refs + plan.w, 1);
     }
     for (int c = rank * kThreads + tid; c < copies; c += all_threads) {
         const int b = -1 - s.dst[c];
-        s.dst[c] = s.free[s.offset[b] & 0x7fffffff];
+        s.dst[c] = s.free[s.plan[b].z & 0x7fffffff];
     }
 }
 
-// Scratch of compact: where held pages go, the moves, totals.
+// Scratch of compact: which move a held page behind is (-1: it is free), the moves, totals.
 struct CompactScratch {
-    int32_t *to, *src, *dst, *head;
+    int32_t *move, *src, *dst, *head;
     __host__ __device__ CompactScratch(void* at, const Table& t) {
         int32_t* p = static_cast<int32_t*>(at);
-        head = p;  // [0] moves, [1] held pages, [2..] those of each CTA, [10..] free ones in front, [18..] held ones behind
-        to = head + 32;
-        src = to + t.num_pages;
+        head = p;  // [0] moves, [1] held pages
+        move = head + 16;
+        src = move + t.num_pages;
         dst = src + t.num_pages;
     }
 };
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
-    compact_kernel(const Table t, int32_t* held, void* scratch) {
-    __shared__ u64 warps[32];
+    compact_kernel(const Table t, int32_t* held_out, void* scratch) {
+    __shared__ u64 warps[32], totals[2][kCtas];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), tid = threadIdx.x, all_threads = kCtas * kThreads;
+    cluster.barrier_arrive();  // this CTA runs
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
     const CompactScratch s(scratch, t);
-    const Span span = span_of(t.num_pages, rank);
-    // held pages
-    u64 x = 0, all;
-    each_page(t, span, [&](int, int r) { x += r > 0 ? 1 : 0; });
-    block_scan(x, warps, all);
-    if (tid == 0) s.head[2 + rank] = (int)all;
+    const Held held(t, span_of(t.num_pages, rank));
+    u64 all;
+    block_scan(held.count(t), warps, all);
+    cluster.barrier_wait();
+    tell(cluster, totals[0], all);
     cluster.sync();
     int n = 0;
-    for (int c = 0; c < kCtas; ++c) n += s.head[2 + c];
+    for (int c = 0; c < kCtas; ++c) n += (int)totals[0][c];
     // free ones among the first n (low half), held ones behind (high half), and their ranks
-    x = 0;
-    each_page(t, span, [&](int p, int r) { x += p < n ? (r <= 0 ? 1ull : 0) : r > 0 ? 1ull << 32 : 0; });
+    u64 x = 0;
+    held.each(t, [&](int p, bool is_held) { x += p < n ? (is_held ? 0 : 1ull) : is_held ? 1ull << 32 : 0; });
     u64 at = block_scan(x, warps, all);
-    if (tid == 0) {
-        s.head[10 + rank] = (int)(uint32_t)all;
-        s.head[18 + rank] = (int)(all >> 32);
-    }
+    tell(cluster, totals[1], all);
     cluster.sync();
     int moves = 0;
     for (int c = 0; c < kCtas; ++c) {
-        if (c < rank) at += (u64)(uint32_t)s.head[10 + c] | (u64)(uint32_t)s.head[18 + c] << 32;
-        moves += s.head[18 + c];
+        if (c < rank) at += totals[1][c];
+        moves += (int)(totals[1][c] >> 32);
     }
     uint32_t gap = (uint32_t)at, out = (uint32_t)(at >> 32);
-    each_page(t, span, [&](int p, int r) {
+    held.each(t, [&](int p, bool is_held) {
         if (p < n) {
-            if (r <= 0) s.dst[gap++] = p;
-        } else if (r > 0) {
+            if (!is_held) s.dst[gap++] = p;
+        } else if (is_held) {
+            s.move[p] = (int)out;
             s.src[out++] = p;
         } else {
-            s.to[p] = -1;
+            s.move[p] = -1;
         }
     });
     if (rank == 0 && tid == 0) {
         s.head[0] = moves;
         s.head[1] = n;
-        held[0] = n;
-    }
-    cluster.sync();
-    for (int r = rank * kThreads + tid; r < moves; r += all_threads) {
-        const int from = s.src[r], to = s.dst[r];
-        s.to[from] = to;
-        t.refs[to] = t.refs[from];
-        t.refs[from] = 0;
+        held_out[0] = n;
     }
 }
 
 // The rows' entries of pages that move.
-__device__ void retarget(const Table& t, const int32_t* seqlens, const int32_t* to, int n) {
+__device__ __forceinline__ void retarget(const Table& t, const int32_t* seqlens, const CompactScratch& s, int n) {
     const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
     for (int w = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); w < t.batch * kRowParts; w += warps) {
         const int b = w / kRowParts, part = w % kRowParts;
@@ -408,7 +431,8 @@ __device__ void retarget(const Table& t, const int32_t* seqlens, const int32_t* 
             if (!valid_page(t, p)) {
                 raise_status(ATTN_SINK_DEV_PAGE_OOB);
             } else if (p >= n) {
-                if (to[p] >= 0) row[i] = to[p];
+                const int r = s.move[p];
+                if (r >= 0) row[i] = s.dst[r];
                 else raise_status(ATTN_SINK_DEV_POOL);  // held by a row, but not counted
             }
         }
@@ -477,19 +501,25 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const Pools p, const
     copy_pages(p, src, dst, count ? min(n, *count) : n, num_pages, report);
 }
 
-// What follows compact_kernel: the table's entries and the pages.
+// What follows compact_kernel: the counts, the table's entries and the pages.
 __global__ void __launch_bounds__(kCopyThreads) move_kernel(const Pools p, const Table t, const int32_t* seqlens, void* scratch) {
     const CompactScratch s(scratch, t);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the decisions are complete
-    retarget(t, seqlens, s.to, s.head[1]);
-    if (p.count) copy_pages(p, s.src, s.dst, s.head[0], t.num_pages, false);
+    const int moves = s.head[0];
+    for (int r = blockIdx.x * kCopyThreads + threadIdx.x; r < moves; r += gridDim.x * kCopyThreads) {
+        const int from = s.src[r], to = s.dst[r];
+        t.refs[to] = t.refs[from];
+        t.refs[from] = 0;
+    }
+    retarget(t, seqlens, s, s.head[1]);
+    if (p.count) copy_pages(p, s.src, s.dst, moves, t.num_pages, false);
 }
 
 // ---------------------------------------------------------------------------
 // Host side.
 
-size_t reserve_scratch(const Table& t) { return (16 + 3 * (size_t)t.num_pages + 3 * (size_t)t.batch) * 4; }
-size_t compact_scratch(const Table& t) { return (32 + 3 * (size_t)t.num_pages) * 4; }
+size_t reserve_scratch(const Table& t) { return (16 + 3 * (size_t)t.num_pages + 6 * (size_t)t.batch) * 4; }
+size_t compact_scratch(const Table& t) { return (16 + 3 * (size_t)t.num_pages) * 4; }
 
 // Pieces that copies are cut into.
 static Pools with_pieces(const Pools& p) {
