@@ -147,6 +147,27 @@ def test_a_pool_of_many_pages(ext):
     assert ext.device_status() == 0
 
 
+@pytest.mark.parametrize("pool,rows,skew", [(600000, 3, 0), (700001, 3, 1), (20000, 9000, 0), (3000, 70, 3)])
+def test_more_pages_and_requests_than_threads_hold(ext, pool, rows, skew):
+    """Pools above 524288 pages, more requests than the cluster has threads, counts off a 16-byte border."""
+    g = np.random.default_rng(pool)
+    top = pool // (3 * rows)
+    s = Both(ext, g.integers(0, top + 1, rows).tolist(), 1, pool, top + 2, seed=1, kinds=("scales",))
+    refs = torch.zeros(pool + skew, dtype=torch.int32, device="cuda")[skew:]
+    s.refs = refs.copy_(s.refs)
+    s.compact()
+    s.same()
+    s.reserve((s.m.lens + g.integers(0, 3, rows)).clip(max=top + 2).tolist())
+    s.same()
+    s.release((s.m.lens // 2).tolist())
+    s.fork(g.integers(0, rows, rows).tolist())
+    s.reserve((s.m.lens + 1).tolist())
+    s.same()
+    s.compact()
+    s.same()
+    assert ext.device_status() == 0
+
+
 def test_copies(ext):
     for shape, dtype in (((9, 13), torch.uint8), ((9, 16, 2, 64), torch.bfloat16), ((9, 3), torch.float32), ((9, 70001), torch.int16),
                          ((9, 1 << 18), torch.float32)):
