@@ -1053,7 +1053,7 @@ int run_attend_q8(const char* who, const attn::q8::AttendArgs& a, const attn::q8
 
 // Which kernels compute new tokens over an 8-bit cache, by what a request has at most (n new tokens,
 // g query heads of a KV head; times of 16 requests of 1k to 16k tokens, 8 KV heads):
-//  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 139 us, chain
+//  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 133 us, chain
 //    149; 16: 266, chain 152), 32 at 128 (16 rows: 87, chain 260; 64: 319, chain 285), and up
 //    to four times as many where its CTAs are all resident at once (one request of 2000 tokens,
 //    128 rows: 14.4 us, chain 27; 256: 18.5, chain 31);

@@ -581,15 +581,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : D == 64 ? 4 : 3) atten
     }
 }
 
-// One block per (query head, new token, request): its warps take the splits in turn, 4 in flight, a lane
-// D / 32 dims.
-template <int D, int NT>
+// A row (query head, new token, request) by W warps of a block, which take its splits in turn, 4 in flight, a
+// lane D / 32 dims.
+template <int D, int NT, int W>
 __global__ void __launch_bounds__(128) attend_combine_kernel(const Params p) {
-    constexpr int N = D / 32, kW = 4;
-    __shared__ float sm[kW][D + 2];
-    const int head = blockIdx.x, tok = blockIdx.y, b = blockIdx.z, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int N = D / 32, kHeads = 4 / W;
+    __shared__ float sm[4][D + 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+    const int head = blockIdx.x * kHeads + warp / W, tok = blockIdx.y, b = blockIdx.z;
     const Request r = request_of(p, b, false);
-    if (tok >= r.Lq) {  // (no grid behind this one starts before attend_kernel has ended)
+    if (tok >= r.Lq || (kHeads > 1 && head >= p.hq)) {  // (no grid behind this one starts before attend_kernel has ended)
         asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
@@ -601,17 +602,18 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(const Params p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const size_t row = (size_t)(r.q_start + tok) * p.hq + head, base = row * p.max_splits;
     float M = -INFINITY, Z = 0.f, acc[N] = {};
-    for (int s0 = warp; s0 < nsplit; s0 += 4 * kW) {
+    for (int s0 = part; s0 < nsplit; s0 += 4 * W) {
         float2 ml[4];
-        float o[4][N];
+        alignas(16) float o[4][N];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int s = s0 + i * kW;
+            const int s = s0 + i * W;
             ml[i] = make_float2(-INFINITY, 0.f);
             if (s < nsplit) {
                 ml[i] = p.part_ml[base + s];
-#pragma unroll
-                for (int k = 0; k < N; ++k) o[i][k] = p.part_o[(base + s) * D + lane * N + k];
+                const float* const from = p.part_o + (base + s) * D + lane * N;
+                if constexpr (N == 2) *reinterpret_cast<float2*>(o[i]) = *reinterpret_cast<const float2*>(from);
+                else *reinterpret_cast<float4*>(o[i]) = *reinterpret_cast<const float4*>(from);
             }
         }
         const float m = fmaxf(M, fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)));
@@ -622,38 +624,50 @@ __global__ void __launch_bounds__(128) attend_combine_kernel(const Params p) {
         for (int k = 0; k < N; ++k) acc[k] *= g * g;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (s0 + i * kW < nsplit) {
+            if (s0 + i * W < nsplit) {
                 const float f = half_factor(ml[i].x - ref);
                 Z += ml[i].y * f * f;
 #pragma unroll
                 for (int k = 0; k < N; ++k) acc[k] += o[i][k] * f * f;
             }
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k) sm[warp][lane * N + k] = acc[k];
-    if (lane == 0) {
-        sm[warp][D] = M;
-        sm[warp][D + 1] = Z;
-    }
-    __syncthreads();
-    const int dd = threadIdx.x;
-    if (dd >= D) return;
     const float sg = p.sink ? p.sink[head] * ATTN_LOG2E : -INFINITY;
-    M = sg;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) M = fmaxf(M, sm[w][D]);
-    const float ref = M == -INFINITY ? 0.f : M;
-    Z = fast_exp2(sg - ref);
-    float a = 0.f;
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-        const float f = half_factor(sm[w][D] - ref);
-        Z += sm[w][D + 1] * f * f;
-        a += sm[w][dd] * f * f;
-    }
     float lse;
-    p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, a, lse));
-    if (p.lse && dd == 0) p.lse[p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row] = lse;
+    const size_t lse_at = p.lse_by_head ? (size_t)head * p.total_q + r.q_start + tok : row;
+    if constexpr (W == 1) {
+        const float m = fmaxf(M, sg), ref = m == -INFINITY ? 0.f : m, f = half_factor(M - ref);
+        Z = fast_exp2(sg - ref) + Z * f * f;
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+            const float a0 = finish(m, Z, acc[k] * f * f, lse), a1 = finish(m, Z, acc[k + 1] * f * f, lse);
+            *reinterpret_cast<uint32_t*>(p.out + row * D + lane * N + k) = pack_bf16x2(a0, a1);
+        }
+        if (p.lse && lane == 0) p.lse[lse_at] = lse;
+    } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) sm[warp][lane * N + k] = acc[k];
+        if (lane == 0) {
+            sm[warp][D] = M;
+            sm[warp][D + 1] = Z;
+        }
+        __syncthreads();
+        const int dd = threadIdx.x;
+        if (dd >= D) return;
+        M = sg;
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, sm[w][D]);
+        const float ref = M == -INFINITY ? 0.f : M;
+        Z = fast_exp2(sg - ref);
+        float a = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float f = half_factor(sm[w][D] - ref);
+            Z += sm[w][D + 1] * f * f;
+            a += sm[w][dd] * f * f;
+        }
+        p.out[row * D + dd] = __float2bfloat16_rn(finish(M, Z, a, lse));
+        if (p.lse && dd == 0) p.lse[lse_at] = lse;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -676,7 +690,7 @@ AttendPlan make_plan(const AttendArgs& a) {
     if (nvis < 1) nvis = 1;
     // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
     // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
-    // 81 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
+    // 79 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
     // share chunks converted once in shared memory, 100).
     const long long kv = (long long)a.batch * a.c.hkv, most8 = (long long)num_sms() * (a.c.head_dim == 64 ? 6 : 3);
     const long long least = (nvis + 255) / 256;
@@ -749,15 +763,22 @@ static cudaError_t run_form(const Params& p, const AttendArgs& a, const AttendPl
         if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
     }
     if constexpr (gather) return cudaGetLastError();
+    // A row's splits by one warp where the rows alone are 8 warps an SM and have few splits, by four else (8 drafted
+    // tokens of 16 requests 133 us, 139 by four; 64 requests of 1k to 32k tokens 207 and 208; 12 heads
+    // of 64 requests 153.2 and 152.4; at d 128, where a warp's share of a row is twice as long, 1 to 2 us slower).
+    const bool lone = D == 64 && pl.max_splits <= 16 && (long long)a.hq * a.total_q >= 8LL * num_sms();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.hq, a.max_q, a.batch);
+    cfg.gridDim = dim3(lone ? (a.hq + 3) / 4 : a.hq, a.max_q, a.batch);
     cfg.blockDim = dim3(128);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if ((e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT>, p)) != cudaSuccess) return e;
+    if constexpr (D == 64)
+        if (lone) e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT, 1>, p);
+    if (!lone) e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT, 4>, p);
+    if (e != cudaSuccess) return e;
     return cudaGetLastError();
 }
 

@@ -363,6 +363,37 @@ def test_extend_matches_definition(ext, case, fmt):
         at += n
 
 
+@pytest.mark.parametrize("requests,hq,most,fmt", [(450, 7, 1, "e4m3"), (420, 7, 1, "int8"), (80, 14, 4, "e4m3"), (70, 30, 2, "int8")])
+def test_many_rows_of_a_few_splits(ext, requests, hq, most, fmt):
+    """Batches whose rows each have their splits merged by one warp: requests of several splits among short
+    ones, ones without tokens and ones without rows, query heads that are no multiple of four."""
+    rng = np.random.default_rng(requests)
+    total = rng.integers(0, 200, requests)
+    total[:8] = [9000, 0, 6001, 2049, 1, 257, 4096, 8999]
+    new = np.minimum(rng.integers(0, most + 1, requests), total) if most > 1 else np.ones(requests, int)
+    new[:8] = [most, 0 if most > 1 else 1, most, most, 1, most, most, most]
+    c = Cache(total.tolist(), 1, 64, 16, 8, fmt, seed=requests)
+    g = torch.Generator().manual_seed(4)
+    q = torch.randn(int(new.sum()), hq, 64, generator=g).bfloat16()
+    sk = torch.rand(hq, generator=g) * 6 - 2
+    lens = torch.from_numpy(total).int().cuda()
+    for sink in (None, sk):
+        s = None if sink is None else sink.cuda()
+        if most == 1:
+            out, lse = ext.attn_sink_decode_paged_q8(q.cuda(), *c.dev(), lens, s)
+            lse = lse.t()
+        else:
+            out, lse = ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu(new.tolist()).cuda(), lens, most, int(total.max()), s)
+        assert ext.device_status() == 0
+        full = [so.expand(x.numpy(), z.numpy(), fmt) for x, z in zip(c.codes, c.scales)]
+        for b in list(range(8)) + rng.integers(8, requests, 20).tolist():
+            at, n, t = int(new[:b].sum()), int(new[b]), np.arange(total[b])
+            k, v = (x[c.table[b].numpy()[t // 16], t % 16] for x in full)
+            if n:
+                check(out[at:at + n].cpu(), lse[:, at:at + n].cpu(), q[at:at + n], k, v, so.chunk_seen(int(total[b]), n, 0, 0),
+                      None if sink is None else sink.numpy(), 2.0 ** -11)
+
+
 @pytest.mark.parametrize("n,hq", [(5, 4), (40, 32), (200, 4)])
 def test_extend_leaves_other_rows_alone(ext, n, hq):
     """Rows behind the last request's and rows past max_seqlen_q stay; requests with fewer tokens
