@@ -674,7 +674,9 @@ int attn_sink_pages_copy(void* const* pools, const long long* page_bytes, int nu
  * tokens), with its length; refs follow: the old rows' entries are given up, the new ones'
  * are held.  Nothing else is copied: a row that then grows into a page that it shares calls
  * attn_sink_pages_reserve first.  Entries behind a row's pages are -1.  out_table and
- * out_seqlens must not be the inputs.
+ * out_seqlens must not be the inputs.  An old length below 0 counts as 0 (the row gives a new
+ * one without tokens, and its own pages stay counted), one above the row as the whole row; a
+ * src outside [-1, batch) counts as -1.
  */
 int attn_sink_pages_fork(const int32_t* page_table, int32_t* refs, const int32_t* seqlens,
                          const int32_t* src, int batch, int out_batch, int max_pages, int page_size,
@@ -682,8 +684,8 @@ int attn_sink_pages_fork(const int32_t* page_table, int32_t* refs, const int32_t
 
 /*
  * Gives back the pages of requests that shrink from seqlens[b] to new_seqlens[b] tokens (0: all
- * of them): their entries become -1.  A new length above the old one sets ATTN_SINK_DEV_POOL
- * and changes nothing.
+ * of them): their entries become -1.  A new length above the old one (ATTN_SINK_DEV_POOL), and a
+ * new or old one out of range, change nothing.
  */
 int attn_sink_pages_release(int32_t* page_table, int32_t* refs, const int32_t* seqlens,
                             const int32_t* new_seqlens, int batch, int max_pages, int page_size, int num_pages,
@@ -708,7 +710,8 @@ int attn_sink_pages_reserve(void* const* pools, const long long* page_bytes, int
  * Brings the n held pages to the front: the i-th held page behind the first n goes to the i-th
  * free page among them, in all tensors, in the rows' entries and in refs.  The pages from n on are
  * free then.  Every entry that holds a page has to be in the given table: a page that is only
- * counted moves too, and who else remembers its number loses it.
+ * counted moves too, and who else remembers its number loses it.  In a row whose length is out of
+ * range every entry that names a page follows it.
  *   held     (1,) int32: n
  */
 int attn_sink_pages_compact(void* const* pools, const long long* page_bytes, int num_pools,

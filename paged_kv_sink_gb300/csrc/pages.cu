@@ -40,15 +40,18 @@ __device__ __forceinline__ int pages_of(int tokens, int page_size) {
     return tokens / page_size + (tokens % page_size ? 1 : 0);
 }
 
+// Whether a row can have `L` tokens; reported if not.
+__device__ __forceinline__ bool valid_length(const Table& t, int L) {
+    const bool fits = L >= 0 && L <= (long long)t.max_pages * t.page_size;
+    if (!fits) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
+    return fits;
+}
+
 // A length as the row can hold it.
 __device__ __forceinline__ int length_of(const Table& t, const int32_t* seqlens, int b) {
-    const long long cap = (long long)t.max_pages * t.page_size;
     const int L = seqlens[b];
-    if (L < 0 || L > cap) {
-        raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
-        return L < 0 ? 0 : (int)cap;
-    }
-    return L;
+    if (valid_length(t, L)) return L;
+    return L < 0 ? 0 : (int)((long long)t.max_pages * t.page_size);
 }
 
 __device__ __forceinline__ bool valid_page(const Table& t, int p) { return (unsigned)p < (unsigned)t.num_pages; }
@@ -101,7 +104,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) release_kernel(const Table t, 
                                                                  const int32_t* new_seqlens) {
     const int b = blockIdx.x * kRowWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (b >= t.batch) return;
-    const int L = length_of(t, seqlens, b), to = length_of(t, new_seqlens, b);
+    // (a row of which a length is no length keeps its pages: nobody knows which of them are in use)
+    const int L = seqlens[b], to = new_seqlens[b];
+    if (!valid_length(t, L) || !valid_length(t, to)) return;
     if (to > L && lane == 0) raise_status(ATTN_SINK_DEV_POOL);
     const int held = pages_of(L, t.page_size), keep = pages_of(to, t.page_size);
     int32_t* const row = t.table + (size_t)b * t.max_pages;
@@ -419,21 +424,23 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     }
 }
 
-// The rows' entries of pages that move.
+// The rows' entries of pages that move: those that a row holds, and all that are pages in a row
+// whose length is no length (its pages move as well).
 __device__ __forceinline__ void retarget(const Table& t, const int32_t* seqlens, const CompactScratch& s, int n) {
     const int lane = threadIdx.x & 31, warps = gridDim.x * (blockDim.x / 32);
     for (int w = blockIdx.x * (blockDim.x / 32) + (threadIdx.x >> 5); w < t.batch * kRowParts; w += warps) {
         const int b = w / kRowParts, part = w % kRowParts;
-        const int pages = pages_of(length_of(t, seqlens, b), t.page_size);
+        const bool known = valid_length(t, seqlens[b]);
+        const int pages = known ? pages_of(seqlens[b], t.page_size) : t.max_pages;
         int32_t* const row = t.table + (size_t)b * t.max_pages;
         for (int i = part * 32 + lane; i < pages; i += 32 * kRowParts) {
             const int p = row[i];
             if (!valid_page(t, p)) {
-                raise_status(ATTN_SINK_DEV_PAGE_OOB);
+                if (known) raise_status(ATTN_SINK_DEV_PAGE_OOB);
             } else if (p >= n) {
                 const int r = s.move[p];
                 if (r >= 0) row[i] = s.dst[r];
-                else raise_status(ATTN_SINK_DEV_POOL);  // held by a row, but not counted
+                else if (known) raise_status(ATTN_SINK_DEV_POOL);  // held by a row, but not counted
             }
         }
     }
