@@ -504,7 +504,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 0 : D == 64 ? 4 : 3) atten
             const float l = sum_g(l_run[nt][col]);
             const int j = nt * 8 + 2 * cc + col;
             if (g == 0) {
-                sm_m[warp * H + j] = ref[nt][col] == kNoRef ? -INFINITY : ref[nt][col];
+                // (a NaN moves no reference, but its sum is not 0: it is to be seen in the output)
+                sm_m[warp * H + j] = ref[nt][col] == kNoRef && l == 0.f ? -INFINITY : ref[nt][col];
                 sm_l[warp * H + j] = l;
             }
             float* const dst = sm_o + (warp * H + j) * D + g * (D / 8);

@@ -1,0 +1,54 @@
+"""The 8-bit attention where callers go to its ends: queries that are not numbers, scales far apart, more rows
+than announced, windows over requests with fewer tokens than rows, chains in rounds.
+
+Tolerances are those of test_q8_gpu.py; where V's scales lie 2^100 apart a weight's exponent is a number up to
+2^7, whose roundings (half a step of 2^-17 of the exponent, of its difference from the reference, and lg2's
+2^-22) change it by at most ln 2 (2^-18 + 2^-18 + 2^-22) < 2^-17, relative."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_ops_oracle as co
+from oracle import serving_oracle as so
+from cache_ops import cu, same
+from test_q8_gpu import Cache, check, ext  # noqa: F401  (ext: the fixture)
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+def lens_of(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("lens,new", [([100, 40], 1), ([1500, 900], 1), ([30000] + [64] * 70, 1), ([100, 40], 3), ([20000] + [64] * 70, 4)])
+def test_queries_that_are_not_numbers_show(ext, lens, new, sink, fmt):  # noqa: F811
+    """A NaN in a row's query makes its output and lse NaN (not the empty row's 0 and -inf), and no other's:
+    one CTA a row, splits merged as a cluster, and by a launch of their own."""
+    c = Cache(lens, 2, 64, 16, 16, fmt, seed=4)
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(len(lens) * new, 8, 64, generator=g).bfloat16()
+    bad = q.clone()
+    where = torch.zeros(q.shape[:2], dtype=torch.bool)
+    for row, head, dim in ((0, 0, slice(None)), (0, 6, 17), (new, 3, 63)):
+        bad[row, head, dim] = NAN
+        where[row, head] = True
+    sk = torch.rand(8, generator=g).cuda() if sink else None
+    dev, sl, c_q = c.dev(), lens_of(lens), cu([new] * len(lens)).cuda()
+
+    def call(x):
+        if new == 1:
+            return ext.attn_sink_decode_paged_q8(x.cuda(), *dev, sl, sk)
+        out, lse = ext.attn_sink_fwd_paged_q8(x.cuda(), *dev, c_q, sl, new, max(lens), sk)
+        return out, lse.t().contiguous()
+
+    (out, lse), (good, good_lse) = call(bad), call(q)
+    where = where.cuda()
+    assert torch.all(torch.isnan(out[where])) and torch.all(torch.isnan(lse[where]))
+    # (the references that others move to may differ, and with them the last bits: twice the tolerance, A <= max |v|)
+    out, good_out, most = out[~where].float(), good[~where].float(), float(c.scales[1].max()) * so.QMAX[fmt]
+    assert torch.all((out - good_out).abs() <= 2.0 ** -7 * good_out.abs() + 2.0 ** -9 * most)
+    assert torch.all((lse[~where] - good_lse[~where]).abs() <= 2.0 ** -9)
+    assert not torch.any(torch.isnan(good)) and ext.device_status() == 0
