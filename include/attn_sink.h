@@ -596,6 +596,9 @@ int attn_sink_decode_paged_q8(const attn_bf16* q, const void* k_cache, const voi
  * attn_sink_fwd_paged, with their rounding of the weights to bf16 (2^-8).  Position i of a
  * request's n rows is seqlens_k - n + i; rows before position 0 see nothing.  What rows that see
  * a token behind an out-of-range page id get is not defined; nothing outside the cache is read.
+ *   max_seqlen_q  host upper bound of a request's rows.  A request with more sets
+ *                 ATTN_SINK_DEV_SEQLEN_OOB; its rows up to the bound keep their positions, those past
+ *                 it are left as they were or computed
  *   max_seqlen_k  host upper bound of seqlens_k, which must hold (it sizes scratch and launches;
  *                 no memory behind the page table or the scratch is read where it does not)
  *   lse           (hq, total_q) fp32; may be NULL

@@ -1208,6 +1208,7 @@ int attn_sink_fwd_paged_q8(const attn_bf16* q, const void* k_cache, const void* 
         x.seqlens = seqlens_k + b0;
         x.batch = batch - b0 < round ? batch - b0 : round;
         x.pages = pages;
+        x.max_q = max_seqlen_q;
         x.win_first = win_first;
         x.win_last = win_last;
         x.k_out = reinterpret_cast<__nv_bfloat16*>(base);

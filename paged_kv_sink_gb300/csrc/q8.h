@@ -47,7 +47,7 @@ struct ExpandArgs {
     Cache c;
     const int32_t* cu_q;
     const int32_t* seqlens;
-    int batch, pages, win_first, win_last;
+    int batch, pages, max_q, win_first, win_last;  // max_q: rows of a request at most, else reported
     __nv_bfloat16* k_out;
     __nv_bfloat16* v_out;
     int32_t* table_out;  // (batch, pages)

@@ -293,6 +293,7 @@ __global__ void __launch_bounds__(kExpandThreads) expand_kernel(const ExpandArgs
         if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
         L = (int)cap;
     }
+    if (Lq > a.max_q && blockIdx.x == 0 && threadIdx.x == 0) raise_status(ATTN_SINK_DEV_SEQLEN_OOB);
     if (blockIdx.x == 0 && threadIdx.x == 0) a.lens_out[b] = max(L, 0);
     const int t0 = blockIdx.x * kExpandTokens;
     if (Lq == 0 || t0 >= L) return;

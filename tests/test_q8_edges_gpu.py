@@ -52,3 +52,27 @@ def test_queries_that_are_not_numbers_show(ext, lens, new, sink, fmt):  # noqa: 
     assert torch.all((out - good_out).abs() <= 2.0 ** -7 * good_out.abs() + 2.0 ** -9 * most)
     assert torch.all((lse[~where] - good_lse[~where]).abs() <= 2.0 ** -9)
     assert not torch.any(torch.isnan(good)) and ext.device_status() == 0
+
+
+@pytest.mark.parametrize("n,most,hq", [(9, 5, 4), (60, 40, 32), (400, 200, 4)])
+def test_more_rows_than_announced(ext, n, most, hq):  # noqa: F811
+    """A request of n rows where max_seqlen_q is fewer, in the row kernel, as a chain and in the forward: reported; the
+    rows up to the bound are right at their uncut positions, as are the other request's, and the rows behind both
+    requests stay.  (Those past the bound stay where the path goes by rows.)"""
+    lens, rows = [500, 300], [n, most - 1]
+    c = Cache(lens, 2, 64, 16, 16, "e4m3", seed=12)
+    q = torch.randn(sum(rows) + 3, hq, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    for first, last in ((0, 0), (20, 70)):
+        out, lse = torch.full_like(q, 7).cuda(), torch.full((hq, q.shape[0]), 7.0).cuda()
+        ext.device_status()
+        ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu(rows).cuda(), lens_of(lens), most, 500, None, first, last, out=out, lse=lse)
+        assert ext.device_status() == ext._lib.DEV_SEQLEN_OOB
+        assert torch.all(out[sum(rows):] == 7) and torch.all(lse[:, sum(rows):] == 7)
+        if most < 128:
+            assert torch.all(out[most:n] == 7) and torch.all(lse[:, most:n] == 7)
+        k, v = c.tokens(0)
+        seen = so.chunk_seen(500, n, first, last)[:most]
+        check(out[:most].cpu(), lse[:, :most].cpu(), q[:most], k, v, seen, None, 2.0 ** -8)
+        k, v = c.tokens(1)
+        at = slice(n, sum(rows))
+        check(out[at].cpu(), lse[:, at].cpu(), q[at], k, v, so.chunk_seen(300, most - 1, first, last), None, 2.0 ** -8)
