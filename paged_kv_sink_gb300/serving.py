@@ -100,7 +100,8 @@ def attn_sink_fwd_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu
                            max_seqlen_k, sink=None, win_first=0, win_last=0, causal=True, scale=0.0, out=None, lse=None,
                            return_lse=True, stream=None):
     """attn_sink_fwd_paged over an 8-bit cache that has the chunk's tokens already
-    (attn_sink_kv_append_q8): one to many query rows a request.  Returns (out, lse (Hq, T))."""
+    (attn_sink_kv_append_q8): one to many query rows a request.  max_seqlen_q and max_seqlen_k are
+    host bounds of the rows and lengths.  Returns (out, lse (Hq, T))."""
     dev = _device("q", q)
     if q.dim() != 3 or not _is(q, _BF16, dev, q.shape):
         _expect("q", q, _BF16, dev, (None, None, None))
@@ -109,9 +110,10 @@ def attn_sink_fwd_paged_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu
     npages, ps, hkv, _, max_pages, block, fmt = _expect_q8(k_cache, v_cache, k_scale, v_scale, page_table, dev, B, d)
     _expect_i32("cu_seqlens_q", cu_seqlens_q, dev, B + 1)
     out, lse, sp, op, lp = _outputs(q, dev, (hq, T), sink, out, lse, return_lse, stream)
+    max_seqlen_q, max_seqlen_k = min(int(max_seqlen_q), _NO_BOUND), min(int(max_seqlen_k), _NO_BOUND)
     _run("attn_sink_fwd_paged_q8", dev, stream, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
          v_scale.data_ptr(), block, fmt, page_table.data_ptr(), max_pages, cu_seqlens_q.data_ptr(), seqlens_k.data_ptr(), B,
-         T, hq, hkv, d, ps, npages, int(max_seqlen_q), int(max_seqlen_k), sp, int(win_first), int(win_last),
+         T, hq, hkv, d, ps, npages, max_seqlen_q, max_seqlen_k, sp, int(win_first), int(win_last),
          1 if causal else 0, float(scale), op, lp)
     return out, lse
 

@@ -76,3 +76,17 @@ def test_more_rows_than_announced(ext, n, most, hq):  # noqa: F811
         k, v = c.tokens(1)
         at = slice(n, sum(rows))
         check(out[at].cpu(), lse[:, at].cpu(), q[at], k, v, so.chunk_seen(300, most - 1, first, last), None, 2.0 ** -8)
+
+
+def test_bounds_above_int32_are_no_bounds(ext):  # noqa: F811
+    """A length bound that no int holds is taken as none; more rows than one call takes are refused."""
+    c = Cache([90, 40], 2, 64, 16, 16, "e4m3", seed=1)
+    q = torch.randn(10, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    args = (q, *c.dev(), cu([6, 4]).cuda(), lens_of([90, 40]))
+    want = ext.attn_sink_fwd_paged_q8(*args, 6, 2 ** 31 - 1)
+    for bound in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 40):
+        got = ext.attn_sink_fwd_paged_q8(*args, 6, bound)
+        assert same(got[0], want[0]) and same(got[1], want[1])
+        with pytest.raises(RuntimeError):
+            ext.attn_sink_fwd_paged_q8(*args, bound, 90)
+    assert ext.device_status() == 0
