@@ -29,9 +29,10 @@
 //    by attend_combine_kernel where it has more.
 // Bound by HBM: half the bytes of the bf16 cache.  64 requests of 1k to 32k tokens, 64 query
 // heads over 8 of 64 (1.2 GB): 207 us, of which the split grid has 200 (6.0 TB/s; the copy's rate is
-// 6.8); 32 windows of 8192 tokens, 32 over 8 of 128 (0.54 GB): 97 us.  24 warps an SM at d 64
-// (80 registers, 38 KB a CTA), 12 at d 128: more warps were worth more than more bytes in
-// flight (a third stage of the ring: 222 us).
+// 6.8); 32 windows of 8192 tokens, 32 over 8 of 128 (0.54 GB): 97 us.  Warps an SM, 38 KB of
+// shared memory a CTA at d 64, tiles of 8 rows: 24 in the e4m3 split grid (80 registers), 20
+// in the other seven forms (81 to 96), 12 at d 128: more warps were worth more than more bytes
+// in flight (a third stage of the ring: 222 us).
 #include "q8.cuh"
 
 #include <cooperative_groups.h>
@@ -39,6 +40,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 namespace cg = cooperative_groups;
 
@@ -679,48 +681,34 @@ static int max_tokens(const AttendArgs& a) {
     return a.max_seqlen < cap ? a.max_seqlen : (int)cap;
 }
 
-AttendPlan make_plan(const AttendArgs& a) {
-    AttendPlan pl;
-    const int group = a.hq / a.c.hkv;
-    const long long rows = (long long)group * a.max_q;
-    long long nvis = max_tokens(a);
-    if (a.win_last > 0) {  // a tile's rows are at most 16 tokens apart
-        const long long w = (long long)a.win_first + a.win_last + (a.max_q > 1 ? 16 : 0);
-        nvis = w < nvis ? w : nvis;
-    }
-    if (nvis < 1) nvis = 1;
-    // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
-    // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
-    // 79 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
-    // share chunks converted once in shared memory, 100).
-    const long long kv = (long long)a.batch * a.c.hkv, most8 = (long long)num_sms() * (a.c.head_dim == 64 ? 6 : 3);
-    const long long least = (nvis + 255) / 256;
-    pl.nt = rows <= 8 || (rows <= 4096 && least <= kGather && kv * ((rows + 7) / 8) * least <= most8) ? 1 : 2;
-    pl.tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
-    // Splits of 256 to 2048 tokens, in steps of what the CTA's warps take at once: those for which the
-    // waves of resident CTAs are shortest, a CTA's start and end counted as kStart tokens
-    // (64 requests of 1k to 32k tokens at d 128, 1024 a split: 402 us, 2048: 385; 32 windows of 8192,
-    // 4 and 8 splits: 107 us, 5: 99).
-    constexpr int kStep = kWarps * kTokens, kStart = 128, kLeast = 256, kMost = 2048;
-    const long long units = kv * pl.tiles;
-    const long long slots = pl.nt == 1 ? most8 : (long long)num_sms() * (a.c.head_dim == 64 ? 4 : 3);
-    long long best = -1;
-    for (int sp = kMost; sp >= kLeast; sp -= kStep) {
-        const long long n = (nvis + sp - 1) / sp, waves = (units * n + slots - 1) / slots, cost = waves * (sp + kStart);
-        if (best < 0 || cost < best) {
-            best = cost;
-            pl.split_tokens = sp;
-            pl.max_splits = (int)n;
-        }
-    }
-    // Few splits that are all resident at once merge as clusters (one launch, no scratch; 5 new tokens
-    // of one request of 2000 18.6 -> 14.4 us).  In a batch of several waves the CTAs that end early
-    // would wait for their cluster (64 requests of 1k to 16k tokens, 12 heads 162 -> 258 us).
-    pl.gather = pl.max_splits == 1 || (pl.max_splits <= kGather && units * pl.max_splits <= slots);
-    const size_t parts = !pl.gather ? (size_t)a.total_q * a.hq * pl.max_splits : 0;
-    pl.part_o_bytes = parts * a.c.head_dim * sizeof(float);
-    pl.part_ml_bytes = parts * sizeof(float2);
-    return pl;
+// One compiled form of attend_kernel.
+template <int D_, int NT_, int F_, bool kRows_, bool gather_>
+struct Form {
+    static constexpr int D = D_, NT = NT_, F = F_;
+    static constexpr bool kRows = kRows_, gather = gather_;
+    // Two stages and more CTAs rather than three (d 64: 6 of 38 KB instead of 4, 222 -> 212 us on 64
+    // requests of 1k to 32k tokens; d 128: 3 instead of 2, 426 -> 406).
+    static constexpr int kStages = 2;
+    static constexpr int kMerge = (kWarps + (gather ? 1 : 0)) * 8 * NT * (D + 2) * 4;
+    static constexpr int kSmem = Smem<D, kStages>::kBytes > kMerge ? Smem<D, kStages>::kBytes : kMerge;
+    static auto kernel() { return attend_kernel<D, NT, kStages, F, kRows, gather>; }
+};
+
+// f(form) of the form that a call takes.
+template <class Fn>
+static auto with_form(int head_dim, int nt, int format, bool rows, bool gather, Fn f) {
+    auto tail = [&](auto d, auto n, auto fm) {
+        constexpr int D = decltype(d)::value, NT = decltype(n)::value, F = decltype(fm)::value;
+        if (rows) return gather ? f(Form<D, NT, F, true, true>{}) : f(Form<D, NT, F, true, false>{});
+        return gather ? f(Form<D, NT, F, false, true>{}) : f(Form<D, NT, F, false, false>{});
+    };
+    auto middle = [&](auto d, auto n) {
+        return format == kE4M3 ? tail(d, n, std::integral_constant<int, kE4M3>{}) : tail(d, n, std::integral_constant<int, kInt8>{});
+    };
+    auto head = [&](auto d) {
+        return nt == 1 ? middle(d, std::integral_constant<int, 1>{}) : middle(d, std::integral_constant<int, 2>{});
+    };
+    return head_dim == 64 ? head(std::integral_constant<int, 64>{}) : head(std::integral_constant<int, 128>{});
 }
 
 // Shared memory above 48 KB is asked for once per kernel and device.
@@ -737,33 +725,122 @@ static cudaError_t allow_smem(Kernel kern, int bytes, std::atomic<uint64_t>& all
     return e;
 }
 
-template <int D, int NT, int F, bool kRows, bool gather>
-static cudaError_t run_form(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
-    // Two stages and more CTAs rather than three (d 64: 6 of 38 KB instead of 4, 222 -> 212 us on 64
-    // requests of 1k to 32k tokens; d 128: 3 instead of 2, 426 -> 406).
-    constexpr int STAGES = 2;
-    int smem = Smem<D, STAGES>::kBytes;
-    const int merge = (kWarps + (gather ? 1 : 0)) * 8 * NT * (D + 2) * 4;
-    if (smem < merge) smem = merge;
-    auto kern = attend_kernel<D, NT, STAGES, F, kRows, gather>;
+template <class Form>
+static cudaError_t allow_smem() {
     static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have its shared memory
-    cudaError_t e = allow_smem(kern, smem, allowed);
+    return allow_smem(Form::kernel(), Form::kSmem, allowed);
+}
+
+// Clusters of `size` CTAs of a form that `dev`, the current device, holds at once; the driver is asked
+// once for each form, size and device.
+template <class Form>
+static int resident_clusters(int dev, int size) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][kGather + 1];
+    int n = dev < kDevices ? known[dev][size].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    cudaError_t e = allow_smem<Form>();
+    if (e == cudaSuccess) {
+        if (size == 1) {
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, Form::kernel(), kThreads, Form::kSmem);
+            n *= num_sms();
+        } else {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = size;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(size, 32768);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = Form::kSmem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, Form::kernel(), &cfg);
+        }
+    }
+    if (e != cudaSuccess || n < 1) {
+        cudaGetLastError();  // (the launch reports what is wrong)
+        return 1;
+    }
+    if (dev < kDevices) known[dev][size].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+AttendPlan make_plan(const AttendArgs& a) {
+    AttendPlan pl;
+    const int group = a.hq / a.c.hkv;
+    const long long rows = (long long)group * a.max_q;
+    const bool several = a.max_q > 1 || !a.causal;
+    // What the device holds at once: CTAs of the split grid, clusters that merge.
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
+    auto ctas = [&](int nt) {
+        return (long long)with_form(a.c.head_dim, nt, a.c.format, several, false,
+                                    [=](auto form) { return resident_clusters<decltype(form)>(dev, 1); });
+    };
+    auto clusters = [&](int nt, int size) {
+        return (long long)with_form(a.c.head_dim, nt, a.c.format, several, true,
+                                    [=](auto form) { return resident_clusters<decltype(form)>(dev, size); });
+    };
+    long long nvis = max_tokens(a);
+    if (a.win_last > 0) {  // a tile's rows are at most 16 tokens apart
+        const long long w = (long long)a.win_first + a.win_last + (a.max_q > 1 ? 16 : 0);
+        nvis = w < nvis ? w : nvis;
+    }
+    if (nvis < 1) nvis = 1;
+    // Rows of a tile: 8 where that leaves all CTAs resident at once (5 new tokens of one request of 2000, 8 heads
+    // a KV head: 10.3 us, 16 rows 12.3, 32 14.4), else 16 (drafts of 4 tokens of 16 requests of 1k to 16k:
+    // 79 us; 8 rows 110, which read K and V four times; 32 rows, with half the warps, 92; 32 rows by warps that
+    // share chunks converted once in shared memory, 100).
+    const long long kv = (long long)a.batch * a.c.hkv, least = (nvis + 255) / 256;
+    pl.nt = rows <= 8 || (rows <= 4096 && least <= kGather && kv * ((rows + 7) / 8) <= clusters(1, (int)least)) ? 1 : 2;
+    pl.tiles = (int)((rows + 8 * pl.nt - 1) / (8 * pl.nt));
+    // Splits of 256 to 2048 tokens, in steps of what the CTA's warps take at once: those for which the
+    // waves of resident CTAs are shortest, a CTA's start and end counted as kStart tokens
+    // (64 requests of 1k to 32k tokens at d 128, 1024 a split: 402 us, 2048: 385; 32 windows of 8192,
+    // 4 and 8 splits: 107 us, 5: 99).
+    constexpr int kStep = kWarps * kTokens, kStart = 128, kLeast = 256, kMost = 2048;
+    const long long units = kv * pl.tiles, slots = ctas(pl.nt);
+    long long best = -1;
+    for (int sp = kMost; sp >= kLeast; sp -= kStep) {
+        const long long n = (nvis + sp - 1) / sp, waves = (units * n + slots - 1) / slots, cost = waves * (sp + kStart);
+        if (best < 0 || cost < best) {
+            best = cost;
+            pl.split_tokens = sp;
+            pl.max_splits = (int)n;
+        }
+    }
+    // Few splits that are all resident at once merge as clusters (one launch, no scratch; 5 new tokens
+    // of one request of 2000 18.6 -> 14.4 us).  In a batch of several waves the CTAs that end early
+    // would wait for their cluster (64 requests of 1k to 16k tokens, 12 heads 162 -> 258 us); clusters that
+    // just do not fit cost as much (50 requests of 2000 tokens, d 64: merged 34.0 us, split 28.7).
+    pl.gather = pl.max_splits == 1 || (pl.max_splits <= kGather && units <= clusters(pl.nt, pl.max_splits));
+    const size_t parts = !pl.gather ? (size_t)a.total_q * a.hq * pl.max_splits : 0;
+    pl.part_o_bytes = parts * a.c.head_dim * sizeof(float);
+    pl.part_ml_bytes = parts * sizeof(float2);
+    return pl;
+}
+
+template <class Form>
+static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
+    constexpr int D = Form::D, NT = Form::NT;
+    cudaError_t e = allow_smem<Form>();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
     {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(pl.max_splits, a.c.hkv * pl.tiles, a.batch);
         cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
+        cfg.dynamicSmemBytes = Form::kSmem;
         cfg.stream = s;
         attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = gather ? pl.max_splits : 1;
+        attr[0].val.clusterDim.x = Form::gather ? pl.max_splits : 1;
         attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        if ((e = cudaLaunchKernelEx(&cfg, kern, p)) != cudaSuccess) return e;
+        if ((e = cudaLaunchKernelEx(&cfg, Form::kernel(), p)) != cudaSuccess) return e;
     }
-    if constexpr (gather) return cudaGetLastError();
+    if constexpr (Form::gather) return cudaGetLastError();
     // A row's splits by one warp where the rows alone are 8 warps an SM and have few splits, by four else (8 drafted
     // tokens of 16 requests 133 us, 139 by four; 64 requests of 1k to 32k tokens 207 and 208; 12 heads
     // of 64 requests 153.2 and 152.4; at d 128, where a warp's share of a row is twice as long, 1 to 2 us slower).
@@ -781,18 +858,6 @@ static cudaError_t run_form(const Params& p, const AttendArgs& a, const AttendPl
     if (!lone) e = cudaLaunchKernelEx(&cfg, attend_combine_kernel<D, NT, 4>, p);
     if (e != cudaSuccess) return e;
     return cudaGetLastError();
-}
-
-template <int D, int NT, int F, bool kRows>
-static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
-    return pl.gather ? run_form<D, NT, F, kRows, true>(p, a, pl, s) : run_form<D, NT, F, kRows, false>(p, a, pl, s);
-}
-
-template <int D, int F>
-static cudaError_t pick(const Params& p, const AttendArgs& a, const AttendPlan& pl, cudaStream_t s) {
-    const bool rows = a.max_q > 1 || !a.causal;
-    if (pl.nt == 1) return rows ? run<D, 1, F, true>(p, a, pl, s) : run<D, 1, F, false>(p, a, pl, s);
-    return rows ? run<D, 2, F, true>(p, a, pl, s) : run<D, 2, F, false>(p, a, pl, s);
 }
 
 cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part_o, float2* part_ml, cudaStream_t s) {
@@ -823,8 +888,8 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part
     p.split_tokens = pl.split_tokens;
     p.max_splits = pl.max_splits;
     p.scale_log2 = a.scale * ATTN_LOG2E;
-    if (a.c.head_dim == 64) return a.c.format == kE4M3 ? pick<64, kE4M3>(p, a, pl, s) : pick<64, kInt8>(p, a, pl, s);
-    return a.c.format == kE4M3 ? pick<128, kE4M3>(p, a, pl, s) : pick<128, kInt8>(p, a, pl, s);
+    return with_form(a.c.head_dim, pl.nt, a.c.format, a.max_q > 1 || !a.causal, pl.gather,
+                     [&](auto form) { return run<decltype(form)>(p, a, pl, s); });
 }
 
 ATTN_DEFINE_STATUS_ACCESSOR(attend_status_exchange)
