@@ -21,6 +21,7 @@
 #include "prefill.h"
 #include "q8.h"
 #include "rope.h"
+#include "status.h"
 #include "tree.h"
 #include "verify.h"
 
@@ -1458,20 +1459,29 @@ int attn_sink_pages_compact(void* const* pools, const long long* page_bytes, int
 
 int attn_sink_device_status(void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // every unit's word
+    constexpr cudaError_t (*kUnits[])(int**) = {
+        attn::decode::status_word,
+        attn::prefill::status_word,
+        attn::bwd::status_word,
+        attn::kvappend::status_word,
+        attn::rope::status_word,
+        attn::tree::status_word,
+        attn::evict::status_word,
+        attn::q8::append_status_word,
+        attn::q8::attend_status_word,
+        attn::verify::status_word,
+        attn::pages::status_word,
+        attn::selftest::status_word,
+    };
+    constexpr int kCount = sizeof(kUnits) / sizeof(kUnits[0]);
+    static_assert(kCount <= attn::status::kMaxWords, "a lane per word");
+    attn::status::Words w = {};
     int bits = 0;
-    int e = attn::decode::status_exchange(s, &bits);
-    if (!e) e = attn::prefill::status_exchange(s, &bits);
-    if (!e) e = attn::bwd::status_exchange(s, &bits);
-    if (!e) e = attn::kvappend::status_exchange(s, &bits);
-    if (!e) e = attn::rope::status_exchange(s, &bits);
-    if (!e) e = attn::tree::status_exchange(s, &bits);
-    if (!e) e = attn::evict::status_exchange(s, &bits);
-    if (!e) e = attn::q8::append_status_exchange(s, &bits);
-    if (!e) e = attn::q8::attend_status_exchange(s, &bits);
-    if (!e) e = attn::verify::status_exchange(s, &bits);
-    if (!e) e = attn::pages::status_exchange(s, &bits);
-    if (!e) e = attn::selftest::status_exchange(s, &bits);
-    if (e) return cuda_fail(static_cast<cudaError_t>(e), "device_status");
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < kCount && e == cudaSuccess; ++i) e = kUnits[i](&w.at[i]);
+    if (e == cudaSuccess) e = attn::status::exchange(w, s, &bits);
+    if (e != cudaSuccess) return cuda_fail(e, "device_status");
     return bits;
 }
 

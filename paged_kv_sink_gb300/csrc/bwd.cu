@@ -1511,7 +1511,7 @@ cudaError_t launch(const Args& a, void* workspace, size_t ws_bytes, cudaStream_t
     return a.head_dim == 128 ? launch_d<128>(a, workspace, s, what) : launch_d<64>(a, workspace, s, what);
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace bwd
 }  // namespace attn

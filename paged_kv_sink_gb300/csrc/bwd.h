@@ -35,7 +35,7 @@ struct Args {
 
 size_t workspace_bytes(const Args& a);
 cudaError_t launch(const Args& a, void* workspace, size_t ws_bytes, cudaStream_t s, std::string* what);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace bwd
 }  // namespace attn

@@ -13,28 +13,18 @@
 namespace attn {
 
 // Sticky device status word (ATTN_SINK_DEV_* bits).  Each translation unit
-// has its own copy (no relocatable device code is needed); the host side ORs
-// them together through the accessor each unit defines with
-// ATTN_DEFINE_STATUS_ACCESSOR.
+// has its own copy (no relocatable device code is needed); the host side finds
+// them through the accessor each unit defines with ATTN_DEFINE_STATUS_ACCESSOR
+// and has them read together (status.h).
 static __device__ int g_dev_status;
 
 __device__ __forceinline__ void raise_status(int bits) { atomicOr(&g_dev_status, bits); }
 
-// Defines `int fn(cudaStream_t s, int* bits)`: adds this unit's status bits
-// to *bits and clears them (stream-ordered; the caller synchronises).
-#define ATTN_DEFINE_STATUS_ACCESSOR(fn)                                              \
-    int fn(cudaStream_t s, int* host_bits) {                                         \
-        int v = 0;                                                                   \
-        cudaError_t e = cudaMemcpyFromSymbolAsync(&v, attn::g_dev_status, sizeof(int), 0, \
-                                                  cudaMemcpyDeviceToHost, s);       \
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);                          \
-        if (e != cudaSuccess) return (int)e;                                         \
-        *host_bits |= v;                                                             \
-        int zero = 0;                                                                \
-        e = cudaMemcpyToSymbolAsync(attn::g_dev_status, &zero, sizeof(int), 0,       \
-                                    cudaMemcpyHostToDevice, s);                      \
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);                          \
-        return (int)e;                                                               \
+// Defines `cudaError_t fn(int** word)`: where this unit's status word is on the
+// current device.
+#define ATTN_DEFINE_STATUS_ACCESSOR(fn)                                               \
+    cudaError_t fn(int** word) {                                                      \
+        return cudaGetSymbolAddress(reinterpret_cast<void**>(word), attn::g_dev_status); \
     }
 
 // SMs of the current device (152 on GB300), asked for once per device and unit.

@@ -750,7 +750,7 @@ cudaError_t launch_visible_slots(const int32_t* seqlens, const int32_t* page_tab
     return cudaGetLastError();
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace decode
 }  // namespace attn

@@ -85,7 +85,7 @@ cudaError_t launch_visible_ranges(const int32_t* seqlens, int batch, int win_fir
 cudaError_t launch_visible_slots(const int32_t* seqlens, const int32_t* page_table, int max_pages,
                                  int batch, int page_size, int num_pages, int win_first, int win_last,
                                  int32_t* slots, int max_visible, cudaStream_t s);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace decode
 

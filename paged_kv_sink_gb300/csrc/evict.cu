@@ -494,7 +494,7 @@ cudaError_t launch_move(const MoveArgs& a, cudaStream_t s) {
     return a.first_moved ? choose(std::false_type{}) : choose(std::true_type{});
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace evict
 }  // namespace attn

@@ -38,7 +38,7 @@ struct MoveArgs {
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t s);
 cudaError_t launch_move(const MoveArgs& a, cudaStream_t s);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace evict
 }  // namespace attn

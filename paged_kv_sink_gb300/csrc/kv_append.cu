@@ -68,7 +68,7 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace kvappend
 }  // namespace attn

@@ -606,7 +606,7 @@ cudaError_t launch_compact(const Pools& p, const Table& t, const int32_t* seqlen
     return launch_behind((unsigned)grid, true, s, move_kernel, q, t, seqlens, scratch);
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace pages
 }  // namespace attn

@@ -40,7 +40,7 @@ cudaError_t launch_reserve(const Pools& p, const Table& t, const int32_t* seqlen
                            int32_t* missing, void* scratch, cudaStream_t s);
 cudaError_t launch_compact(const Pools& p, const Table& t, const int32_t* seqlens, int32_t* held, void* scratch,
                            cudaStream_t s);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace pages
 }  // namespace attn

@@ -32,7 +32,7 @@ struct FwdArgs {
 };
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s, std::string* what);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace prefill
 }  // namespace attn

@@ -1191,7 +1191,7 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t s, std::string* what) {
     return launch_fwd_d<64>(a, s, what);
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace prefill
 }  // namespace attn

@@ -81,8 +81,8 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t s);
 AttendPlan make_plan(const AttendArgs& a);
 cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part_o, float2* part_ml, cudaStream_t s);
-int append_status_exchange(cudaStream_t s, int* host_bits);
-int attend_status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t append_status_word(int** word);
+cudaError_t attend_status_word(int** word);
 
 }  // namespace q8
 }  // namespace attn

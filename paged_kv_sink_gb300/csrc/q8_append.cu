@@ -380,7 +380,7 @@ cudaError_t launch_expand(const ExpandArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(append_status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(append_status_word)
 
 }  // namespace q8
 }  // namespace attn

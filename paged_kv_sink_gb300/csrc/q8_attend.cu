@@ -892,7 +892,7 @@ cudaError_t launch_attend(const AttendArgs& a, const AttendPlan& pl, float* part
                      [&](auto form) { return run<decltype(form)>(p, a, pl, s); });
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(attend_status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(attend_status_word)
 
 }  // namespace q8
 }  // namespace attn

@@ -291,7 +291,7 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
                              : launch_d<128, kHalfAny>(a, s);
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace rope
 }  // namespace attn

@@ -31,7 +31,7 @@ cudaError_t launch_wait(int complete, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace selftest
 }  // namespace attn

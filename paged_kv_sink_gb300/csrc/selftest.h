@@ -7,7 +7,7 @@ namespace attn {
 namespace selftest {
 
 cudaError_t launch_wait(int complete, cudaStream_t s);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace selftest
 }  // namespace attn

@@ -1149,7 +1149,7 @@ cudaError_t launch(const Args& a, const Plan& pl, void* scratch, cudaStream_t s,
     return a.head_dim == 64 ? launch_d<64>(a, pl, scratch, s, what) : launch_d<128>(a, pl, scratch, s, what);
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace tree
 }  // namespace attn

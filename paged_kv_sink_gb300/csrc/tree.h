@@ -40,7 +40,7 @@ struct Plan {
 
 Plan make_plan(const Args& a);
 cudaError_t launch(const Args& a, const Plan& pl, void* scratch, cudaStream_t s, std::string* what);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace tree
 }  // namespace attn

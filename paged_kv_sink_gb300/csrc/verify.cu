@@ -526,7 +526,7 @@ cudaError_t launch(const Args& a, cudaStream_t s) {
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-ATTN_DEFINE_STATUS_ACCESSOR(status_exchange)
+ATTN_DEFINE_STATUS_ACCESSOR(status_word)
 
 }  // namespace verify
 }  // namespace attn

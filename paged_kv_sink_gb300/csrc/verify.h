@@ -28,7 +28,7 @@ struct Args {
 };
 
 cudaError_t launch(const Args& a, cudaStream_t s);
-int status_exchange(cudaStream_t s, int* host_bits);
+cudaError_t status_word(int** word);
 
 }  // namespace verify
 }  // namespace attn
