@@ -565,13 +565,14 @@ int attn_sink_kv_append_q8(const attn_bf16* k_new, const attn_bf16* v_new, long 
                            void* k_cache, void* v_cache, float* k_scale, float* v_scale, void* stream);
 
 /*
- * attn_sink_decode_paged over the 8-bit cache.  Scales may be any positive finite numbers
- * (those of V count as at least 2^-64), not only those that the append writes; the codes of a
- * request's tokens have to be numbers (the append writes no NaN).  The products are
+ * attn_sink_decode_paged over the 8-bit cache.  Scales may be any positive numbers up to 2^122
+ * (those of V count as at least 2^-64), not only the powers of two that the append writes; the codes
+ * of a request's tokens have to be numbers (the append writes no NaN).  The products are
  * fp16 with fp32 accumulation, in which both formats are exact: q enters them off by at
- * most 2^-25 of its row's largest magnitude, the weights by at most 2^-11 of each, and
- * weights below 2^-31 of the largest (times its V scale) are lost; scores, sums and
- * lse are fp32.
+ * most 2^-25 of its row's largest magnitude, a weight times its V scale by at most 2^-11 of
+ * itself or 2^-32 of the row's largest such product, whichever is more; scores, sums and lse are
+ * fp32.  Where V's scales of the tokens that a row sees are more than 2^100 apart, tokens
+ * of the small ones may be missing from the denominator and lse too.
  *
  *   max_seqlen  host bound of seqlens (INT_MAX: none); sizes launches and scratch.  Lengths
  *               past it are cut there (ATTN_SINK_DEV_SEQLEN_OOB)

@@ -20,10 +20,11 @@
 //  * Scales stay out of the products: ks multiplies the scores; vs is folded into the
 //    weights as log2(vs) in the exponent, P = 2^(s log2 e + log2 vs - ref), with the
 //    reference kept 7 to 15 below the running maximum of the exponents (it moves, and what came
-//    before is rescaled, only where a weight would pass 2^15): P never leaves fp16's range,
-//    and what falls below 2^-31 of the largest weight is lost.  Its rounding to fp16 is off by
-//    at most 2^-11 of each weight (bf16: 2^-8).  The denominator sums P / vs, unrounded, in
-//    fp32.
+//    before is rescaled, only where a weight would pass 2^15): P never leaves fp16's range.
+//    Its rounding to fp16 is off by at most 2^-11 of a weight (bf16: 2^-8), and among fp16's
+//    subnormals, below 2^-21 of the largest, by half their step: at most 2^-32 of the
+//    largest.  The denominator sums P / vs, unrounded, in fp32: it loses a token where P falls
+//    below 2^-126, which takes V scales 2^100 apart and more, or a share below 2^-33.
 //  * The splits are merged in the log-sum-exp sense and the sink is folded in once: by the
 //    cluster that they form, through distributed shared memory, where a row has at most 8,
 //    by attend_combine_kernel where it has more.

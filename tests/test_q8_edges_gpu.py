@@ -54,6 +54,54 @@ def test_queries_that_are_not_numbers_show(ext, lens, new, sink, fmt):  # noqa: 
     assert not torch.any(torch.isnan(good)) and ext.device_status() == 0
 
 
+@pytest.mark.parametrize("apart", [24, 28, 30])
+def test_weights_beside_much_larger_scales(ext, apart):  # noqa: F811
+    """Blocks of V's scale 2^apart whose codes are 0 in the upper dims, where only the other blocks (scale 1)
+    count: their weights are off by 2^-11 of each or 2^-32 of the largest, times the V scales, whichever is more."""
+    n, d, block = 512, 64, 16
+    c = Cache([n], 1, d, 16, block, "int8", seed=apart, spread=0)
+    t = np.arange(n)
+    page = c.table[0].numpy()[t // 16]
+    large = (t // block) % 2 == 0
+    c.scales[0][:] = 2.0 ** -9
+    c.scales[1][:] = 1.0
+    c.scales[1][page[large]] = 2.0 ** apart
+    codes = c.codes[1].view(torch.int8)
+    for p in np.unique(page[large]):
+        codes[p, :, :, 32:] = 0
+    q = torch.randn(1, 4, d, generator=torch.Generator().manual_seed(1)).bfloat16()
+    out, lse = ext.attn_sink_decode_paged_q8(q.cuda(), *c.dev(), lens_of([n]))
+    k, v = c.tokens(0)
+    O, L, P, A = co.attend(q, k, v, np.ones((1, n), bool), None, d ** -0.5)
+    P = np.asarray(P).reshape(4, n)
+    vs = np.where(large, 2.0 ** apart, 1.0)
+    off = np.maximum(2.0 ** -11 * P * vs, 2.0 ** -32 * (P * vs).max(1, keepdims=True))
+    bound = np.einsum("ht,td->hd", off / vs, np.abs(v[:, 0]))
+    S = d ** -0.5 * np.abs(co.to_np(q)).max() * np.abs(k).sum(-1).max()
+    delta = (d + 8) * 2.0 ** -24 * S
+    err = np.abs(co.to_np(out)[0] - O[0])
+    assert np.all(err <= 2.0 ** -8 * np.abs(O[0]) + bound + (2 * delta + 2.0 ** -17) * A[0])
+    assert np.all(np.abs(co.to_np(lse)[0] - L[:, 0]) <= delta + 2.0 ** -17)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("new", [1, 4])
+def test_scales_of_v_up_to_two_to_the_hundred_apart(ext, new, fmt):  # noqa: F811
+    """The denominator and lse know nothing of V's scales."""
+    n, d = 700, 64
+    c = Cache([n], 2, d, 16, 16, fmt, seed=9)
+    g = torch.Generator().manual_seed(9)
+    c.scales[1] = torch.exp2(50.0 * (torch.randint(0, 2, c.scales[1].shape, generator=g) * 2 - 1))
+    q = torch.randn(new, 8, d, generator=g).bfloat16()
+    out, lse = ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu([new]).cuda(), lens_of([n]), new, n)
+    k, v = c.tokens(0)
+    O, L, P, A = co.attend(q, k, v, so.chunk_seen(n, new), None, d ** -0.5)
+    S = d ** -0.5 * np.abs(co.to_np(q)).max() * np.abs(k).sum(-1).max()
+    delta = (d + 8) * 2.0 ** -24 * S
+    assert np.all(np.abs(co.to_np(lse) - L) <= delta + 2.0 ** -17)
+    assert np.all(np.abs(co.to_np(out) - O) <= 2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2 * delta + 2.0 ** -16) * A)
+
+
 @pytest.mark.parametrize("n,most,hq", [(9, 5, 4), (60, 40, 32), (400, 200, 4)])
 def test_more_rows_than_announced(ext, n, most, hq):  # noqa: F811
     """A request of n rows where max_seqlen_q is fewer, in the row kernel, as a chain and in the forward: reported; the
