@@ -126,6 +126,46 @@ def test_more_rows_than_announced(ext, n, most, hq):  # noqa: F811
         check(out[at].cpu(), lse[:, at].cpu(), q[at], k, v, so.chunk_seen(300, most - 1, first, last), None, 2.0 ** -8)
 
 
+@pytest.mark.parametrize("n,hq,d", [(6, 4, 64), (40, 32, 64), (90, 32, 128), (200, 4, 64)])
+@pytest.mark.parametrize("first,last", [(0, 3), (4, 9), (2, 500)])
+def test_windows_over_fewer_tokens_than_rows(ext, n, hq, d, first, last):  # noqa: F811
+    """Requests whose first rows stand before position 0 and see nothing, under a window, in each path."""
+    lens = [n - 3, 1, 0, n // 2]
+    c = Cache(lens, 2, d, 16, 16, "int8", seed=n)
+    q = torch.randn(4 * n, hq, d, generator=torch.Generator().manual_seed(2)).bfloat16()
+    out, lse = ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu([n] * 4).cuda(), lens_of(lens), n, max(lens), None, first, last)
+    assert ext.device_status() == 0
+    for b, length in enumerate(lens):
+        at = slice(b * n, (b + 1) * n)
+        k, v = c.tokens(b)
+        check(out[at].cpu(), lse[:, at].cpu(), q[at], k, v, so.chunk_seen(length, n, first, last), None, 2.0 ** -8)
+        none = max(0, n - length)
+        assert torch.all(out[at][:none] == 0) and torch.all(lse[:, at][:, :none] == float("-inf"))
+
+
+@pytest.mark.parametrize("first,last", [(0, 0), (30, 100)])
+def test_chains_go_in_rounds(ext, first, last):  # noqa: F811
+    """Chains whose expanded tokens do not fit the scratch together: requests of every round, ones with no rows
+    among them, against the definition."""
+    lens = [150 + 37 * b for b in range(24)]
+    rows = [(b * 7) % 41 for b in range(24)]
+    c = Cache(lens, 8, 64, 16, 16, "e4m3", seed=13)
+    wide = torch.full((24, 65536 // 16), -1, dtype=torch.int32)
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    q = torch.randn(sum(rows), 64, 64, generator=torch.Generator().manual_seed(1)).bfloat16()
+    sk = torch.rand(64, generator=torch.Generator().manual_seed(2)) * 4
+    # 24 requests of up to 65536 tokens at 2 KB each: 3.2 GB
+    out, lse = ext.attn_sink_fwd_paged_q8(q.cuda(), *c.dev(), cu(rows).cuda(), lens_of(lens), 40, 65536, sk.cuda(), first, last)
+    assert ext.device_status() == 0
+    at = 0
+    for b, n in enumerate(rows):
+        if n and b in (1, 2, 5, 11, 12, 13, 20, 23):
+            k, v = c.tokens(b)
+            check(out[at:at + n].cpu(), lse[:, at:at + n].cpu(), q[at:at + n], k, v, so.chunk_seen(lens[b], n, first, last), sk.numpy(), 2.0 ** -8)
+        at += n
+
+
 def test_bounds_above_int32_are_no_bounds(ext):  # noqa: F811
     """A length bound that no int holds is taken as none; more rows than one call takes are refused."""
     c = Cache([90, 40], 2, 64, 16, 16, "e4m3", seed=1)
