@@ -9,22 +9,7 @@
 namespace attn {
 namespace q8 {
 
-// Two codes (the low 16 bits of w) as a pair of fp16: both formats are exact in it.
-template <int F>
-__device__ __forceinline__ uint32_t pair_to_f16(uint32_t w) {
-    uint32_t r;
-    if constexpr (F == kE4M3) {
-        asm("{\n .reg .b16 lo;\n cvt.u16.u32 lo, %1;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n}" : "=r"(r) : "r"(w));
-    } else {
-        // 0x6400 + u is 1024 + u for a byte u = code + 128
-        const uint32_t u = __byte_perm(w ^ 0x8080u, 0x64646464u, 0x4140);
-        const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480)));
-        r = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return r;
-}
-
-// Four codes as two pairs of fp16, in order.
+// Four codes as two pairs of fp16, in order: both formats are exact in it.
 template <int F>
 __device__ __forceinline__ void quad_to_f16(uint32_t w, uint32_t& a, uint32_t& b) {
     if constexpr (F == kE4M3) {
@@ -32,7 +17,7 @@ __device__ __forceinline__ void quad_to_f16(uint32_t w, uint32_t& a, uint32_t& b
             : "=r"(a), "=r"(b)
             : "r"(w));
     } else {
-        const uint32_t x = w ^ 0x80808080u;
+        const uint32_t x = w ^ 0x80808080u;  // bytes u = code + 128; 0x6400 + u is 1024 + u
         const uint32_t u = __byte_perm(x, 0x64646464u, 0x4140), v = __byte_perm(x, 0x64646464u, 0x4342);
         const __half2 c = __half2half2(__ushort_as_half(0x6480));
         const __half2 p = __hsub2(*reinterpret_cast<const __half2*>(&u), c);
