@@ -1055,12 +1055,15 @@ int run_attend_q8(const char* who, const attn::q8::AttendArgs& a, const attn::q8
 // Which kernels compute new tokens over an 8-bit cache, by what a request has at most (n new tokens,
 // g query heads of a KV head; times of 16 requests of 1k to 16k tokens, 8 KV heads):
 //  * the row kernel, which reads codes, up to 64 rows n g at head dim 64 (8 tokens, g 8: 133 us, chain
-//    149; 16: 266, chain 152), 32 at 128 (16 rows: 87, chain 260; 64: 319, chain 285), and up
-//    to four times as many where its CTAs are all resident at once (one request of 2000 tokens,
-//    128 rows: 14.4 us, chain 27; 256: 18.5, chain 31);
+//    145; 9: 164, chain 145; int8 8: 146, chain 158; 10: 181, chain 158), 32 at 128 (g 4, int8, 32 rows:
+//    144, chain 277; on the chain's side of the border, 40: 186, chain 280; 64: 247, chain 283; e4m3 40: 176,
+//    chain 260; 56: 230, chain 261), and up to four times as many where its CTAs are all resident
+//    at once (one request of 2000 tokens, 128 rows: 14.4 us, chain 27; 256: 18.5, chain 31);
 //  * else, on the tokens expanded to bf16, the kernel of drafted trees on a chain, whose tiles hold
 //    (token, head) rows, up to 48 tokens at head dim 64 (32 tokens: 190 us, forward 403; 64 of 4
-//    requests: 79, forward 74), 96 at 128 (64: 89, forward 122; 128: 137, forward 127), g > 1;
+//    requests: 79, forward 74), 96 at 128 (64: 89, forward 122; 128: 137, forward 127), g > 1.
+//    g 2 at 64: 48 tokens 159, forward 200; 64: 170, 200; g 16: 363, 637; 477, 641.  g 2 at 128: 64
+//    tokens 313, 385; 96: 432, 389; 128: 460, 391; g 16: 954, 1146; 1440, 1155; 1995, 1163;
 //  * else the forward's, whose tiles hold 128 tokens of one head.
 bool few_rows(const attn::q8::AttendArgs& a, const attn::q8::AttendPlan& pl) {
     const long long rows = a.max_q * (long long)(a.hq / a.c.hkv), most = a.c.head_dim == 64 ? 64 : 32;

@@ -843,8 +843,9 @@ static cudaError_t run(const Params& p, const AttendArgs& a, const AttendPlan& p
     }
     if constexpr (Form::gather) return cudaGetLastError();
     // A row's splits by one warp where the rows alone are 8 warps an SM and have few splits, by four else (8 drafted
-    // tokens of 16 requests 133 us, 139 by four; 64 requests of 1k to 32k tokens 207 and 208; 12 heads
-    // of 64 requests 153.2 and 152.4; at d 128, where a warp's share of a row is twice as long, 1 to 2 us slower).
+    // tokens of 16 requests 133 us, 139 by four; 64 requests of 1k to 32k tokens, 16 splits, 207.9 and 209.2; 12 heads
+    // of 64 requests 153.2 and 152.4; beyond the border, 24 splits: decode 285.8 and 285.3, 8 drafted tokens 336 and
+    // 341, 32 splits: 392.5 and 392.4; at d 128, where a warp's share of a row is twice as long, 1 to 2 us slower).
     const bool lone = D == 64 && pl.max_splits <= 16 && (long long)a.hq * a.total_q >= 8LL * num_sms();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(lone ? (a.hq + 3) / 4 : a.hq, a.max_q, a.batch);

@@ -8,6 +8,8 @@
 // p_i = P + depth_i and sees the prefix tokens and its ancestors and itself, all by
 // the first/last-window rule at their positions:
 //     O_i = sum_j e^{s_ij - M} v_j / (e^{sink - M} + sum_j e^{s_ij - M}).
+// As a chain (node i on node i - 1: new tokens over an expanded 8-bit cache) a request may have
+// fewer tokens than nodes; P is negative then, and nodes before position 0 see nothing.
 //
 // All query heads of a KV head share its keys, so the 128 rows of a tensor-core
 // tile are (node, head of the group) pairs: 128 / G nodes of the G heads of one KV
